@@ -79,7 +79,12 @@ typedef enum {
 } nvmoe_status;
 
 /* Element types of activation / output buffers. */
-typedef enum { NVMOE_BF16 = 0, NVMOE_F32 = 1, NVMOE_F16 = 2 } nvmoe_dtype;
+typedef enum {
+  NVMOE_BF16 = 0,
+  NVMOE_F32 = 1,
+  NVMOE_F16 = 2,
+  NVMOE_E4M3 = 3   /* key / value caches only */
+} nvmoe_dtype;
 
 /* Programmatic dependent launch on the multi-launch path (routing,
  * quantisation, both GEMMs, requantisation, reduce): each kernel is launched
@@ -101,8 +106,8 @@ const char* nvmoe_status_str(int status);
    overwritten by the next failing call.  Host only, no device work. */
 const char* nvmoe_last_cuda_error(void);
 
-/* Library ABI version (major * 100 + minor): 200 (nvmoe_taps gained the
- * ready-flag members). */
+/* Library ABI version (major * 100 + minor): 201 (2.0: nvmoe_taps gained the
+ * ready-flag members; 2.1: the attn_* entry points). */
 int nvmoe_version(void);
 
 /* Number of kernels this library has enqueued in this process so far (all
@@ -590,6 +595,131 @@ int moe_nvfp4_layer_forward(const nvmoe_weights* weights, const void* x, int x_d
                             const int32_t* topk_ids, const float* topk_w, int64_t T, int k,
                             void* y, int y_dtype, const nvmoe_taps* taps, void* workspace,
                             size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------- attention of the layer --
+ * The operators in front of the expert FFN in a decoder layer: per-head RMS
+ * norm of queries and keys with the rotary embedding, appending keys and
+ * values to a paged cache, and attention of each request's new tokens over
+ * that cache.  No counterpart in the source pages.
+ *
+ * Head rows.  Queries, keys and values are bf16 [T, heads, head_dim] with a
+ * stride between tokens and one between heads, in elements (so views of one
+ * packed projection output are taken as they are); head_dim is contiguous.
+ * head_dim is 64 or 128.  Pointers are 16-byte aligned and strides multiples
+ * of 8 elements.
+ *
+ * Norm and rotation of a head row x, in fp32, rounded to bf16 (or E4M3) once:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        (weight NULL: y = x)
+ *   for each frequency i < rotary_dim / 2 with (a, b) = (y_i, y_{i + rotary_dim/2}),
+ *   or (y_{2i}, y_{2i+1}) when interleaved:
+ *     a' = a cos(p, i) - b sin(p, i),  b' = b cos(p, i) + a sin(p, i)
+ *   elements past rotary_dim are not turned.
+ *   weight      bf16 [head_dim] or NULL, one for queries and one for keys
+ *   rope        float [rope_positions, rotary_dim]: row p holds the
+ *               rotary_dim / 2 cosines of position p, then the sines; NULL:
+ *               no rotation.  rotary_dim is a multiple of 16, at most head_dim.
+ *
+ * attn_qk_norm_rope — both transforms in one launch, to dense or strided
+ * outputs.
+ *   positions   int32 [T]; a token whose position is outside
+ *               [0, rope_positions) sets NVMOE_ERR_DEVICE_BAD_INDEX in the
+ *               workspace status word and its rows are not written.  (Not
+ *               read, may be NULL, when rope is NULL.)
+ *   q_out, k_out  may be q and k themselves (with the same strides); other
+ *               overlaps are not allowed.
+ *   q or k may be NULL with 0 heads.
+ *   workspace   at least 256 bytes (the status word).
+ * Limits: T * (q_heads + kv_heads) < 2^31. */
+int attn_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                      const void* k, int64_t k_token_stride, int64_t k_head_stride, int kv_heads,
+                      int64_t T, int head_dim, const int32_t* positions, const float* rope,
+                      int64_t rope_positions, int rotary_dim, int interleaved,
+                      const void* q_weight, const void* k_weight, float eps, void* q_out,
+                      int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                      int64_t k_out_token_stride, int64_t k_out_head_stride, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+
+/* A paged cache of keys and values.  Element (page, offset, head, i) of k and
+ * of v lies at page * page_stride + offset * token_stride + head *
+ * head_stride + i (elements), so tokens-first [pages, page_size, kv_heads,
+ * head_dim] and heads-first [pages, kv_heads, page_size, head_dim] caches are
+ * both taken.
+ *   dtype       NVMOE_BF16, or NVMOE_E4M3: the stored value times k_scale[h]
+ *               (v_scale[h]) is the key (value); scales NULL: 1.
+ *   page_size   a power of two, 16 .. 1024; num_pages < 2^31
+ *   strides     multiples of 16 bytes, positive, below 2^40 bytes */
+typedef struct {
+  void* k;
+  void* v;
+  int dtype;
+  int kv_heads, head_dim, page_size;
+  int64_t num_pages;
+  int64_t page_stride, token_stride, head_stride;
+  const float* k_scale;   /* float [kv_heads] or NULL */
+  const float* v_scale;
+} nvmoe_kv_cache;
+
+/* The requests of one step.  Request r has the new tokens (rows of q, k, v)
+ * q_start[r] .. q_start[r+1]-1; they are the last ones of its kv_len[r] cached
+ * tokens, so token q_start[r] + i has position kv_len[r] - n + i with
+ * n = q_start[r+1] - q_start[r].  Position p lies in page
+ * page_table[r * max_pages + p / page_size] at offset p % page_size; table
+ * entries past a request's length are not read.
+ *   max_new     host-known bound on the new tokens of any request (>= 1) */
+typedef struct {
+  int batch;
+  int max_new;
+  int64_t tokens;             /* rows of q, k and v */
+  int64_t max_pages;          /* entries of a request's page table row */
+  const int32_t* q_start;     /* [batch + 1], ascending from 0 */
+  const int32_t* kv_len;      /* [batch] */
+  const int32_t* page_table;  /* [batch, max_pages] */
+} nvmoe_attn_batch;
+
+/* attn_kv_append — norm and rotation (at the cache position) of the new keys,
+ * and the new values as they are, into the cache; with q given, the queries'
+ * transform to q_out in the same launch.  E4M3: the fp32 value divided by the
+ * head's scale, saturating at +-448, rounded to nearest even.
+ * A token whose position is negative, past its page table row or (with rope)
+ * outside [0, rope_positions), or whose page id is outside [0, num_pages),
+ * sets NVMOE_ERR_DEVICE_BAD_INDEX and nothing of it is written; rows of no
+ * request (before q_start[0], from q_start[batch] on) are left alone.
+ *   q NULL (q_heads 0): keys and values only.  q_out may be q itself.
+ *   workspace   at least 256 bytes (the status word).
+ * Limits: tokens * (q_heads + 2 * kv_heads) < 2^31. */
+int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, const void* k,
+                   int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                   int64_t v_token_stride, int64_t v_head_stride, const void* q,
+                   int64_t q_token_stride, int64_t q_head_stride, int q_heads, void* q_out,
+                   int64_t q_out_token_stride, int64_t q_out_head_stride, const float* rope,
+                   int64_t rope_positions, int rotary_dim, int interleaved,
+                   const void* q_weight, const void* k_weight, float eps, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* attn_paged_forward — attention of every new token over its request's cache.
+ * Query head h reads key head h / (q_heads / kv_heads).  Token at position p
+ * sees the keys j <= p, with window > 0 only those with j > p - window:
+ *   s_j = scale * (q . k_j),  lse = log sum_j exp(s_j),
+ *   out = sum_j exp(s_j - lse) v_j        (bf16, rounded once)
+ * A token that sees no key (negative position) gets out = 0 and lse = -inf.
+ * Sums are fp32; exp(s_j - max) is rounded to 16 bits for the product with v.
+ *   out         bf16 [tokens, q_heads, head_dim] with strides
+ *   lse         float [tokens, q_heads] or NULL (natural logarithm)
+ *   workspace   attn_paged_workspace_size(...) bytes, whose first word is the
+ *               status word.
+ * A page id outside [0, num_pages) within a request's length, a kv_len past
+ * the page table row or more than max_new new tokens set
+ * NVMOE_ERR_DEVICE_BAD_INDEX: the page reads as zeros, the length is cut, the
+ * further tokens' rows are not written.  Rows of no request are left alone.
+ * Cache contents past a request's length are not used, whatever they hold.
+ * Limits: q_heads a multiple of kv_heads, tokens * q_heads < 2^31,
+ * max_pages * page_size < 2^31. */
+size_t attn_paged_workspace_size(int batch, int64_t tokens, int max_new, int q_heads,
+                                 int kv_heads, int head_dim);
+int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                       const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, float scale,
+                       int window, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                       float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

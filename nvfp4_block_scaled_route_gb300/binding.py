@@ -20,7 +20,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libnvfp4moe_debug.so" if os.environ.get("NVMOE_LIBRARY") == "debug"
                         else "libnvfp4moe.so")
 
-BF16, F32, F16 = 0, 1, 2
+BF16, F32, F16, E4M3 = 0, 1, 2, 3
 NVMOE_ERR_CUDA = 5
 TILE_ROWS = 128
 
@@ -51,11 +51,27 @@ class Taps(ctypes.Structure):
                 ("ready_value", ctypes.c_int), ("ready_wait_us", ctypes.c_int)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class AttnBatchArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_new", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
 PATH_AUTO, PATH_SEPARATE, PATH_FUSED, PATH_LAYER, PATH_SEPARATE_SINGLE = 0, 1, 2, 3, 4
 
 
 # name -> (restype, argtypes)
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "nvmoe_status_str": (ctypes.c_char_p, [_I]),
     "nvmoe_last_cuda_error": (ctypes.c_char_p, []),
@@ -93,6 +109,13 @@ SIGNATURES = {
     "moe_nvfp4_layer_workspace_size": (_SZ, [_I64, _I, _I, _I, _I]),
     "moe_nvfp4_layer_forward": (_I, [ctypes.POINTER(Weights), _P, _I, _P, _P, _I64, _I, _P, _I,
                                      ctypes.POINTER(Taps), _P, _SZ, _P]),
+    "attn_qk_norm_rope": (_I, [_P, _I64, _I64, _I, _P, _I64, _I64, _I, _I64, _I, _P, _P, _I64, _I,
+                               _I, _P, _P, _F, _P, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P]),
+    "attn_kv_append": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _I64,
+                            _I64, _P, _I64, _I, _I, _P, _P, _F, _P, _SZ, _P]),
+    "attn_paged_workspace_size": (_SZ, [_I, _I64, _I, _I, _I, _I]),
+    "attn_paged_forward": (_I, [_P, _I64, _I64, _I, _P, _P, _F, _I, _P, _I64, _I64, _P, _P, _SZ,
+                                _P]),
 }
 
 
@@ -490,6 +513,189 @@ def unpermute_reduce(slot_out: torch.Tensor, slot_of: torch.Tensor, topk_w: torc
         _ptr(slot_out), scode, _ptr(slot_of), _ptr(topk_w), T, k, H, _ptr(y), code,
         _stream(stream)))
     return y
+
+
+# -------------------------------------------------------------- attention --
+def attn_workspace(device="cuda") -> torch.Tensor:
+    """Workspace (status word) of qk_norm_rope and kv_append."""
+    return _workspace(256, device)
+
+
+def _rows(t: torch.Tensor, what: str):
+    """(address, token stride, head stride) of bf16 head rows [T, heads, D]."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{what} must be a bf16 CUDA tensor [tokens, heads, head_dim]")
+    st, sh, sd = t.stride()
+    T, H, _ = t.shape
+    if sd != 1:
+        raise ValueError(f"{what}: head_dim must be contiguous")
+    # the stride of an axis of length 1 is never used
+    return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != (n,):
+        raise ValueError(f"{what} must be {dtype} [{n}]")
+    return _ptr(t)
+
+
+def _rope(rope: Optional[torch.Tensor]):
+    if rope is None:
+        return None, 0, 0
+    if rope.dtype != torch.float32 or rope.dim() != 2:
+        raise ValueError("rope must be float32 [positions, rotary_dim]")
+    return _ptr(rope), rope.shape[0], rope.shape[1]
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
+                 rope: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Per-head RMS norm (where a weight is given) and rotation (where rope is
+    given) of bf16 q [T, Hq, D] and k [T, Hkv, D], strided views taken as they
+    are; positions int32 [T].  q_out / k_out may be q and k themselves.
+    Returns (q_out, k_out)."""
+    T, hq, D = q.shape
+    hk = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("q and k must agree in tokens and head_dim")
+    q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty((T, hk, D), dtype=k.dtype, device=k.device) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    ws = attn_workspace(q.device) if ws is None else ws
+    table, npos, rot = _rope(rope)
+    _check("attn_qk_norm_rope", lib().attn_qk_norm_rope(
+        *_rows(q, "q"), hq, *_rows(k, "k"), hk, T, D,
+        _vector(positions, T, torch.int32, "positions"), table, npos, rot, int(interleaved),
+        _vector(q_weight, D, torch.bfloat16, "q_weight"),
+        _vector(k_weight, D, torch.bfloat16, "k_weight"), eps, *_rows(q_out, "q_out"),
+        *_rows(k_out, "k_out"), _ptr(ws), ws.numel(), _stream(stream)))
+    return q_out, k_out
+
+
+class PagedKVCache:
+    """A paged cache: k and v, bf16 or float8_e4m3fn, [pages, page_size, Hkv, D]
+    or with heads_first [pages, Hkv, page_size, D] (D contiguous, other axes
+    strided); k_scale / v_scale float32 [Hkv] for an E4M3 cache (None: 1)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, heads_first: bool = False,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-D and agree in shape and type")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("the cache must be bf16 or float8_e4m3fn")
+        if not (k.is_cuda and v.is_cuda):
+            raise ValueError("expected CUDA tensors")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides, head_dim contiguous")
+        pages, a, b, D = k.shape
+        heads, page = (a, b) if heads_first else (b, a)
+        sp = k.stride(0)
+        st, sh = (k.stride(2), k.stride(1)) if heads_first else (k.stride(1), k.stride(2))
+        # an axis of length 1 is never stepped along
+        sp, sh = (sp if pages > 1 else D), (sh if heads > 1 else D)
+        self.k, self.v, self.heads_first = k, v, heads_first
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.heads, self.head_dim, self.page_size = heads, D, page
+        self.struct = KvCache(
+            k.data_ptr(), v.data_ptr(), BF16 if k.dtype == torch.bfloat16 else E4M3, heads, D,
+            page, pages, sp, st, sh, _vector(k_scale, heads, torch.float32, "k_scale"),
+            _vector(v_scale, heads, torch.float32, "v_scale"))
+        self._ref = ctypes.byref(self.struct)
+
+
+class AttnBatch:
+    """The requests of a step, in device int32 tensors: q_start [B + 1] (rows of
+    q, k and v per request), kv_len [B] (cached tokens, the new ones counted),
+    page_table [B, max_pages]; max_new: host-known bound on a request's new
+    tokens.  The tensors may be refilled in place between steps."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                 max_new: int):
+        B = kv_len.shape[0]
+        if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32:
+            raise ValueError("page_table must be int32 [B, max_pages]")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.batch, self.max_new = B, int(max_new)
+        self.struct = AttnBatchArgs(B, self.max_new, 0, page_table.shape[1],
+                                    _vector(q_start, B + 1, torch.int32, "q_start"),
+                                    _vector(kv_len, B, torch.int32, "kv_len"), _ptr(page_table))
+        self._ref = ctypes.byref(self.struct)
+
+    def rows(self, tokens: int):
+        self.struct.tokens = tokens
+        return self._ref
+
+
+def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.Tensor,
+              rope: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              q: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+              ws: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Norm and rotate the new keys at their cache positions and append them
+    with the new values (bf16 [T, Hkv, D]); with q given, norm and rotate it in
+    the same launch.  Returns q_out (None without q)."""
+    T, D = k.shape[0], cache.head_dim
+    if k.shape != v.shape or k.shape[1] != cache.heads or k.shape[2] != D:
+        raise ValueError("k and v must be [tokens, kv heads, head_dim] of the cache")
+    hq, q_args, out_args = 0, (None, 0, 0), (None, 0, 0)
+    if q is not None:
+        hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q and k must agree in tokens and head_dim")
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        q_args, out_args = _rows(q, "q"), _rows(q_out, "q_out")
+    ws = attn_workspace(k.device) if ws is None else ws
+    table, npos, rot = _rope(rope)
+    _check("attn_kv_append", lib().attn_kv_append(
+        cache._ref, batch.rows(T), *_rows(k, "k"), *_rows(v, "v"), *q_args, hq, *out_args, table,
+        npos, rot, int(interleaved), _vector(q_weight, D, torch.bfloat16, "q_weight"),
+        _vector(k_weight, D, torch.bfloat16, "k_weight"), eps, _ptr(ws), ws.numel(),
+        _stream(stream)))
+    return q_out
+
+
+def paged_attention_workspace(cache: PagedKVCache, batch: AttnBatch, q_heads: int,
+                              tokens: Optional[int] = None, device=None) -> torch.Tensor:
+    """Workspace of paged_attention for up to `tokens` rows (default: batch *
+    max_new) of q_heads heads."""
+    tokens = batch.batch * batch.max_new if tokens is None else tokens
+    return _workspace(lib().attn_paged_workspace_size(batch.batch, tokens, batch.max_new, q_heads,
+                                                      cache.heads, cache.head_dim),
+                      cache.k.device if device is None else device)
+
+
+def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
+                    scale: Optional[float] = None, window: int = 0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of the new tokens' queries, bf16 [T, Hq, D], over their
+    requests' cached keys (the new ones appended before).  window > 0: only the
+    last `window` positions.  lse: optional float32 [T, Hq], written.  Returns
+    out, bf16 [T, Hq, D]."""
+    T, hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError("q and the cache must agree in head_dim")
+    if out is None:
+        out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, hq)):
+        raise ValueError("lse must be float32 [tokens, q heads]")
+    if ws is None:
+        ws = paged_attention_workspace(cache, batch, hq, T)
+    _check("attn_paged_forward", lib().attn_paged_forward(
+        *_rows(q, "q"), hq, cache._ref, batch.rows(T), D ** -0.5 if scale is None else scale,
+        window, *_rows(out, "out"), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    return out
 
 
 # -------------------------------------------------------- whole forward --

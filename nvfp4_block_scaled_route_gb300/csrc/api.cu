@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "nvfp4moe.h"
+#include "attn.cuh"
 #include "internal.h"
 
 using namespace nvmoe;
@@ -173,14 +174,14 @@ const char* nvmoe_status_str(int s) {
     case NVMOE_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case NVMOE_ERR_CUDA: return "CUDA error";
     case NVMOE_ERR_TIMEOUT: return "device wait timed out";
-    case NVMOE_ERR_DEVICE_BAD_INDEX: return "expert id out of range";
+    case NVMOE_ERR_DEVICE_BAD_INDEX: return "index out of range (expert id, position or page)";
     case NVMOE_ERR_RANGE: return "value beyond the range of its storage type";
     case NVMOE_ERR_DEVICE_BOUNDS: return "index outside its buffer (debug-bounds build)";
     default: return "unknown status";
   }
 }
 
-int nvmoe_version(void) { return 200; }
+int nvmoe_version(void) { return 201; }
 
 int nvmoe_set_pdl(int enable) {
   const int old = g_pdl.exchange(enable != 0 ? 1 : 0);
@@ -932,6 +933,194 @@ int moe_nvfp4_layer_forward(const nvmoe_weights* w, const void* x, int x_dtype,
   if (st != NVMOE_OK) return st;
   return moe_unpermute_reduce(b.slot_out, NVMOE_F16, slot_of, topk_w, T, k, H, y, y_dtype,
                               stream);
+}
+
+// --------------------------------------------------------- attention ----
+namespace {
+
+// Head rows [T, heads, D] with element strides: an nvmoe_status.
+int check_rows(const void* p, int64_t token_stride, int64_t head_stride, int heads, int D) {
+  if (p == nullptr) return NVMOE_ERR_INVALID_ARG;
+  if (!aligned16(p)) return NVMOE_ERR_MISALIGNED;
+  constexpr int64_t kMost = int64_t{1} << 31;      // with T * heads < 2^31: offsets fit int64
+  if (token_stride < 0 || head_stride < 0 || token_stride >= kMost || head_stride >= kMost)
+    return NVMOE_ERR_INVALID_ARG;
+  if (heads > 1 && head_stride < D) return NVMOE_ERR_INVALID_ARG;
+  return token_stride % 8 == 0 && head_stride % 8 == 0 ? NVMOE_OK : NVMOE_ERR_MISALIGNED;
+}
+
+int check_transform(const float* rope, int64_t rope_positions, int rotary_dim, int D,
+                    const void* q_weight, const void* k_weight, float eps) {
+  if (!(eps >= 0.0f)) return NVMOE_ERR_INVALID_ARG;
+  if (rope != nullptr) {
+    if (rope_positions < 1) return NVMOE_ERR_INVALID_ARG;
+    if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > D)
+      return NVMOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(rope)) return NVMOE_ERR_MISALIGNED;
+  }
+  return aligned16(q_weight) && aligned16(k_weight) ? NVMOE_OK : NVMOE_ERR_MISALIGNED;
+}
+
+int check_cache(const nvmoe_kv_cache* c, KvCacheView* v) {
+  if (c == nullptr || c->kv_heads < 1 || c->num_pages < 0) return NVMOE_ERR_INVALID_ARG;
+  if (c->dtype != NVMOE_BF16 && c->dtype != NVMOE_E4M3) return NVMOE_ERR_INVALID_ARG;
+  const int D = c->head_dim, P = c->page_size;
+  if ((D != 64 && D != 128) || P < 16 || P > 1024 || (P & (P - 1)) != 0 ||
+      c->num_pages >= (int64_t{1} << 31))
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->num_pages > 0 && (c->k == nullptr || c->v == nullptr)) return NVMOE_ERR_INVALID_ARG;
+  const int64_t el = c->dtype == NVMOE_BF16 ? 2 : 1;
+  for (int64_t s : {c->page_stride, c->token_stride, c->head_stride}) {
+    if (s < D || s >= (int64_t{1} << 40) / el) return NVMOE_ERR_INVALID_ARG;
+    if (s * el % 16 != 0) return NVMOE_ERR_MISALIGNED;
+  }
+  if (!aligned16(c->k) || !aligned16(c->v)) return NVMOE_ERR_MISALIGNED;
+  *v = KvCacheView{c->k, c->v, c->dtype == NVMOE_E4M3, c->kv_heads, D, 0, c->num_pages,
+                   c->page_stride, c->token_stride, c->head_stride, c->k_scale, c->v_scale};
+  while ((1 << v->page_shift) < P) ++v->page_shift;
+  if (!v->fp8) v->k_scale = v->v_scale = nullptr;
+  return NVMOE_OK;
+}
+
+int check_batch(const nvmoe_attn_batch* b, int page_size, BatchView* v) {
+  if (b == nullptr || b->batch < 0 || b->tokens < 0 || b->max_new < 1 || b->max_pages < 0)
+    return NVMOE_ERR_INVALID_ARG;
+  if (b->max_pages >= (int64_t{1} << 31) / page_size || b->tokens >= (int64_t{1} << 31))
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  if (b->batch > 0 && b->tokens > 0 &&
+      (b->q_start == nullptr || b->kv_len == nullptr ||
+       (b->max_pages > 0 && b->page_table == nullptr)))
+    return NVMOE_ERR_INVALID_ARG;
+  *v = BatchView{b->batch, b->max_new, b->tokens, b->max_pages, b->q_start, b->kv_len,
+                 b->page_table};
+  return NVMOE_OK;
+}
+
+}  // namespace
+
+int attn_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                      const void* k, int64_t k_token_stride, int64_t k_head_stride, int kv_heads,
+                      int64_t T, int head_dim, const int32_t* positions, const float* rope,
+                      int64_t rope_positions, int rotary_dim, int interleaved,
+                      const void* q_weight, const void* k_weight, float eps, void* q_out,
+                      int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                      int64_t k_out_token_stride, int64_t k_out_head_stride, void* ws,
+                      size_t ws_bytes, cudaStream_t stream) {
+  const NvtxRange nvtx_range("attn_qk_norm_rope");
+  if (T < 0 || q_heads < 0 || kv_heads < 0 || ws == nullptr) return NVMOE_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return NVMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(ws)) return NVMOE_ERR_MISALIGNED;
+  if (head_dim != 64 && head_dim != 128) return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  const int64_t heads = int64_t{q_heads} + kv_heads;
+  if (heads > 0 && T > INT32_MAX / heads) return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  int st = check_transform(rope, rope_positions, rotary_dim, head_dim, q_weight, k_weight, eps);
+  if (st != NVMOE_OK) return st;
+  if (T == 0 || heads == 0) return NVMOE_OK;
+  if (rope != nullptr && positions == nullptr) return NVMOE_ERR_INVALID_ARG;
+  if (q_heads > 0) {
+    st = check_rows(q, q_token_stride, q_head_stride, q_heads, head_dim);
+    if (st == NVMOE_OK)
+      st = check_rows(q_out, q_out_token_stride, q_out_head_stride, q_heads, head_dim);
+    if (st != NVMOE_OK) return st;
+  }
+  if (kv_heads > 0) {
+    st = check_rows(k, k_token_stride, k_head_stride, kv_heads, head_dim);
+    if (st == NVMOE_OK)
+      st = check_rows(k_out, k_out_token_stride, k_out_head_stride, kv_heads, head_dim);
+    if (st != NVMOE_OK) return st;
+  }
+  const HeadTransform tr{rope, rope_positions, rope != nullptr ? rotary_dim : 0, interleaved != 0,
+                         static_cast<const __nv_bfloat16*>(q_weight),
+                         static_cast<const __nv_bfloat16*>(k_weight), eps};
+  return status_of(counted(
+      launch_qk_norm_rope({const_cast<void*>(q), q_token_stride, q_head_stride, q_heads},
+                          {const_cast<void*>(k), k_token_stride, k_head_stride, kv_heads}, T,
+                          head_dim, positions, tr,
+                          {q_out, q_out_token_stride, q_out_head_stride, q_heads},
+                          {k_out, k_out_token_stride, k_out_head_stride, kv_heads},
+                          static_cast<int*>(ws), stream),
+      1));
+}
+
+int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, const void* k,
+                   int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                   int64_t v_token_stride, int64_t v_head_stride, const void* q,
+                   int64_t q_token_stride, int64_t q_head_stride, int q_heads, void* q_out,
+                   int64_t q_out_token_stride, int64_t q_out_head_stride, const float* rope,
+                   int64_t rope_positions, int rotary_dim, int interleaved,
+                   const void* q_weight, const void* k_weight, float eps, void* ws,
+                   size_t ws_bytes, cudaStream_t stream) {
+  const NvtxRange nvtx_range("attn_kv_append");
+  KvCacheView cv;
+  BatchView bv;
+  int st = check_cache(cache, &cv);
+  if (st == NVMOE_OK) st = check_batch(batch, cache->page_size, &bv);
+  if (st != NVMOE_OK) return st;
+  if (ws == nullptr || q_heads < 0) return NVMOE_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return NVMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(ws)) return NVMOE_ERR_MISALIGNED;
+  const int D = cv.head_dim;
+  if (bv.tokens > INT32_MAX / (int64_t{q_heads} + 2 * int64_t{cv.heads}))
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  st = check_transform(rope, rope_positions, rotary_dim, D, q_weight, k_weight, eps);
+  if (st != NVMOE_OK) return st;
+  if (bv.tokens == 0 || bv.batch == 0) return NVMOE_OK;
+  st = check_rows(k, k_token_stride, k_head_stride, cv.heads, D);
+  if (st == NVMOE_OK) st = check_rows(v, v_token_stride, v_head_stride, cv.heads, D);
+  if (st == NVMOE_OK && q_heads > 0) {
+    st = check_rows(q, q_token_stride, q_head_stride, q_heads, D);
+    if (st == NVMOE_OK) st = check_rows(q_out, q_out_token_stride, q_out_head_stride, q_heads, D);
+  }
+  if (st != NVMOE_OK) return st;
+  const HeadTransform tr{rope, rope_positions, rope != nullptr ? rotary_dim : 0, interleaved != 0,
+                         static_cast<const __nv_bfloat16*>(q_weight),
+                         static_cast<const __nv_bfloat16*>(k_weight), eps};
+  return status_of(
+      counted(launch_kv_append({const_cast<void*>(q), q_token_stride, q_head_stride, q_heads},
+                               {const_cast<void*>(k), k_token_stride, k_head_stride, cv.heads},
+                               {const_cast<void*>(v), v_token_stride, v_head_stride, cv.heads}, cv,
+                               bv, tr, {q_out, q_out_token_stride, q_out_head_stride, q_heads},
+                               static_cast<int*>(ws), stream),
+              1));
+}
+
+size_t attn_paged_workspace_size(int batch, int64_t tokens, int max_new, int q_heads,
+                                 int kv_heads, int head_dim) {
+  if (batch < 0 || tokens < 0 || max_new < 1 || kv_heads < 1 || q_heads < kv_heads ||
+      q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return kStatusBytes;
+}
+
+int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                       const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, float scale,
+                       int window, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                       float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const NvtxRange nvtx_range("attn_paged_forward");
+  AttnArgs a{};
+  int st = check_cache(cache, &a.cache);
+  if (st == NVMOE_OK) st = check_batch(batch, cache->page_size, &a.batch);
+  if (st != NVMOE_OK) return st;
+  if (q_heads < 1 || window < 0 || ws == nullptr || !(scale > 0.0f) || scale > 3.0e38f)
+    return NVMOE_ERR_INVALID_ARG;
+  if (q_heads % a.cache.heads != 0 || a.batch.tokens > INT32_MAX / q_heads)
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(ws)) return NVMOE_ERR_MISALIGNED;
+  if (ws_bytes < attn_paged_workspace_size(a.batch.batch, a.batch.tokens, a.batch.max_new, q_heads,
+                                           a.cache.heads, a.cache.head_dim))
+    return NVMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (a.batch.tokens == 0 || a.batch.batch == 0) return NVMOE_OK;
+  st = check_rows(q, q_token_stride, q_head_stride, q_heads, a.cache.head_dim);
+  if (st == NVMOE_OK)
+    st = check_rows(out, out_token_stride, out_head_stride, q_heads, a.cache.head_dim);
+  if (st != NVMOE_OK) return st;
+  a.q = {const_cast<void*>(q), q_token_stride, q_head_stride, q_heads};
+  a.out = {out, out_token_stride, out_head_stride, q_heads};
+  a.lse = lse;
+  a.scale = scale;
+  a.window = window;
+  a.status = static_cast<int*>(ws);
+  return status_of(counted(launch_paged_attention(a, stream), 1));
 }
 
 }  // extern "C"

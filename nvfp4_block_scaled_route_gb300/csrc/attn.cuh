@@ -1,0 +1,134 @@
+// Shared by the attention operators (attn_rope.cu, attention.cu): the views
+// of head rows, paged cache and batch that the C-ABI layer fills in, and the
+// device helpers that read them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace nvmoe {
+
+// bf16 rows [T, heads, head_dim] with strides in elements.
+struct HeadRows {
+  void* data;
+  int64_t token_stride, head_stride;
+  int heads;
+};
+
+struct KvCacheView {
+  void* k;
+  void* v;
+  bool fp8;                 // E4M3, else bf16
+  int heads, head_dim;
+  int page_shift;           // page_size = 1 << page_shift
+  int64_t num_pages;
+  int64_t page_stride, token_stride, head_stride;   // elements
+  const float* k_scale;     // [heads] or null
+  const float* v_scale;
+};
+
+struct BatchView {
+  int batch, max_new;
+  int64_t tokens, max_pages;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+};
+
+// Norm and rotation of head rows (the weights are bf16 [head_dim] or null).
+struct HeadTransform {
+  const float* rope;        // [rope_positions, rotary_dim] or null
+  int64_t rope_positions;
+  int rotary_dim, interleaved;
+  const __nv_bfloat16* q_weight;
+  const __nv_bfloat16* k_weight;
+  float eps;
+};
+
+// q and k (either may have 0 heads) to q_out and k_out at given positions.
+cudaError_t launch_qk_norm_rope(const HeadRows& q, const HeadRows& k, int64_t T, int head_dim,
+                                const int32_t* positions, const HeadTransform& tr,
+                                const HeadRows& q_out, const HeadRows& k_out, int* status,
+                                cudaStream_t stream);
+// k and v into the cache (and q, if it has heads, to q_out) at the cache
+// positions of the batch.
+cudaError_t launch_kv_append(const HeadRows& q, const HeadRows& k, const HeadRows& v,
+                             const KvCacheView& cache, const BatchView& batch,
+                             const HeadTransform& tr, const HeadRows& q_out, int* status,
+                             cudaStream_t stream);
+
+struct AttnArgs {
+  HeadRows q;
+  HeadRows out;
+  float* lse;               // [tokens, q heads] or null
+  KvCacheView cache;
+  BatchView batch;
+  float scale;
+  int window;
+  int* status;
+};
+cudaError_t launch_paged_attention(const AttnArgs& args, cudaStream_t stream);
+
+// New tokens and cached length of request r as the kernels take them, kept
+// inside the buffers whatever q_start and kv_len hold: rows [first, first + n)
+// of q, the first of them at cache position pos0 (negative if the length is
+// below n), `len` keys.
+struct Request {
+  int64_t first;
+  int n;
+  int pos0, len;
+};
+__device__ __forceinline__ Request load_request(const BatchView& b, int page_shift, int r,
+                                                int* status) {
+  Request q;
+  int64_t a = b.q_start[r], e = b.q_start[r + 1];
+  const int64_t cap = b.max_pages << page_shift;   // < 2^31, checked on the host
+  int64_t len = b.kv_len[r];
+  if (a < 0) a = 0;
+  if (e > b.tokens) e = b.tokens;
+  int64_t n = e > a ? e - a : 0;
+  const int64_t pos0 = len - n;
+  if (n > b.max_new || len > cap) record_status(status, kErrBadIndex);
+  if (n > b.max_new) n = b.max_new;
+  if (len > cap) len = cap;
+  if (len < 0) len = 0;
+  q.first = a;
+  q.n = static_cast<int>(n);
+  q.pos0 = pos0 < -(int64_t{1} << 30) ? -(1 << 30) : static_cast<int>(pos0);
+  q.len = static_cast<int>(len);
+  return q;
+}
+
+// Eight bf16 of a 16-byte word as floats.
+__device__ __forceinline__ void bf16x8_to_float(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two E4M3 (satfinite, nearest even; NaN stays NaN), `lo` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace nvmoe
