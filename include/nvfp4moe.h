@@ -646,7 +646,7 @@ int attn_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * both taken.
  *   dtype       NVMOE_BF16, or NVMOE_E4M3: the stored value times k_scale[h]
  *               (v_scale[h]) is the key (value); scales NULL: 1.
- *   page_size   a power of two, 16 .. 1024; num_pages < 2^31
+ *   page_size   a power of two, 16 .. 1024; 1 <= num_pages < 2^31
  *   strides     multiples of 16 bytes, positive, below 2^40 bytes */
 typedef struct {
   void* k;

@@ -2,8 +2,9 @@
 // argument checks, workspace carving, TMA descriptor encoding and kernel
 // launches.  No allocation, no host synchronisation on the compute calls.
 #include <nvtx3/nvToolsExt.h>
-#include <cstring>
+#include <algorithm>
 #include <atomic>
+#include <cstring>
 #include <mutex>
 
 #include "nvfp4moe.h"
@@ -962,13 +963,13 @@ int check_transform(const float* rope, int64_t rope_positions, int rotary_dim, i
 }
 
 int check_cache(const nvmoe_kv_cache* c, KvCacheView* v) {
-  if (c == nullptr || c->kv_heads < 1 || c->num_pages < 0) return NVMOE_ERR_INVALID_ARG;
+  if (c == nullptr || c->kv_heads < 1 || c->num_pages < 1) return NVMOE_ERR_INVALID_ARG;
   if (c->dtype != NVMOE_BF16 && c->dtype != NVMOE_E4M3) return NVMOE_ERR_INVALID_ARG;
   const int D = c->head_dim, P = c->page_size;
   if ((D != 64 && D != 128) || P < 16 || P > 1024 || (P & (P - 1)) != 0 ||
       c->num_pages >= (int64_t{1} << 31))
     return NVMOE_ERR_UNSUPPORTED_SHAPE;
-  if (c->num_pages > 0 && (c->k == nullptr || c->v == nullptr)) return NVMOE_ERR_INVALID_ARG;
+  if (c->k == nullptr || c->v == nullptr) return NVMOE_ERR_INVALID_ARG;
   const int64_t el = c->dtype == NVMOE_BF16 ? 2 : 1;
   for (int64_t s : {c->page_stride, c->token_stride, c->head_stride}) {
     if (s < D || s >= (int64_t{1} << 40) / el) return NVMOE_ERR_INVALID_ARG;
@@ -1084,12 +1085,54 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
               1));
 }
 
+namespace {
+
+// One side of a paged cache as [num_pages, heads, page_size, D] by its
+// strides; box: 128 bytes of the row (all of it, if shorter) x up to 128
+// tokens of one page and head.
+bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t el = c.fp8 ? 1 : 2;
+  const uint32_t page = 1u << c.page_shift, line = std::min<uint32_t>(128, c.head_dim * el);
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), page,
+                        static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t strides[3] = {c.token_stride * el, c.head_stride * el, c.page_stride * el};
+  cuuint32_t box[4] = {line / static_cast<uint32_t>(el), std::min<uint32_t>(page, kAttnTileKeys),
+                       1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// The pieces of segments that CTAs share (few rows): the rows of a segment.
+size_t attn_layout(int max_new, int q_heads, int kv_heads, int D, uint8_t* base, AttnArgs* a) {
+  Carve c{base};
+  const int64_t all = int64_t{max_new} * (q_heads / kv_heads);
+  const int64_t rows = std::min<int64_t>(all, kAttnFewRows);
+  a->status = c.take<int>(kStatusBytes);
+  {
+    a->piece_rows = static_cast<int>(all <= kAttnFewRows ? rows : 0);
+    a->pieces = c.take<AttnPiece>(kMaxGrid * sizeof(AttnPiece));
+    a->piece_ml = c.take<float2>(2 * kMaxGrid * rows * sizeof(float2));
+    a->piece_o = c.take<float>(2 * kMaxGrid * rows * D * sizeof(float));
+  }
+  return c.off;
+}
+
+}  // namespace
+
 size_t attn_paged_workspace_size(int batch, int64_t tokens, int max_new, int q_heads,
                                  int kv_heads, int head_dim) {
   if (batch < 0 || tokens < 0 || max_new < 1 || kv_heads < 1 || q_heads < kv_heads ||
       q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
     return 0;
-  return kStatusBytes;
+  AttnArgs a{};
+  return attn_layout(max_new, q_heads, kv_heads, head_dim, nullptr, &a);
 }
 
 int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
@@ -1119,8 +1162,18 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   a.lse = lse;
   a.scale = scale;
   a.window = window;
-  a.status = static_cast<int*>(ws);
-  return status_of(counted(launch_paged_attention(a, stream), 1));
+  attn_layout(a.batch.max_new, q_heads, a.cache.heads, a.cache.head_dim,
+              static_cast<uint8_t*>(ws), &a);
+  if (a.piece_rows == 0) return status_of(counted(launch_attention_chunk(a, stream), 1));
+  CUtensorMap map_k, map_v;
+  if (!make_kv_map(&map_k, a.cache.k, a.cache) || !make_kv_map(&map_v, a.cache.v, a.cache))
+    return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
+  const int nsm = sm_count();
+  if (nsm <= 0) return fail(cudaErrorNoDevice);
+  const int grid = std::min(nsm, kMaxGrid);
+  const cudaError_t e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);
+  if (e != cudaSuccess) return fail(e);
+  return status_of(counted(launch_attn_combine(a, grid, stream), 1));
 }
 
 }  // extern "C"

@@ -60,6 +60,21 @@ cudaError_t launch_kv_append(const HeadRows& q, const HeadRows& k, const HeadRow
                              const HeadTransform& tr, const HeadRows& q_out, int* status,
                              cudaStream_t stream);
 
+// Keys of a tile: the unit in which attention work is shared out.
+constexpr int kAttnTileKeys = 128;
+
+// A segment (the keys that one block of rows sees) cut by borders between
+// CTAs: begun by CTA b (as its last piece, slot 1), ended by CTA `last`; the
+// CTAs after b hold their part in slot 0.  rows = 0: CTA b begins none.
+struct AttnPiece {
+  int rows;          // valid rows
+  int head;          // key head
+  int64_t first;     // first token of the request
+  int row0;          // first row: row i is token first + (row0 + i) / group
+  int last;
+  long long total;   // tiles of the launch (CTA c has [total c / G, total (c + 1) / G))
+};
+
 struct AttnArgs {
   HeadRows q;
   HeadRows out;
@@ -69,8 +84,21 @@ struct AttnArgs {
   float scale;
   int window;
   int* status;
+  // pieces of cut segments: [grid], [grid][2][piece_rows][D] sums before the
+  // division, [grid][2][piece_rows] (maximum in powers of two, weight sum)
+  AttnPiece* pieces;
+  float* piece_o;
+  float2* piece_ml;
+  int piece_rows;
 };
-cudaError_t launch_paged_attention(const AttnArgs& args, cudaStream_t stream);
+// Rows of a segment up to which attention_rows_kernel takes the call.
+constexpr int kAttnFewRows = 64;
+// map_k, map_v: [num_pages, heads, page_size, D] by strides, boxes of up to
+// 128 tokens of one page and head.
+cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
+                                  const CUtensorMap& map_v, int grid, cudaStream_t stream);
+cudaError_t launch_attention_chunk(const AttnArgs& args, cudaStream_t stream);
+cudaError_t launch_attn_combine(const AttnArgs& args, int grid, cudaStream_t stream);
 
 // New tokens and cached length of request r as the kernels take them, kept
 // inside the buffers whatever q_start and kv_len hold: rows [first, first + n)
@@ -129,6 +157,25 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Two E4M3 (low 16 bits) as two fp16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return r;
+}
+
+// 2^x (relative error about 2^-22; 0 at -inf).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Natural logarithm of sum * 2^m, -inf for a row that saw no key.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace nvmoe
