@@ -1109,17 +1109,26 @@ bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
   return r == CUDA_SUCCESS;
 }
 
-// The pieces of segments that CTAs share (few rows): the rows of a segment.
-size_t attn_layout(int max_new, int q_heads, int kv_heads, int D, uint8_t* base, AttnArgs* a) {
+// Workspace: the pieces of segments that CTAs share and, for more rows than
+// the few-row kernel takes, the plan.  Grows with each argument, so that a
+// workspace for the largest step serves the smaller ones.
+size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_heads, int D,
+                   uint8_t* base, AttnArgs* a) {
   Carve c{base};
-  const int64_t all = int64_t{max_new} * (q_heads / kv_heads);
-  const int64_t rows = std::min<int64_t>(all, kAttnFewRows);
+  const int64_t group = q_heads / kv_heads, rows = max_new * group;
+  const bool few = rows <= kAttnFewRows;
+  a->piece_rows = few ? static_cast<int>(rows) : kAttnBlockRows;
+  const int64_t blocks = few ? 0 : ceil_div(tokens * group, kAttnBlockRows) + batch;
+  a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
   a->status = c.take<int>(kStatusBytes);
-  {
-    a->piece_rows = static_cast<int>(all <= kAttnFewRows ? rows : 0);
-    a->pieces = c.take<AttnPiece>(kMaxGrid * sizeof(AttnPiece));
-    a->piece_ml = c.take<float2>(2 * kMaxGrid * rows * sizeof(float2));
-    a->piece_o = c.take<float>(2 * kMaxGrid * rows * D * sizeof(float));
+  a->pieces = c.take<AttnPiece>(kMaxGrid * sizeof(AttnPiece));
+  a->piece_ml = c.take<float2>(2 * kMaxGrid * a->piece_rows * sizeof(float2));
+  a->piece_o = c.take<float>(2 * kMaxGrid * static_cast<size_t>(a->piece_rows) * D *
+                             sizeof(float));
+  if (!few) {
+    a->starts = c.take<AttnStart>(kMaxGrid * sizeof(AttnStart));
+    a->plan_block0 = c.take<int>((static_cast<size_t>(batch) + 1) * sizeof(int));
+    a->plan_tile0 = c.take<long long>((static_cast<size_t>(blocks) + 1) * sizeof(long long));
   }
   return c.off;
 }
@@ -1129,10 +1138,11 @@ size_t attn_layout(int max_new, int q_heads, int kv_heads, int D, uint8_t* base,
 size_t attn_paged_workspace_size(int batch, int64_t tokens, int max_new, int q_heads,
                                  int kv_heads, int head_dim) {
   if (batch < 0 || tokens < 0 || max_new < 1 || kv_heads < 1 || q_heads < kv_heads ||
-      q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+      q_heads % kv_heads != 0 || tokens > INT32_MAX / q_heads ||
+      (head_dim != 64 && head_dim != 128))
     return 0;
   AttnArgs a{};
-  return attn_layout(max_new, q_heads, kv_heads, head_dim, nullptr, &a);
+  return attn_layout(batch, tokens, max_new, q_heads, kv_heads, head_dim, nullptr, &a);
 }
 
 int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
@@ -1162,16 +1172,23 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   a.lse = lse;
   a.scale = scale;
   a.window = window;
-  attn_layout(a.batch.max_new, q_heads, a.cache.heads, a.cache.head_dim,
-              static_cast<uint8_t*>(ws), &a);
-  if (a.piece_rows == 0) return status_of(counted(launch_attention_chunk(a, stream), 1));
+  attn_layout(a.batch.batch, a.batch.tokens, a.batch.max_new, q_heads, a.cache.heads,
+              a.cache.head_dim, static_cast<uint8_t*>(ws), &a);
+  const bool few = a.piece_rows <= kAttnFewRows;
+  if (!few && a.cache.fp8) return status_of(counted(launch_paged_attention(a, stream), 1));
   CUtensorMap map_k, map_v;
   if (!make_kv_map(&map_k, a.cache.k, a.cache) || !make_kv_map(&map_v, a.cache.v, a.cache))
     return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);
   const int grid = std::min(nsm, kMaxGrid);
-  const cudaError_t e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);
+  cudaError_t e;
+  if (few) {
+    e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);
+  } else {
+    e = counted(launch_attn_plan(a, grid, stream), 1);
+    if (e == cudaSuccess) e = counted(launch_attention_chunk(a, map_k, map_v, grid, stream), 1);
+  }
   if (e != cudaSuccess) return fail(e);
   return status_of(counted(launch_attn_combine(a, grid, stream), 1));
 }

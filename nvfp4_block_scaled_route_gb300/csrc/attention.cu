@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
 
 }  // namespace
 
-cudaError_t launch_attention_chunk(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
   const unsigned blocks =
       static_cast<unsigned>(ceil_div(a.batch.tokens * a.q.heads, kThreads / 32));
   const bool wide = a.cache.head_dim == 128;

@@ -75,6 +75,13 @@ struct AttnPiece {
   long long total;   // tiles of the launch (CTA c has [total c / G, total (c + 1) / G))
 };
 
+// Where a CTA of the chunk kernel starts: `left` tiles from tile `tile` of the
+// segment (request, key head, row block).
+struct AttnStart {
+  long long total, left;
+  int request, head, block, tile;
+};
+
 struct AttnArgs {
   HeadRows q;
   HeadRows out;
@@ -90,14 +97,24 @@ struct AttnArgs {
   float* piece_o;
   float2* piece_ml;
   int piece_rows;
+  // chunk kernel: blocks before each request [batch + 1], key tiles before
+  // each block [max_blocks + 1] (one key head), the CTAs' starts [grid]
+  int* plan_block0;
+  long long* plan_tile0;
+  AttnStart* starts;
+  int max_blocks;
 };
+constexpr int kAttnBlockRows = 256;
 // Rows of a segment up to which attention_rows_kernel takes the call.
 constexpr int kAttnFewRows = 64;
 // map_k, map_v: [num_pages, heads, page_size, D] by strides, boxes of up to
 // 128 tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
-cudaError_t launch_attention_chunk(const AttnArgs& args, cudaStream_t stream);
+cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);
+cudaError_t launch_attention_chunk(const AttnArgs& args, const CUtensorMap& map_k,
+                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
+cudaError_t launch_paged_attention(const AttnArgs& args, cudaStream_t stream);
 cudaError_t launch_attn_combine(const AttnArgs& args, int grid, cudaStream_t stream);
 
 // New tokens and cached length of request r as the kernels take them, kept
