@@ -1088,9 +1088,9 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
 namespace {
 
 // One side of a paged cache as [num_pages, heads, page_size, D] by its
-// strides; box: 128 bytes of the row (all of it, if shorter) x up to 128
-// tokens of one page and head.
-bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
+// strides; box: 128 bytes of the row (all of it, if shorter) x up to
+// box_tokens tokens of one page and head.
+bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c, uint32_t box_tokens) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t el = c.fp8 ? 1 : 2;
@@ -1098,8 +1098,8 @@ bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), page,
                         static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_pages)};
   cuuint64_t strides[3] = {c.token_stride * el, c.head_stride * el, c.page_stride * el};
-  cuuint32_t box[4] = {line / static_cast<uint32_t>(el), std::min<uint32_t>(page, kAttnTileKeys),
-                       1, 1};
+  cuuint32_t box[4] = {line / static_cast<uint32_t>(el), std::min<uint32_t>(page, box_tokens), 1,
+                       1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                   const_cast<void*>(base), dims, strides, box, estr,
@@ -1177,11 +1177,14 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   const bool few = a.piece_rows <= kAttnFewRows;
   if (!few && a.cache.fp8) return status_of(counted(launch_paged_attention(a, stream), 1));
   CUtensorMap map_k, map_v;
-  if (!make_kv_map(&map_k, a.cache.k, a.cache) || !make_kv_map(&map_v, a.cache.v, a.cache))
+  const uint32_t box = few ? kAttnTileKeys : kAttnTileKeys / 2;
+  if (!make_kv_map(&map_k, a.cache.k, a.cache, box) ||
+      !make_kv_map(&map_v, a.cache.v, a.cache, box))
     return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);
-  const int grid = std::min(nsm, kMaxGrid);
+  // shares of the work: a CTA's, or a pair of CTAs' (chunks)
+  const int grid = std::min(few ? nsm : std::max(nsm / 2, 1), kMaxGrid);
   cudaError_t e;
   if (few) {
     e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);

@@ -108,12 +108,12 @@ constexpr int kAttnBlockRows = 256;
 // Rows of a segment up to which attention_rows_kernel takes the call.
 constexpr int kAttnFewRows = 64;
 // map_k, map_v: [num_pages, heads, page_size, D] by strides, boxes of up to
-// 128 tokens of one page and head.
+// 128 (chunk kernel: 64) tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
 cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);
 cudaError_t launch_attention_chunk(const AttnArgs& args, const CUtensorMap& map_k,
-                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
+                                   const CUtensorMap& map_v, int clusters, cudaStream_t stream);
 cudaError_t launch_paged_attention(const AttnArgs& args, cudaStream_t stream);
 cudaError_t launch_attn_combine(const AttnArgs& args, int grid, cudaStream_t stream);
 
