@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
 SOURCES = ["api.cu", "quantize.cu", "route.cu", "reduce.cu", "gemm.cu", "router.cu", "peak.cu",
-           "ep.cu", "attn_rope.cu", "attention.cu", "attn_rows.cu",
+           "ep.cu", "attn_rope.cu", "attn_join.cu", "attn_rows.cu",
            "attn_chunk.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "quant.cuh", "attn.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

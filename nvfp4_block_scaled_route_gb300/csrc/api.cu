@@ -1175,7 +1175,6 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   attn_layout(a.batch.batch, a.batch.tokens, a.batch.max_new, q_heads, a.cache.heads,
               a.cache.head_dim, static_cast<uint8_t*>(ws), &a);
   const bool few = a.piece_rows <= kAttnFewRows;
-  if (!few && a.cache.fp8) return status_of(counted(launch_paged_attention(a, stream), 1));
   CUtensorMap map_k, map_v;
   const uint32_t box = few ? kAttnTileKeys : kAttnTileKeys / 2;
   if (!make_kv_map(&map_k, a.cache.k, a.cache, box) ||

@@ -1,4 +1,4 @@
-// Shared by the attention operators (attn_rope.cu, attention.cu): the views
+// Shared by the attention operators (attn_rope.cu, attn_rows.cu, attn_chunk.cu, attn_join.cu): the views
 // of head rows, paged cache and batch that the C-ABI layer fills in, and the
 // device helpers that read them.
 #pragma once
@@ -114,7 +114,6 @@ cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k
 cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);
 cudaError_t launch_attention_chunk(const AttnArgs& args, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int clusters, cudaStream_t stream);
-cudaError_t launch_paged_attention(const AttnArgs& args, cudaStream_t stream);
 cudaError_t launch_attn_combine(const AttnArgs& args, int grid, cudaStream_t stream);
 
 // New tokens and cached length of request r as the kernels take them, kept

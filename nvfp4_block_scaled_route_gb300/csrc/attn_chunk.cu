@@ -22,6 +22,12 @@
 // fed: an MMA of 128 x 128 x 16 takes 64 cycles and few are queued, while a
 // tile's four commits and three waits take some 600.)
 //
+// E4M3 caches: two warps each turn the key and value tiles into fp16 (exact)
+// on their way to the tensor cores, from a ring of raw tiles to a ring of
+// operand tiles.  Queries and weights are then fp16 too; a query row is scaled
+// by a power of two to a maximum in [1, 2), which keeps every element above
+// 2^-16 of it exact, and the factor goes back in with the softmax scale.
+//
 // m is a reference, not always the maximum: O is rescaled only when a row's
 // maximum has grown by more than 2^8 over its reference (any reference gives
 // the same quotient; weights stay below 2^8, sums are fp32).
@@ -38,9 +44,14 @@ namespace {
 constexpr int kKeys = kAttnTileKeys;
 constexpr int kTile = 128;                   // query rows of a tile
 constexpr int kBlock = kAttnBlockRows;       // rows of a segment
-constexpr int kLoadK = 8, kLoadV = 9, kIssueS = 10, kIssueO = 11;
-constexpr int kThreads = 384;
+constexpr int kLoadK = 8, kLoadV = 9, kIssueS = 10;   // and 11: P V
+constexpr int kConvert = 12;                 // warps 12-13: keys, 14-15: values (E4M3)
 constexpr int kSoftmaxThreads = 256;
+constexpr int kConvertThreads = 64;          // of a side
+// E4M3: registers of a thread; the launch gives each 128 (the most for 512
+// threads), the softmax warps take what the others leave.
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
+static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= 128 * 512, "registers");
 constexpr int kPlanThreads = 1024;
 
 // Rows [row0, row0 + rows) of a request and the key tiles that they see.
@@ -208,19 +219,31 @@ struct Walk {
   }
 };
 
-template <int D>
+template <int D, bool FP8>
 struct Cfg {
-  static constexpr int kHalves = D / 64;               // 128-byte column blocks
-  static constexpr int kBytes = kKeys * D * 2;         // a key or value tile
-  static constexpr int kBufs = D == 128 ? 7 : 14;
-  static constexpr int kKBufs = kBufs - kBufs / 2, kVBufs = kBufs / 2;
-  static constexpr int kSmem = kBufs * kBytes + 512 + 2 * kTile * 4;
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kBytes = kKeys * D * 2;         // an operand tile
+  static constexpr int kLoadBytes = FP8 ? kKeys * D : kBytes;   // a tile as loaded
+  static constexpr int kRow = D * (FP8 ? 1 : 2);
+  static constexpr int kLine = kRow < 128 ? kRow : 128;   // bytes of a box row
+  static constexpr int kHalves = kRow / kLine;         // column blocks
+  // operand tiles of keys and of values (bf16: as loaded), raw E4M3 tiles
+  static constexpr int kK = (FP8 ? 2 : 4) * (D == 128 ? 1 : 2) - (FP8 || D == 128 ? 0 : 1);
+  static constexpr int kV = FP8 ? kK : (D == 128 ? 3 : 7);
+  static constexpr int kRaw = FP8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kRing = (kK + kV) * kBytes + 2 * kRaw * kLoadBytes;
+  static constexpr int kSmem = kRing + 512 + 4 * kTile * 4;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr uint32_t kTmemO = 256, kTmemQ = 384;   // S: columns 0 and 128
+  // instruction descriptors: fp16 operands are format 0, bf16 format 1; V is MN-major
+  static constexpr uint32_t kFormats = FP8 ? (1u << 7) | (1u << 10) : 0u;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kKeys) ^ kFormats;
+  static constexpr uint32_t kIdescO = (idesc_bf16_f32(kTile, D) ^ kFormats) | (1u << 16);
 };
 
 struct Bars {
-  uint64_t full[14], empty[14];                        // keys, then values
+  uint64_t full[14], empty[14];                        // loaded tiles: keys, then values
+  uint64_t op_full[8], op_empty[8];                    // E4M3: operand tiles
   // by parity of the CTA's tile counter; its next bit is the barrier's phase
   uint64_t s_full[2], p_ready[2], pv_done[2];
   uint64_t q_ready, done[2];
@@ -292,28 +315,34 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
-  using C = Cfg<D>;
+  using C = Cfg<D, FP8>;
   // the swizzle goes by the address: tiles start at multiples of 1024 bytes,
   // and there is no room to round up to one
-  extern __shared__ __align__(1024) uint8_t ring[];
+  extern __shared__ __align__(1024) uint8_t ring[];     // operand tiles, raw tiles
   if ((smem_u32(ring) & 1023u) != 0) {
     record_status(a.status, kErrBounds);
     return;
   }
-  Bars* bars = reinterpret_cast<Bars*>(ring + C::kBufs * C::kBytes);
+  uint8_t* raw = ring + (C::kK + C::kV) * C::kBytes;
+  Bars* bars = reinterpret_cast<Bars*>(ring + C::kRing);
   float* swap = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());   // query tile of the block
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kBufs; ++i) {
+    for (int i = 0; i < (FP8 ? 2 * C::kRaw : C::kK + C::kV); ++i) {
       mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 2);                      // both CTAs' issuers
+      // both CTAs' readers: an issuer, or two converting warps
+      mbar_init(&bars->empty[i], FP8 ? 4 : 2);
+    }
+    for (int i = 0; FP8 && i < C::kK + C::kV; ++i) {
+      mbar_init(&bars->op_full[i], kConvertThreads);
+      mbar_init(&bars->op_empty[i], 1);
     }
     mbar_init(&bars->q_ready, kSoftmaxThreads);
     for (int i = 0; i < 2; ++i) {
@@ -353,12 +382,16 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     t = wk.b.t0 + st.tile;
   }
 
+  if (warp >= kLoadK) {
+    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kLoadK || warp == kLoadV) {
     // ---- this CTA's half (64 keys) of the key or value tiles, to both CTAs:
     // lane = box (page part, column block) ----
     const bool keys = warp == kLoadK;
     const CUtensorMap* map = keys ? &map_k : &map_v;
-    const int bufs = keys ? C::kKBufs : C::kVBufs, buf0 = keys ? 0 : C::kKBufs;
+    const int bufs = FP8 ? C::kRaw : (keys ? C::kK : C::kV);
+    const int buf0 = keys ? 0 : (FP8 ? C::kRaw : C::kK);
+    uint8_t* base = FP8 ? raw : ring;
     const int box = min(kKeys / 2, 1 << a.cache.page_shift);
     const int b = lane & 7, half = lane >> 3;
     const uint64_t policy = policy_evict_normal();
@@ -387,11 +420,13 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         ok = mbar_wait(&bars->empty[n], phase ^ 1u, a.status, abort);
         if (!ok) break;
         if (lane == 0)
-          mbar_arrive_expect_tx(&bars->full[n], static_cast<uint32_t>(loads * box * 128));
+          mbar_arrive_expect_tx(&bars->full[n], static_cast<uint32_t>(loads * box * C::kLine));
         __syncwarp();
         if (take)
-          tma_load_4d_both(ring + n * C::kBytes + half * kKeys * 128 + b * box * 128, map,
-                           half * 64, in_page, wk.h, page, &bars->full[n], policy);
+          tma_load_4d_both(base + n * C::kLoadBytes + half * kKeys * C::kLine +
+                               b * box * C::kLine,
+                           map, half * (FP8 ? C::kLine : C::kLine / 2), in_page, wk.h, page,
+                           &bars->full[n], policy);
         if (++buf == bufs) {
           buf = 0;
           phase ^= 1u;
@@ -402,12 +437,64 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         t = wk.b.t0;
       }
     }
-  } else if (warp == kIssueS || warp == kIssueO) {
+  } else if (FP8 && warp >= kConvert) {
+    // ---- E4M3 tiles to fp16: a side's 64 threads take 16 bytes at a time,
+    // eight rows of one column side by side (no bank conflicts either way) ----
+    constexpr int kChunks = D / 16;                     // of a row
+    const bool keys = warp < kConvert + 2;
+    const int thread = threadIdx.x & (kConvertThreads - 1);
+    const int raw0 = keys ? 0 : C::kRaw, op0 = keys ? 0 : C::kK, ops = keys ? C::kK : C::kV;
+    int in = 0, out = 0;
+    uint32_t in_phase = 0, out_phase = 0;
+    while (left > 0) {
+      const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
+      left -= stop - t;
+      for (; t < stop; ++t) {
+        mbar_wait(&bars->full[raw0 + in], in_phase, a.status, abort);
+        mbar_wait(&bars->op_empty[op0 + out], out_phase ^ 1u, a.status, abort);
+        const uint8_t* src = raw + (raw0 + in) * C::kLoadBytes;
+        uint8_t* dst = ring + (op0 + out) * C::kBytes;
+        // values that no row sees may hold anything: make them zeros
+        const int lo = keys ? -(1 << 30) : wk.b.kbeg - t * kKeys;
+        const int hi = keys ? 1 << 30 : wk.b.kend - t * kKeys;
+#pragma unroll 4
+        for (int i = thread; i < kKeys * kChunks; i += kConvertThreads) {
+          const int row = (i & 7) + ((i >> 3) / kChunks) * 8, ch = (i >> 3) % kChunks;
+          const uint32_t at = D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4)
+                                       : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+          uint4 u = *reinterpret_cast<const uint4*>(src + at);
+          if (row < lo || row >= hi) u = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + tile_at(row, 2 * ch)) =
+              make_uint4(e4m3x2_to_f16x2(u.x), e4m3x2_to_f16x2(u.x >> 16),
+                         e4m3x2_to_f16x2(u.y), e4m3x2_to_f16x2(u.y >> 16));
+          *reinterpret_cast<uint4*>(dst + tile_at(row, 2 * ch + 1)) =
+              make_uint4(e4m3x2_to_f16x2(u.z), e4m3x2_to_f16x2(u.z >> 16),
+                         e4m3x2_to_f16x2(u.w), e4m3x2_to_f16x2(u.w >> 16));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->op_full[op0 + out]);
+        __syncwarp();
+        if (lane < 2)                                   // this warp has read the raw tile
+          mbar_arrive_cluster(map_shared_rank(smem_u32(&bars->empty[raw0 + in]), lane));
+        if (++in == C::kRaw) {
+          in = 0;
+          in_phase ^= 1u;
+        }
+        if (++out == ops) {
+          out = 0;
+          out_phase ^= 1u;
+        }
+      }
+      if (left > 0) {
+        if (!wk.next(a, group)) break;
+        t = wk.b.t0;
+      }
+    }
+  } else {
     // ---- MMAs ----
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kKeys);
-    constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D) | (1u << 16);     // B is MN-major
     const bool keys = warp == kIssueS;
-    const int bufs = keys ? C::kKBufs : C::kVBufs, buf0 = keys ? 0 : C::kKBufs;
+    const int bufs = keys ? C::kK : C::kV, buf0 = keys ? 0 : C::kK;
+    uint64_t* full = FP8 ? bars->op_full : bars->full;
     // A tile's descriptors are this one plus multiples of 16 bytes (building
     // each anew takes the issuing thread longer than the MMA does the pipe).
     const uint64_t desc0 = smem_desc(smem_u32(ring + buf0 * C::kBytes),
@@ -428,7 +515,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         const bool mine = t >= j0 && t < j1;
         const uint32_t sb = n & 1u, parity = (n >> 1) & 1u;
         const uint64_t desc = desc0 + static_cast<uint32_t>(buf) * (C::kBytes >> 4);
-        mbar_wait(&bars->full[buf0 + buf], phase, a.status, abort);
+        mbar_wait(&full[buf0 + buf], phase, a.status, abort);
         if (keys) {
           if (mine) {
             // S goes where P (n - 2) was
@@ -438,13 +525,13 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
                 mma_f16_ts(tmem + sb * 128, tmem + C::kTmemQ + ks * 8,
-                           desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), kIdescS,
+                           desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), C::kIdescS,
                            ks != 0);
               tc_commit(&bars->s_full[sb]);
             }
           }
         } else {
-          if (t * kKeys < wk.b.kbeg || (t + 1) * kKeys > wk.b.kend) {
+          if (!FP8 && (t * kKeys < wk.b.kbeg || (t + 1) * kKeys > wk.b.kend)) {
             // values that no row sees may hold anything: make them zeros
             for (int i = lane; i < kKeys * (D / 8); i += 32) {
               const int row = i / (D / 8), key = t * kKeys + row;
@@ -462,12 +549,15 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
 #pragma unroll
               for (int ks = 0; ks < kKeys / 16; ++ks)
                 mma_f16_ts(tmem + C::kTmemO, tmem + sb * 128 + ks * 8,
-                           desc + ks * (2048 >> 4), kIdescO, t != j0 || ks != 0);
+                           desc + ks * (2048 >> 4), C::kIdescO, t != j0 || ks != 0);
               tc_commit(&bars->pv_done[sb]);
             }
           }
         }
-        if (lane == 0) tc_commit_both(&bars->empty[buf0 + buf]);
+        if (lane == 0) {
+          if (FP8) tc_commit(&bars->op_empty[buf0 + buf]);
+          else tc_commit_both(&bars->empty[buf0 + buf]);
+        }
         if (mine) ++n;
         if (++buf == bufs) {
           buf = 0;
@@ -482,8 +572,10 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     // every arrival that the tensor cores still owe the barriers
     if (lane == 0) tc_commit(&bars->done[keys]);
     mbar_wait(&bars->done[keys], 0, a.status, abort);
+  }
   } else {
     // ---- softmax: a row's keys 0-63 and 64-127 in two threads ----
+    if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int half = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -492,13 +584,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     const uint32_t to = tmem + C::kTmemO + half * (D / 2) + lanes;    // output columns
     const uint32_t tq = tmem + C::kTmemQ + half * (D / 4) + lanes;    // and query columns
     const int pair_bar = 1 + (warp & 3);                              // the two warps of 32 rows
+    // words of a row's two threads: [tile parity][half][row].  A tile's word has
+    // been read once its thread has met the other one at the next tile's.
     float* mine = swap + half * kTile + row;
-    float* other = swap + (half ^ 1) * kTile + row;
+    const float* other = swap + (half ^ 1) * kTile + row;
     const long long hi = st.total * (cluster + 1) / clusters;
     uint32_t n = 0;                                     // tiles so far
     AttnPiece* piece = a.pieces + cluster;
     bool begun = false;
-    const float c = a.scale * 1.4426950408889634f;      // scores in powers of two
     while (left > 0) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       const bool whole = t == wk.b.t0 && stop == wk.b.t1;
@@ -513,22 +606,49 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       const int64_t tk = wk.rq.first + tok;
       const int head = wk.h * group + my - tok * group;
       float m = -INFINITY, l = 0.0f;
+      float c = a.scale * 1.4426950408889634f;          // scores in powers of two
+      if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[wk.h];
       if (j1 > j0) {
         // this row's half of the query (the last S with the previous ones has landed)
         {
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const __nv_bfloat16*>(a.q.data) + tk * a.q.token_stride +
               head * a.q.head_stride + half * (D / 2));
-          uint4 u[D / 16];
+          uint32_t w[D / 4];
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) u[i] = src[i];
+          for (int i = 0; i < D / 16; ++i) {
+            const uint4 u = src[i];
+            w[4 * i] = u.x;
+            w[4 * i + 1] = u.y;
+            w[4 * i + 2] = u.z;
+            w[4 * i + 3] = u.w;
+          }
+          if (FP8) {
+            float most = 0.0f;
 #pragma unroll
-          for (int i = 0; i < D / 16; i += 4) {
-            const uint32_t w[16] = {u[i].x, u[i].y, u[i].z, u[i].w,
-                                    u[i + 1].x, u[i + 1].y, u[i + 1].z, u[i + 1].w,
-                                    u[i + 2].x, u[i + 2].y, u[i + 2].z, u[i + 2].w,
-                                    u[i + 3].x, u[i + 3].y, u[i + 3].z, u[i + 3].w};
-            tmem_st_32x32b_x16(tq + i * 4, w);
+            for (int i = 0; i < D / 4; ++i)
+              most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
+                                       fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+            mine[((n + 1) & 1u) * 2 * kTile] = most;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+            most = fmaxf(most, other[((n + 1) & 1u) * 2 * kTile]);
+            // 2^(127 - e) and 2^(e - 127); rows of zeros or infinities stay as they are
+            int e = static_cast<int>(__float_as_uint(most) >> 23);
+            e = e == 0 || e == 255 ? 127 : min(e, 253);
+            const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+            c *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i)
+              w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up,
+                                __uint_as_float(w[i] & 0xFFFF0000u) * up);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < D / 4; i += 16) {
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = w[i + k];
+            tmem_st_32x32b_x16(tq + i, v);
           }
         }
         tmem_st_wait();
@@ -564,9 +684,9 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
               t4[k] = max3(t4[k], __uint_as_float(s[i >> 5][(i & 31) + 2 * k]),
                            __uint_as_float(s[i >> 5][(i & 31) + 2 * k + 1]));
           float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          *mine = top;
+          mine[sb * 2 * kTile] = top;
           asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-          top = fmaxf(top, *other) * c;
+          top = fmaxf(top, other[sb * 2 * kTile]) * c;
           // a new reference where some row's maximum has left the old one behind
           if (__any_sync(0xFFFFFFFFu, top > m + 8.0f)) {
             const float mn = fmaxf(m, top);
@@ -603,7 +723,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
               x = exp2_approx(x);
               y = exp2_approx(y);
               sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
-              p[k] = pack_bf16x2(x, y);
+              p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
             }
             tmem_st_32x32b_x16(tp + sb * 128 + i * 16, p);
           }
@@ -618,12 +738,13 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         __syncwarp();
         tc_fence_after();
         // the row's other sum
-        *mine = l;
+        mine[(n & 1u) * 2 * kTile] = l;
         asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-        l += *other;
+        l += other[(n & 1u) * 2 * kTile];
       }
       // ---- the rows out (a tile that saw no key here: zeros) ----
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      if (FP8 && a.cache.v_scale != nullptr) inv *= a.cache.v_scale[wk.h];
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + tk * a.out.token_stride +
                            head * a.out.head_stride + half * (D / 2);
       const int64_t at = (2 * static_cast<int64_t>(cluster) + slot) * a.piece_rows +
@@ -685,6 +806,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     tc_fence_before();
   }
   __syncthreads();
+  drain_after_abort(abort);
   cluster_sync();                       // the other CTA may still write here until now
   if (warp == kIssueS) {
     tc_fence_after();
@@ -692,13 +814,13 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
   }
 }
 
-template <int D>
+template <int D, bool FP8>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int clusters,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
-  auto kernel = attention_chunk_kernel<D>;
+  auto kernel = attention_chunk_kernel<D, FP8>;
   cudaError_t e =
-      set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), Cfg<D>::kSmem);
+      set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), Cfg<D, FP8>::kSmem);
   if (e != cudaSuccess) return e;
   // its prologue overlaps the plan; it waits for the plan before it reads anything
   cudaLaunchAttribute attr[2];
@@ -709,8 +831,8 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+  cfg.blockDim = dim3(Cfg<D, FP8>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<D, FP8>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -726,8 +848,11 @@ cudaError_t launch_attn_plan(const AttnArgs& a, int grid, cudaStream_t stream) {
 
 cudaError_t launch_attention_chunk(const AttnArgs& a, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int clusters, cudaStream_t stream) {
-  return a.cache.head_dim == 128 ? launch<128>(a, map_k, map_v, clusters, stream)
-                                 : launch<64>(a, map_k, map_v, clusters, stream);
+  if (a.cache.fp8)
+    return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, clusters, stream)
+                                   : launch<64, true>(a, map_k, map_v, clusters, stream);
+  return a.cache.head_dim == 128 ? launch<128, false>(a, map_k, map_v, clusters, stream)
+                                 : launch<64, false>(a, map_k, map_v, clusters, stream);
 }
 
 }  // namespace nvmoe

@@ -1,0 +1,70 @@
+// Joining the pieces of paged attention (attn_rows.cu, attn_chunk.cu).
+#include "attn.cuh"
+
+namespace nvmoe {
+namespace {
+
+// Joins the pieces of the segments that were cut between CTAs: block x takes
+// the segment that CTA x begins, a thread four dimensions of a row.  With the
+// largest maximum M, o = sum_c 2^(m_c - M) o_c and l likewise, in the order of
+// the CTAs, so results do not depend on timing.
+template <int D>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
+  pdl_wait();
+  const AttnPiece p = a.pieces[blockIdx.x];
+  const int item = blockIdx.y * 256 + threadIdx.x;
+  const int row = item / (D / 4), d = (item % (D / 4)) * 4;
+  if (row >= p.rows) return;
+  const int G = gridDim.x;
+  float top = -INFINITY;
+  const auto slot_of = [&](int c) { return 2 * static_cast<int64_t>(c) + (c == blockIdx.x); };
+  const auto has = [&](int c) { return p.total * c / G < p.total * (c + 1) / G; };
+  for (int c = blockIdx.x; c <= p.last; ++c)
+    if (has(c)) top = fmaxf(top, a.piece_ml[slot_of(c) * a.piece_rows + row].x);
+  const float use = top == -INFINITY ? 0.0f : top;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int c = blockIdx.x; c <= p.last; ++c) {
+    if (!has(c)) continue;
+    const int64_t at = slot_of(c) * a.piece_rows + row;
+    const float2 ml = a.piece_ml[at];
+    const float4 x = *reinterpret_cast<const float4*>(a.piece_o + at * D + d);
+    const float f = exp2_approx(ml.x - use);
+    sum = fmaf(f, ml.y, sum);
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+  }
+  const int group = a.q.heads / a.cache.heads;
+  const int tok = (p.row0 + row) / group;
+  const int64_t t = p.first + tok;
+  const int head = p.head * group + p.row0 + row - tok * group;
+  float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (a.cache.v_scale != nullptr) inv *= a.cache.v_scale[p.head];
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out.data) + t * a.out.token_stride +
+                            head * a.out.head_stride + d) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (d == 0 && a.lse != nullptr) a.lse[t * a.q.heads + head] = lse_of(top, sum);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_combine(const AttnArgs& a, int grid, cudaStream_t stream) {
+  // launched while the attention kernel runs; it waits for that kernel's end
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, static_cast<unsigned>(
+                               ceil_div(int64_t{a.piece_rows} * a.cache.head_dim / 4, 256)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return a.cache.head_dim == 128 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, a)
+                                 : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, a);
+}
+
+}  // namespace nvmoe

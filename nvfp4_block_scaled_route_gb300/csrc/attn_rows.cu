@@ -225,12 +225,13 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
     const uint64_t policy = policy_evict_first();
     int buf = 0;
     uint32_t phase = 0;
-    while (left > 0) {
+    bool ok = true;
+    while (left > 0 && ok) {
       const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
       const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
       const int stop = static_cast<int>(min(static_cast<long long>(wk.sp.t1), t + left));
       left -= stop - t;
-      for (; t < stop; ++t) {
+      for (; t < stop && ok; ++t) {
         const int key = t * kKeys + b * box;
         const bool take = b < boxes && half < T::kHalves && key < kend && key + box > kbeg;
         int page = 0;
@@ -245,7 +246,8 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         const int in_page = key & ((1 << a.cache.page_shift) - 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (!mbar_wait(&bars->empty[buf], phase ^ 1u, a.status, abort)) return;
+          ok = ok && mbar_wait(&bars->empty[buf], phase ^ 1u, a.status, abort);
+          if (!ok) break;
           if (lane == 0)
             mbar_arrive_expect_tx(&bars->full[buf],
                                   static_cast<uint32_t>(loads * box * T::kLine));
@@ -261,10 +263,12 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         }
       }
       if (left > 0) {
-        if (!wk.next_segment(a)) return;
+        if (!wk.next_segment(a)) break;
         t = wk.sp.t0;
       }
     }
+    __syncthreads();
+    drain_after_abort(abort);
     return;
   }
 
@@ -610,6 +614,8 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
     }
   }
   if (threadIdx.x == 0 && slot1_rows == 0) piece->rows = 0;
+  __syncthreads();
+  drain_after_abort(abort);
 }
 
 template <int D, bool FP8, int MT>

@@ -123,6 +123,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
+// After a wait has given up, roles of the CTA go on without their waits: time
+// (1 ms) for the copies and MMAs in flight to land before the CTA hands back
+// its shared memory and TMEM.  Called by every thread after a barrier.
+__device__ __forceinline__ void drain_after_abort(volatile int* abort) {
+  if (!*abort) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) {
+  }
+}
+
 // Arrive on the mbarrier at shared::cluster address `cluster_addr` (this
 // CTA's or the peer's, from mapa), with the default semantics (release at
 // CTA scope).  Between the CTAs of a pair this is the hand-over the pair's

@@ -460,3 +460,62 @@ def test_append_then_attend_is_attention_of_the_whole_prompt(nb):
     want, _, bound, _ = case.reference(qr.cpu())
     for o in outs:
         _within(o, want, bound, "prompt")
+
+
+def _dense(q, k, v, pos, window):
+    """Attention in 64 bits on the GPU, one request: q [n, Hq, D] at positions pos,
+    k and v [L, Hkv, D] -> (out, lse, bounds) as tests/_attention_reference.py has them."""
+    n, hq, D = q.shape
+    g = hq // k.shape[1]
+    scale = D ** -0.5
+    j = torch.arange(k.shape[0], device=DEV)
+    see = j <= pos[:, None]
+    if window:
+        see &= j > pos[:, None] - window
+    outs = []
+    for h in range(hq):
+        x, kk, vv = q[:, h].double(), k[:, h // g].double(), v[:, h // g].double()
+        s = (x @ kk.T * scale).masked_fill(~see, -math.inf)
+        ds = (x.abs() @ kk.abs().T * scale).masked_fill(~see, 0).amax(1) * (D + 8) * 2.0 ** -23
+        p = torch.softmax(s, 1)
+        o, ev, ls = p @ vv, p @ vv.abs(), torch.logsumexp(s, 1)
+        outs.append((o, ls, (ref.U + 2 * ds[:, None] + 2.0 ** -18) * ev + ref.U * o.abs(),
+                     ds + 2.0 ** -18 * (1 + ls.abs())))
+    return tuple(torch.stack(t, 1).cpu() for t in zip(*outs))
+
+
+@pytest.mark.parametrize("n,prior,hq,hk,D,window", [
+    (2000, 0, 32, 16, 128, 0), (1999, 1500, 24, 24, 64, 0), (3001, 500, 16, 8, 128, 300),
+    (700, 9000, 56, 8, 128, 0), (4, 9000, 56, 8, 128, 0), (1, 20000, 64, 64, 64, 0)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_paged_attention_many_segments(nb, n, prior, hq, hk, D, window, fp8):
+    """Enough work that every SM walks through several heads and row blocks;
+    the same bits every time."""
+    g = torch.Generator(device=DEV).manual_seed(n + hq)
+    L, page = n + prior, 64
+    pages = -(-L // page)
+    k, v = (torch.randn(pages, page, hk, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    q = (torch.randn(n, hq, D, generator=g, device=DEV) * 1.5).bfloat16()
+    table = torch.randperm(pages, generator=g, device=DEV).int()
+    scales = torch.rand(2, hk, generator=g, device=DEV) * 0.02 + 0.01
+    if fp8:
+        k, v = ((x / sc[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn) for x, sc in zip((k, v), scales))
+        cache = nb.PagedKVCache(k, v, k_scale=scales[0], v_scale=scales[1])
+        k, v = (x.double() * sc[:, None] for x, sc in zip((k, v), scales))
+    else:
+        cache = nb.PagedKVCache(k, v)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)   # noqa: E731
+    batch = nb.AttnBatch(i32(0, n), i32(L), table[None], max_new=n)
+    lse = torch.empty(n, hq, device=DEV)
+    ws = nb.paged_attention_workspace(cache, batch, hq, n)
+    out = nb.paged_attention(q, cache, batch, window=window, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    flat = lambda t: t[table.long()].flatten(0, 1)[:L]   # noqa: E731
+    want, wlse, b_out, b_lse = _dense(q, flat(k), flat(v), torch.arange(prior, L, device=DEV), window)
+    _within(out, want, b_out, "out")
+    _within(lse, wlse, b_lse, "lse")
+    again = [nb.paged_attention(q, cache, batch, window=window, ws=ws) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    assert all(torch.equal(a, out) for a in again)
