@@ -154,8 +154,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:
+        # the handle of torch.cuda.current_stream() without its Python object,
+        # whose making costs more than a small kernel's launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def sf_mma_bytes(rows: int, cols: int) -> int:
@@ -523,20 +526,18 @@ def attn_workspace(device="cuda") -> torch.Tensor:
 
 def _rows(t: torch.Tensor, what: str):
     """(address, token stride, head stride) of bf16 head rows [T, heads, D]."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or len(s) != 3 or not t.is_cuda:
         raise ValueError(f"{what} must be a bf16 CUDA tensor [tokens, heads, head_dim]")
-    st, sh, sd = t.stride()
-    T, H, _ = t.shape
-    if sd != 1:
+    if s[2] != 1:
         raise ValueError(f"{what}: head_dim must be contiguous")
-    # the stride of an axis of length 1 is never used
-    return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
+    return t.data_ptr(), s[0], s[1]
 
 
 def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != (n,):
+    if t.dtype is not dtype or t.shape != (n,):
         raise ValueError(f"{what} must be {dtype} [{n}]")
     return _ptr(t)
 
@@ -544,9 +545,10 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
 def _rope(rope: Optional[torch.Tensor]):
     if rope is None:
         return None, 0, 0
-    if rope.dtype != torch.float32 or rope.dim() != 2:
+    shape = rope.shape
+    if rope.dtype is not torch.float32 or len(shape) != 2:
         raise ValueError("rope must be float32 [positions, rotary_dim]")
-    return _ptr(rope), rope.shape[0], rope.shape[1]
+    return _ptr(rope), shape[0], shape[1]
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],

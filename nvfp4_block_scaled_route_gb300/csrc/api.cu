@@ -939,9 +939,13 @@ int moe_nvfp4_layer_forward(const nvmoe_weights* w, const void* x, int x_dtype,
 // --------------------------------------------------------- attention ----
 namespace {
 
-// Head rows [T, heads, D] with element strides: an nvmoe_status.
-int check_rows(const void* p, int64_t token_stride, int64_t head_stride, int heads, int D) {
+// Head rows [T, heads, D] with element strides: an nvmoe_status.  (The stride
+// of an axis of length 1 is never used.)
+int check_rows(const void* p, int64_t token_stride, int64_t head_stride, int64_t T, int heads,
+               int D) {
   if (p == nullptr) return NVMOE_ERR_INVALID_ARG;
+  if (T == 1) token_stride = 0;
+  if (heads == 1) head_stride = 0;
   if (!aligned16(p)) return NVMOE_ERR_MISALIGNED;
   constexpr int64_t kMost = int64_t{1} << 31;      // with T * heads < 2^31: offsets fit int64
   if (token_stride < 0 || head_stride < 0 || token_stride >= kMost || head_stride >= kMost)
@@ -1019,15 +1023,15 @@ int attn_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
   if (T == 0 || heads == 0) return NVMOE_OK;
   if (rope != nullptr && positions == nullptr) return NVMOE_ERR_INVALID_ARG;
   if (q_heads > 0) {
-    st = check_rows(q, q_token_stride, q_head_stride, q_heads, head_dim);
+    st = check_rows(q, q_token_stride, q_head_stride, T, q_heads, head_dim);
     if (st == NVMOE_OK)
-      st = check_rows(q_out, q_out_token_stride, q_out_head_stride, q_heads, head_dim);
+      st = check_rows(q_out, q_out_token_stride, q_out_head_stride, T, q_heads, head_dim);
     if (st != NVMOE_OK) return st;
   }
   if (kv_heads > 0) {
-    st = check_rows(k, k_token_stride, k_head_stride, kv_heads, head_dim);
+    st = check_rows(k, k_token_stride, k_head_stride, T, kv_heads, head_dim);
     if (st == NVMOE_OK)
-      st = check_rows(k_out, k_out_token_stride, k_out_head_stride, kv_heads, head_dim);
+      st = check_rows(k_out, k_out_token_stride, k_out_head_stride, T, kv_heads, head_dim);
     if (st != NVMOE_OK) return st;
   }
   const HeadTransform tr{rope, rope_positions, rope != nullptr ? rotary_dim : 0, interleaved != 0,
@@ -1066,11 +1070,11 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
   st = check_transform(rope, rope_positions, rotary_dim, D, q_weight, k_weight, eps);
   if (st != NVMOE_OK) return st;
   if (bv.tokens == 0 || bv.batch == 0) return NVMOE_OK;
-  st = check_rows(k, k_token_stride, k_head_stride, cv.heads, D);
-  if (st == NVMOE_OK) st = check_rows(v, v_token_stride, v_head_stride, cv.heads, D);
+  st = check_rows(k, k_token_stride, k_head_stride, bv.tokens, cv.heads, D);
+  if (st == NVMOE_OK) st = check_rows(v, v_token_stride, v_head_stride, bv.tokens, cv.heads, D);
   if (st == NVMOE_OK && q_heads > 0) {
-    st = check_rows(q, q_token_stride, q_head_stride, q_heads, D);
-    if (st == NVMOE_OK) st = check_rows(q_out, q_out_token_stride, q_out_head_stride, q_heads, D);
+    st = check_rows(q, q_token_stride, q_head_stride, bv.tokens, q_heads, D);
+    if (st == NVMOE_OK) st = check_rows(q_out, q_out_token_stride, q_out_head_stride, bv.tokens, q_heads, D);
   }
   if (st != NVMOE_OK) return st;
   const HeadTransform tr{rope, rope_positions, rope != nullptr ? rotary_dim : 0, interleaved != 0,
@@ -1163,9 +1167,10 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
                                            a.cache.heads, a.cache.head_dim))
     return NVMOE_ERR_WORKSPACE_TOO_SMALL;
   if (a.batch.tokens == 0 || a.batch.batch == 0) return NVMOE_OK;
-  st = check_rows(q, q_token_stride, q_head_stride, q_heads, a.cache.head_dim);
+  st = check_rows(q, q_token_stride, q_head_stride, a.batch.tokens, q_heads, a.cache.head_dim);
   if (st == NVMOE_OK)
-    st = check_rows(out, out_token_stride, out_head_stride, q_heads, a.cache.head_dim);
+    st = check_rows(out, out_token_stride, out_head_stride, a.batch.tokens, q_heads,
+                    a.cache.head_dim);
   if (st != NVMOE_OK) return st;
   a.q = {const_cast<void*>(q), q_token_stride, q_head_stride, q_heads};
   a.out = {out, out_token_stride, out_head_stride, q_heads};

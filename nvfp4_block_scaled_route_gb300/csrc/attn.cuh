@@ -72,15 +72,26 @@ struct AttnPiece {
   int64_t first;     // first token of the request
   int row0;          // first row: row i is token first + (row0 + i) / group
   int last;
-  long long total;   // tiles of the launch (CTA c has [total c / G, total (c + 1) / G))
 };
 
 // Where a CTA of the chunk kernel starts: `left` tiles from tile `tile` of the
 // segment (request, key head, row block).
 struct AttnStart {
-  long long total, left;
+  long long left, until;      // until: the next cluster's first tile
   int request, head, block, tile;
 };
+
+// First tile of share c when `total` tiles are dealt to g <= total takers (so
+// that none is without).
+__device__ __forceinline__ long long share_begin(long long total, int c, int g) {
+  if (total < (1 << 22))       // (c <= g <= 256: the product fits 32 bits)
+    return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(g);
+  return total * c / g;
+}
+// Takers among `grid` CTAs (or clusters).
+__device__ __forceinline__ int share_takers(long long total, int grid) {
+  return total < grid ? static_cast<int>(total) : grid;
+}
 
 struct AttnArgs {
   HeadRows q;

@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
   if (threadIdx.x == 0) a.plan_tile0[blocks] = tiles;
   __syncthreads();
   total = tiles * a.cache.heads;
+  const int takers = share_takers(total, G);
   for (int c = threadIdx.x; c < G; c += kPlanThreads) {
     AttnStart s;
-    const long long lo = total * c / G;
-    s.total = total;
-    s.left = total * (c + 1) / G - lo;
+    const long long lo = c < takers ? share_begin(total, c, takers) : total;
+    s.until = c < takers ? share_begin(total, c + 1, takers) : total;
+    s.left = s.until - lo;
     s.request = s.head = s.block = s.tile = 0;
     if (s.left > 0) {
       const auto base = [&](int k) { return a.plan_tile0[a.plan_block0[k]] * a.cache.heads; };
@@ -332,7 +333,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
   float* swap = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());   // query tile of the block
-  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const int cluster = blockIdx.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < (FP8 ? 2 * C::kRaw : C::kK + C::kV); ++i) {
@@ -588,7 +589,6 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     // been read once its thread has met the other one at the next tile's.
     float* mine = swap + half * kTile + row;
     const float* other = swap + (half ^ 1) * kTile + row;
-    const long long hi = st.total * (cluster + 1) / clusters;
     uint32_t n = 0;                                     // tiles so far
     AttnPiece* piece = a.pieces + cluster;
     bool begun = false;
@@ -783,16 +783,15 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       }
       if (threadIdx.x == 0 && rank == 0 && !whole && slot == 1) {
         // this cluster begins a cut segment: where its pieces end, for the join
-        const long long end = hi + (wk.b.t1 - stop);
+        const long long end = st.until + (wk.b.t1 - stop);
         int last = cluster + 1;
-        while (st.total * (last + 1) / clusters < end) ++last;
+        while (2 * (last + 1) < static_cast<int>(gridDim.x) && a.starts[last].until < end) ++last;
         AttnPiece p;
         p.rows = wk.b.rows;
         p.head = wk.h;
         p.first = wk.rq.first;
         p.row0 = wk.b.row0;
         p.last = last;
-        p.total = st.total;
         *piece = p;
         begun = true;
       }

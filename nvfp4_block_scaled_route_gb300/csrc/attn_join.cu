@@ -15,27 +15,47 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
   const int item = blockIdx.y * 256 + threadIdx.x;
   const int row = item / (D / 4), d = (item % (D / 4)) * 4;
   if (row >= p.rows) return;
-  const int G = gridDim.x;
+  // piece i: the CTA that begins the segment holds it in its slot 1, the
+  // others in their slot 0
+  const int n = p.last - static_cast<int>(blockIdx.x) + 1;
+  const auto at = [&](int i) {
+    return (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * a.piece_rows + row;
+  };
+  // batches of independent loads: what bounds this kernel is their latency
+  constexpr int kBatch = 8;
   float top = -INFINITY;
-  const auto slot_of = [&](int c) { return 2 * static_cast<int64_t>(c) + (c == blockIdx.x); };
-  const auto has = [&](int c) { return p.total * c / G < p.total * (c + 1) / G; };
-  for (int c = blockIdx.x; c <= p.last; ++c)
-    if (has(c)) top = fmaxf(top, a.piece_ml[slot_of(c) * a.piece_rows + row].x);
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float m[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      m[i] = i0 + i < n ? a.piece_ml[at(i0 + i)].x : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
+  }
   const float use = top == -INFINITY ? 0.0f : top;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float sum = 0.0f;
-#pragma unroll 4
-  for (int c = blockIdx.x; c <= p.last; ++c) {
-    if (!has(c)) continue;
-    const int64_t at = slot_of(c) * a.piece_rows + row;
-    const float2 ml = a.piece_ml[at];
-    const float4 x = *reinterpret_cast<const float4*>(a.piece_o + at * D + d);
-    const float f = exp2_approx(ml.x - use);
-    sum = fmaf(f, ml.y, sum);
-    o.x = fmaf(f, x.x, o.x);
-    o.y = fmaf(f, x.y, o.y);
-    o.z = fmaf(f, x.z, o.z);
-    o.w = fmaf(f, x.w, o.w);
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i0 + i < n) {
+        ml[i] = a.piece_ml[at(i0 + i)];
+        x[i] = *reinterpret_cast<const float4*>(a.piece_o + at(i0 + i) * D + d);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float f = exp2_approx(ml[i].x - use);
+      sum = fmaf(f, ml[i].y, sum);
+      o.x = fmaf(f, x[i].x, o.x);
+      o.y = fmaf(f, x[i].y, o.y);
+      o.z = fmaf(f, x[i].z, o.z);
+      o.w = fmaf(f, x[i].w, o.w);
+    }
   }
   const int group = a.q.heads / a.cache.heads;
   const int tok = (p.row0 + row) / group;

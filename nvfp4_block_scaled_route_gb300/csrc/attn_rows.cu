@@ -62,7 +62,10 @@ struct Bars {
   uint64_t full[kMaxBufs];
   uint64_t empty[kMaxBufs];
   int abort;
-  long long walk[2];          // request of the CTA's first tile, tile within the request
+  // where the CTA starts: request, tile within it
+  Request rq;
+  int r;
+  long long tile;
 };
 
 template <int D, bool FP8, int MT>
@@ -188,32 +191,40 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const long long lo = total * blockIdx.x / gridDim.x;
-  const long long hi = total * (blockIdx.x + 1) / gridDim.x;
+  const int takers = share_takers(total, gridDim.x);
   AttnPiece* piece = a.pieces + blockIdx.x;
-  if (lo >= hi) {
+  if (static_cast<int>(blockIdx.x) >= takers) {
     if (threadIdx.x == 0) piece->rows = 0;
     return;
   }
+  const long long lo = share_begin(total, blockIdx.x, takers);
+  const long long hi = share_begin(total, blockIdx.x + 1, takers);
   long long first = before + upto - mine;
   if (lo >= first && lo < first + mine) {
     int r = r_begin;
-    while (r + 1 < r_end) {
-      const Span s = tiles_of(load_request(a.batch, a.cache.page_shift, r, a.status), a.window);
+    Request rq;
+    while (true) {
+      rq = load_request(a.batch, a.cache.page_shift, r, a.status);
+      const Span s = tiles_of(rq, a.window);
       const long long c = static_cast<long long>(s.t1 - s.t0) * a.cache.heads;
-      if (lo < first + c) break;
+      if (lo < first + c || r + 1 >= r_end) break;
       first += c;
       ++r;
     }
-    bars->walk[0] = r;
-    bars->walk[1] = lo - first;
+    bars->rq = rq;
+    bars->r = r;
+    bars->tile = lo - first;
   }
   __syncthreads();
   Walk wk;
-  wk.load(a, static_cast<int>(bars->walk[0]));
+  wk.r = bars->r;
+  wk.rq = bars->rq;
+  wk.sp = tiles_of(wk.rq, a.window);
   const int span0 = max(1, wk.sp.t1 - wk.sp.t0);
-  wk.h = static_cast<int>(bars->walk[1] / span0);
-  int t = wk.sp.t0 + static_cast<int>(bars->walk[1] % span0);
+  const long long tile = bars->tile;
+  wk.h = tile < (1ll << 32) ? static_cast<uint32_t>(tile) / static_cast<uint32_t>(span0)
+                            : static_cast<int>(tile / span0);
+  int t = wk.sp.t0 + static_cast<int>(tile - static_cast<long long>(wk.h) * span0);
   long long left = hi - lo;
   volatile int* abort = &bars->abort;
 
@@ -597,14 +608,13 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
       // this CTA begins a cut segment: where its pieces end, for the join
       long long end = hi + (wk.sp.t1 - stop);
       int last = blockIdx.x + 1;
-      while (total * (last + 1) / gridDim.x < end) ++last;
+      while (last + 1 < takers && share_begin(total, last + 1, takers) < end) ++last;
       AttnPiece p;
       p.rows = rows;
       p.head = wk.h;
       p.first = wk.rq.first;
       p.row0 = 0;
       p.last = last;
-      p.total = total;
       *piece = p;
       slot1_rows = rows;
     }
