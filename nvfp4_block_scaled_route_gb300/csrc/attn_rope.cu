@@ -3,20 +3,33 @@
 //
 // Both are one pass over the data: x is read once, its transform written
 // once, so the bound is HBM (for few tokens, the launch and two dependent
-// round trips to memory).  With rstd = rsqrt(mean x^2 + eps) the transform of
-// element i with rotation partner j is
-//   out_i = rstd * (x_i * A_i + x_j * B_i),  A_i = w_i cos, B_i = -+ w_j sin
-// (A_i = w_i, B_i = 0 past rotary_dim), and A and B depend only on the token
-// and on q or k.  A group of head_dim / 8 lanes (16-byte loads) therefore
-// keeps A and B in registers and runs over several heads of one token; the
-// partner's eight elements come from another lane of the group by four
-// shuffles of the packed bf16 words, or from the same lane (interleaved).
+// round trips to memory).  With rstd = rsqrt(mean x^2 + eps) a pair (a, b) of
+// a head turns into
+//   a' = rstd * (a * (w_a cos) - b * (w_b sin)),
+//   b' = rstd * (b * (w_b cos) + a * (w_a sin)),
+// and the four products in brackets depend only on the token and on q or k.  A
+// group of head_dim / 8 lanes keeps them in registers and runs over up to
+// HEADS heads of q, of k or of v of one token, whose loads are all in flight
+// at once.  A lane holds whole pairs, so nothing passes between lanes but the
+// sum of squares: four elements of each half of the rotated part (8-byte
+// loads), or eight neighbours where pairs are neighbours or nothing is turned.
 #include "attn.cuh"
 
 namespace nvmoe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Many rows: eight heads a group and 64 registers a thread; into the cache
+// four and 48, which hides the longer chain of loads (request, length, page,
+// rotation) before a row can be stored.  Measured, 4096 tokens of 56 + 8 heads
+// of 128 and 21 k tokens into an E4M3 cache: 8 heads of 64 registers 29.8 us
+// and 188 us, 4 of 48 32.4 and 162, 8 of 90 registers 31.3 and 264.
+// Below kWideRows head rows two heads a group spread few tokens wider.
+constexpr int64_t kWideRows = 16384;
+template <bool APPEND>
+constexpr int kWideHeads = APPEND ? 4 : 8;
+template <bool APPEND>
+constexpr int kMinBlocks = APPEND ? 10 : 8;
 
 struct RopeArgs {
   HeadRows q, k, v;           // v.heads = 0: no cache
@@ -26,13 +39,15 @@ struct RopeArgs {
   HeadTransform tr;
   const int32_t* positions;
   int64_t T;
-  int chunks;                 // head chunks per token
+  int q_chunks, kv_chunks;    // chunks of HEADS heads: q's, k's (and as many of v)
+  int chunks;                 // of a token
   int* status;
 };
 
 // The request that holds row t: the last r with q_start[r] <= t (so empty
 // requests are passed over); -1 for a row of no request.
-__device__ __forceinline__ int request_of(const BatchView& b, int64_t t) {
+__device__ __forceinline__ int request_of(const BatchView& b, uint32_t row) {
+  const int64_t t = row;
   if (t >= b.q_start[b.batch] || t < b.q_start[0]) return -1;
   int lo = 0, hi = b.batch - 1;
   while (lo < hi) {
@@ -43,205 +58,244 @@ __device__ __forceinline__ int request_of(const BatchView& b, int64_t t) {
   return lo;
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0];
-  const float4 b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// Four bf16 (8 bytes) as two pairs of floats.
+__device__ __forceinline__ void bf16x4_to_f32x2(const uint2& u, uint64_t (&x)[2]) {
+  x[0] = f32x2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u));
+  x[1] = f32x2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint2 f32x2_to_bf16x4(const uint64_t (&x)[2]) {
+  float a, b, c, d;
+  f32x2_split(x[0], a, b);
+  f32x2_split(x[1], c, d);
+  return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x4(const uint64_t (&x)[2]) {
+  float a, b, c, d;
+  f32x2_split(x[0], a, b);
+  f32x2_split(x[1], c, d);
+  return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 
-// HEADS heads of one token per group, loaded together.  APPEND: k and v go to
-// the cache.
-template <int D, int HEADS, bool APPEND>
-__global__ void __launch_bounds__(kThreads) head_transform_kernel(const RopeArgs a) {
+// APPEND: k and v go to the cache.  PAIRS: neighbours form the pairs.
+template <int D, int HEADS, bool APPEND, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, kMinBlocks<APPEND>)
+head_transform_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 8;                       // lanes of a group
   const int sub = threadIdx.x & (kLanes - 1);
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) +
-                       threadIdx.x / kLanes;
-  const int heads = a.q.heads + a.k.heads + (APPEND ? a.v.heads : 0);
-  int64_t t = item / a.chunks;
-  const int h0 = static_cast<int>(item - t * a.chunks) * HEADS;
-  // lanes of groups past the end stay for the shuffles of their warp
-  bool live = t < a.T && h0 < heads;
-  if (!live) t = 0;
+  const uint32_t mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const uint32_t item = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const uint32_t t = item / static_cast<uint32_t>(a.chunks);
+  if (t >= a.T) return;
+  int chunk = static_cast<int>(item - t * a.chunks);
+  int kind = 0;                                       // 0: q, 1: k, 2: v
+  if (chunk >= a.q_chunks) {
+    chunk -= a.q_chunks;
+    kind = 1;
+    if (APPEND && chunk >= a.kv_chunks) {
+      chunk -= a.kv_chunks;
+      kind = 2;
+    }
+  }
+  const HeadRows& src = kind == 0 ? a.q : (APPEND && kind == 2 ? a.v : a.k);
+  const int h0 = chunk * HEADS;
+  const int heads = min(HEADS, src.heads - h0);
+  // this lane's elements: i0 .. i0+3 and i1 .. i1+3
+  const int half = a.tr.rotary_dim / 2;
+  const bool inside = sub * 8 < a.tr.rotary_dim;      // of the rotated part
+  const int i0 = !PAIRS && inside ? sub * 4 : sub * 8;
+  const int i1 = !PAIRS && inside ? half + sub * 4 : sub * 8 + 4;
 
   // the rows first: their loads do not depend on the position
-  uint4 raw[HEADS];
+  uint2 raw[HEADS][2];
+  {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src.data) +
+                             t * src.token_stride + h0 * src.head_stride;
 #pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = h0 + i;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (live && h < heads) {
-      const HeadRows& src = h < a.q.heads ? a.q : (h < a.q.heads + a.k.heads ? a.k : a.v);
-      const int hs = h < a.q.heads ? h
-                     : (h < a.q.heads + a.k.heads ? h - a.q.heads : h - a.q.heads - a.k.heads);
-      raw[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src.data) +
-                                               t * src.token_stride + hs * src.head_stride +
-                                               sub * 8);
+    for (int i = 0; i < HEADS; ++i) {
+      if (i < heads) {
+        raw[i][0] = *reinterpret_cast<const uint2*>(p + i0);
+        raw[i][1] = *reinterpret_cast<const uint2*>(p + i1);
+      }
+      p += src.head_stride;
     }
   }
 
   int64_t pos = 0;
   int64_t slot = 0;                                   // element offset of (page, offset)
-  if (live) {
-    if (APPEND) {
-      const int r = request_of(a.batch, t);
-      bool ok = false;
-      if (r >= 0) {
-        pos = static_cast<int64_t>(a.batch.kv_len[r]) - a.batch.q_start[r + 1] + t;
-        const int64_t page_i = pos >> a.cache.page_shift;
-        if (pos >= 0 && page_i < a.batch.max_pages) {
-          const int64_t page = a.batch.page_table[r * a.batch.max_pages + page_i];
-          ok = page >= 0 && page < a.cache.num_pages;
-          slot = page * a.cache.page_stride +
-                 (pos & ((int64_t{1} << a.cache.page_shift) - 1)) * a.cache.token_stride;
+  if (APPEND) {
+    const int r = request_of(a.batch, t);
+    if (r < 0) return;
+    pos = static_cast<int64_t>(a.batch.kv_len[r]) - a.batch.q_start[r + 1] + t;
+    const int64_t page_i = pos >> a.cache.page_shift;
+    bool ok = pos >= 0 && page_i < a.batch.max_pages &&
+              (a.tr.rope == nullptr || pos < a.tr.rope_positions);
+    if (ok) {
+      const int64_t page = a.batch.page_table[r * a.batch.max_pages + page_i];
+      ok = page >= 0 && page < a.cache.num_pages;
+      slot = page * a.cache.page_stride +
+             (pos & ((int64_t{1} << a.cache.page_shift) - 1)) * a.cache.token_stride;
+    }
+    if (!ok) {
+      record_status(a.status, kErrBadIndex);
+      return;
+    }
+  } else if (a.tr.rope != nullptr) {
+    pos = a.positions[t];
+    if (pos < 0 || pos >= a.tr.rope_positions) {
+      record_status(a.status, kErrBadIndex);
+      return;
+    }
+  }
+
+  // The products of weights, cosines and sines.  Halves: x_0 = elements i0.. ,
+  // x_1 = elements i1.. are the a and b of four pairs, y_0 = x_0 P_0 + x_1 Q_0,
+  // y_1 = x_1 P_1 + x_0 Q_1.  Neighbours: y = x P + x' Q with x' the elements
+  // exchanged within their pairs.
+  const __nv_bfloat16* weight = kind == 0 ? a.tr.q_weight : a.tr.k_weight;
+  const bool plain = APPEND && kind == 2;
+  const bool turned = !plain && inside;               // (rotary_dim is 0 without rope)
+  uint64_t P[2][2], Q[2][2];
+  {
+    const uint64_t one = f32x2(1.0f, 1.0f);
+    uint64_t w[2][2] = {{one, one}, {one, one}};
+    if (!plain && weight != nullptr) {
+      bf16x4_to_f32x2(*reinterpret_cast<const uint2*>(weight + i0), w[0]);
+      bf16x4_to_f32x2(*reinterpret_cast<const uint2*>(weight + i1), w[1]);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        P[s][j] = w[s][j];
+        Q[s][j] = 0;
+      }
+    if (turned) {
+      const float* row = a.tr.rope + pos * a.tr.rotary_dim + sub * 4;
+      const float4 c = *reinterpret_cast<const float4*>(row);
+      const float4 s = *reinterpret_cast<const float4*>(row + half);
+      if (PAIRS) {
+        const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float w0, w1;
+          f32x2_split(w[k >> 1][k & 1], w0, w1);
+          P[k >> 1][k & 1] = f32x2(w0 * cv[k], w1 * cv[k]);
+          Q[k >> 1][k & 1] = f32x2(-w1 * sv[k], w0 * sv[k]);
         }
-        if (a.tr.rope != nullptr && pos >= a.tr.rope_positions) ok = false;
-        if (!ok) record_status(a.status, kErrBadIndex);
-      }
-      live = ok;
-    } else if (a.tr.rope != nullptr) {
-      pos = a.positions[t];
-      if (pos < 0 || pos >= a.tr.rope_positions) {
-        record_status(a.status, kErrBadIndex);
-        live = false;
+      } else {
+        const uint64_t cc[2] = {f32x2(c.x, c.y), f32x2(c.z, c.w)};
+        const uint64_t ss[2] = {f32x2(s.x, s.y), f32x2(s.z, s.w)};
+        const uint64_t minus = f32x2(-1.0f, -1.0f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          P[0][j] = mul_f32x2(w[0][j], cc[j]);
+          P[1][j] = mul_f32x2(w[1][j], cc[j]);
+          Q[0][j] = mul_f32x2(mul_f32x2(w[1][j], ss[j]), minus);
+          Q[1][j] = mul_f32x2(w[0][j], ss[j]);
+        }
       }
     }
   }
-  if (!live) pos = 0;
 
-  // cosines and sines of this lane's elements; `from`: the lane of the group
-  // that holds the partners
-  const int e0 = sub * 8;
-  const int half = a.tr.rotary_dim / 2;
-  const bool turned = a.tr.rope != nullptr && e0 < a.tr.rotary_dim;
-  int from = sub;
-  float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-  }
-  if (turned) {
-    const float* row = a.tr.rope + pos * a.tr.rotary_dim;
-    if (a.tr.interleaved) {
-      const float4 cc = *reinterpret_cast<const float4*>(row + e0 / 2);
-      const float4 ss = *reinterpret_cast<const float4*>(row + half + e0 / 2);
-      const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = cv[i / 2];
-        s[i] = (i & 1) ? sv[i / 2] : -sv[i / 2];
-      }
-    } else {
-      const bool second = e0 >= half;
-      const int f = second ? e0 - half : e0;
-      from = second ? sub - half / 8 : sub + half / 8;
-      load8(row + f, c);
-      load8(row + half + f, s);
-      if (!second)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = -s[i];
-    }
-  }
-  const int from_lane = (threadIdx.x & 31 & ~(kLanes - 1)) + from;
-
-  float A[8], B[8];
-  int kind = -1;                                      // 0: q, 1: k
-  const __nv_bfloat16* weight = nullptr;
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
+    if (i >= heads) break;
     const int h = h0 + i;
-    const bool is_v = APPEND && h >= a.q.heads + a.k.heads;
-    const int want = h < a.q.heads ? 0 : 1;
-    if (want != kind) {
-      kind = want;
-      weight = kind == 0 ? a.tr.q_weight : a.tr.k_weight;
-      float w[8], wp[8];
+    uint64_t x[2][2];
+    bf16x4_to_f32x2(raw[i][0], x[0]);
+    bf16x4_to_f32x2(raw[i][1], x[1]);
+    if (!plain) {
+      uint64_t y[2][2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = wp[j] = 1.0f;
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          y[s][j] = mul_f32x2(x[s][j], P[s][j]);
+          // (not turned: no product with a partner, which may be infinite)
+          if (turned) {
+            uint64_t partner = x[s ^ 1][j];
+            if (PAIRS) {
+              float x0, x1;
+              f32x2_split(x[s][j], x0, x1);
+              partner = f32x2(x1, x0);
+            }
+            y[s][j] = fma_f32x2(partner, Q[s][j], y[s][j]);
+          }
+        }
       if (weight != nullptr) {
-        bf16x8_to_float(*reinterpret_cast<const uint4*>(weight + e0), w);
-        bf16x8_to_float(*reinterpret_cast<const uint4*>(weight + from * 8), wp);
+        uint64_t sq = mul_f32x2(x[0][0], x[0][0]);
+        sq = fma_f32x2(x[0][1], x[0][1], sq);
+        sq = fma_f32x2(x[1][0], x[1][0], sq);
+        sq = fma_f32x2(x[1][1], x[1][1], sq);
+        float s0, s1;
+        f32x2_split(sq, s0, s1);
+        float sum = s0 + s1;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+        const float rstd = rsqrtf(fmaf(sum, 1.0f / D, a.tr.eps));
+        const uint64_t r2 = f32x2(rstd, rstd);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) y[s][j] = mul_f32x2(y[s][j], r2);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        A[j] = w[j] * c[j];
-        B[j] = (a.tr.interleaved ? wp[j ^ 1] : wp[j]) * s[j];
-      }
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) x[s][j] = y[s][j];
     }
-    float x[8], xp[8];
-    bf16x8_to_float(raw[i], x);
-    uint4 other;
-    other.x = __shfl_sync(0xFFFFFFFFu, raw[i].x, from_lane);
-    other.y = __shfl_sync(0xFFFFFFFFu, raw[i].y, from_lane);
-    other.z = __shfl_sync(0xFFFFFFFFu, raw[i].z, from_lane);
-    other.w = __shfl_sync(0xFFFFFFFFu, raw[i].w, from_lane);
-    bf16x8_to_float(other, xp);
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (!live || h >= heads) continue;
-    float y[8];
-    if (is_v) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = x[j];
-    } else {
-      const float rstd = weight != nullptr ? rsqrtf(sum * (1.0f / D) + a.tr.eps) : 1.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // (not turned: no product with the partner, which may be infinite)
-        const float p = a.tr.interleaved ? xp[j ^ 1] : xp[j];
-        y[j] = rstd * (turned ? fmaf(p, B[j], x[j] * A[j]) : x[j] * A[j]);
-      }
-    }
-    if (APPEND && h >= a.q.heads) {
-      const int hk = is_v ? h - a.q.heads - a.k.heads : h - a.q.heads;
-      const int64_t at = slot + hk * a.cache.head_stride + e0;
-      void* dst = is_v ? a.cache.v : a.cache.k;
+    if (APPEND && kind != 0) {
+      const int64_t at = slot + h * a.cache.head_stride;
+      void* dst = plain ? a.cache.v : a.cache.k;
       if (a.cache.fp8) {
-        const float* sc = is_v ? a.cache.v_scale : a.cache.k_scale;
-        const float d = sc != nullptr ? sc[hk] : 1.0f;
-        uint2 o;
-        o.x = pack_e4m3x2(y[0] / d, y[1] / d) | (pack_e4m3x2(y[2] / d, y[3] / d) << 16);
-        o.y = pack_e4m3x2(y[4] / d, y[5] / d) | (pack_e4m3x2(y[6] / d, y[7] / d) << 16);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + at) = o;
+        const float* sc = plain ? a.cache.v_scale : a.cache.k_scale;
+        const float inv = sc != nullptr ? 1.0f / sc[h] : 1.0f;
+        const uint64_t inv2 = f32x2(inv, inv);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint64_t z[2] = {mul_f32x2(x[s][0], inv2), mul_f32x2(x[s][1], inv2)};
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(dst) + at + (s == 0 ? i0 : i1)) =
+              f32x2_to_e4m3x4(z);
+        }
       } else {
-        uint4 o = raw[i];
-        if (!is_v)
-          o = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                         pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + at) = o;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dst) + at;
+        *reinterpret_cast<uint2*>(o + i0) = plain ? raw[i][0] : f32x2_to_bf16x4(x[0]);
+        *reinterpret_cast<uint2*>(o + i1) = plain ? raw[i][1] : f32x2_to_bf16x4(x[1]);
       }
     } else {
-      const HeadRows& dst = h < a.q.heads ? a.q_out : a.k_out;
-      const int hd = h < a.q.heads ? h : h - a.q.heads;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst.data) + t * dst.token_stride +
-                                hd * dst.head_stride + e0) =
-          make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                     pack_bf16x2(y[6], y[7]));
+      const HeadRows& dst = kind == 0 ? a.q_out : a.k_out;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dst.data) + t * dst.token_stride +
+                         h * dst.head_stride;
+      *reinterpret_cast<uint2*>(o + i0) = f32x2_to_bf16x4(x[0]);
+      *reinterpret_cast<uint2*>(o + i1) = f32x2_to_bf16x4(x[1]);
     }
   }
 }
 
-template <int D, bool APPEND>
+template <int D, bool APPEND, bool PAIRS>
 cudaError_t launch_d(RopeArgs a, cudaStream_t stream) {
-  const int heads = a.q.heads + a.k.heads + a.v.heads;
   constexpr int kGroups = kThreads / (D / 8);
   const auto go = [&](auto kernel, int per) {
-    a.chunks = static_cast<int>(ceil_div(heads, per));
+    a.q_chunks = static_cast<int>(ceil_div(a.q.heads, per));
+    a.kv_chunks = static_cast<int>(ceil_div(a.k.heads, per));
+    a.chunks = a.q_chunks + (APPEND ? 2 : 1) * a.kv_chunks;
     const int64_t blocks = ceil_div(a.T * a.chunks, kGroups);
     kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
   };
-  return go(head_transform_kernel<D, 4, APPEND>, 4);
+  const int64_t heads = a.q.heads + a.k.heads + a.v.heads;
+  constexpr int kWide = kWideHeads<APPEND>;
+  return a.T * heads >= kWideRows ? go(head_transform_kernel<D, kWide, APPEND, PAIRS>, kWide)
+                                  : go(head_transform_kernel<D, 2, APPEND, PAIRS>, 2);
 }
 
 template <bool APPEND>
 cudaError_t launch(const RopeArgs& a, int head_dim, cudaStream_t stream) {
-  return head_dim == 128 ? launch_d<128, APPEND>(a, stream) : launch_d<64, APPEND>(a, stream);
+  if (a.tr.interleaved)
+    return head_dim == 128 ? launch_d<128, APPEND, true>(a, stream)
+                           : launch_d<64, APPEND, true>(a, stream);
+  return head_dim == 128 ? launch_d<128, APPEND, false>(a, stream)
+                         : launch_d<64, APPEND, false>(a, stream);
 }
 
 }  // namespace
