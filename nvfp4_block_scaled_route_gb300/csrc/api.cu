@@ -1121,8 +1121,10 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
   Carve c{base};
   const int64_t group = q_heads / kv_heads, rows = max_new * group;
   const bool few = rows <= kAttnFewRows;
-  a->piece_rows = few ? static_cast<int>(rows) : kAttnBlockRows;
-  const int64_t blocks = few ? 0 : ceil_div(tokens * group, kAttnBlockRows) + batch;
+  // few rows: all of a segment; else a tile of the chunk kernel, or two
+  a->piece_rows = few ? static_cast<int>(rows)
+                      : (rows <= kAttnTileRows ? kAttnTileRows : 2 * kAttnTileRows);
+  const int64_t blocks = few ? 0 : ceil_div(tokens * group, kAttnTileRows) + batch;
   a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
   a->status = c.take<int>(kStatusBytes);
   a->pieces = c.take<AttnPiece>(kMaxGrid * sizeof(AttnPiece));
@@ -1181,14 +1183,15 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
               a.cache.head_dim, static_cast<uint8_t*>(ws), &a);
   const bool few = a.piece_rows <= kAttnFewRows;
   CUtensorMap map_k, map_v;
-  const uint32_t box = few ? kAttnTileKeys : kAttnTileKeys / 2;
+  const bool pairs = a.piece_rows > kAttnTileRows;
+  const uint32_t box = pairs ? kAttnTileKeys / 2 : kAttnTileKeys;
   if (!make_kv_map(&map_k, a.cache.k, a.cache, box) ||
       !make_kv_map(&map_v, a.cache.v, a.cache, box))
     return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);
   // shares of the work: a CTA's, or a pair of CTAs' (chunks)
-  const int grid = std::min(few ? nsm : std::max(nsm / 2, 1), kMaxGrid);
+  const int grid = std::min(pairs ? std::max(nsm / 2, 1) : nsm, kMaxGrid);
   cudaError_t e;
   if (few) {
     e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);

@@ -115,11 +115,12 @@ struct AttnArgs {
   AttnStart* starts;
   int max_blocks;
 };
-constexpr int kAttnBlockRows = 256;
+constexpr int kAttnTileRows = 128;    // query rows of a tile of the chunk kernel, which
+                                      // takes blocks (piece_rows) of one tile or two
 // Rows of a segment up to which attention_rows_kernel takes the call.
-constexpr int kAttnFewRows = 64;
+constexpr int kAttnFewRows = 32;
 // map_k, map_v: [num_pages, heads, page_size, D] by strides, boxes of up to
-// 128 (chunk kernel: 64) tokens of one page and head.
+// 128 (chunk kernel with two tiles: 64) tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
 cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);

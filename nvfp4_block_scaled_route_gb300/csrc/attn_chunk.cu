@@ -3,7 +3,8 @@
 // The rows of a request and key head -- new tokens x query heads of the key
 // head, token-major -- are taken in blocks of 256 by a cluster of two CTAs, a
 // tile of 128 rows each, which share every key and value tile: each CTA loads
-// half of its pages and multicasts them to both.  Per 128 keys a CTA runs two
+// half of its pages and multicasts them to both.  (Where no request has more
+// than 128 rows, single CTAs take blocks of 128.)  Per 128 keys a CTA runs two
 // products of 128 x 128 x D and 128 x 128 exponentials; the tensor pipe is the
 // bound (4 * rows * keys * D flops).
 //
@@ -43,7 +44,6 @@ namespace {
 
 constexpr int kKeys = kAttnTileKeys;
 constexpr int kTile = 128;                   // query rows of a tile
-constexpr int kBlock = kAttnBlockRows;       // rows of a segment
 constexpr int kLoadK = 8, kLoadV = 9, kIssueS = 10;   // and 11: P V
 constexpr int kConvert = 12;                 // warps 12-13: keys, 14-15: values (E4M3)
 constexpr int kSoftmaxThreads = 256;
@@ -61,10 +61,11 @@ struct Block {
   int a0[2], a1[2];                          // of each query tile; empty if a1 <= a0
   int kbeg, kend;                            // keys that any row sees
 };
-__device__ __forceinline__ Block block_of(const Request& q, int group, int window, int p) {
+__device__ __forceinline__ Block block_of(const Request& q, int group, int window, int rows,
+                                          int p) {
   Block b;
-  b.row0 = p * kBlock;
-  b.rows = min(kBlock, q.n * group - b.row0);
+  b.row0 = p * rows;
+  b.rows = min(rows, q.n * group - b.row0);
   b.t0 = b.t1 = b.kbeg = b.kend = 0;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
@@ -88,8 +89,8 @@ __device__ __forceinline__ Block block_of(const Request& q, int group, int windo
   if (b.t1 == 0) b.t1 = 1;                   // nothing seen: a tile all the same, rows get zeros
   return b;
 }
-__device__ __forceinline__ int blocks_of(const Request& q, int group) {
-  return static_cast<int>((static_cast<int64_t>(q.n) * group + kBlock - 1) / kBlock);
+__device__ __forceinline__ int blocks_of(const Request& q, int group, int rows) {
+  return static_cast<int>((static_cast<int64_t>(q.n) * group + rows - 1) / rows);
 }
 
 __device__ __forceinline__ long long block_scan(long long v, long long* sums, long long* total) {
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
   for (int r0 = 0; r0 < B; r0 += kPlanThreads) {
     const int r = r0 + threadIdx.x;
     int n = 0;
-    if (r < B) n = blocks_of(load_request(a.batch, a.cache.page_shift, r, a.status), group);
+    if (r < B) n = blocks_of(load_request(a.batch, a.cache.page_shift, r, a.status), group,
+                             a.piece_rows);
     const long long at = blocks + block_scan(n, sums, &total);
     if (r < B) a.plan_block0[r] = static_cast<int>(min(at, static_cast<long long>(a.max_blocks)));
     blocks += total;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     if (i < blocks) {
       const int r = last_le(0, B, i, [&](int k) { return a.plan_block0[k]; });
       const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
-      const Block b = block_of(rq, group, a.window, i - a.plan_block0[r]);
+      const Block b = block_of(rq, group, a.window, a.piece_rows, i - a.plan_block0[r]);
       n = b.t1 - b.t0;
     }
     const long long at = tiles + block_scan(n, sums, &total);
@@ -201,7 +203,7 @@ struct Walk {
   __device__ __forceinline__ void load(const AttnArgs& a, int group, int request) {
     r = request;
     rq = load_request(a.batch, a.cache.page_shift, r, a.status);
-    blocks = blocks_of(rq, group);
+    blocks = blocks_of(rq, group, a.piece_rows);
   }
   // (only called while tiles are left; false if the batch ends all the same)
   __device__ __forceinline__ bool next(const AttnArgs& a, int group) {
@@ -215,7 +217,7 @@ struct Walk {
         } while (blocks == 0);
       }
     }
-    b = block_of(rq, group, a.window, p);
+    b = block_of(rq, group, a.window, a.piece_rows, p);
     return true;
   }
 };
@@ -297,7 +299,8 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <int D, bool FP8>
+// CL: CTAs of a cluster, a query tile each.
+template <int D, bool FP8, int CL>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
@@ -313,14 +316,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
   Bars* bars = reinterpret_cast<Bars*>(ring + C::kRing);
   float* swap = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());   // query tile of the block
-  const int cluster = blockIdx.x >> 1;
+  const int rank = CL == 1 ? 0 : static_cast<int>(cluster_ctarank());   // query tile
+  const int cluster = blockIdx.x / CL;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < (FP8 ? 2 * C::kRaw : C::kK + C::kV); ++i) {
       mbar_init(&bars->full[i], 1);
-      // both CTAs' readers: an issuer, or two converting warps
-      mbar_init(&bars->empty[i], FP8 ? 4 : 2);
+      // every CTA's readers: an issuer, or two converting warps
+      mbar_init(&bars->empty[i], (FP8 ? 2 : 1) * CL);
     }
     for (int i = 0; FP8 && i < C::kK + C::kV; ++i) {
       mbar_init(&bars->op_full[i], kConvertThreads);
@@ -344,7 +347,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (CL > 1) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
@@ -360,21 +363,21 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     wk.load(a, group, st.request);
     wk.h = st.head;
     wk.p = st.block;
-    wk.b = block_of(wk.rq, group, a.window, wk.p);
+    wk.b = block_of(wk.rq, group, a.window, a.piece_rows, wk.p);
     t = wk.b.t0 + st.tile;
   }
 
   if (warp >= kLoadK) {
     if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kLoadK || warp == kLoadV) {
-    // ---- this CTA's half (64 keys) of the key or value tiles, to both CTAs:
-    // lane = box (page part, column block) ----
+    // ---- this CTA's share (128 / CL keys) of the key or value tiles, to all CTAs
+    // of the cluster: lane = box (page part, column block) ----
     const bool keys = warp == kLoadK;
     const CUtensorMap* map = keys ? &map_k : &map_v;
     const int bufs = FP8 ? C::kRaw : (keys ? C::kK : C::kV);
     const int buf0 = keys ? 0 : (FP8 ? C::kRaw : C::kK);
     uint8_t* base = FP8 ? raw : ring;
-    const int box = min(kKeys / 2, 1 << a.cache.page_shift);
+    const int box = min(kKeys / CL, 1 << a.cache.page_shift);
     const int b = lane & 7, half = lane >> 3;
     const uint64_t policy = policy_evict_normal();
     int buf = 0;
@@ -387,7 +390,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         const int key = t * kKeys + b * box;
         const bool in = b * box < kKeys && half < C::kHalves && key < wk.b.kend &&
                         key + box > wk.b.kbeg;
-        const bool take = in && (b * box >= kKeys / 2) == (rank == 1);
+        const bool take = in && b * box / (kKeys / CL) == rank;
         int page = 0;
         if (take) {
           page = a.batch.page_table[wk.r * a.batch.max_pages + (key >> a.cache.page_shift)];
@@ -404,11 +407,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         if (lane == 0)
           mbar_arrive_expect_tx(&bars->full[n], static_cast<uint32_t>(loads * box * C::kLine));
         __syncwarp();
-        if (take)
-          tma_load_4d_both(base + n * C::kLoadBytes + half * kKeys * C::kLine +
-                               b * box * C::kLine,
-                           map, half * (FP8 ? C::kLine : C::kLine / 2), in_page, wk.h, page,
-                           &bars->full[n], policy);
+        if (take) {
+          uint8_t* dst = base + n * C::kLoadBytes + half * kKeys * C::kLine + b * box * C::kLine;
+          const int x = half * (FP8 ? C::kLine : C::kLine / 2);
+          if (CL > 1)
+            tma_load_4d_both(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
+          else
+            tma_load_4d(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
+        }
         if (++buf == bufs) {
           buf = 0;
           phase ^= 1u;
@@ -456,7 +462,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         fence_proxy_async_smem();
         mbar_arrive(&bars->op_full[op0 + out]);
         __syncwarp();
-        if (lane < 2)                                   // this warp has read the raw tile
+        if (lane < CL)                                  // this warp has read the raw tile
           mbar_arrive_cluster(map_shared_rank(smem_u32(&bars->empty[raw0 + in]), lane));
         if (++in == C::kRaw) {
           in = 0;
@@ -538,7 +544,8 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         }
         if (lane == 0) {
           if (FP8) tc_commit(&bars->op_empty[buf0 + buf]);
-          else tc_commit_both(&bars->empty[buf0 + buf]);
+          else if (CL > 1) tc_commit_both(&bars->empty[buf0 + buf]);
+          else tc_commit(&bars->empty[buf0 + buf]);
         }
         if (mine) ++n;
         if (++buf == bufs) {
@@ -582,6 +589,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       const int j0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
       const int j1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
       const int row0 = wk.b.row0 + rank * kTile;
+      const bool busy = (warp & 3) * 32 < rows;          // some row of this warp is real
       const int my = row0 + min(row, max(rows, 1) - 1);  // rows past the end act as the last
       const int tok = my / group;
       const int64_t tk = wk.rq.first + tok;
@@ -645,6 +653,10 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         for (int j = j0; j < j1; ++j, ++n) {
           const uint32_t sb = n & 1u;
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
+          if (!busy) {                                  // what these rows hold is not used
+            mbar_arrive(&bars->p_ready[sb]);
+            continue;
+          }
           __syncwarp();
           tc_fence_after();
           uint32_t s[2][32];
@@ -766,7 +778,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         // this cluster begins a cut segment: where its pieces end, for the join
         const long long end = st.until + (wk.b.t1 - stop);
         int last = cluster + 1;
-        while (2 * (last + 1) < static_cast<int>(gridDim.x) && a.starts[last].until < end) ++last;
+        while (CL * (last + 1) < static_cast<int>(gridDim.x) && a.starts[last].until < end) ++last;
         AttnPiece p;
         p.rows = wk.b.rows;
         p.head = wk.h;
@@ -787,36 +799,43 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
   }
   __syncthreads();
   drain_after_abort(abort);
-  cluster_sync();                       // the other CTA may still write here until now
+  if (CL > 1) cluster_sync();           // the other CTA may still write here until now
   if (warp == kIssueS) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int CL>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int clusters,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
-  auto kernel = attention_chunk_kernel<D, FP8>;
-  cudaError_t e =
-      set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), Cfg<D, FP8>::kSmem);
+  using C = Cfg<D, FP8>;
+  auto kernel = attention_chunk_kernel<D, FP8, CL>;
+  cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
   // its prologue overlaps the plan; it waits for the plan before it reads anything
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = CL;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(Cfg<D, FP8>::kThreads);
-  cfg.dynamicSmemBytes = Cfg<D, FP8>::kSmem;
+  cfg.gridDim = dim3(CL * clusters);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a, mk, mv);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_cl(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                      int clusters, cudaStream_t stream) {
+  return a.piece_rows == kTile ? launch<D, FP8, 1>(a, mk, mv, clusters, stream)
+                               : launch<D, FP8, 2>(a, mk, mv, clusters, stream);
 }
 
 }  // namespace
@@ -829,10 +848,10 @@ cudaError_t launch_attn_plan(const AttnArgs& a, int grid, cudaStream_t stream) {
 cudaError_t launch_attention_chunk(const AttnArgs& a, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int clusters, cudaStream_t stream) {
   if (a.cache.fp8)
-    return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, clusters, stream)
-                                   : launch<64, true>(a, map_k, map_v, clusters, stream);
-  return a.cache.head_dim == 128 ? launch<128, false>(a, map_k, map_v, clusters, stream)
-                                 : launch<64, false>(a, map_k, map_v, clusters, stream);
+    return a.cache.head_dim == 128 ? launch_cl<128, true>(a, map_k, map_v, clusters, stream)
+                                   : launch_cl<64, true>(a, map_k, map_v, clusters, stream);
+  return a.cache.head_dim == 128 ? launch_cl<128, false>(a, map_k, map_v, clusters, stream)
+                                 : launch_cl<64, false>(a, map_k, map_v, clusters, stream);
 }
 
 }  // namespace nvmoe

@@ -1,5 +1,5 @@
 // Paged attention for few query rows per key head (single tokens, drafted
-// tokens): rows = new tokens * (query heads / key heads) <= 64.
+// tokens): rows = new tokens * (query heads / key heads) <= 32.
 //
 // Every key and value is read once and used by all the rows of its head, so
 // the bound is HBM: 2 * 2 * D bytes of a bf16 key and value against 4 * rows *
@@ -16,7 +16,7 @@
 // shared memory, and for the weighted sum a warp takes D / 8 of the
 // dimensions over all keys.  So a warp holds few accumulators (no partial sums
 // of whole rows to join per tile), and both products run on mma.sync
-// m16n8k16: with at most 64 rows the tensor pipe is far from its limit even so.
+// m16n8k16: with at most 32 rows the tensor pipe is far from its limit even so.
 //
 // E4M3 caches: keys and values are exact in fp16, so the products run in fp16.
 // A query row is scaled by a power of two to a maximum in [1, 2), which keeps
@@ -35,9 +35,9 @@ constexpr int kComputeThreads = kComputeWarps * 32;
 constexpr int kThreads = kComputeThreads + 32;
 constexpr int kMaxBufs = 16;
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8>
 struct Tile {
-  static constexpr int kRingBytes = (MT == 4 ? 160 : 192) * 1024;
+  static constexpr int kRingBytes = 192 * 1024;
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
   static constexpr int kLine = kRowBytes < 128 ? kRowBytes : 128;   // bytes of a TMA box row
   static constexpr int kHalves = kRowBytes / kLine;
@@ -71,7 +71,7 @@ struct Bars {
 template <int D, bool FP8, int MT>
 constexpr int smem_bytes() {
   constexpr int rows = MT * 16;
-  return 1024 + Tile<D, FP8, MT>::kBufs * Tile<D, FP8, MT>::kBytes + rows * D * 2 + rows * kKeys * 2 +
+  return 1024 + Tile<D, FP8>::kBufs * Tile<D, FP8>::kBytes + rows * D * 2 + rows * kKeys * 2 +
          rows * kComputeWarps * 4 + rows * 4 + static_cast<int>(sizeof(Bars));
 }
 
@@ -144,7 +144,7 @@ template <int D, bool FP8, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
-  using T = Tile<D, FP8, MT>;
+  using T = Tile<D, FP8>;
   constexpr int kRows = MT * 16;
   constexpr int kQRow = D * 2, kPRow = kKeys * 2;
   extern __shared__ uint8_t raw_smem[];
@@ -645,8 +645,7 @@ template <int D, bool FP8>
 cudaError_t launch_mt(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                       cudaStream_t stream) {
   if (a.piece_rows <= 16) return launch<D, FP8, 1>(a, mk, mv, grid, stream);
-  if (a.piece_rows <= 32) return launch<D, FP8, 2>(a, mk, mv, grid, stream);
-  return launch<D, FP8, 4>(a, mk, mv, grid, stream);
+  return launch<D, FP8, 2>(a, mk, mv, grid, stream);
 }
 
 }  // namespace
