@@ -9,12 +9,14 @@
 // bound (4 * rows * keys * D flops).
 //
 //   S = Q K^T       Q from TMEM, K from shared memory (K-major), into TMEM
-//   P = 2^(cS - m)  TMEM -> registers -> 16 bits -> TMEM, over S
+//   P = 2^(cS - m)  TMEM -> registers -> 16 bits -> TMEM
 //   O += P V        P from TMEM, V from shared memory (MN-major)
 //
-// TMEM holds S twice: while the softmax of tile j is computed, the tensor
-// cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA would fill
-// TMEM with one S and O each, and the pipe would wait for every softmax.)
+// TMEM holds S twice and P once: while the softmax of tile j is computed, the
+// tensor cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA
+// would fill TMEM with one S and O each, and the pipe would wait for every
+// softmax.)  The next segment's queries go in before a segment's rows go out,
+// so that its first scores are computed meanwhile.
 //
 // Roles: warps 0-7 hold the softmax, a row's keys 0-63 and 64-127 in two
 // threads that exchange maxima through shared memory; warps 8 and 9 load key
@@ -237,7 +239,7 @@ struct Cfg {
   static constexpr int kRing = (kK + kV) * kBytes + 2 * kRaw * kLoadBytes;
   static constexpr int kSmem = kRing + 512 + 4 * kTile * 4;
   static_assert(kSmem <= 232448, "shared memory");
-  static constexpr uint32_t kTmemO = 256, kTmemQ = 384;   // S: columns 0 and 128
+  static constexpr uint32_t kTmemO = 256, kTmemQ = 384, kTmemP = 448;   // S: 0, 128
   // instruction descriptors: fp16 operands are format 0, bf16 format 1; V is MN-major
   static constexpr uint32_t kFormats = FP8 ? (1u << 7) | (1u << 10) : 0u;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kKeys) ^ kFormats;
@@ -247,8 +249,8 @@ struct Cfg {
 struct Bars {
   uint64_t full[14], empty[14];                        // loaded tiles: keys, then values
   uint64_t op_full[8], op_empty[8];                    // E4M3: operand tiles
-  // by parity of the CTA's tile counter; its next bit is the barrier's phase
-  uint64_t s_full[2], p_ready[2], pv_done[2];
+  // S by parity of the CTA's tile counter, whose next bit is then the phase
+  uint64_t s_full[2], s_free[2], p_ready, pv_done;
   uint64_t q_ready, done[2];
   uint32_t tmem;
   int abort;
@@ -332,10 +334,11 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     mbar_init(&bars->q_ready, kSoftmaxThreads);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_ready[i], kSoftmaxThreads);
-      mbar_init(&bars->pv_done[i], 1);
+      mbar_init(&bars->s_free[i], kSoftmaxThreads);
       mbar_init(&bars->done[i], 1);
     }
+    mbar_init(&bars->p_ready, kSoftmaxThreads);
+    mbar_init(&bars->pv_done, 1);
     bars->abort = 0;
     fence_mbarrier_init();
     prefetch_tensormap(&map_k);
@@ -429,8 +432,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     // ---- E4M3 tiles to fp16: a side's 64 threads take 16 bytes at a time,
     // eight rows of one column side by side (no bank conflicts either way) ----
     constexpr int kChunks = D / 16;                     // of a row
+    constexpr int kStepRows = kConvertThreads / kChunks, kSteps = kKeys / kStepRows;
     const bool keys = warp < kConvert + 2;
     const int thread = threadIdx.x & (kConvertThreads - 1);
+    const int ch = (thread >> 3) % kChunks, row0 = (thread & 7) + (thread >> 3) / kChunks * 8;
+    // (a step's rows are a multiple of 8 on: the swizzles stay, 1024 bytes of raw tile)
+    const uint32_t src0 = D == 128 ? row0 * 128 + ((ch ^ (row0 & 7)) << 4)
+                                   : row0 * 64 + ((ch ^ ((row0 >> 1) & 3)) << 4);
+    const uint32_t dst0 = tile_at(row0, 2 * ch), dst1 = tile_at(row0, 2 * ch + 1);
     const int raw0 = keys ? 0 : C::kRaw, op0 = keys ? 0 : C::kK, ops = keys ? C::kK : C::kV;
     int in = 0, out = 0;
     uint32_t in_phase = 0, out_phase = 0;
@@ -440,24 +449,33 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       for (; t < stop; ++t) {
         mbar_wait(&bars->full[raw0 + in], in_phase, a.status, abort);
         mbar_wait(&bars->op_empty[op0 + out], out_phase ^ 1u, a.status, abort);
-        const uint8_t* src = raw + (raw0 + in) * C::kLoadBytes;
+        const uint8_t* src = raw + (raw0 + in) * C::kLoadBytes + src0;
         uint8_t* dst = ring + (op0 + out) * C::kBytes;
         // values that no row sees may hold anything: make them zeros
-        const int lo = keys ? -(1 << 30) : wk.b.kbeg - t * kKeys;
-        const int hi = keys ? 1 << 30 : wk.b.kend - t * kKeys;
-#pragma unroll 4
-        for (int i = thread; i < kKeys * kChunks; i += kConvertThreads) {
-          const int row = (i & 7) + ((i >> 3) / kChunks) * 8, ch = (i >> 3) % kChunks;
-          const uint32_t at = D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4)
-                                       : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
-          uint4 u = *reinterpret_cast<const uint4*>(src + at);
-          if (row < lo || row >= hi) u = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + tile_at(row, 2 * ch)) =
-              make_uint4(e4m3x2_to_f16x2(u.x), e4m3x2_to_f16x2(u.x >> 16),
-                         e4m3x2_to_f16x2(u.y), e4m3x2_to_f16x2(u.y >> 16));
-          *reinterpret_cast<uint4*>(dst + tile_at(row, 2 * ch + 1)) =
-              make_uint4(e4m3x2_to_f16x2(u.z), e4m3x2_to_f16x2(u.z >> 16),
-                         e4m3x2_to_f16x2(u.w), e4m3x2_to_f16x2(u.w >> 16));
+        const int lo = wk.b.kbeg - t * kKeys, hi = wk.b.kend - t * kKeys;
+        const bool cut = !keys && (lo > 0 || hi < kKeys);
+#pragma unroll
+        for (int i0 = 0; i0 < kSteps; i0 += 8) {
+          uint4 u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            u[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 1024);
+          if (cut)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = row0 + (i0 + i) * kStepRows;
+              if (row < lo || row >= hi) u[i] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint8_t* to = dst + (i0 + i) * kStepRows * 128;
+            *reinterpret_cast<uint4*>(to + dst0) =
+                make_uint4(e4m3x2_to_f16x2(u[i].x), e4m3x2_to_f16x2(u[i].x >> 16),
+                           e4m3x2_to_f16x2(u[i].y), e4m3x2_to_f16x2(u[i].y >> 16));
+            *reinterpret_cast<uint4*>(to + dst1) =
+                make_uint4(e4m3x2_to_f16x2(u[i].z), e4m3x2_to_f16x2(u[i].z >> 16),
+                           e4m3x2_to_f16x2(u[i].w), e4m3x2_to_f16x2(u[i].w >> 16));
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars->op_full[op0 + out]);
@@ -506,8 +524,8 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
         mbar_wait(&full[buf0 + buf], phase, a.status, abort);
         if (keys) {
           if (mine) {
-            // S goes where P (n - 2) was
-            mbar_wait(&bars->pv_done[sb], parity ^ 1u, a.status, abort);
+            // S (n - 2) is in registers
+            mbar_wait(&bars->s_free[sb], parity ^ 1u, a.status, abort);
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
@@ -531,14 +549,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
             __syncwarp();
           }
           if (mine) {
-            mbar_wait(&bars->p_ready[sb], parity, a.status, abort);
+            mbar_wait(&bars->p_ready, n & 1u, a.status, abort);
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
               for (int ks = 0; ks < kKeys / 16; ++ks)
-                mma_f16_ts(tmem + C::kTmemO, tmem + sb * 128 + ks * 8,
+                mma_f16_ts(tmem + C::kTmemO, tmem + C::kTmemP + ks * 8,
                            desc + ks * (2048 >> 4), C::kIdescO, t != j0 || ks != 0);
-              tc_commit(&bars->pv_done[sb]);
+              tc_commit(&bars->pv_done);
             }
           }
         }
@@ -569,7 +587,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + half * 64 + lanes;                     // this thread's scores,
-    const uint32_t tp = tmem + half * 32 + lanes;                     // weights,
+    const uint32_t tp = tmem + C::kTmemP + half * 32 + lanes;         // weights,
     const uint32_t to = tmem + C::kTmemO + half * (D / 2) + lanes;    // output columns
     const uint32_t tq = tmem + C::kTmemQ + half * (D / 4) + lanes;    // and query columns
     const int pair_bar = 1 + (warp & 3);                              // the two warps of 32 rows
@@ -577,72 +595,106 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     // been read once its thread has met the other one at the next tile's.
     float* mine = swap + half * kTile + row;
     const float* other = swap + (half ^ 1) * kTile + row;
-    uint32_t n = 0;                                     // tiles so far
     AttnPiece* piece = a.pieces + cluster;
     bool begun = false;
-    while (left > 0) {
-      const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
-      const bool whole = t == wk.b.t0 && stop == wk.b.t1;
-      const int slot = t == wk.b.t0 ? 1 : 0;
+    uint32_t n = 0;                                     // tiles so far
+    // the segment: its tiles in this CTA, this thread's row
+    int stop = 0, j0 = 0, j1 = 0, rows = 0, row0 = 0, tok = 0, head = 0, slot = 0;
+    int64_t tk = 0;
+    bool whole = false, busy = false;                   // busy: some row of this warp is real
+    float c = 0.0f;                                     // scores in powers of two
+    const auto open = [&] {
+      stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
+      whole = t == wk.b.t0 && stop == wk.b.t1;
+      slot = t == wk.b.t0 ? 1 : 0;
       left -= stop - t;
-      const int rows = min(kTile, wk.b.rows - rank * kTile);
-      const int j0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
-      const int j1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
-      const int row0 = wk.b.row0 + rank * kTile;
-      const bool busy = (warp & 3) * 32 < rows;          // some row of this warp is real
+      rows = min(kTile, wk.b.rows - rank * kTile);
+      j0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
+      j1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
+      row0 = wk.b.row0 + rank * kTile;
+      busy = (warp & 3) * 32 < rows;
       const int my = row0 + min(row, max(rows, 1) - 1);  // rows past the end act as the last
-      const int tok = my / group;
-      const int64_t tk = wk.rq.first + tok;
-      const int head = wk.h * group + my - tok * group;
-      float m = -INFINITY, l = 0.0f;
-      float c = a.scale * 1.4426950408889634f;          // scores in powers of two
+      tok = my / group;
+      tk = wk.rq.first + tok;
+      head = wk.h * group + my - tok * group;
+      if (threadIdx.x == 0 && rank == 0 && !whole && slot == 1) {
+        // this cluster begins a cut segment: where its pieces end, for the join
+        const long long end = st.until + (wk.b.t1 - stop);
+        int last = cluster + 1;
+        while (CL * (last + 1) < static_cast<int>(gridDim.x) && a.starts[last].until < end) ++last;
+        AttnPiece p;
+        p.rows = wk.b.rows;
+        p.head = wk.h;
+        p.first = wk.rq.first;
+        p.row0 = wk.b.row0;
+        p.last = last;
+        *piece = p;
+        begun = true;
+      }
+      c = a.scale * 1.4426950408889634f;
       if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[wk.h];
-      if (j1 > j0) {
-        // this row's half of the query (the last S with the previous ones has landed)
-        {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(a.q.data) + tk * a.q.token_stride +
-              head * a.q.head_stride + half * (D / 2));
-          uint32_t w[D / 4];
+      if (j1 <= j0) return;
+      // this row's half of the query (the last S with the previous ones has landed)
+      if (busy) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(a.q.data) + tk * a.q.token_stride +
+            head * a.q.head_stride);
+        uint32_t w[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 u = src[half * (D / 16) + i];
+          w[4 * i] = u.x;
+          w[4 * i + 1] = u.y;
+          w[4 * i + 2] = u.z;
+          w[4 * i + 3] = u.w;
+        }
+        if (FP8) {
+          uint32_t most2 = 0;                           // of both halves, as bf16 pairs
+          const auto take = [&](uint32_t v) {
+            const __nv_bfloat162 x = __habs2(*reinterpret_cast<__nv_bfloat162*>(&v));
+            const __nv_bfloat162 y = __hmax2(x, *reinterpret_cast<__nv_bfloat162*>(&most2));
+            most2 = *reinterpret_cast<const uint32_t*>(&y);
+          };
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            const uint4 u = src[i];
-            w[4 * i] = u.x;
-            w[4 * i + 1] = u.y;
-            w[4 * i + 2] = u.z;
-            w[4 * i + 3] = u.w;
+            const uint4 u = src[(half ^ 1) * (D / 16) + i];
+            take(u.x);
+            take(u.y);
+            take(u.z);
+            take(u.w);
           }
-          if (FP8) {
-            float most = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i)
-              most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
-                                       fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-            mine[((n + 1) & 1u) * 2 * kTile] = most;
-            asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-            most = fmaxf(most, other[((n + 1) & 1u) * 2 * kTile]);
-            // 2^(127 - e) and 2^(e - 127); rows of zeros or infinities stay as they are
-            int e = static_cast<int>(__float_as_uint(most) >> 23);
-            e = e == 0 || e == 255 ? 127 : min(e, 253);
-            const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-            c *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+          for (int i = 0; i < D / 4; ++i) take(w[i]);
+          const float most = fmaxf(__uint_as_float(most2 << 16),
+                                   __uint_as_float(most2 & 0xFFFF0000u));
+          // 2^(127 - e) and 2^(e - 127); rows of zeros or infinities stay as they are
+          int e = static_cast<int>(__float_as_uint(most) >> 23);
+          e = e == 0 || e == 255 ? 127 : min(e, 253);
+          const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          c *= __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i)
-              w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up,
-                                __uint_as_float(w[i] & 0xFFFF0000u) * up);
-          }
-          __syncwarp();
+          for (int i = 0; i < D / 4; ++i)
+            w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up,
+                              __uint_as_float(w[i] & 0xFFFF0000u) * up);
+        }
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < D / 4; i += 16) {
-            uint32_t v[16];
+        for (int i = 0; i < D / 4; i += 16) {
+          uint32_t v[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = w[i + k];
-            tmem_st_32x32b_x16(tq + i, v);
-          }
+          for (int k = 0; k < 16; ++k) v[k] = w[i + k];
+          tmem_st_32x32b_x16(tq + i, v);
         }
         tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars->q_ready);
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->q_ready);
+    };
+    bool more = left > 0;
+    if (more) open();
+    while (more) {
+      float m = -INFINITY, l = 0.0f;
+      if (j1 > j0) {
         const int pos = wk.rq.pos0 + tok;
         const int vis_hi = min(pos + 1, wk.rq.len) - half * 64;
         const int vis_lo = (a.window > 0 ? pos - a.window + 1 : 0) - half * 64;
@@ -654,7 +706,9 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           const uint32_t sb = n & 1u;
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
           if (!busy) {                                  // what these rows hold is not used
-            mbar_arrive(&bars->p_ready[sb]);
+            mbar_arrive(&bars->s_free[sb]);
+            if (n > 0) mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
+            mbar_arrive(&bars->p_ready);
             continue;
           }
           __syncwarp();
@@ -663,11 +717,19 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           tmem_ld_32x32b_x32(ts + sb * 128, s[0]);
           tmem_ld_32x32b_x32(ts + sb * 128 + 32, s[1]);
           tmem_ld_wait();
-          if ((j + 1) * kKeys > all_hi || j * kKeys < all_lo) {
-            const int h = vis_hi - j * kKeys, lw = vis_lo - j * kKeys;
+          tc_fence_before();
+          mbar_arrive(&bars->s_free[sb]);
+          if ((j + 1) * kKeys > all_hi) {
+            const int h = vis_hi - j * kKeys;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (i >= h || i < lw) s[i >> 5][i & 31] = 0xFF800000u;      // -inf
+              if (i >= h) s[i >> 5][i & 31] = 0xFF800000u;              // -inf
+          }
+          if (j * kKeys < all_lo) {
+            const int lw = vis_lo - j * kKeys;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i < lw) s[i >> 5][i & 31] = 0xFF800000u;
           }
           float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -685,7 +747,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
             const float mn = fmaxf(m, top);
             if (j > j0) {
               // O holds P V up to tile j - 1
-              mbar_wait(&bars->pv_done[sb ^ 1u], ((n - 1) >> 1) & 1u, a.status, abort);
+              mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
               __syncwarp();
               tc_fence_after();
               const float f = exp2_approx(m - (mn == -INFINITY ? 0.0f : mn));
@@ -705,94 +767,94 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           const float use = m == -INFINITY ? 0.0f : m;  // a row without keys so far
           uint64_t sum[2] = {0, 0};
           const uint64_t c2 = f32x2(c, c), use2 = f32x2(-use, -use);
+          uint32_t p[32];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x, y;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[i][2 * k]),
-                                          __uint_as_float(s[i][2 * k + 1])), c2, use2), x, y);
-              x = exp2_approx(x);
-              y = exp2_approx(y);
-              sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
-              p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-            }
-            tmem_st_32x32b_x16(tp + sb * 128 + i * 16, p);
+          for (int k = 0; k < 32; ++k) {
+            float x, y;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[k >> 4][(2 * k) & 31]),
+                                        __uint_as_float(s[k >> 4][(2 * k + 1) & 31])), c2, use2),
+                        x, y);
+            x = exp2_approx(x);
+            y = exp2_approx(y);
+            sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
+            p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
           }
+          if (n > 0) {                                  // P V (n - 1) has read its weights
+            mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
+            __syncwarp();
+            tc_fence_after();
+          }
+          tmem_st_32x32b_x32(tp, p);
           float s0, s1;
           f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&bars->p_ready[sb]);
+          mbar_arrive(&bars->p_ready);
         }
-        mbar_wait(&bars->pv_done[(n - 1) & 1u], ((n - 1) >> 1) & 1u, a.status, abort);
-        __syncwarp();
-        tc_fence_after();
-        // the row's other sum
-        mine[(n & 1u) * 2 * kTile] = l;
-        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-        l += other[(n & 1u) * 2 * kTile];
       }
-      // ---- the rows out (a tile that saw no key here: zeros) ----
-      float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      if (FP8 && a.cache.v_scale != nullptr) inv *= a.cache.v_scale[wk.h];
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + tk * a.out.token_stride +
-                           head * a.out.head_stride + half * (D / 2);
+      // ---- the next segment's queries, then this one's rows ----
+      const bool seen = j1 > j0, real = row < rows, live = busy, to_out = whole;
+      const int64_t tk_out = tk;
+      const int head_out = head;
       const int64_t at = (2 * static_cast<int64_t>(cluster) + slot) * a.piece_rows +
                          rank * kTile + row;
+      const float v_scale =
+          FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
+      more = left > 0;
+      if (more) {
+        more = wk.next(a, group);
+        t = wk.b.t0;
+      }
+      if (more) open();
+      if (!live) continue;
+      if (seen) {
+        mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
+        __syncwarp();
+        tc_fence_after();
+        // the row's other sum.  (All have read the words of the last tile, whose
+        // P V is done; the next tile's are the others.)
+        mine[((n + 1) & 1u) * 2 * kTile] = l;
+        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+        l += other[((n + 1) & 1u) * 2 * kTile];
+      }
+      // (a tile that saw no key here: zeros)
+      const float inv = l == 0.0f ? 0.0f : v_scale / l;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + tk_out * a.out.token_stride +
+                           head_out * a.out.head_stride + half * (D / 2);
 #pragma unroll 1
       for (int i = 0; i < D / 2; i += 32) {
         uint32_t o[32];
         __syncwarp();
-        if (j1 > j0) {
+        if (seen) {
           tmem_ld_32x32b_x32(to + i, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
-        if (row < rows && whole) {
+        if (real && to_out) {
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             uint32_t w[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              w[n] = pack_bf16x2(__uint_as_float(o[k + 2 * n]) * inv,
-                                 __uint_as_float(o[k + 2 * n + 1]) * inv);
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(o[k + 2 * e]) * inv,
+                                 __uint_as_float(o[k + 2 * e + 1]) * inv);
             *reinterpret_cast<uint4*>(out + i + k) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else if (row < rows) {
+        } else if (real) {
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
             *reinterpret_cast<uint4*>(a.piece_o + at * D + half * (D / 2) + i + k) =
                 make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
-      if (row < rows && half == 0) {
-        if (!whole) a.piece_ml[at] = make_float2(m, l);
-        else if (a.lse != nullptr) a.lse[tk * a.q.heads + head] = lse_of(m, l);
+      if (real && half == 0) {
+        if (!to_out) a.piece_ml[at] = make_float2(m, l);
+        else if (a.lse != nullptr) a.lse[tk_out * a.q.heads + head_out] = lse_of(m, l);
       }
-      if (threadIdx.x == 0 && rank == 0 && !whole && slot == 1) {
-        // this cluster begins a cut segment: where its pieces end, for the join
-        const long long end = st.until + (wk.b.t1 - stop);
-        int last = cluster + 1;
-        while (CL * (last + 1) < static_cast<int>(gridDim.x) && a.starts[last].until < end) ++last;
-        AttnPiece p;
-        p.rows = wk.b.rows;
-        p.head = wk.h;
-        p.first = wk.rq.first;
-        p.row0 = wk.b.row0;
-        p.last = last;
-        *piece = p;
-        begun = true;
-      }
-      t = stop;
-      if (left > 0) {
-        if (!wk.next(a, group)) break;
-        t = wk.b.t0;
-      }
+      tc_fence_before();
     }
     if (threadIdx.x == 0 && rank == 0 && !begun) piece->rows = 0;
     tc_fence_before();
