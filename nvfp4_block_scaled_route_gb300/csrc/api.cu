@@ -1178,6 +1178,7 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   a.out = {out, out_token_stride, out_head_stride, q_heads};
   a.lse = lse;
   a.scale = scale;
+  a.group = FastDiv(static_cast<uint32_t>(q_heads / a.cache.heads));
   a.window = window;
   attn_layout(a.batch.batch, a.batch.tokens, a.batch.max_new, q_heads, a.cache.heads,
               a.cache.head_dim, static_cast<uint8_t*>(ws), &a);

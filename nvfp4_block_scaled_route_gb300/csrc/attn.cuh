@@ -93,6 +93,23 @@ __device__ __forceinline__ int share_takers(long long total, int grid) {
   return total < grid ? static_cast<int>(total) : grid;
 }
 
+// x / d for 0 <= x < 2^31 by a product and shifts (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t divisor) : d(divisor), shift(0) {
+    while ((uint64_t{1} << shift) < divisor) ++shift;              // ceil(log2 d)
+    mul = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << shift) - divisor)) /
+                                    divisor + 1);
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    const uint32_t t = __umulhi(mul, static_cast<uint32_t>(x));
+    const uint32_t half = (static_cast<uint32_t>(x) - t) >> (shift > 0 ? 1 : 0);
+    return static_cast<int>((t + half) >> (shift > 0 ? shift - 1 : 0));
+  }
+};
+
 struct AttnArgs {
   HeadRows q;
   HeadRows out;
@@ -102,6 +119,7 @@ struct AttnArgs {
   float scale;
   int window;
   int* status;
+  FastDiv group;            // query heads of a key head
   // pieces of cut segments: [grid], [grid][2][piece_rows][D] sums before the
   // division, [grid][2][piece_rows] (maximum in powers of two, weight sum)
   AttnPiece* pieces;

@@ -8,12 +8,12 @@
 // products of 128 x 128 x D and 128 x 128 exponentials; the tensor pipe is the
 // bound (4 * rows * keys * D flops).
 //
-//   S = Q K^T       Q from TMEM, K from shared memory (K-major), into TMEM
+//   S = Q K^T       both from shared memory (K-major), into TMEM
 //   P = 2^(cS - m)  TMEM -> registers -> 16 bits -> TMEM
 //   O += P V        P from TMEM, V from shared memory (MN-major)
 //
-// TMEM holds S twice and P once: while the softmax of tile j is computed, the
-// tensor cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA
+// TMEM holds S and P twice: while the softmax of tile j is computed, the tensor
+// cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA
 // would fill TMEM with one S and O each, and the pipe would wait for every
 // softmax.)  The next segment's queries go in before a segment's rows go out,
 // so that its first scores are computed meanwhile.
@@ -63,19 +63,19 @@ struct Block {
   int a0[2], a1[2];                          // of each query tile; empty if a1 <= a0
   int kbeg, kend;                            // keys that any row sees
 };
-__device__ __forceinline__ Block block_of(const Request& q, int group, int window, int rows,
-                                          int p) {
+__device__ __forceinline__ Block block_of(const Request& q, const FastDiv& group, int window,
+                                          int rows, int p) {
   Block b;
   b.row0 = p * rows;
-  b.rows = min(rows, q.n * group - b.row0);
+  b.rows = min(rows, q.n * static_cast<int>(group.d) - b.row0);
   b.t0 = b.t1 = b.kbeg = b.kend = 0;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     b.a0[a] = b.a1[a] = 0;
     const int rows = min(kTile, b.rows - a * kTile);
     if (rows <= 0) continue;
-    const int first = q.pos0 + (b.row0 + a * kTile) / group;
-    const int last = q.pos0 + (b.row0 + a * kTile + rows - 1) / group;
+    const int first = q.pos0 + group(b.row0 + a * kTile);
+    const int last = q.pos0 + group(b.row0 + a * kTile + rows - 1);
     const int end = min(q.len, last + 1);
     const int beg = window > 0 ? max(0, first - window + 1) : 0;
     if (end <= beg) continue;
@@ -136,7 +136,7 @@ __device__ __forceinline__ int last_le(int lo, int hi, long long x, F f) {
 // the attention kernel starts.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int G) {
   __shared__ long long sums[32];
-  const int B = a.batch.batch, group = a.q.heads / a.cache.heads;
+  const int B = a.batch.batch, group = static_cast<int>(a.group.d);
   pdl_trigger();
   long long total = 0, blocks = 0;
   for (int r0 = 0; r0 < B; r0 += kPlanThreads) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     if (i < blocks) {
       const int r = last_le(0, B, i, [&](int k) { return a.plan_block0[k]; });
       const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
-      const Block b = block_of(rq, group, a.window, a.piece_rows, i - a.plan_block0[r]);
+      const Block b = block_of(rq, a.group, a.window, a.piece_rows, i - a.plan_block0[r]);
       n = b.t1 - b.t0;
     }
     const long long at = tiles + block_scan(n, sums, &total);
@@ -219,7 +219,7 @@ struct Walk {
         } while (blocks == 0);
       }
     }
-    b = block_of(rq, group, a.window, a.piece_rows, p);
+    b = block_of(rq, a.group, a.window, a.piece_rows, p);
     return true;
   }
 };
@@ -233,13 +233,12 @@ struct Cfg {
   static constexpr int kLine = kRow < 128 ? kRow : 128;   // bytes of a box row
   static constexpr int kHalves = kRow / kLine;         // column blocks
   // operand tiles of keys and of values (bf16: as loaded), raw E4M3 tiles
-  static constexpr int kK = (FP8 ? 2 : 4) * (D == 128 ? 1 : 2) - (FP8 || D == 128 ? 0 : 1);
-  static constexpr int kV = FP8 ? kK : (D == 128 ? 3 : 7);
-  static constexpr int kRaw = FP8 ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int kRing = (kK + kV) * kBytes + 2 * kRaw * kLoadBytes;
-  static constexpr int kSmem = kRing + 512 + 4 * kTile * 4;
+  static constexpr int kK = (FP8 ? 2 : 3) * (D == 128 ? 1 : 2), kV = kK;
+  static constexpr int kRaw = FP8 ? (D == 128 ? 2 : 5) : 0;
+  static constexpr int kRing = (1 + kK + kV) * kBytes + 2 * kRaw * kLoadBytes;  // queries too
+  static constexpr int kSmem = kRing + 512 + 5 * kTile * 4;
   static_assert(kSmem <= 232448, "shared memory");
-  static constexpr uint32_t kTmemO = 256, kTmemQ = 384, kTmemP = 448;   // S: 0, 128
+  static constexpr uint32_t kTmemO = 256, kTmemP = 384;   // S: columns 0 and 128
   // instruction descriptors: fp16 operands are format 0, bf16 format 1; V is MN-major
   static constexpr uint32_t kFormats = FP8 ? (1u << 7) | (1u << 10) : 0u;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kKeys) ^ kFormats;
@@ -249,8 +248,8 @@ struct Cfg {
 struct Bars {
   uint64_t full[14], empty[14];                        // loaded tiles: keys, then values
   uint64_t op_full[8], op_empty[8];                    // E4M3: operand tiles
-  // S by parity of the CTA's tile counter, whose next bit is then the phase
-  uint64_t s_full[2], s_free[2], p_ready, pv_done;
+  // by parity of the CTA's tile counter, whose next bit is then the phase
+  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];
   uint64_t q_ready, done[2];
   uint32_t tmem;
   int abort;
@@ -309,14 +308,18 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
   using C = Cfg<D, FP8>;
   // the swizzle goes by the address: tiles start at multiples of 1024 bytes,
   // and there is no room to round up to one
-  extern __shared__ __align__(1024) uint8_t ring[];     // operand tiles, raw tiles
-  if ((smem_u32(ring) & 1023u) != 0) {
+  extern __shared__ __align__(1024) uint8_t sq[];       // queries, operand tiles, raw tiles
+  if ((smem_u32(sq) & 1023u) != 0) {
     record_status(a.status, kErrBounds);
     return;
   }
+  uint8_t* ring = sq + C::kBytes;
   uint8_t* raw = ring + (C::kK + C::kV) * C::kBytes;
-  Bars* bars = reinterpret_cast<Bars*>(ring + C::kRing);
+  Bars* bars = reinterpret_cast<Bars*>(sq + C::kRing);
   float* swap = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512);
+  // E4M3: each query row's power of two, [segment parity][row] (a thread may be
+  // a segment ahead of another)
+  uint8_t* q_exp = reinterpret_cast<uint8_t*>(swap + 4 * kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 1 ? 0 : static_cast<int>(cluster_ctarank());   // query tile
   const int cluster = blockIdx.x / CL;
@@ -335,10 +338,10 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_free[i], kSoftmaxThreads);
+      mbar_init(&bars->p_ready[i], kSoftmaxThreads);
+      mbar_init(&bars->pv_done[i], 1);
       mbar_init(&bars->done[i], 1);
     }
-    mbar_init(&bars->p_ready, kSoftmaxThreads);
-    mbar_init(&bars->pv_done, 1);
     bars->abort = 0;
     fence_mbarrier_init();
     prefetch_tensormap(&map_k);
@@ -359,14 +362,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
 
   const AttnStart st = a.starts[cluster];
   long long left = st.left;
-  const int group = a.q.heads / a.cache.heads;
+  const int group = static_cast<int>(a.group.d);
   Walk wk;
   int t = 0;
   if (left > 0) {
     wk.load(a, group, st.request);
     wk.h = st.head;
     wk.p = st.block;
-    wk.b = block_of(wk.rq, group, a.window, a.piece_rows, wk.p);
+    wk.b = block_of(wk.rq, a.group, a.window, a.piece_rows, wk.p);
     t = wk.b.t0 + st.tile;
   }
 
@@ -505,6 +508,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     // each anew takes the issuing thread longer than the MMA does the pipe).
     const uint64_t desc0 = smem_desc(smem_u32(ring + buf0 * C::kBytes),
                                      keys ? 16 : kKeys * 128, 1024, 2);
+    const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 1024, 2);
     int buf = 0;
     uint32_t phase = 0, q_phase = 0;
     uint32_t n = 0;                                     // tiles so far
@@ -530,9 +534,9 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
             if (lane == 0) {
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
-                mma_f16_ts(tmem + sb * 128, tmem + C::kTmemQ + ks * 8,
-                           desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), C::kIdescS,
-                           ks != 0);
+                mma_f16(tmem + sb * 128, q_desc + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
+                        desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), C::kIdescS,
+                        ks != 0);
               tc_commit(&bars->s_full[sb]);
             }
           }
@@ -549,14 +553,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
             __syncwarp();
           }
           if (mine) {
-            mbar_wait(&bars->p_ready, n & 1u, a.status, abort);
+            mbar_wait(&bars->p_ready[sb], parity, a.status, abort);
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
               for (int ks = 0; ks < kKeys / 16; ++ks)
-                mma_f16_ts(tmem + C::kTmemO, tmem + C::kTmemP + ks * 8,
+                mma_f16_ts(tmem + C::kTmemO, tmem + C::kTmemP + sb * 64 + ks * 8,
                            desc + ks * (2048 >> 4), C::kIdescO, t != j0 || ks != 0);
-              tc_commit(&bars->pv_done);
+              tc_commit(&bars->pv_done[sb]);
             }
           }
         }
@@ -589,7 +593,6 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     const uint32_t ts = tmem + half * 64 + lanes;                     // this thread's scores,
     const uint32_t tp = tmem + C::kTmemP + half * 32 + lanes;         // weights,
     const uint32_t to = tmem + C::kTmemO + half * (D / 2) + lanes;    // output columns
-    const uint32_t tq = tmem + C::kTmemQ + half * (D / 4) + lanes;    // and query columns
     const int pair_bar = 1 + (warp & 3);                              // the two warps of 32 rows
     // words of a row's two threads: [tile parity][half][row].  A tile's word has
     // been read once its thread has met the other one at the next tile's.
@@ -597,12 +600,16 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     const float* other = swap + (half ^ 1) * kTile + row;
     AttnPiece* piece = a.pieces + cluster;
     bool begun = false;
+    // 32-byte stores of the output rows
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.out.data) | a.out.token_stride * 2 |
+                        a.out.head_stride * 2) & 31) == 0;
     uint32_t n = 0;                                     // tiles so far
     // the segment: its tiles in this CTA, this thread's row
     int stop = 0, j0 = 0, j1 = 0, rows = 0, row0 = 0, tok = 0, head = 0, slot = 0;
     int64_t tk = 0;
     bool whole = false, busy = false;                   // busy: some row of this warp is real
     float c = 0.0f;                                     // scores in powers of two
+    int seg = 0;                                        // parity of the queries' segment
     const auto open = [&] {
       stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       whole = t == wk.b.t0 && stop == wk.b.t1;
@@ -614,7 +621,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       row0 = wk.b.row0 + rank * kTile;
       busy = (warp & 3) * 32 < rows;
       const int my = row0 + min(row, max(rows, 1) - 1);  // rows past the end act as the last
-      tok = my / group;
+      tok = a.group(my);
       tk = wk.rq.first + tok;
       head = wk.h * group + my - tok * group;
       if (threadIdx.x == 0 && rank == 0 && !whole && slot == 1) {
@@ -634,60 +641,42 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       c = a.scale * 1.4426950408889634f;
       if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[wk.h];
       if (j1 <= j0) return;
-      // this row's half of the query (the last S with the previous ones has landed)
-      if (busy) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(a.q.data) + tk * a.q.token_stride +
-            head * a.q.head_stride);
-        uint32_t w[D / 4];
+      seg ^= 1;
+      // the queries, D / 8 lanes a row (the last S with the previous ones has landed)
+      constexpr int kLanes = D / 8, kStep = kSoftmaxThreads / kLanes;
+      const int ch = threadIdx.x & (kLanes - 1), i0 = threadIdx.x / kLanes;
+      uint4 u[kTile / kStep];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 u = src[half * (D / 16) + i];
-          w[4 * i] = u.x;
-          w[4 * i + 1] = u.y;
-          w[4 * i + 2] = u.z;
-          w[4 * i + 3] = u.w;
+      for (int i = 0; i < kTile / kStep; ++i) {
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (i0 + i * kStep < rows) {
+          const int r = row0 + i0 + i * kStep, k = a.group(r);
+          u[i] = *reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(a.q.data) + (wk.rq.first + k) * a.q.token_stride +
+              (wk.h * group + r - k * group) * a.q.head_stride + ch * 8);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < kTile / kStep; ++i) {
         if (FP8) {
-          uint32_t most2 = 0;                           // of both halves, as bf16 pairs
-          const auto take = [&](uint32_t v) {
-            const __nv_bfloat162 x = __habs2(*reinterpret_cast<__nv_bfloat162*>(&v));
-            const __nv_bfloat162 y = __hmax2(x, *reinterpret_cast<__nv_bfloat162*>(&most2));
-            most2 = *reinterpret_cast<const uint32_t*>(&y);
-          };
+          float x[8], most = 0.0f;
+          bf16x8_to_float(u[i], x);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint4 u = src[(half ^ 1) * (D / 16) + i];
-            take(u.x);
-            take(u.y);
-            take(u.z);
-            take(u.w);
-          }
+          for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[k]));
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) take(w[i]);
-          const float most = fmaxf(__uint_as_float(most2 << 16),
-                                   __uint_as_float(most2 & 0xFFFF0000u));
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
           // 2^(127 - e) and 2^(e - 127); rows of zeros or infinities stay as they are
           int e = static_cast<int>(__float_as_uint(most) >> 23);
           e = e == 0 || e == 255 ? 127 : min(e, 253);
           const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-          c *= __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i)
-            w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up,
-                              __uint_as_float(w[i] & 0xFFFF0000u) * up);
+          if (ch == 0) q_exp[seg * kTile + i0 + i * kStep] = static_cast<uint8_t>(e);
+          u[i] = make_uint4(pack_f16x2(x[0] * up, x[1] * up), pack_f16x2(x[2] * up, x[3] * up),
+                            pack_f16x2(x[4] * up, x[5] * up), pack_f16x2(x[6] * up, x[7] * up));
         }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < D / 4; i += 16) {
-          uint32_t v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = w[i + k];
-          tmem_st_32x32b_x16(tq + i, v);
-        }
-        tmem_st_wait();
+        *reinterpret_cast<uint4*>(sq + tile_at(i0 + i * kStep, ch)) = u[i];
       }
-      tc_fence_before();
+      fence_proxy_async_smem();
       mbar_arrive(&bars->q_ready);
     };
     bool more = left > 0;
@@ -695,20 +684,25 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     while (more) {
       float m = -INFINITY, l = 0.0f;
       if (j1 > j0) {
+        float cr = c;
+        const int seg_now = seg;
         const int pos = wk.rq.pos0 + tok;
         const int vis_hi = min(pos + 1, wk.rq.len) - half * 64;
         const int vis_lo = (a.window > 0 ? pos - a.window + 1 : 0) - half * 64;
         // keys that every row of the tile sees
-        const int all_hi = min(wk.rq.pos0 + row0 / group + 1, wk.rq.len);
+        const int all_hi = min(wk.rq.pos0 + a.group(row0) + 1, wk.rq.len);
         const int all_lo =
-            a.window > 0 ? wk.rq.pos0 + (row0 + rows - 1) / group - a.window + 1 : 0;
+            a.window > 0 ? wk.rq.pos0 + a.group(row0 + rows - 1) - a.window + 1 : 0;
         for (int j = j0; j < j1; ++j, ++n) {
           const uint32_t sb = n & 1u;
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
+          // (S follows the arrivals of all that wrote the queries and their factors)
+          if (FP8 && j == j0)
+            cr = c * __uint_as_float(static_cast<uint32_t>(q_exp[seg_now * kTile + row]) << 23);
           if (!busy) {                                  // what these rows hold is not used
             mbar_arrive(&bars->s_free[sb]);
-            if (n > 0) mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
-            mbar_arrive(&bars->p_ready);
+            if (n > 1) mbar_wait(&bars->pv_done[sb], ((n - 2) >> 1) & 1u, a.status, abort);
+            mbar_arrive(&bars->p_ready[sb]);
             continue;
           }
           __syncwarp();
@@ -741,13 +735,15 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           mine[sb * 2 * kTile] = top;
           asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-          top = fmaxf(top, other[sb * 2 * kTile]) * c;
+          top = fmaxf(top, other[sb * 2 * kTile]) * cr;
           // a new reference where some row's maximum has left the old one behind
           if (__any_sync(0xFFFFFFFFu, top > m + 8.0f)) {
             const float mn = fmaxf(m, top);
             if (j > j0) {
-              // O holds P V up to tile j - 1
-              mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
+              // O holds P V up to tile j - 1.  (That P V (n - 2) is done says that
+              // the other barrier's phase is that of tile n - 1.)
+              if (n > 1) mbar_wait(&bars->pv_done[sb], ((n - 2) >> 1) & 1u, a.status, abort);
+              mbar_wait(&bars->pv_done[sb ^ 1u], ((n - 1) >> 1) & 1u, a.status, abort);
               __syncwarp();
               tc_fence_after();
               const float f = exp2_approx(m - (mn == -INFINITY ? 0.0f : mn));
@@ -766,7 +762,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           }
           const float use = m == -INFINITY ? 0.0f : m;  // a row without keys so far
           uint64_t sum[2] = {0, 0};
-          const uint64_t c2 = f32x2(c, c), use2 = f32x2(-use, -use);
+          const uint64_t c2 = f32x2(cr, cr), use2 = f32x2(-use, -use);
           uint32_t p[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -779,18 +775,18 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
             sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
             p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
           }
-          if (n > 0) {                                  // P V (n - 1) has read its weights
-            mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
+          if (n > 1) {                                  // P V (n - 2) has read its weights
+            mbar_wait(&bars->pv_done[sb], ((n - 2) >> 1) & 1u, a.status, abort);
             __syncwarp();
             tc_fence_after();
           }
-          tmem_st_32x32b_x32(tp, p);
+          tmem_st_32x32b_x32(tp + sb * 64, p);
           float s0, s1;
           f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&bars->p_ready);
+          mbar_arrive(&bars->p_ready[sb]);
         }
       }
       // ---- the next segment's queries, then this one's rows ----
@@ -801,6 +797,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
                          rank * kTile + row;
       const float v_scale =
           FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
+      const uint32_t end = n - 1;                       // the last tile
       more = left > 0;
       if (more) {
         more = wk.next(a, group);
@@ -809,7 +806,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       if (more) open();
       if (!live) continue;
       if (seen) {
-        mbar_wait(&bars->pv_done, (n - 1) & 1u, a.status, abort);
+        mbar_wait(&bars->pv_done[end & 1u], (end >> 1) & 1u, a.status, abort);
         __syncwarp();
         tc_fence_after();
         // the row's other sum.  (All have read the words of the last tile, whose
@@ -834,20 +831,30 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
         if (real && to_out) {
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t w[4];
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (wide) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(o[k + 2 * e]) * inv,
-                                 __uint_as_float(o[k + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + i + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 16; k += 8) {
+              const uint32_t v[8] = {w[k],     w[k + 1], w[k + 2], w[k + 3],
+                                     w[k + 4], w[k + 5], w[k + 6], w[k + 7]};
+              st_global_v8_b32(out + i + 2 * k, v);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(out + i + 2 * k) =
+                  make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
           }
         } else if (real) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<uint4*>(a.piece_o + at * D + half * (D / 2) + i + k) =
-                make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 32; k += 8) {
+            const uint32_t v[8] = {o[k],     o[k + 1], o[k + 2], o[k + 3],
+                                   o[k + 4], o[k + 5], o[k + 6], o[k + 7]};
+            st_global_v8_b32(a.piece_o + at * D + half * (D / 2) + i + k, v);
+          }
         }
       }
       if (real && half == 0) {

@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
       o.w = fmaf(f, x[i].w, o.w);
     }
   }
-  const int group = a.q.heads / a.cache.heads;
-  const int tok = (p.row0 + row) / group;
+  const int group = static_cast<int>(a.group.d);
+  const int tok = a.group(p.row0 + row);
   const int64_t t = p.first + tok;
   const int head = p.head * group + p.row0 + row - tok * group;
   float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
