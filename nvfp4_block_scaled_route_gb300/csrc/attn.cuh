@@ -176,6 +176,14 @@ __device__ __forceinline__ Request load_request(const BatchView& b, int page_shi
   return q;
 }
 
+// Of the boxes of `box` keys that make up a tile from key0 on, how many hold a
+// key of [kbeg, kend).
+__device__ __forceinline__ int boxes_of(int key0, int box, int kbeg, int kend) {
+  const int first = max(0, kbeg - key0) / box;
+  const int last = (min(kAttnTileKeys, max(0, kend - key0)) + box - 1) / box;
+  return max(0, last - first);
+}
+
 // Eight bf16 of a 16-byte word as floats.
 __device__ __forceinline__ void bf16x8_to_float(const uint4& u, float (&x)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};

@@ -405,14 +405,14 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
             page = static_cast<int>(a.cache.num_pages);       // past the map: zeros
           }
         }
-        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, in));
+        const int loads = C::kHalves * boxes_of(t * kKeys, box, wk.b.kbeg, wk.b.kend);
         const int in_page = key & ((1 << a.cache.page_shift) - 1);
         const int n = buf0 + buf;
+        // (nothing here joins the lanes again: in a failing CTA some may go on)
         ok = mbar_wait(&bars->empty[n], phase ^ 1u, a.status, abort);
         if (!ok) break;
         if (lane == 0)
           mbar_arrive_expect_tx(&bars->full[n], static_cast<uint32_t>(loads * box * C::kLine));
-        __syncwarp();
         if (take) {
           uint8_t* dst = base + n * C::kLoadBytes + half * kKeys * C::kLine + b * box * C::kLine;
           const int x = half * (FP8 ? C::kLine : C::kLine / 2);

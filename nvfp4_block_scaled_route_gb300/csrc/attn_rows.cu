@@ -18,6 +18,14 @@
 // of whole rows to join per tile), and both products run on mma.sync
 // m16n8k16: with at most 32 rows the tensor pipe is far from its limit even so.
 //
+// E4M3 caches and up to 16 rows: two groups of eight warps take the tiles in
+// turn, each with its own sums and maxima and a ring of its own (so that it
+// waits for every phase of its barriers), and the second hands its part of a
+// segment to the first.  A tile's chain of products, exchanges and products
+// takes 1900 cycles of latency, an E4M3 tile's bytes 1400 of HBM: two requests
+// of up to 131072 tokens 72 -> 66 us.  A bf16 tile takes 2800 anyway, and there
+// the second group costs (64 requests 228 -> 240 us).
+//
 // E4M3 caches: keys and values are exact in fp16, so the products run in fp16.
 // A query row is scaled by a power of two to a maximum in [1, 2), which keeps
 // every element above 2^-16 of it exact, and the factor goes back in with the
@@ -30,9 +38,12 @@ namespace nvmoe {
 namespace {
 
 constexpr int kKeys = kAttnTileKeys;
-constexpr int kComputeWarps = 8;
+constexpr int kComputeWarps = 8;                  // of a group
 constexpr int kComputeThreads = kComputeWarps * 32;
-constexpr int kThreads = kComputeThreads + 32;
+template <bool FP8, int MT>
+constexpr int kGroups = FP8 && MT == 1 ? 2 : 1;
+template <bool FP8, int MT>
+constexpr int kThreads = kGroups<FP8, MT> * kComputeThreads + 32;
 constexpr int kMaxBufs = 16;
 
 template <int D, bool FP8>
@@ -70,9 +81,10 @@ struct Bars {
 
 template <int D, bool FP8, int MT>
 constexpr int smem_bytes() {
-  constexpr int rows = MT * 16;
-  return 1024 + Tile<D, FP8>::kBufs * Tile<D, FP8>::kBytes + rows * D * 2 + rows * kKeys * 2 +
-         rows * kComputeWarps * 4 + rows * 4 + static_cast<int>(sizeof(Bars));
+  constexpr int rows = MT * 16, groups = kGroups<FP8, MT>;
+  return 1024 + Tile<D, FP8>::kBufs * Tile<D, FP8>::kBytes + rows * D * 2 +
+         groups * (rows * kKeys * 2 + rows * kComputeWarps * 4) + rows * 4 +
+         (groups - 1) * (rows * D * 4 + rows * 8) + static_cast<int>(sizeof(Bars));
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -101,8 +113,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void compute_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory");
+// The warps of one group; those of all.
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kComputeThreads) : "memory");
+}
+template <int GROUPS>
+__device__ __forceinline__ void all_sync() {
+  asm volatile("bar.sync 3, %0;" ::"n"(GROUPS * kComputeThreads) : "memory");
 }
 
 // 128-key tiles of a request: [t0, t1), empty without new tokens.  A request
@@ -141,7 +158,7 @@ struct Walk {
 };
 
 template <int D, bool FP8, int MT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<FP8, MT>, 1)
 attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
   using T = Tile<D, FP8>;
@@ -151,15 +168,19 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
   uint8_t* ring = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint8_t* sq = ring + T::kBufs * T::kBytes;
   uint8_t* sp_ = sq + kRows * kQRow;
-  float* smax = reinterpret_cast<float*>(sp_ + kRows * kPRow);    // [kRows][8]
-  float* sfac = smax + kRows * kComputeWarps;                     // [kRows]
-  Bars* bars = reinterpret_cast<Bars*>(sfac + kRows);
+  constexpr int kG = kGroups<FP8, MT>, kWarps = kThreads<FP8, MT> / 32;
+  constexpr int kPer = T::kBufs / kG;                               // buffers of a group
+  float* smax = reinterpret_cast<float*>(sp_ + kG * kRows * kPRow);      // [group][kRows][8]
+  float* sfac = smax + kG * kRows * kComputeWarps;                       // [kRows]
+  float* join_o = sfac + kRows;                       // second group's sums, by thread
+  float2* join_ml = reinterpret_cast<float2*>(join_o + (kG - 1) * kRows * D);  // [kRows]
+  Bars* bars = reinterpret_cast<Bars*>(join_ml + (kG - 1) * kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
 
   // ---- this CTA's share of the tiles ----
-  long long* scan = reinterpret_cast<long long*>(smax);           // [9] warp sums
-  const int per = (a.batch.batch + kThreads - 1) / kThreads;
+  long long* scan = reinterpret_cast<long long*>(smax);           // [kWarps] warp sums
+  const int per = (a.batch.batch + kThreads<FP8, MT> - 1) / kThreads<FP8, MT>;
   const int r_begin = min(a.batch.batch, static_cast<int>(threadIdx.x) * per);
   const int r_end = min(a.batch.batch, r_begin + per);
   long long mine = 0;
@@ -175,7 +196,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
   }
   if (lane == 31) scan[warp] = upto;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < T::kBufs; ++i) {
+    for (int i = 0; i < kG * kPer; ++i) {
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->empty[i], kComputeWarps);
     }
@@ -187,7 +208,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
@@ -228,14 +249,14 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
   long long left = hi - lo;
   volatile int* abort = &bars->abort;
 
-  if (warp == kComputeWarps) {
+  if (warp == kG * kComputeWarps) {
     // ---- producer: lane = box of the tile (page part, half row) ----
     const int box = min(kKeys, 1 << a.cache.page_shift);
     const int boxes = kKeys / box;
     const int b = lane & 7, half = lane >> 3;
     const uint64_t policy = policy_evict_first();
-    int buf = 0;
-    uint32_t phase = 0;
+    int buf[kG] = {}, side = 0;
+    uint32_t phase[kG] = {};
     bool ok = true;
     while (left > 0 && ok) {
       const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
@@ -253,25 +274,26 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
             page = static_cast<int>(a.cache.num_pages);     // past the map: zeros
           }
         }
-        const int loads = __popc(__ballot_sync(0xFFFFFFFFu, take));
+        const int loads = T::kHalves * boxes_of(t * kKeys, box, kbeg, kend);
         const int in_page = key & ((1 << a.cache.page_shift) - 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && mbar_wait(&bars->empty[buf], phase ^ 1u, a.status, abort);
+          const int n = side * kPer + buf[side];
+          // (nothing here joins the lanes again: in a failing CTA some may go on)
+          ok = ok && mbar_wait(&bars->empty[n], phase[side] ^ 1u, a.status, abort);
           if (!ok) break;
           if (lane == 0)
-            mbar_arrive_expect_tx(&bars->full[buf],
-                                  static_cast<uint32_t>(loads * box * T::kLine));
-          __syncwarp();
+            mbar_arrive_expect_tx(&bars->full[n], static_cast<uint32_t>(loads * box * T::kLine));
           if (take)
-            tma_load_4d(ring + buf * T::kBytes + half * kKeys * T::kLine + b * box * T::kLine,
+            tma_load_4d(ring + n * T::kBytes + half * kKeys * T::kLine + b * box * T::kLine,
                         kv == 0 ? &map_k : &map_v, half * (T::kLine / (FP8 ? 1 : 2)), in_page,
-                        wk.h, page, &bars->full[buf], policy);
-          if (++buf == T::kBufs) {
-            buf = 0;
-            phase ^= 1u;
+                        wk.h, page, &bars->full[n], policy);
+          if (++buf[side] == kPer) {
+            buf[side] = 0;
+            phase[side] ^= 1u;
           }
         }
+        if (kG == 2) side ^= 1;                         // the groups take turns
       }
       if (left > 0) {
         if (!wk.next_segment(a)) break;
@@ -283,13 +305,27 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
     return;
   }
 
-  // ---- compute warps ----
+  // ---- compute warps: group `side`, warp `w` of it ----
+  const int side = kG == 2 ? warp >> 3 : 0, w = warp & 7;
+  const int thread = threadIdx.x & (kComputeThreads - 1);
   const int group = a.q.heads / a.cache.heads;
+  sp_ += side * kRows * kPRow;
+  smax += side * kRows * kComputeWarps;
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   constexpr int kN = (D == 128) ? 2 : 1;            // 8-wide accumulator tiles of a warp
-  const uint32_t ring_u = smem_u32(ring), sq_u = smem_u32(sq), sp_u = smem_u32(sp_);
+  const uint32_t sq_u = smem_u32(sq), sp_u = smem_u32(sp_);
+  ring += side * kPer * T::kBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  uint64_t* full = bars->full + side * kPer;
+  uint64_t* empty = bars->empty + side * kPer;
   int buf = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, seq = 0;
+  const auto next_buffer = [&] {
+    if (++buf == kPer) {
+      buf = 0;
+      phase ^= 1u;
+    }
+  };
   int slot1_rows = 0;
   while (left > 0) {
     const int rows = wk.rq.n * group;               // <= kRows, checked on the host
@@ -302,7 +338,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
 
     // queries to shared memory
     constexpr int kLanes = D / 8;
-    for (int row = threadIdx.x / kLanes; row < kRows; row += kComputeThreads / kLanes) {
+    for (int row = threadIdx.x / kLanes; row < kRows; row += kG * kComputeThreads / kLanes) {
       const int ch = threadIdx.x & (kLanes - 1);
       uint4 u = make_uint4(0, 0, 0, 0);
       if (row < rows) {
@@ -338,7 +374,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         }
       }
     }
-    compute_sync();
+    all_sync<kG>();
 
     float o[MT][kN][4], m[MT][2], l[MT][2], cr[MT][2];
     int vis_hi[MT][2], vis_lo[MT][2];
@@ -363,7 +399,8 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
     const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
     const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
 
-    for (; t < stop; ++t) {
+    for (; t < stop; ++t, ++seq) {
+      if (kG == 2 && static_cast<int>(seq & 1u) != side) continue;
       const int key0 = t * kKeys;
       // scores of this warp's 16 keys
       float s[MT][2][4];
@@ -373,10 +410,10 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[i][n][e] = 0.0f;
-      mbar_wait(&bars->full[buf], phase, a.status, abort);
+      mbar_wait(&full[buf], phase, a.status, abort);
       {
         const uint32_t kb = ring_u + buf * T::kBytes;
-        const int krow = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+        const int krow = w * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
         for (int ks = 0; ks < D / (FP8 ? 32 : 16); ++ks) {
           uint32_t kf[4];
@@ -404,11 +441,8 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->empty[buf]);
-      if (++buf == T::kBufs) {
-        buf = 0;
-        phase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive(&empty[buf]);
+      next_buffer();
 
       const bool masked = key0 + kKeys > all_hi || key0 < all_lo;
 #pragma unroll
@@ -423,16 +457,16 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
               float& x = s[i][n][2 * e + j];
               x *= cr[i][e];
               if (masked) {
-                const int key = key0 + warp * 16 + n * 8 + c2 + j;
+                const int key = key0 + w * 16 + n * 8 + c2 + j;
                 if (key >= vis_hi[i][e] || key < vis_lo[i][e]) x = -INFINITY;
               }
               top = fmaxf(top, x);
             }
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          if ((lane & 3) == 0) smax[(i * 16 + e * 8 + g) * kComputeWarps + warp] = top;
+          if ((lane & 3) == 0) smax[(i * 16 + e * 8 + g) * kComputeWarps + w] = top;
         }
-      compute_sync();
+      group_sync(side);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -452,7 +486,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
             const float p0 = exp2_approx(s[i][n][2 * e] - use);
             const float p1 = exp2_approx(s[i][n][2 * e + 1] - use);
             sum += p0 + p1;
-            *reinterpret_cast<uint32_t*>(sp_ + mat_at<kPRow>(row, warp * 2 + n) + c2 * 2) =
+            *reinterpret_cast<uint32_t*>(sp_ + mat_at<kPRow>(row, w * 2 + n) + c2 * 2) =
                 FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
           l[i][e] = fmaf(l[i][e], f, sum);
@@ -462,11 +496,11 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
             o[i][n][2 * e + 1] *= f;
           }
         }
-      mbar_wait(&bars->full[buf], phase, a.status, abort);
+      mbar_wait(&full[buf], phase, a.status, abort);
       const bool cut = key0 < kbeg || key0 + kKeys > kend;
       if (cut) {
         // values that no row sees may hold anything: make them zeros
-        for (int i = threadIdx.x; i < kKeys * (T::kRowBytes / 16); i += kComputeThreads) {
+        for (int i = thread; i < kKeys * (T::kRowBytes / 16); i += kComputeThreads) {
           const int row = i / (T::kRowBytes / 16), ch = i % (T::kRowBytes / 16);
           if (key0 + row < kbeg || key0 + row >= kend)
             *reinterpret_cast<uint4*>(ring + buf * T::kBytes + T::at(row, ch)) =
@@ -474,7 +508,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         }
         fence_proxy_async_smem();                   // before the next TMA into this buffer
       }
-      compute_sync();
+      group_sync(side);
       // weighted sum over the 128 keys of this warp's dimensions
       const uint32_t vb = ring_u + buf * T::kBytes;
 #pragma unroll
@@ -482,31 +516,31 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         uint32_t b0[2][kN], b1[2][kN];              // k16 step, accumulator tile
         if (FP8) {
           uint32_t v[4];
-          ldsm4_t(vb + T::at(k2 * 32 + lane, D == 128 ? warp : warp >> 1), v);
+          ldsm4_t(vb + T::at(k2 * 32 + lane, D == 128 ? w : w >> 1), v);
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
-            uint32_t w[4];
-            w[0] = e4m3x2_to_f16x2(v[2 * st]);              // (key, dims d and d + 1)
-            w[1] = e4m3x2_to_f16x2(v[2 * st] >> 16);        // (key + 1, ...)
-            w[2] = e4m3x2_to_f16x2(v[2 * st + 1]);
-            w[3] = e4m3x2_to_f16x2(v[2 * st + 1] >> 16);
+            uint32_t h[4];
+            h[0] = e4m3x2_to_f16x2(v[2 * st]);              // (key, dims d and d + 1)
+            h[1] = e4m3x2_to_f16x2(v[2 * st] >> 16);        // (key + 1, ...)
+            h[2] = e4m3x2_to_f16x2(v[2 * st + 1]);
+            h[3] = e4m3x2_to_f16x2(v[2 * st + 1] >> 16);
             if (D == 128) {
 #pragma unroll
               for (int n = 0; n < kN; ++n) {
-                b0[st][n] = __byte_perm(w[0], w[1], n == 0 ? 0x5410 : 0x7632);
-                b1[st][n] = __byte_perm(w[2], w[3], n == 0 ? 0x5410 : 0x7632);
+                b0[st][n] = __byte_perm(h[0], h[1], n == 0 ? 0x5410 : 0x7632);
+                b1[st][n] = __byte_perm(h[2], h[3], n == 0 ? 0x5410 : 0x7632);
               }
             } else {
-              const uint32_t sel = (warp & 1) == 0 ? 0x5410 : 0x7632;
-              b0[st][0] = __byte_perm(w[0], w[1], sel);
-              b1[st][0] = __byte_perm(w[2], w[3], sel);
+              const uint32_t sel = (w & 1) == 0 ? 0x5410 : 0x7632;
+              b0[st][0] = __byte_perm(h[0], h[1], sel);
+              b1[st][0] = __byte_perm(h[2], h[3], sel);
             }
           }
         } else if (D == 128) {
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             uint32_t v[4];
-            ldsm4_t(vb + T::at(k2 * 32 + st * 16 + (lane & 15), warp * 2 + (lane >> 4)), v);
+            ldsm4_t(vb + T::at(k2 * 32 + st * 16 + (lane & 15), w * 2 + (lane >> 4)), v);
             b0[st][0] = v[0];
             b1[st][0] = v[1];
             b0[st][kN - 1] = v[2];
@@ -514,7 +548,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
           }
         } else {
           uint32_t v[4];
-          ldsm4_t(vb + T::at(k2 * 32 + lane, warp), v);
+          ldsm4_t(vb + T::at(k2 * 32 + lane, w), v);
           b0[0][0] = v[0];
           b1[0][0] = v[1];
           b0[1][0] = v[2];
@@ -531,11 +565,8 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
           }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->empty[buf]);
-      if (++buf == T::kBufs) {
-        buf = 0;
-        phase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive(&empty[buf]);
+      next_buffer();
     }
 
     // ---- weight sums over the warps, then the rows out ----
@@ -546,9 +577,48 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         float x = l[i][e];
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-        if ((lane & 3) == 0) smax[(i * 16 + e * 8 + g) * kComputeWarps + warp] = x;
+        if ((lane & 3) == 0) smax[(i * 16 + e * 8 + g) * kComputeWarps + w] = x;
       }
-    compute_sync();
+    group_sync(side);
+    float lsum[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4* sm =
+            reinterpret_cast<const float4*>(smax + (i * 16 + e * 8 + g) * kComputeWarps);
+        const float4 u = sm[0], v = sm[1];
+        lsum[i][e] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+      }
+    if (kG == 2) {
+      // the second group's part to the first
+      if (side == 1) {
+#pragma unroll
+        for (int k = 0; k < kN * 4; ++k) join_o[k * kComputeThreads + thread] = o[0][k >> 2][k & 3];
+        if (w == 0 && (lane & 3) == 0)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) join_ml[e * 8 + g] = make_float2(m[0][e], lsum[0][e]);
+      }
+      all_sync<kG>();
+      if (side == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 ml = join_ml[e * 8 + g];
+          const float mn = fmaxf(m[0][e], ml.x), use = mn == -INFINITY ? 0.0f : mn;
+          const float f0 = exp2_approx(m[0][e] - use), f1 = exp2_approx(ml.x - use);
+          m[0][e] = mn;
+          lsum[0][e] = lsum[0][e] * f0 + ml.y * f1;
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int k = n * 4 + 2 * e + j;
+              o[0][n][2 * e + j] =
+                  o[0][n][2 * e + j] * f0 + join_o[k * kComputeThreads + thread] * f1;
+            }
+        }
+      }
+    }
     const float v_scale = FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
     const int64_t pc = 2 * static_cast<int64_t>(blockIdx.x) + slot;
 #pragma unroll
@@ -556,10 +626,8 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = i * 16 + e * 8 + g;
-        if (row >= rows) continue;
-        const float4* sm = reinterpret_cast<const float4*>(smax + row * kComputeWarps);
-        const float4 u = sm[0], v = sm[1];
-        const float sum = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+        if (row >= rows || side != 0) continue;
+        const float sum = lsum[i][e];
         const int tok = row / group;
         const int64_t tk = wk.rq.first + tok;
         const int head = wk.h * group + row - tok * group;
@@ -569,7 +637,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         float* po = a.piece_o + (pc * a.piece_rows + row) * D;
         // the dimensions of this thread's accumulators
         if (FP8 && D == 128) {
-          const int d = warp * 16 + c2 * 2;
+          const int d = w * 16 + c2 * 2;
           const float y[4] = {o[i][0][2 * e], o[i][kN - 1][2 * e], o[i][0][2 * e + 1],
                               o[i][kN - 1][2 * e + 1]};
           if (whole)
@@ -579,7 +647,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
           else
             *reinterpret_cast<float4*>(po + d) = make_float4(y[0], y[1], y[2], y[3]);
         } else if (FP8) {
-          const int d = (warp >> 1) * 16 + c2 * 2 + (warp & 1);
+          const int d = (w >> 1) * 16 + c2 * 2 + (w & 1);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (whole) out[d + 2 * j] = __float2bfloat16_rn(o[i][0][2 * e + j] * inv);
@@ -588,7 +656,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         } else {
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
-            const int d = (warp * kN + n) * 8 + c2;
+            const int d = (w * kN + n) * 8 + c2;
             const float y0 = o[i][n][2 * e], y1 = o[i][n][2 * e + 1];
             if (whole)
               *reinterpret_cast<uint32_t*>(out + d) = pack_bf16x2(y0 * inv, y1 * inv);
@@ -596,7 +664,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
               *reinterpret_cast<float2*>(po + d) = make_float2(y0, y1);
           }
         }
-        if (warp == 0 && (lane & 3) == 0) {
+        if (w == 0 && (lane & 3) == 0) {
           if (whole) {
             if (a.lse != nullptr) a.lse[tk * a.q.heads + head] = lse_of(m[i][e], sum);
           } else {
@@ -637,7 +705,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
   auto kernel = attention_rows_kernel<D, FP8, MT>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, bytes, stream>>>(a, mk, mv);
+  kernel<<<grid, kThreads<FP8, MT>, bytes, stream>>>(a, mk, mv);
   return cudaGetLastError();
 }
 

@@ -486,7 +486,8 @@ def _dense(q, k, v, pos, window):
 
 @pytest.mark.parametrize("n,prior,hq,hk,D,window", [
     (2000, 0, 32, 16, 128, 0), (1999, 1500, 24, 24, 64, 0), (3001, 500, 16, 8, 128, 300),
-    (700, 9000, 56, 8, 128, 0), (4, 9000, 56, 8, 128, 0), (1, 20000, 64, 64, 64, 0)])
+    (700, 9000, 56, 8, 128, 0), (4, 9000, 56, 8, 128, 0), (1, 20000, 64, 64, 64, 0),
+    (1, 3000, 64, 64, 128, 0), (1, 40000, 56, 8, 128, 0), (2, 5000, 48, 3, 128, 1000)])
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 def test_paged_attention_many_segments(nb, n, prior, hq, hk, D, window, fp8):
     """Enough work that every SM walks through several heads and row blocks;
