@@ -256,4 +256,86 @@ __device__ __forceinline__ float lse_of(float m, float sum) {
   return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
+
+// Query row `row` (of the request's rows for key head h) once more, by one warp
+// and from the cache, if it has come out infinite or NaN: its sums over the keys
+// of the tiles [t0, t1) that it sees.  To the output, or to the piece's row `po`
+// relative to the piece's maximum po_m.
+//
+// The kernels multiply whole tiles, in which a key that a row does not see has
+// weight 0, and 0 * inf is not 0.  They note whether any sum is not finite, and if
+// so come here after the last segment.  What a row does see may make it infinite or
+// NaN all the same.  (A test of each partly visible tile before its product cost
+// 5 to 25 % of a chunk; the note costs nothing that shows.)
+inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, int t0,
+                                             int t1, float* po, const float2* po_ml) {
+  const int lane = threadIdx.x & 31, D = a.cache.head_dim;
+  const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
+  const int tok = a.group(row), pos = rq.pos0 + tok;
+  const int head = h * static_cast<int>(a.group.d) + row - tok * static_cast<int>(a.group.d);
+  const int all_lo = t0 * kAttnTileKeys, all_hi = min(t1 * kAttnTileKeys, rq.len);
+  const int lo = a.window > 0 ? max(all_lo, pos - a.window + 1) : all_lo;
+  const int hi = min(all_hi, pos + 1);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
+                       (rq.first + tok) * a.out.token_stride + head * a.out.head_stride;
+  bool bad = false;
+  for (int d = lane; d < D; d += 32)
+    bad = bad || !isfinite(po != nullptr ? po[d] : __bfloat162float(out[d]));
+  if (!__any_sync(0xFFFFFFFFu, bad) || (lo == all_lo && hi == all_hi)) return;
+
+  float c = a.scale * 1.4426950408889634f, v_scale = 1.0f;
+  if (a.cache.fp8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[h];
+  if (a.cache.fp8 && a.cache.v_scale != nullptr) v_scale = a.cache.v_scale[h];
+  const auto load = [&](const void* x, int64_t i) {
+    return a.cache.fp8 ? e4m3_to_float(static_cast<const uint8_t*>(x)[i])
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
+  };
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) +
+                           (rq.first + tok) * a.q.token_stride + head * a.q.head_stride;
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+  for (int key0 = lo; key0 < hi; key0 += 32) {
+    // a lane's key: its place and its weight
+    const int key = min(key0 + lane, hi - 1);
+    int64_t page = a.batch.page_table[r * a.batch.max_pages + (key >> a.cache.page_shift)];
+    if (page < 0 || page >= a.cache.num_pages) page = 0;    // (has been reported)
+    const int64_t at = page * a.cache.page_stride +
+                       (key & ((1 << a.cache.page_shift) - 1)) * a.cache.token_stride +
+                       h * a.cache.head_stride;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), load(a.cache.k, at + d), s);
+    s = key0 + lane < hi ? s * c : -INFINITY;
+    float mn = fmaxf(m, s);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, k));
+    const float use = mn == -INFINITY ? 0.0f : mn, f = exp2_approx(m - use);
+    const float w = exp2_approx(s - use);
+    m = mn;
+    l = l * f + w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= f;
+    // the lanes' dimensions
+#pragma unroll 1
+    for (int k = 0; k < min(32, hi - key0); ++k) {
+      const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+      const int64_t v = __shfl_sync(0xFFFFFFFFu, at, k) + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * 32 < D) o[i] = fmaf(wk, load(a.cache.v, v + i * 32), o[i]);
+    }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
+  const float y = po != nullptr ? (m == -INFINITY ? 0.0f : exp2_approx(m - po_ml->x))
+                                : (l == 0.0f ? 0.0f : v_scale / l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 32 < D) {
+      const int d = lane + i * 32;
+      if (po != nullptr) po[d] = o[i] * y;
+      else out[d] = __float2bfloat16_rn(o[i] * y);
+    }
+}
+
 }  // namespace nvmoe

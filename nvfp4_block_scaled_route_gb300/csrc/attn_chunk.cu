@@ -253,6 +253,7 @@ struct Bars {
   uint64_t q_ready, done[2];
   uint32_t tmem;
   int abort;
+  int spoilt;                                          // some sum is not finite
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
 
@@ -303,7 +304,8 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 // CL: CTAs of a cluster, a query tile each.
 template <int D, bool FP8, int CL>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
-attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+attention_chunk_kernel(const __grid_constant__ AttnArgs a,
+                       const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D, FP8>;
   // the swizzle goes by the address: tiles start at multiples of 1024 bytes,
@@ -343,6 +345,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       mbar_init(&bars->done[i], 1);
     }
     bars->abort = 0;
+    bars->spoilt = 0;
     fence_mbarrier_init();
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_v);
@@ -819,6 +822,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
       const float inv = l == 0.0f ? 0.0f : v_scale / l;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + tk_out * a.out.token_stride +
                            head_out * a.out.head_stride + half * (D / 2);
+      float probe = 0.0f;                               // NaN if some sum is not finite
 #pragma unroll 1
       for (int i = 0; i < D / 2; i += 32) {
         uint32_t o[32];
@@ -830,6 +834,8 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) probe = fmaf(__uint_as_float(o[k]), 0.0f, probe);
         if (real && to_out) {
           uint32_t w[16];
 #pragma unroll
@@ -857,6 +863,7 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
           }
         }
       }
+      if (real && probe != 0.0f) bars->spoilt = 1;
       if (real && half == 0) {
         if (!to_out) a.piece_ml[at] = make_float2(m, l);
         else if (a.lse != nullptr) a.lse[tk_out * a.q.heads + head_out] = lse_of(m, l);
@@ -865,6 +872,31 @@ attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map
     }
     if (threadIdx.x == 0 && rank == 0 && !begun) piece->rows = 0;
     tc_fence_before();
+    asm volatile("bar.sync 9, %0;" ::"n"(kSoftmaxThreads) : "memory");
+    if (bars->spoilt != 0 && st.left > 0) {
+      // ---- rows that hidden keys may have spoilt: the same walk again ----
+      wk.load(a, group, st.request);
+      wk.h = st.head;
+      wk.p = st.block;
+      wk.b = block_of(wk.rq, a.group, a.window, a.piece_rows, wk.p);
+      t = wk.b.t0 + st.tile;
+      for (left = st.left; left > 0; t = wk.b.t0) {
+        const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
+        const bool whole = t == wk.b.t0 && stop == wk.b.t1;
+        left -= stop - t;
+        const int t0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
+        const int t1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
+        for (int row = warp; row < min(kTile, wk.b.rows - rank * kTile); row += 8) {
+          const int64_t at =
+              (2 * static_cast<int64_t>(cluster) + (t == wk.b.t0 ? 1 : 0)) * a.piece_rows +
+              rank * kTile + row;
+          if (t1 > t0)
+            mend_row(a, wk.r, wk.h, wk.b.row0 + rank * kTile + row, t0, t1,
+                     whole ? nullptr : a.piece_o + at * D, a.piece_ml + at);
+        }
+        if (left > 0 && !wk.next(a, group)) break;
+      }
+    }
   }
   __syncthreads();
   drain_after_abort(abort);

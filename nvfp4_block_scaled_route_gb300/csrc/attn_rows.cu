@@ -73,6 +73,7 @@ struct Bars {
   uint64_t full[kMaxBufs];
   uint64_t empty[kMaxBufs];
   int abort;
+  int spoilt;                         // some sum is not finite
   // where the CTA starts: request, tile within it
   Request rq;
   int r;
@@ -159,7 +160,7 @@ struct Walk {
 
 template <int D, bool FP8, int MT>
 __global__ void __launch_bounds__(kThreads<FP8, MT>, 1)
-attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
   using T = Tile<D, FP8>;
   constexpr int kRows = MT * 16;
@@ -201,6 +202,7 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
       mbar_init(&bars->empty[i], kComputeWarps);
     }
     bars->abort = 0;
+    bars->spoilt = 0;
     fence_mbarrier_init();
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_v);
@@ -632,6 +634,11 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
         const int64_t tk = wk.rq.first + tok;
         const int head = wk.h * group + row - tok * group;
         const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
+        float probe = 0.0f;                         // NaN if some sum is not finite
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+          probe = fmaf(o[i][n][2 * e], 0.0f, fmaf(o[i][n][2 * e + 1], 0.0f, probe));
+        if (probe != 0.0f) bars->spoilt = 1;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
                              tk * a.out.token_stride + head * a.out.head_stride;
         float* po = a.piece_o + (pc * a.piece_rows + row) * D;
@@ -694,6 +701,22 @@ attention_rows_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_
   if (threadIdx.x == 0 && slot1_rows == 0) piece->rows = 0;
   __syncthreads();
   drain_after_abort(abort);
+  if (bars->spoilt == 0) return;
+  // ---- rows that hidden keys may have spoilt: the same walk again ----
+  wk.load(a, bars->r);
+  wk.h = static_cast<int>(bars->tile / max(1, wk.sp.t1 - wk.sp.t0));
+  t = wk.sp.t0 + static_cast<int>(bars->tile % max(1, wk.sp.t1 - wk.sp.t0));
+  for (left = hi - lo; left > 0; t = wk.sp.t0) {
+    const int stop = static_cast<int>(min(static_cast<long long>(wk.sp.t1), t + left));
+    const bool whole = t == wk.sp.t0 && stop == wk.sp.t1;
+    left -= stop - t;
+    for (int row = warp; row < wk.rq.n * group; row += kG * kComputeWarps) {
+      const int64_t at =
+          (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows + row;
+      mend_row(a, wk.r, wk.h, row, t, stop, whole ? nullptr : a.piece_o + at * D, a.piece_ml + at);
+    }
+    if (left > 0 && !wk.next_segment(a)) break;
+  }
 }
 
 template <int D, bool FP8, int MT>

@@ -88,9 +88,11 @@ def attention(q, k_cache, v_cache, q_start, kv_len, table, heads_first=False, k_
                 none = ~see.any(1) if length else torch.ones(n, dtype=torch.bool)
                 p = torch.softmax(s, 1) if length else s
                 p = torch.where(none[:, None], torch.zeros_like(p), p)
-                # hidden values take no part, whatever they are
-                o = torch.stack([p[i][see[i]] @ v[see[i]] for i in range(n)])
-                ev = torch.stack([p[i][see[i]] @ v[see[i]].abs() for i in range(n)])
+                # hidden values take no part, whatever they are; elementwise, since a
+                # matrix product may skip a weight of zero whose value is infinite
+                w = [(p[i][see[i]][:, None], v[see[i]]) for i in range(n)]
+                o = torch.stack([(a * b).sum(0) for a, b in w])
+                ev = torch.stack([(a * b.abs()).sum(0) for a, b in w])
                 ls = torch.logsumexp(s, 1) if length else torch.full((n,), -math.inf).double()
                 out[a:e, h], lse[a:e, h] = o, ls
                 b_out[a:e, h] = (U + 2 * ds[:, None] + 2.0 ** -18) * ev + U * o.abs()

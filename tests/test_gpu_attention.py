@@ -283,6 +283,46 @@ def test_paged_attention_in_a_graph_follows_the_batch(nb):
     assert nb.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("reqs,hq,hk,D", [([(5, 200), (3, 3)], 6, 2, 128), ([(5, 133)], 4, 4, 64),
+                                          ([(90, 300), (20, 20)], 4, 2, 128), ([(90, 90)], 1, 1, 64),
+                                          ([(300, 450)], 2, 1, 128), ([(260, 260)], 3, 3, 64)])
+def test_paged_attention_hidden_values_that_are_not_finite(nb, reqs, hq, hk, D, window, fp8):
+    """Infinities and NaN in keys and values reach the tokens that see them, and no
+    others: they stand at keys that the window or the causal order hides from some
+    tokens of the same chunk."""
+    case = Paged(reqs, hk, D, 16, seed=31, fp8=fp8)
+    g = torch.Generator().manual_seed(5)
+    inf = math.nan if fp8 else math.inf                # (E4M3 has no infinity)
+    for r, (n, length) in enumerate(reqs):
+        for back, what in ((2, "v"), (n // 2, "v"), (n, "v"), (min(length, n + 30), "v"), (1, "k")):
+            j = length - back
+            p, o = int(case.table[r, j // 16]), j % 16
+            for c, nm in ((case.k, "k"), (case.v, "v")):
+                if nm == what:
+                    x = c[p, o].float()
+                    x[:, int(torch.randint(0, D, (1,), generator=g))] = inf
+                    x[0, int(torch.randint(0, D, (1,), generator=g))] = math.nan if what == "v" else inf
+                    x[-1, 3] = -inf
+                    c[p, o] = x.to(c.dtype)
+    q = torch.randn(case.T, hq, D, generator=g).bfloat16()
+    cache, batch = case.handles(nb)
+    lse = torch.empty(case.T, hq, device=DEV)
+    ws = nb.paged_attention_workspace(cache, batch, hq, case.T)
+    out = nb.paged_attention(q.to(DEV), cache, batch, window=window, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    want, wlse, b_out, b_lse = case.reference(q, window=window)
+    for got, w, b in ((out, want, b_out), (lse, wlse, b_lse)):
+        got = got.double().cpu()
+        fine = w.isfinite()
+        assert fine.any()
+        assert torch.equal(got.isfinite(), fine)
+        over = (got - w).abs()[fine] - b[fine]
+        assert (over <= 0).all(), over.max()
+
+
 @pytest.mark.parametrize("n", [1, 60])
 def test_paged_attention_reports_bad_input(nb, n):
     """A page id out of range reads as zeros and is reported; a length past the
