@@ -645,7 +645,8 @@ int attn_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * head_dim] and heads-first [pages, kv_heads, page_size, head_dim] caches are
  * both taken.
  *   dtype       NVMOE_BF16, or NVMOE_E4M3: the stored value times k_scale[h]
- *               (v_scale[h]) is the key (value); scales NULL: 1.
+ *               (v_scale[h]) is the key (value); scales are positive and
+ *               finite; NULL: 1.
  *   page_size   a power of two, 16 .. 1024; 1 <= num_pages < 2^31
  *   strides     multiples of 16 bytes, positive, below 2^40 bytes */
 typedef struct {
@@ -711,7 +712,8 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  * the page table row or more than max_new new tokens set
  * NVMOE_ERR_DEVICE_BAD_INDEX: the page reads as zeros, the length is cut, the
  * further tokens' rows are not written.  Rows of no request are left alone.
- * Cache contents past a request's length are not used, whatever they hold.
+ * Cache contents past a request's length, and keys and values that a token
+ * does not see, are not used, whatever they hold (infinities and NaN too).
  * Limits: q_heads a multiple of kv_heads, tokens * q_heads < 2^31,
  * max_pages * page_size < 2^31. */
 size_t attn_paged_workspace_size(int batch, int64_t tokens, int max_new, int q_heads,
