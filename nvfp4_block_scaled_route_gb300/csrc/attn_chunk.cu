@@ -692,10 +692,9 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         const int pos = wk.rq.pos0 + tok;
         const int vis_hi = min(pos + 1, wk.rq.len) - half * 64;
         const int vis_lo = (a.window > 0 ? pos - a.window + 1 : 0) - half * 64;
-        // keys that every row of the tile sees
-        const int all_hi = min(wk.rq.pos0 + a.group(row0) + 1, wk.rq.len);
-        const int all_lo =
-            a.window > 0 ? wk.rq.pos0 + a.group(row0 + rows - 1) - a.window + 1 : 0;
+        // keys that every row of the warp sees (rows come in order)
+        const int all_hi = __shfl_sync(0xFFFFFFFFu, vis_hi, 0);
+        const int all_lo = __shfl_sync(0xFFFFFFFFu, vis_lo, 31);
         for (int j = j0; j < j1; ++j, ++n) {
           const uint32_t sb = n & 1u;
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
@@ -716,7 +715,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           tmem_ld_wait();
           tc_fence_before();
           mbar_arrive(&bars->s_free[sb]);
-          if ((j + 1) * kKeys > all_hi) {
+          if (j * kKeys + 64 > all_hi) {
             const int h = vis_hi - j * kKeys;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
