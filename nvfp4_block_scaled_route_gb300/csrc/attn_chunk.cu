@@ -395,6 +395,17 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     while (left > 0 && ok) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       left -= stop - t;
+      // the segment's queries to L2, ahead of the softmax warps' loads
+      if (keys)
+        for (int i = lane; i < min(kTile, wk.b.rows - rank * kTile); i += 32) {
+          const int r = wk.b.row0 + rank * kTile + i, k = a.group(r);
+          const __nv_bfloat16* q =
+              static_cast<const __nv_bfloat16*>(a.q.data) + (wk.rq.first + k) * a.q.token_stride +
+              (wk.h * group + r - k * group) * a.q.head_stride;
+#pragma unroll
+          for (int d = 0; d < D; d += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
+        }
       for (; t < stop; ++t) {
         const int key = t * kKeys + b * box;
         const bool in = b * box < kKeys && half < C::kHalves && key < wk.b.kend &&
