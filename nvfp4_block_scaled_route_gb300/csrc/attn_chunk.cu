@@ -25,11 +25,15 @@
 // fed: an MMA of 128 x 128 x 16 takes 64 cycles and few are queued, while a
 // tile's four commits and three waits take some 600.)
 //
-// E4M3 caches: two warps each turn the key and value tiles into fp16 (exact)
-// on their way to the tensor cores, from a ring of raw tiles to a ring of
-// operand tiles.  Queries and weights are then fp16 too; a query row is scaled
-// by a power of two to a maximum in [1, 2), which keeps every element above
-// 2^-16 of it exact, and the factor goes back in with the softmax scale.
+// E4M3 caches: the keys go to the tensor cores as they are, and a query as the
+// sum of two E4M3 numbers, S = Qhi K^T + Qlo K^T, at twice the rate of 16-bit
+// products.  A query row is scaled by a power of two to a maximum in [128, 256),
+// and the factor goes back in with the softmax scale; the two hold the 8 bits of
+// its elements exactly down to 2^-9 of the maximum, smaller ones to within
+// 2^-17 of it.  The values are turned into fp16 (exact) by four warps on their
+// way from a ring of raw tiles to a ring of operand tiles, for weights in fp16.
+// (Keys converted likewise, by two of the four warps: 248.6 us where this takes
+// 233.5 us, 4 requests of up to 512 new tokens.)
 //
 // m is a reference, not always the maximum: O is rescaled only when a row's
 // maximum has grown by more than 2^8 over its reference (any reference gives
@@ -47,12 +51,13 @@ namespace {
 constexpr int kKeys = kAttnTileKeys;
 constexpr int kTile = 128;                   // query rows of a tile
 constexpr int kLoadK = 8, kLoadV = 9, kIssueS = 10;   // and 11: P V
-constexpr int kConvert = 12;                 // warps 12-13: keys, 14-15: values (E4M3)
+constexpr int kConvert = 12;                 // warps 12-15: values to fp16 (E4M3)
 constexpr int kSoftmaxThreads = 256;
-constexpr int kConvertThreads = 64;          // of a side
+constexpr int kConvertThreads = 128;
 // E4M3: registers of a thread; the launch gives each 128 (the most for 512
-// threads), the softmax warps take what the others leave.
-constexpr int kRegsSoftmax = 168, kRegsOther = 88;
+// threads), the softmax warps take what the others leave.  (168 and 88: the
+// others' loops spill, 252 us instead of 233.5.)
+constexpr int kRegsSoftmax = 152, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= 128 * 512, "registers");
 constexpr int kPlanThreads = 1024;
 
@@ -232,22 +237,26 @@ struct Cfg {
   static constexpr int kRow = D * (FP8 ? 1 : 2);
   static constexpr int kLine = kRow < 128 ? kRow : 128;   // bytes of a box row
   static constexpr int kHalves = kRow / kLine;         // column blocks
-  // operand tiles of keys and of values (bf16: as loaded), raw E4M3 tiles
-  static constexpr int kK = (FP8 ? 2 : 3) * (D == 128 ? 1 : 2), kV = kK;
+  // tiles of keys (as loaded), operand tiles of values (bf16: as loaded), raw
+  // tiles of E4M3 values
+  static constexpr int kK = (FP8 ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
   static constexpr int kRaw = FP8 ? (D == 128 ? 2 : 5) : 0;
-  static constexpr int kRing = (1 + kK + kV) * kBytes + 2 * kRaw * kLoadBytes;  // queries too
+  static constexpr int kVAt = kBytes;                  // after the queries: values, keys, raw
+  static constexpr int kKAt = kVAt + kV * kBytes, kRawAt = kKAt + kK * kLoadBytes;
+  static constexpr int kRing = kRawAt + kRaw * kLoadBytes;
   static constexpr int kSmem = kRing + 512 + 5 * kTile * 4;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr uint32_t kTmemO = 256, kTmemP = 384;   // S: columns 0 and 128
   // instruction descriptors: fp16 operands are format 0, bf16 format 1; V is MN-major
   static constexpr uint32_t kFormats = FP8 ? (1u << 7) | (1u << 10) : 0u;
-  static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kKeys) ^ kFormats;
+  static constexpr uint32_t kIdescS =
+      FP8 ? idesc_e4m3_f32(kTile, kKeys) : idesc_bf16_f32(kTile, kKeys);
   static constexpr uint32_t kIdescO = (idesc_bf16_f32(kTile, D) ^ kFormats) | (1u << 16);
 };
 
 struct Bars {
   uint64_t full[14], empty[14];                        // loaded tiles: keys, then values
-  uint64_t op_full[8], op_empty[8];                    // E4M3: operand tiles
+  uint64_t op_full[6], op_empty[6];                    // E4M3: operand tiles of values
   // by parity of the CTA's tile counter, whose next bit is then the phase
   uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];
   uint64_t q_ready, done[2];
@@ -301,6 +310,13 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// Likewise in an E4M3 tile (K-major for the tensor cores, as TMA writes it: the
+// swizzle of 128 bytes, or of 64 where a row has no more).
+template <int D>
+__device__ __forceinline__ uint32_t raw_at(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
 // CL: CTAs of a cluster, a query tile each.
 template <int D, bool FP8, int CL>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
@@ -315,8 +331,6 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     record_status(a.status, kErrBounds);
     return;
   }
-  uint8_t* ring = sq + C::kBytes;
-  uint8_t* raw = ring + (C::kK + C::kV) * C::kBytes;
   Bars* bars = reinterpret_cast<Bars*>(sq + C::kRing);
   float* swap = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512);
   // E4M3: each query row's power of two, [segment parity][row] (a thread may be
@@ -327,12 +341,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   const int cluster = blockIdx.x / CL;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < (FP8 ? 2 * C::kRaw : C::kK + C::kV); ++i) {
+    for (int i = 0; i < C::kK + (FP8 ? C::kRaw : C::kV); ++i) {
       mbar_init(&bars->full[i], 1);
-      // every CTA's readers: an issuer, or two converting warps
-      mbar_init(&bars->empty[i], (FP8 ? 2 : 1) * CL);
+      // every CTA's readers: an issuer, or four converting warps
+      mbar_init(&bars->empty[i], (FP8 && i >= C::kK ? 4 : 1) * CL);
     }
-    for (int i = 0; FP8 && i < C::kK + C::kV; ++i) {
+    for (int i = 0; FP8 && i < C::kV; ++i) {
       mbar_init(&bars->op_full[i], kConvertThreads);
       mbar_init(&bars->op_empty[i], 1);
     }
@@ -383,9 +397,9 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     // of the cluster: lane = box (page part, column block) ----
     const bool keys = warp == kLoadK;
     const CUtensorMap* map = keys ? &map_k : &map_v;
-    const int bufs = FP8 ? C::kRaw : (keys ? C::kK : C::kV);
-    const int buf0 = keys ? 0 : (FP8 ? C::kRaw : C::kK);
-    uint8_t* base = FP8 ? raw : ring;
+    const int bufs = keys ? C::kK : (FP8 ? C::kRaw : C::kV);
+    const int buf0 = keys ? 0 : C::kK;                  // barriers
+    uint8_t* base = sq + (keys ? C::kKAt : (FP8 ? C::kRawAt : C::kVAt));
     const int box = min(kKeys / CL, 1 << a.cache.page_shift);
     const int b = lane & 7, half = lane >> 3;
     const uint64_t policy = policy_evict_normal();
@@ -428,7 +442,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         if (lane == 0)
           mbar_arrive_expect_tx(&bars->full[n], static_cast<uint32_t>(loads * box * C::kLine));
         if (take) {
-          uint8_t* dst = base + n * C::kLoadBytes + half * kKeys * C::kLine + b * box * C::kLine;
+          uint8_t* dst = base + buf * C::kLoadBytes + half * kKeys * C::kLine + b * box * C::kLine;
           const int x = half * (FP8 ? C::kLine : C::kLine / 2);
           if (CL > 1)
             tma_load_4d_both(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
@@ -446,64 +460,58 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       }
     }
   } else if (FP8 && warp >= kConvert) {
-    // ---- E4M3 tiles to fp16: a side's 64 threads take 16 bytes at a time,
-    // eight rows of one column side by side (no bank conflicts either way) ----
+    // ---- E4M3 values to fp16: 16 bytes at a time, eight rows of one column side
+    // by side (no bank conflicts either way) ----
     constexpr int kChunks = D / 16;                     // of a row
     constexpr int kStepRows = kConvertThreads / kChunks, kSteps = kKeys / kStepRows;
-    const bool keys = warp < kConvert + 2;
     const int thread = threadIdx.x & (kConvertThreads - 1);
     const int ch = (thread >> 3) % kChunks, row0 = (thread & 7) + (thread >> 3) / kChunks * 8;
-    // (a step's rows are a multiple of 8 on: the swizzles stay, 1024 bytes of raw tile)
-    const uint32_t src0 = D == 128 ? row0 * 128 + ((ch ^ (row0 & 7)) << 4)
-                                   : row0 * 64 + ((ch ^ ((row0 >> 1) & 3)) << 4);
+    // (a step's rows are a multiple of 8 on: the swizzles stay)
+    const uint32_t src0 = raw_at<D>(row0, ch);
     const uint32_t dst0 = tile_at(row0, 2 * ch), dst1 = tile_at(row0, 2 * ch + 1);
-    const int raw0 = keys ? 0 : C::kRaw, op0 = keys ? 0 : C::kK, ops = keys ? C::kK : C::kV;
     int in = 0, out = 0;
     uint32_t in_phase = 0, out_phase = 0;
     while (left > 0) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       left -= stop - t;
       for (; t < stop; ++t) {
-        mbar_wait(&bars->full[raw0 + in], in_phase, a.status, abort);
-        mbar_wait(&bars->op_empty[op0 + out], out_phase ^ 1u, a.status, abort);
-        const uint8_t* src = raw + (raw0 + in) * C::kLoadBytes + src0;
-        uint8_t* dst = ring + (op0 + out) * C::kBytes;
+        mbar_wait(&bars->full[C::kK + in], in_phase, a.status, abort);
+        mbar_wait(&bars->op_empty[out], out_phase ^ 1u, a.status, abort);
+        const uint8_t* src = sq + C::kRawAt + in * C::kLoadBytes + src0;
+        uint8_t* dst = sq + C::kVAt + out * C::kBytes;
         // values that no row sees may hold anything: make them zeros
         const int lo = wk.b.kbeg - t * kKeys, hi = wk.b.kend - t * kKeys;
-        const bool cut = !keys && (lo > 0 || hi < kKeys);
+        const bool cut = lo > 0 || hi < kKeys;
+        uint4 u[kSteps];
 #pragma unroll
-        for (int i0 = 0; i0 < kSteps; i0 += 8) {
-          uint4 u[8];
+        for (int i = 0; i < kSteps; ++i)
+          u[i] = *reinterpret_cast<const uint4*>(src + i * kStepRows * D);
+        if (cut)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            u[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 1024);
-          if (cut)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = row0 + (i0 + i) * kStepRows;
-              if (row < lo || row >= hi) u[i] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint8_t* to = dst + (i0 + i) * kStepRows * 128;
-            *reinterpret_cast<uint4*>(to + dst0) =
-                make_uint4(e4m3x2_to_f16x2(u[i].x), e4m3x2_to_f16x2(u[i].x >> 16),
-                           e4m3x2_to_f16x2(u[i].y), e4m3x2_to_f16x2(u[i].y >> 16));
-            *reinterpret_cast<uint4*>(to + dst1) =
-                make_uint4(e4m3x2_to_f16x2(u[i].z), e4m3x2_to_f16x2(u[i].z >> 16),
-                           e4m3x2_to_f16x2(u[i].w), e4m3x2_to_f16x2(u[i].w >> 16));
+          for (int i = 0; i < kSteps; ++i) {
+            const int row = row0 + i * kStepRows;
+            if (row < lo || row >= hi) u[i] = make_uint4(0, 0, 0, 0);
           }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          uint8_t* to = dst + i * kStepRows * 128;
+          *reinterpret_cast<uint4*>(to + dst0) =
+              make_uint4(e4m3x2_to_f16x2(u[i].x), e4m3x2_to_f16x2(u[i].x >> 16),
+                         e4m3x2_to_f16x2(u[i].y), e4m3x2_to_f16x2(u[i].y >> 16));
+          *reinterpret_cast<uint4*>(to + dst1) =
+              make_uint4(e4m3x2_to_f16x2(u[i].z), e4m3x2_to_f16x2(u[i].z >> 16),
+                         e4m3x2_to_f16x2(u[i].w), e4m3x2_to_f16x2(u[i].w >> 16));
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bars->op_full[op0 + out]);
+        mbar_arrive(&bars->op_full[out]);
         __syncwarp();
         if (lane < CL)                                  // this warp has read the raw tile
-          mbar_arrive_cluster(map_shared_rank(smem_u32(&bars->empty[raw0 + in]), lane));
+          mbar_arrive_cluster(map_shared_rank(smem_u32(&bars->empty[C::kK + in]), lane));
         if (++in == C::kRaw) {
           in = 0;
           in_phase ^= 1u;
         }
-        if (++out == ops) {
+        if (++out == C::kV) {
           out = 0;
           out_phase ^= 1u;
         }
@@ -516,13 +524,19 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   } else {
     // ---- MMAs ----
     const bool keys = warp == kIssueS;
-    const int bufs = keys ? C::kK : C::kV, buf0 = keys ? 0 : C::kK;
-    uint64_t* full = FP8 ? bars->op_full : bars->full;
+    const int bufs = keys ? C::kK : C::kV;
+    const bool made = FP8 && !keys;                     // tiles of the converting warps
+    uint64_t* full = made ? bars->op_full : bars->full + (keys ? 0 : C::kK);
+    uint64_t* empty = made ? bars->op_empty : bars->empty + (keys ? 0 : C::kK);
+    const uint32_t tile_bytes = keys ? C::kLoadBytes : C::kBytes;
     // A tile's descriptors are this one plus multiples of 16 bytes (building
     // each anew takes the issuing thread longer than the MMA does the pipe).
-    const uint64_t desc0 = smem_desc(smem_u32(ring + buf0 * C::kBytes),
-                                     keys ? 16 : kKeys * 128, 1024, 2);
-    const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 1024, 2);
+    // (E4M3 of 64 dimensions: rows of 64 bytes, the 64-byte swizzle)
+    constexpr bool kShort = C::kRow < 128;
+    const uint64_t desc0 =
+        keys ? smem_desc(smem_u32(sq + C::kKAt), 16, kShort ? 512 : 1024, kShort ? 4 : 2)
+             : smem_desc(smem_u32(sq + C::kVAt), kKeys * 128, 1024, 2);
+    const uint64_t q_desc = smem_desc(smem_u32(sq), 16, kShort ? 512 : 1024, kShort ? 4 : 2);
     int buf = 0;
     uint32_t phase = 0, q_phase = 0;
     uint32_t n = 0;                                     // tiles so far
@@ -538,19 +552,28 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       for (; t < stop; ++t) {
         const bool mine = t >= j0 && t < j1;
         const uint32_t sb = n & 1u, parity = (n >> 1) & 1u;
-        const uint64_t desc = desc0 + static_cast<uint32_t>(buf) * (C::kBytes >> 4);
-        mbar_wait(&full[buf0 + buf], phase, a.status, abort);
+        const uint64_t desc = desc0 + static_cast<uint32_t>(buf) * (tile_bytes >> 4);
+        mbar_wait(&full[buf], phase, a.status, abort);
         if (keys) {
           if (mine) {
             // S (n - 2) is in registers
             mbar_wait(&bars->s_free[sb], parity ^ 1u, a.status, abort);
             tc_fence_after();
             if (lane == 0) {
+              if (FP8) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {   // Qhi, then Qlo
+                  const int part = ks / (D / 32), at = ks % (D / 32) * 32;
+                  mma_f8(tmem + sb * 128, q_desc + ((part * kTile * D + at) >> 4),
+                         desc + (at >> 4), C::kIdescS, ks != 0);
+                }
+              } else {
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks)
                 mma_f16(tmem + sb * 128, q_desc + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
                         desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), C::kIdescS,
                         ks != 0);
+              }
               tc_commit(&bars->s_full[sb]);
             }
           }
@@ -560,7 +583,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             for (int i = lane; i < kKeys * (D / 8); i += 32) {
               const int row = i / (D / 8), key = t * kKeys + row;
               if (key < wk.b.kbeg || key >= wk.b.kend)
-                *reinterpret_cast<uint4*>(ring + (buf0 + buf) * C::kBytes +
+                *reinterpret_cast<uint4*>(sq + C::kVAt + buf * C::kBytes +
                                           tile_at(row, i % (D / 8))) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
@@ -579,9 +602,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           }
         }
         if (lane == 0) {
-          if (FP8) tc_commit(&bars->op_empty[buf0 + buf]);
-          else if (CL > 1) tc_commit_both(&bars->empty[buf0 + buf]);
-          else tc_commit(&bars->empty[buf0 + buf]);
+          if (CL > 1 && !made) tc_commit_both(&empty[buf]);
+          else tc_commit(&empty[buf]);
         }
         if (mine) ++n;
         if (++buf == bufs) {
@@ -653,7 +675,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         begun = true;
       }
       c = a.scale * 1.4426950408889634f;
-      if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[wk.h];
+      if (FP8) c *= 0.0078125f * (a.cache.k_scale != nullptr ? a.cache.k_scale[wk.h] : 1.0f);
       if (j1 <= j0) return;
       seg ^= 1;
       // the queries, D / 8 lanes a row (the last S with the previous ones has landed)
@@ -680,15 +702,35 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1)
             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-          // 2^(127 - e) and 2^(e - 127); rows of zeros or infinities stay as they are
+          // 2^(134 - e), and 2^(e - 127) * 2^-7 to undo it (2^-7 is in c); rows of
+          // zeros stay as they are, infinities become NaN
           int e = static_cast<int>(__float_as_uint(most) >> 23);
-          e = e == 0 || e == 255 ? 127 : min(e, 253);
-          const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          const bool finite = e != 255;
+          e = e == 0 || e == 255 ? 127 : min(max(e, 8), 253);
+          const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
           if (ch == 0) q_exp[seg * kTile + i0 + i * kStep] = static_cast<uint8_t>(e);
-          u[i] = make_uint4(pack_f16x2(x[0] * up, x[1] * up), pack_f16x2(x[2] * up, x[3] * up),
-                            pack_f16x2(x[4] * up, x[5] * up), pack_f16x2(x[6] * up, x[7] * up));
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int k = 0; k < 8; k += 4) {
+            float y[4], z[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) y[d] = finite ? x[k + d] * up : x[k + d] - x[k + d];
+            hi[k >> 2] = pack_e4m3x2(y[0], y[1]) | pack_e4m3x2(y[2], y[3]) << 16;
+#pragma unroll
+            for (int d = 0; d < 4; d += 2) {
+              const uint32_t h = e4m3x2_to_f16x2(hi[k >> 2] >> (d * 8));
+              const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
+              z[d] = y[d] - f.x;
+              z[d + 1] = y[d + 1] - f.y;
+            }
+            lo[k >> 2] = pack_e4m3x2(z[0], z[1]) | pack_e4m3x2(z[2], z[3]) << 16;
+          }
+          uint8_t* to = sq + raw_at<D>(i0 + i * kStep, ch >> 1) + (ch & 1) * 8;
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + kTile * D) = make_uint2(lo[0], lo[1]);
+        } else {
+          *reinterpret_cast<uint4*>(sq + tile_at(i0 + i * kStep, ch)) = u[i];
         }
-        *reinterpret_cast<uint4*>(sq + tile_at(i0 + i * kStep, ch)) = u[i];
       }
       fence_proxy_async_smem();
       mbar_arrive(&bars->q_ready);
