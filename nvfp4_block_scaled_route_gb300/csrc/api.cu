@@ -1134,7 +1134,7 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
   if (!few) {
     a->starts = c.take<AttnStart>(kMaxGrid * sizeof(AttnStart));
     a->plan_block0 = c.take<int>((static_cast<size_t>(batch) + 1) * sizeof(int));
-    a->plan_tile0 = c.take<long long>((static_cast<size_t>(blocks) + 1) * sizeof(long long));
+    a->plan_cost0 = c.take<long long>((static_cast<size_t>(blocks) + 1) * sizeof(long long));
   }
   return c.off;
 }

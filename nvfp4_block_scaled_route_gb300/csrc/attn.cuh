@@ -126,10 +126,10 @@ struct AttnArgs {
   float* piece_o;
   float2* piece_ml;
   int piece_rows;
-  // chunk kernel: blocks before each request [batch + 1], key tiles before
-  // each block [max_blocks + 1] (one key head), the CTAs' starts [grid]
+  // chunk kernel: blocks before each request [batch + 1], cost in tiles of those
+  // before each block [max_blocks + 1] (one key head), the CTAs' starts [grid]
   int* plan_block0;
-  long long* plan_tile0;
+  long long* plan_cost0;
   AttnStart* starts;
   int max_blocks;
 };
