@@ -1126,6 +1126,7 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
                       : (rows <= kAttnTileRows ? kAttnTileRows : 2 * kAttnTileRows);
   const int64_t blocks = few ? 0 : ceil_div(tokens * group, kAttnTileRows) + batch;
   a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
+  a->plan_here = batch <= kAttnPlanHere && blocks <= kAttnPlanHere;
   a->status = c.take<int>(kStatusBytes);
   a->pieces = c.take<AttnPiece>(kMaxGrid * sizeof(AttnPiece));
   a->piece_ml = c.take<float2>(2 * kMaxGrid * a->piece_rows * sizeof(float2));
@@ -1197,7 +1198,7 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   if (few) {
     e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);
   } else {
-    e = counted(launch_attn_plan(a, grid, stream), 1);
+    e = a.plan_here ? cudaSuccess : counted(launch_attn_plan(a, grid, stream), 1);
     if (e == cudaSuccess) e = counted(launch_attention_chunk(a, map_k, map_v, grid, stream), 1);
   }
   if (e != cudaSuccess) return fail(e);

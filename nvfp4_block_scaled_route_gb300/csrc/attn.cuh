@@ -77,8 +77,9 @@ struct AttnPiece {
 // Where a CTA of the chunk kernel starts: `left` tiles from tile `tile` of the
 // segment (request, key head, row block).
 struct AttnStart {
-  long long left, until;      // until: the next cluster's first tile
+  long long left;
   int request, head, block, tile;
+  int last;                   // the CTA that ends the segment which this one leaves cut
 };
 
 // First tile of share c when `total` tiles are dealt to g <= total takers (so
@@ -132,6 +133,7 @@ struct AttnArgs {
   long long* plan_cost0;
   AttnStart* starts;
   int max_blocks;
+  bool plan_here;           // in the chunk kernel itself; else by attn_plan_kernel
 };
 constexpr int kAttnTileRows = 128;    // query rows of a tile of the chunk kernel, which
                                       // takes blocks (piece_rows) of one tile or two
@@ -141,6 +143,8 @@ constexpr int kAttnFewRows = 32;
 // 128 (chunk kernel with two tiles: 64) tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
+// Blocks and requests up to which the chunk kernel's CTAs plan for themselves.
+constexpr int kAttnPlanHere = 384;
 cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);
 cudaError_t launch_attention_chunk(const AttnArgs& args, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int clusters, cudaStream_t stream);

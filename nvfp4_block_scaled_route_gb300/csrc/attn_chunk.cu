@@ -67,7 +67,7 @@ constexpr int kPlanThreads = 1024;
 // 102.3 / 99.2 / 96.4 / 98.1, 16 requests of 5 drafted tokens
 // 37.0 / 34.1 / 33.7 / 34.1.
 constexpr int kSegmentTiles = 4;
-static_assert(kMaxGrid < kPlanThreads, "a thread for each start");
+static_assert(kMaxGrid < kPlanThreads && kMaxGrid < 384, "a thread for each start");
 
 // Rows [row0, row0 + rows) of a request and the key tiles that they see.
 struct Block {
@@ -108,6 +108,8 @@ __device__ __forceinline__ int blocks_of(const Request& q, int group, int rows) 
   return static_cast<int>((static_cast<int64_t>(q.n) * group + rows - 1) / rows);
 }
 
+// Sum of the values of the threads before this one; *total: of all.
+template <int THREADS>
 __device__ __forceinline__ long long block_scan(long long v, long long* sums, long long* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long x = v;
@@ -120,7 +122,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sums, lo
   if (lane == 31) sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    long long s = sums[lane];
+    long long s = lane < THREADS / 32 ? sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xFFFFFFFFu, s, o);
@@ -130,7 +132,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sums, lo
   }
   __syncthreads();
   *total = sums[31];
-  return x - v + (warp > 0 ? sums[warp - 1] : 0);      // exclusive
+  return x - v + (warp > 0 ? sums[warp - 1] : 0);
 }
 
 // The largest i in [lo, hi) with f(i) <= x, f ascending, f(lo) <= x.
@@ -144,78 +146,94 @@ __device__ __forceinline__ int last_le(int lo, int hi, long long x, F f) {
   return lo;
 }
 
-// One CTA: prefix sums of the blocks of the requests (block0) and of the cost of
-// the blocks in tiles (cost0, one key head), then where each of the G CTAs of
-// the attention kernel starts.
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int G) {
-  __shared__ long long sums[32];
+// Prefix sums of the blocks of the requests (block0) and of the cost of the
+// blocks in tiles (cost0, one key head), then where each of the G CTAs (or
+// clusters) of the attention kernel starts.  Called by all THREADS > G threads of a
+// CTA; thread c returns the start of c.
+struct PlanShared {
+  long long sums[32];
+  long long tile_of[kMaxGrid + 1];           // of all tiles, a CTA's first
+  long long cut_end[kMaxGrid + 1];           // ... the end of the segment that it is inside of
+};
+template <int THREADS>
+__device__ __forceinline__ AttnStart plan(const AttnArgs& a, int G, PlanShared* sh, int* block0,
+                                          long long* cost0) {
   const int B = a.batch.batch, group = static_cast<int>(a.group.d);
-  pdl_trigger();
   long long total = 0, blocks = 0;
-  for (int r0 = 0; r0 < B; r0 += kPlanThreads) {
+  for (int r0 = 0; r0 < B; r0 += THREADS) {
     const int r = r0 + threadIdx.x;
     int n = 0;
     if (r < B) n = blocks_of(load_request(a.batch, a.cache.page_shift, r, a.status), group,
                              a.piece_rows);
-    const long long at = blocks + block_scan(n, sums, &total);
-    if (r < B) a.plan_block0[r] = static_cast<int>(min(at, static_cast<long long>(a.max_blocks)));
+    const long long at = blocks + block_scan<THREADS>(n, sh->sums, &total);
+    if (r < B) block0[r] = static_cast<int>(min(at, static_cast<long long>(a.max_blocks)));
     blocks += total;
   }
   blocks = min(blocks, static_cast<long long>(a.max_blocks));
-  if (threadIdx.x == 0) a.plan_block0[B] = static_cast<int>(blocks);
+  if (threadIdx.x == 0) block0[B] = static_cast<int>(blocks);
   __syncthreads();
   long long units = 0;
-  for (int i0 = 0; i0 < blocks; i0 += kPlanThreads) {
+  for (int i0 = 0; i0 < blocks; i0 += THREADS) {
     const int i = i0 + threadIdx.x;
     int n = 0;
     if (i < blocks) {
-      const int r = last_le(0, B, i, [&](int k) { return a.plan_block0[k]; });
+      const int r = last_le(0, B, i, [&](int k) { return block0[k]; });
       const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
-      const Block b = block_of(rq, a.group, a.window, a.piece_rows, i - a.plan_block0[r]);
+      const Block b = block_of(rq, a.group, a.window, a.piece_rows, i - block0[r]);
       n = b.t1 - b.t0 + kSegmentTiles;
     }
-    const long long at = units + block_scan(n, sums, &total);
-    if (i < blocks) a.plan_cost0[i] = at;
+    const long long at = units + block_scan<THREADS>(n, sh->sums, &total);
+    if (i < blocks) cost0[i] = at;
     units += total;
   }
-  if (threadIdx.x == 0) a.plan_cost0[blocks] = units;
+  if (threadIdx.x == 0) cost0[blocks] = units;
   __syncthreads();
   const long long total_units = units * a.cache.heads;
   const long long total_tiles = total_units - kSegmentTiles * blocks * a.cache.heads;
   const int takers = share_takers(total_units, G);
-  __shared__ long long tile_of[kMaxGrid + 1];             // of all tiles, a CTA's first
   AttnStart s = {};
   const int c = threadIdx.x;
   if (c <= G) {
     const long long x = c < takers ? share_begin(total_units, c, takers) : total_units;
-    long long first = total_tiles;
+    long long first = total_tiles, end = total_tiles;
     if (x < total_units) {
-      const auto base = [&](int k) { return a.plan_cost0[a.plan_block0[k]] * a.cache.heads; };
+      const auto base = [&](int k) { return cost0[block0[k]] * a.cache.heads; };
       const int r = last_le(0, B, x, base);            // (the last of equals has blocks)
-      const int b0 = a.plan_block0[r], b1 = a.plan_block0[r + 1];
-      const long long u0 = a.plan_cost0[b0], per = a.plan_cost0[b1] - u0;
+      const int b0 = block0[r], b1 = block0[r + 1];
+      const long long u0 = cost0[b0], per = cost0[b1] - u0;
       const long long y = x - u0 * a.cache.heads;
       if (per > 0 && y >= 0 && y / per < a.cache.heads) {    // (not if q_start descends)
         s.request = r;
         s.head = static_cast<int>(y / per);
         const long long z = y - s.head * per + u0;
-        const int b = last_le(b0, b1, z, [&](int k) { return a.plan_cost0[k]; });
-        const long long ub = a.plan_cost0[b];
+        const int b = last_le(b0, b1, z, [&](int k) { return cost0[k]; });
+        const long long ub = cost0[b];
         s.block = b - b0;
         s.tile = max(0, static_cast<int>(z - ub) - kSegmentTiles);
         const long long segments =
             static_cast<long long>(b0) * a.cache.heads + s.head * (b1 - b0) + s.block;
-        first = u0 * a.cache.heads + s.head * per + ub - u0 - kSegmentTiles * segments + s.tile;
+        first = u0 * a.cache.heads + s.head * per + ub - u0 - kSegmentTiles * segments;
+        end = first + (s.tile > 0 ? cost0[b + 1] - ub - kSegmentTiles : 0);
+        first += s.tile;
       }
     }
-    tile_of[c] = first;
+    sh->tile_of[c] = first;
+    sh->cut_end[c] = end;
   }
   __syncthreads();
   if (c < G) {
-    s.until = tile_of[c + 1];
-    s.left = s.until - tile_of[c];
-    a.starts[c] = s;
+    s.left = sh->tile_of[c + 1] - sh->tile_of[c];
+    s.last = c + 1;
+    while (s.last + 1 < G && sh->tile_of[s.last + 1] < sh->cut_end[c + 1]) ++s.last;
   }
+  return s;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int G) {
+  __shared__ PlanShared sh;
+  pdl_trigger();
+  const AttnStart s = plan<kPlanThreads>(a, G, &sh, a.plan_block0, a.plan_cost0);
+  if (static_cast<int>(threadIdx.x) < G) a.starts[threadIdx.x] = s;
 }
 
 // A CTA's walk over its segments.
@@ -279,6 +297,7 @@ struct Bars {
   uint32_t tmem;
   int abort;
   int spoilt;                                          // some sum is not finite
+  AttnStart start;
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
 
@@ -391,9 +410,18 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
   pdl_trigger();
-  pdl_wait();                                          // the plan
+  pdl_wait();                                          // the plan, or what came before
 
-  const AttnStart st = a.starts[cluster];
+  if (a.plan_here) {
+    PlanShared* sh = reinterpret_cast<PlanShared*>(sq);  // where the queries will be
+    long long* cost0 = reinterpret_cast<long long*>(sh + 1);
+    int* block0 = reinterpret_cast<int*>(cost0 + kAttnPlanHere + 1);
+    static_assert(sizeof(PlanShared) + (kAttnPlanHere + 1) * 12 <= C::kBytes, "room");
+    const AttnStart s = plan<C::kThreads>(a, static_cast<int>(gridDim.x) / CL, sh, block0, cost0);
+    if (static_cast<int>(threadIdx.x) == cluster) bars->start = s;
+    __syncthreads();
+  }
+  const AttnStart st = a.plan_here ? bars->start : a.starts[cluster];
   long long left = st.left;
   const int group = static_cast<int>(a.group.d);
   Walk wk;
@@ -678,15 +706,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       head = wk.h * group + my - tok * group;
       if (threadIdx.x == 0 && rank == 0 && !whole && slot == 1) {
         // this cluster begins a cut segment: where its pieces end, for the join
-        const long long end = st.until + (wk.b.t1 - stop);
-        int last = cluster + 1;
-        while (CL * (last + 1) < static_cast<int>(gridDim.x) && a.starts[last].until < end) ++last;
         AttnPiece p;
         p.rows = wk.b.rows;
         p.head = wk.h;
         p.first = wk.rq.first;
         p.row0 = wk.b.row0;
-        p.last = last;
+        p.last = st.last;
         *piece = p;
         begun = true;
       }
