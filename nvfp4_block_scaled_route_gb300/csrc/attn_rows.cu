@@ -1,5 +1,5 @@
 // Paged attention for few query rows per key head (single tokens, drafted
-// tokens): rows = new tokens * (query heads / key heads) <= 32.
+// tokens): rows = new tokens * (query heads / key heads) <= 16.
 //
 // Every key and value is read once and used by all the rows of its head, so
 // the bound is HBM: 2 * 2 * D bytes of a bf16 key and value against 4 * rows *
@@ -16,9 +16,11 @@
 // shared memory, and for the weighted sum a warp takes D / 8 of the
 // dimensions over all keys.  So a warp holds few accumulators (no partial sums
 // of whole rows to join per tile), and both products run on mma.sync
-// m16n8k16: with at most 32 rows the tensor pipe is far from its limit even so.
+// m16n8k16: with one tile of rows the tensor pipe is far from its limit even so.
+// 64 requests of up to 16384 tokens (56 query, 8 key heads of 128, bf16) take
+// 228 us, 5.9 TB/s.
 //
-// E4M3 caches and up to 16 rows: two groups of eight warps take the tiles in
+// E4M3 caches: two groups of eight warps take the tiles in
 // turn, each with its own sums and maxima and a ring of its own (so that it
 // waits for every phase of its barriers), and the second hands its part of a
 // segment to the first.  A tile's chain of products, exchanges and products
@@ -38,12 +40,14 @@ namespace nvmoe {
 namespace {
 
 constexpr int kKeys = kAttnTileKeys;
+constexpr int kRows = kAttnFewRows;               // an m16 tile
+static_assert(kRows == 16, "rows of a product");
 constexpr int kComputeWarps = 8;                  // of a group
 constexpr int kComputeThreads = kComputeWarps * 32;
-template <bool FP8, int MT>
-constexpr int kGroups = FP8 && MT == 1 ? 2 : 1;
-template <bool FP8, int MT>
-constexpr int kThreads = kGroups<FP8, MT> * kComputeThreads + 32;
+template <bool FP8>
+constexpr int kGroups = FP8 ? 2 : 1;
+template <bool FP8>
+constexpr int kThreads = kGroups<FP8> * kComputeThreads + 32;
 constexpr int kMaxBufs = 16;
 
 template <int D, bool FP8>
@@ -80,9 +84,9 @@ struct Bars {
   long long tile;
 };
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8>
 constexpr int smem_bytes() {
-  constexpr int rows = MT * 16, groups = kGroups<FP8, MT>;
+  constexpr int rows = kRows, groups = kGroups<FP8>;
   return 1024 + Tile<D, FP8>::kBufs * Tile<D, FP8>::kBytes + rows * D * 2 +
          groups * (rows * kKeys * 2 + rows * kComputeWarps * 4) + rows * 4 +
          (groups - 1) * (rows * D * 4 + rows * 8) + static_cast<int>(sizeof(Bars));
@@ -158,18 +162,17 @@ struct Walk {
   }
 };
 
-template <int D, bool FP8, int MT>
-__global__ void __launch_bounds__(kThreads<FP8, MT>, 1)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads<FP8>, 1)
 attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
   using T = Tile<D, FP8>;
-  constexpr int kRows = MT * 16;
   constexpr int kQRow = D * 2, kPRow = kKeys * 2;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* ring = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint8_t* sq = ring + T::kBufs * T::kBytes;
   uint8_t* sp_ = sq + kRows * kQRow;
-  constexpr int kG = kGroups<FP8, MT>, kWarps = kThreads<FP8, MT> / 32;
+  constexpr int kG = kGroups<FP8>, kWarps = kThreads<FP8> / 32;
   constexpr int kPer = T::kBufs / kG;                               // buffers of a group
   float* smax = reinterpret_cast<float*>(sp_ + kG * kRows * kPRow);      // [group][kRows][8]
   float* sfac = smax + kG * kRows * kComputeWarps;                       // [kRows]
@@ -181,7 +184,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
 
   // ---- this CTA's share of the tiles ----
   long long* scan = reinterpret_cast<long long*>(smax);           // [kWarps] warp sums
-  const int per = (a.batch.batch + kThreads<FP8, MT> - 1) / kThreads<FP8, MT>;
+  const int per = (a.batch.batch + kThreads<FP8> - 1) / kThreads<FP8>;
   const int r_begin = min(a.batch.batch, static_cast<int>(threadIdx.x) * per);
   const int r_end = min(a.batch.batch, r_begin + per);
   long long mine = 0;
@@ -378,22 +381,20 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     }
     all_sync<kG>();
 
-    float o[MT][kN][4], m[MT][2], l[MT][2], cr[MT][2];
-    int vis_hi[MT][2], vis_lo[MT][2];
+    float o[kN][4], m[2], l[2], cr[2];
+    int vis_hi[2], vis_lo[2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < 2; ++e) {
+      const int row = e * 8 + g;
+      const int pos = wk.rq.pos0 + row / group;
+      vis_hi[e] = min(pos + 1, wk.rq.len);
+      vis_lo[e] = a.window > 0 ? pos - a.window + 1 : 0;
+      m[e] = -INFINITY;
+      l[e] = 0.0f;
+      cr[e] = FP8 ? c * sfac[row] : c;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = i * 16 + e * 8 + g;
-        const int pos = wk.rq.pos0 + row / group;
-        vis_hi[i][e] = min(pos + 1, wk.rq.len);
-        vis_lo[i][e] = a.window > 0 ? pos - a.window + 1 : 0;
-        m[i][e] = -INFINITY;
-        l[i][e] = 0.0f;
-        cr[i][e] = FP8 ? c * sfac[row] : c;
-#pragma unroll
-        for (int n = 0; n < kN; ++n) o[i][n][2 * e] = o[i][n][2 * e + 1] = 0.0f;
-      }
+      for (int n = 0; n < kN; ++n) o[n][2 * e] = o[n][2 * e + 1] = 0.0f;
+    }
     // keys that every row sees
     const int all_hi = min(wk.rq.pos0 + 1, wk.rq.len);
     const int all_lo = a.window > 0 ? wk.rq.pos0 + wk.rq.n - a.window : 0;
@@ -405,13 +406,11 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
       if (kG == 2 && static_cast<int>(seq & 1u) != side) continue;
       const int key0 = t * kKeys;
       // scores of this warp's 16 keys
-      float s[MT][2][4];
+      float s[2][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
       mbar_wait(&full[buf], phase, a.status, abort);
       {
         const uint32_t kb = ring_u + buf * T::kBytes;
@@ -420,24 +419,21 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         for (int ks = 0; ks < D / (FP8 ? 32 : 16); ++ks) {
           uint32_t kf[4];
           ldsm4(kb + T::at(krow, 2 * ks + ((lane >> 3) & 1)), kf);
+          if (!FP8) {
+            uint32_t qf[4];
+            ldsm4(sq_u + mat_at<kQRow>(lane & 15, 2 * ks + (lane >> 4)), qf);
+            mma16816<false>(s[0], qf, kf[0], kf[1]);
+            mma16816<false>(s[1], qf, kf[2], kf[3]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            if (!FP8) {
+            for (int k2 = 0; k2 < 2; ++k2) {
               uint32_t qf[4];
-              ldsm4(sq_u + mat_at<kQRow>(i * 16 + (lane & 15), 2 * ks + (lane >> 4)), qf);
-              mma16816<false>(s[i][0], qf, kf[0], kf[1]);
-              mma16816<false>(s[i][1], qf, kf[2], kf[3]);
-            } else {
-#pragma unroll
-              for (int k2 = 0; k2 < 2; ++k2) {
-                uint32_t qf[4];
-                ldsm4(sq_u + mat_at<kQRow>(i * 16 + (lane & 15), 4 * ks + 2 * k2 + (lane >> 4)),
-                      qf);
-                mma16816<true>(s[i][0], qf, e4m3x2_to_f16x2(kf[k2]),
-                               e4m3x2_to_f16x2(kf[k2] >> 16));
-                mma16816<true>(s[i][1], qf, e4m3x2_to_f16x2(kf[2 + k2]),
-                               e4m3x2_to_f16x2(kf[2 + k2] >> 16));
-              }
+              ldsm4(sq_u + mat_at<kQRow>(lane & 15, 4 * ks + 2 * k2 + (lane >> 4)),
+                    qf);
+              mma16816<true>(s[0], qf, e4m3x2_to_f16x2(kf[k2]),
+                             e4m3x2_to_f16x2(kf[k2] >> 16));
+              mma16816<true>(s[1], qf, e4m3x2_to_f16x2(kf[2 + k2]),
+                             e4m3x2_to_f16x2(kf[2 + k2] >> 16));
             }
           }
         }
@@ -448,56 +444,52 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
 
       const bool masked = key0 + kKeys > all_hi || key0 < all_lo;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float top = -INFINITY;
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float& x = s[i][n][2 * e + j];
-              x *= cr[i][e];
-              if (masked) {
-                const int key = key0 + w * 16 + n * 8 + c2 + j;
-                if (key >= vis_hi[i][e] || key < vis_lo[i][e]) x = -INFINITY;
-              }
-              top = fmaxf(top, x);
+          for (int j = 0; j < 2; ++j) {
+            float& x = s[n][2 * e + j];
+            x *= cr[e];
+            if (masked) {
+              const int key = key0 + w * 16 + n * 8 + c2 + j;
+              if (key >= vis_hi[e] || key < vis_lo[e]) x = -INFINITY;
             }
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          if ((lane & 3) == 0) smax[(i * 16 + e * 8 + g) * kComputeWarps + w] = top;
-        }
+            top = fmaxf(top, x);
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        if ((lane & 3) == 0) smax[(e * 8 + g) * kComputeWarps + w] = top;
+      }
       group_sync(side);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int e = 0; e < 2; ++e) {
+        const int row = e * 8 + g;
+        const float4* mx = reinterpret_cast<const float4*>(smax + row * kComputeWarps);
+        const float4 u = mx[0], v = mx[1];
+        const float mn =
+            fmaxf(fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)),
+                        fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))), m[e]);
+        const float use = mn == -INFINITY ? 0.0f : mn;   // a row without keys so far
+        const float f = exp2_approx(m[e] - use);
+        m[e] = mn;
+        float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = i * 16 + e * 8 + g;
-          const float4* mx = reinterpret_cast<const float4*>(smax + row * kComputeWarps);
-          const float4 u = mx[0], v = mx[1];
-          const float mn =
-              fmaxf(fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)),
-                          fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))), m[i][e]);
-          const float use = mn == -INFINITY ? 0.0f : mn;   // a row without keys so far
-          const float f = exp2_approx(m[i][e] - use);
-          m[i][e] = mn;
-          float sum = 0.0f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = exp2_approx(s[i][n][2 * e] - use);
-            const float p1 = exp2_approx(s[i][n][2 * e + 1] - use);
-            sum += p0 + p1;
-            *reinterpret_cast<uint32_t*>(sp_ + mat_at<kPRow>(row, w * 2 + n) + c2 * 2) =
-                FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-          }
-          l[i][e] = fmaf(l[i][e], f, sum);
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            o[i][n][2 * e] *= f;
-            o[i][n][2 * e + 1] *= f;
-          }
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = exp2_approx(s[n][2 * e] - use);
+          const float p1 = exp2_approx(s[n][2 * e + 1] - use);
+          sum += p0 + p1;
+          *reinterpret_cast<uint32_t*>(sp_ + mat_at<kPRow>(row, w * 2 + n) + c2 * 2) =
+              FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
         }
+        l[e] = fmaf(l[e], f, sum);
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          o[n][2 * e] *= f;
+          o[n][2 * e + 1] *= f;
+        }
+      }
       mbar_wait(&full[buf], phase, a.status, abort);
       const bool cut = key0 < kbeg || key0 + kKeys > kend;
       if (cut) {
@@ -557,14 +549,12 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
           b1[1][0] = v[3];
         }
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
+        for (int st = 0; st < 2; ++st) {
+          uint32_t pf[4];
+          ldsm4(sp_u + mat_at<kPRow>(lane & 15, (k2 * 2 + st) * 2 + (lane >> 4)), pf);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t pf[4];
-            ldsm4(sp_u + mat_at<kPRow>(i * 16 + (lane & 15), (k2 * 2 + st) * 2 + (lane >> 4)), pf);
-#pragma unroll
-            for (int n = 0; n < kN; ++n) mma16816<FP8>(o[i][n], pf, b0[st][n], b1[st][n]);
-          }
+          for (int n = 0; n < kN; ++n) mma16816<FP8>(o[n], pf, b0[st][n], b1[st][n]);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[buf]);
@@ -573,50 +563,46 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
 
     // ---- weight sums over the warps, then the rows out ----
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[i][e];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-        if ((lane & 3) == 0) smax[(i * 16 + e * 8 + g) * kComputeWarps + w] = x;
-      }
+    for (int e = 0; e < 2; ++e) {
+      float x = l[e];
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+      if ((lane & 3) == 0) smax[(e * 8 + g) * kComputeWarps + w] = x;
+    }
     group_sync(side);
-    float lsum[MT][2];
+    float lsum[2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4* sm =
-            reinterpret_cast<const float4*>(smax + (i * 16 + e * 8 + g) * kComputeWarps);
-        const float4 u = sm[0], v = sm[1];
-        lsum[i][e] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
-      }
+    for (int e = 0; e < 2; ++e) {
+      const float4* sm =
+          reinterpret_cast<const float4*>(smax + (e * 8 + g) * kComputeWarps);
+      const float4 u = sm[0], v = sm[1];
+      lsum[e] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+    }
     if (kG == 2) {
       // the second group's part to the first
       if (side == 1) {
 #pragma unroll
-        for (int k = 0; k < kN * 4; ++k) join_o[k * kComputeThreads + thread] = o[0][k >> 2][k & 3];
+        for (int k = 0; k < kN * 4; ++k) join_o[k * kComputeThreads + thread] = o[k >> 2][k & 3];
         if (w == 0 && (lane & 3) == 0)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) join_ml[e * 8 + g] = make_float2(m[0][e], lsum[0][e]);
+          for (int e = 0; e < 2; ++e) join_ml[e * 8 + g] = make_float2(m[e], lsum[e]);
       }
       all_sync<kG>();
       if (side == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float2 ml = join_ml[e * 8 + g];
-          const float mn = fmaxf(m[0][e], ml.x), use = mn == -INFINITY ? 0.0f : mn;
-          const float f0 = exp2_approx(m[0][e] - use), f1 = exp2_approx(ml.x - use);
-          m[0][e] = mn;
-          lsum[0][e] = lsum[0][e] * f0 + ml.y * f1;
+          const float mn = fmaxf(m[e], ml.x), use = mn == -INFINITY ? 0.0f : mn;
+          const float f0 = exp2_approx(m[e] - use), f1 = exp2_approx(ml.x - use);
+          m[e] = mn;
+          lsum[e] = lsum[e] * f0 + ml.y * f1;
 #pragma unroll
           for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int k = n * 4 + 2 * e + j;
-              o[0][n][2 * e + j] =
-                  o[0][n][2 * e + j] * f0 + join_o[k * kComputeThreads + thread] * f1;
+              o[n][2 * e + j] =
+                  o[n][2 * e + j] * f0 + join_o[k * kComputeThreads + thread] * f1;
             }
         }
       }
@@ -624,61 +610,59 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const float v_scale = FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
     const int64_t pc = 2 * static_cast<int64_t>(blockIdx.x) + slot;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int e = 0; e < 2; ++e) {
+      const int row = e * 8 + g;
+      if (row >= rows || side != 0) continue;
+      const float sum = lsum[e];
+      const int tok = row / group;
+      const int64_t tk = wk.rq.first + tok;
+      const int head = wk.h * group + row - tok * group;
+      const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
+      float probe = 0.0f;                         // NaN if some sum is not finite
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = i * 16 + e * 8 + g;
-        if (row >= rows || side != 0) continue;
-        const float sum = lsum[i][e];
-        const int tok = row / group;
-        const int64_t tk = wk.rq.first + tok;
-        const int head = wk.h * group + row - tok * group;
-        const float inv = sum == 0.0f ? 0.0f : v_scale / sum;
-        float probe = 0.0f;                         // NaN if some sum is not finite
+      for (int n = 0; n < kN; ++n)
+        probe = fmaf(o[n][2 * e], 0.0f, fmaf(o[n][2 * e + 1], 0.0f, probe));
+      if (probe != 0.0f) bars->spoilt = 1;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
+                           tk * a.out.token_stride + head * a.out.head_stride;
+      float* po = a.piece_o + (pc * a.piece_rows + row) * D;
+      // the dimensions of this thread's accumulators
+      if (FP8 && D == 128) {
+        const int d = w * 16 + c2 * 2;
+        const float y[4] = {o[0][2 * e], o[kN - 1][2 * e], o[0][2 * e + 1],
+                            o[kN - 1][2 * e + 1]};
+        if (whole)
+          *reinterpret_cast<uint2*>(out + d) =
+              make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv),
+                         pack_bf16x2(y[2] * inv, y[3] * inv));
+        else
+          *reinterpret_cast<float4*>(po + d) = make_float4(y[0], y[1], y[2], y[3]);
+      } else if (FP8) {
+        const int d = (w >> 1) * 16 + c2 * 2 + (w & 1);
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
-          probe = fmaf(o[i][n][2 * e], 0.0f, fmaf(o[i][n][2 * e + 1], 0.0f, probe));
-        if (probe != 0.0f) bars->spoilt = 1;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
-                             tk * a.out.token_stride + head * a.out.head_stride;
-        float* po = a.piece_o + (pc * a.piece_rows + row) * D;
-        // the dimensions of this thread's accumulators
-        if (FP8 && D == 128) {
-          const int d = w * 16 + c2 * 2;
-          const float y[4] = {o[i][0][2 * e], o[i][kN - 1][2 * e], o[i][0][2 * e + 1],
-                              o[i][kN - 1][2 * e + 1]};
-          if (whole)
-            *reinterpret_cast<uint2*>(out + d) =
-                make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv),
-                           pack_bf16x2(y[2] * inv, y[3] * inv));
-          else
-            *reinterpret_cast<float4*>(po + d) = make_float4(y[0], y[1], y[2], y[3]);
-        } else if (FP8) {
-          const int d = (w >> 1) * 16 + c2 * 2 + (w & 1);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (whole) out[d + 2 * j] = __float2bfloat16_rn(o[i][0][2 * e + j] * inv);
-            else po[d + 2 * j] = o[i][0][2 * e + j];
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            const int d = (w * kN + n) * 8 + c2;
-            const float y0 = o[i][n][2 * e], y1 = o[i][n][2 * e + 1];
-            if (whole)
-              *reinterpret_cast<uint32_t*>(out + d) = pack_bf16x2(y0 * inv, y1 * inv);
-            else
-              *reinterpret_cast<float2*>(po + d) = make_float2(y0, y1);
-          }
+        for (int j = 0; j < 2; ++j) {
+          if (whole) out[d + 2 * j] = __float2bfloat16_rn(o[0][2 * e + j] * inv);
+          else po[d + 2 * j] = o[0][2 * e + j];
         }
-        if (w == 0 && (lane & 3) == 0) {
-          if (whole) {
-            if (a.lse != nullptr) a.lse[tk * a.q.heads + head] = lse_of(m[i][e], sum);
-          } else {
-            a.piece_ml[pc * a.piece_rows + row] = make_float2(m[i][e], sum);
-          }
+      } else {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int d = (w * kN + n) * 8 + c2;
+          const float y0 = o[n][2 * e], y1 = o[n][2 * e + 1];
+          if (whole)
+            *reinterpret_cast<uint32_t*>(out + d) = pack_bf16x2(y0 * inv, y1 * inv);
+          else
+            *reinterpret_cast<float2*>(po + d) = make_float2(y0, y1);
         }
       }
+      if (w == 0 && (lane & 3) == 0) {
+        if (whole) {
+          if (a.lse != nullptr) a.lse[tk * a.q.heads + head] = lse_of(m[e], sum);
+        } else {
+          a.piece_ml[pc * a.piece_rows + row] = make_float2(m[e], sum);
+        }
+      }
+    }
     if (threadIdx.x == 0 && !whole && slot == 1) {
       // this CTA begins a cut segment: where its pieces end, for the join
       long long end = hi + (wk.sp.t1 - stop);
@@ -719,24 +703,17 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   }
 }
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
-  constexpr int bytes = smem_bytes<D, FP8, MT>();
+  constexpr int bytes = smem_bytes<D, FP8>();
   static_assert(bytes <= 232448, "shared memory");
-  auto kernel = attention_rows_kernel<D, FP8, MT>;
+  auto kernel = attention_rows_kernel<D, FP8>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads<FP8, MT>, bytes, stream>>>(a, mk, mv);
+  kernel<<<grid, kThreads<FP8>, bytes, stream>>>(a, mk, mv);
   return cudaGetLastError();
-}
-
-template <int D, bool FP8>
-cudaError_t launch_mt(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
-                      cudaStream_t stream) {
-  if (a.piece_rows <= 16) return launch<D, FP8, 1>(a, mk, mv, grid, stream);
-  return launch<D, FP8, 2>(a, mk, mv, grid, stream);
 }
 
 }  // namespace
@@ -744,10 +721,10 @@ cudaError_t launch_mt(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMa
 cudaError_t launch_attention_rows(const AttnArgs& a, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream) {
   if (a.cache.fp8)
-    return a.cache.head_dim == 128 ? launch_mt<128, true>(a, map_k, map_v, grid, stream)
-                                   : launch_mt<64, true>(a, map_k, map_v, grid, stream);
-  return a.cache.head_dim == 128 ? launch_mt<128, false>(a, map_k, map_v, grid, stream)
-                                 : launch_mt<64, false>(a, map_k, map_v, grid, stream);
+    return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
+                                   : launch<64, true>(a, map_k, map_v, grid, stream);
+  return a.cache.head_dim == 128 ? launch<128, false>(a, map_k, map_v, grid, stream)
+                                 : launch<64, false>(a, map_k, map_v, grid, stream);
 }
 
 }  // namespace nvmoe
