@@ -704,6 +704,8 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  *   out = sum_j exp(s_j - lse) v_j        (bf16, rounded once)
  * A token that sees no key (negative position) gets out = 0 and lse = -inf.
  * Sums are fp32; exp(s_j - max) is rounded to 16 bits for the product with v.
+ * On an E4M3 cache an element of q counts to within 2^-17 of its row's largest
+ * (bf16 exactly down to 2^-9 of it).
  *   out         bf16 [tokens, q_heads, head_dim] with strides
  *   lse         float [tokens, q_heads] or NULL (natural logarithm)
  *   workspace   attn_paged_workspace_size(...) bytes, whose first word is the

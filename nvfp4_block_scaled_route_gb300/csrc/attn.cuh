@@ -147,7 +147,8 @@ constexpr int kAttnFewRows = 16;
 // 128 (chunk kernel with two tiles: 64) tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
-// Blocks and requests up to which the chunk kernel's CTAs plan for themselves.
+// Blocks and requests up to which the chunk kernel's CTAs plan for themselves: a
+// thread for each (of 384 or 512).
 constexpr int kAttnPlanHere = 384;
 cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);
 cudaError_t launch_attention_chunk(const AttnArgs& args, const CUtensorMap& map_k,

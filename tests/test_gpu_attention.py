@@ -258,6 +258,46 @@ def test_paged_attention_on_another_stream(nb):
     assert torch.equal(got2, want)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 70])
+def test_paged_attention_e4m3_uneven_queries(nb, n, D):
+    """Query rows with elements far above the rest, rows of zeros and of the smallest
+    numbers, on an E4M3 cache.  Queries are scaled by a row's maximum and held to 16
+    bits or two E4M3 numbers: an element to within 2^-17 of the maximum, so that a
+    score may be off by scale * 2^-17 max|q| sum|k| beside the usual bound."""
+    case = Paged([(n, n + 90)], 1, D, 16, seed=4, fp8=True)
+    g = torch.Generator().manual_seed(n + D)
+    q = torch.randn(n, 8, D, generator=g)
+    q[:, 0, 3] *= 300
+    q[:, 1, ::2] *= 2.0 ** -9
+    q[:, 2] = 0
+    q[:, 3] = 1e-39
+    q[:, 4] *= 2.0 ** -60
+    q[:, 5, D // 2:] = 0
+    q = q.bfloat16()
+    cache, batch = case.handles(nb)
+    lse = torch.empty(n, 8, device=DEV)
+    ws = nb.paged_attention_workspace(cache, batch, 8, n)
+    out = nb.paged_attention(q.to(DEV), cache, batch, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    want, wlse, b_out, b_lse = case.reference(q)
+    k, v = (ref.key_rows(c, case.table[0], 16, n + 90, 0, False, sc)
+            for c, sc in ((case.k, case.k_scale), (case.v, case.v_scale)))
+    extra = D ** -0.5 * 2.0 ** -17 * q.double().abs().amax(-1) * k.abs().sum(1).max()
+    _within(out, want, b_out + 2 * extra[..., None] * v.abs().max(), "out")
+    _within(lse, wlse, b_lse + extra, "lse")
+
+
+@pytest.mark.parametrize("count,hq,hk,D,fp8", [(400, 32, 1, 64, False), (1100, 17, 1, 128, True),
+                                               (1100, 20, 10, 64, False)],
+                         ids=["400", "1100-e4m3", "1100-few"])
+def test_paged_attention_many_requests(nb, count, hq, hk, D, fp8):
+    """More requests than a CTA has threads to plan them with, empty ones among them."""
+    case = Paged([((i * 5 % 7) > 1, (i * 7) % 19 + 1) for i in range(count)], hk, D, 16, seed=8, fp8=fp8)
+    _check(nb, case, hq)
+
+
 def test_paged_attention_in_a_graph_follows_the_batch(nb):
     """Captured once; lengths and pages are device data, refilled in place."""
     a, b = Paged([(1, 300), (1, 70)], 2, 128, 16, seed=1), Paged([(1, 33), (1, 301)], 2, 128, 16, seed=1)
@@ -560,3 +600,10 @@ def test_paged_attention_many_segments(nb, n, prior, hq, hk, D, window, fp8):
     torch.cuda.synchronize()
     assert nb.read_status(ws) == 0
     assert all(torch.equal(a, out) for a in again)
+
+
+@pytest.mark.parametrize("n,prior,window", [(1600, 100, 0), (3100, 0, 200)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_paged_attention_many_blocks(nb, n, prior, window, fp8):
+    """More row blocks than are planned in place."""
+    test_paged_attention_many_segments(nb, n, prior, 32, 1, 64, window, fp8)
