@@ -181,6 +181,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   Bars* bars = reinterpret_cast<Bars*>(join_ml + (kG - 1) * kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
+  pdl_wait();                                       // for what came before
 
   // ---- this CTA's share of the tiles ----
   long long* scan = reinterpret_cast<long long*>(smax);           // [kWarps] warp sums
@@ -712,8 +713,18 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
   auto kernel = attention_rows_kernel<D, FP8>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads<FP8>, bytes, stream>>>(a, mk, mv);
-  return cudaGetLastError();
+  // its start overlaps the end of the kernel before
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads<FP8>);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, mk, mv);
 }
 
 }  // namespace
