@@ -24,6 +24,10 @@ constexpr int kThreads = 128;
 // rotation) before a row can be stored.  Measured, 4096 tokens of 56 + 8 heads
 // of 128 and 21 k tokens into an E4M3 cache: 8 heads of 64 registers 29.8 us
 // and 188 us, 4 of 48 32.4 and 162, 8 of 90 registers 31.3 and 264.
+// (With its start over the end of the kernel before, a launch takes 27.3 and 159.5:
+// 4.96 and 4.74 TB/s.  Into the cache instructions bound it, each group finds its
+// request, page and rotation anew; groups that keep them for 8 or 16 heads in
+// rounds of 4 took 187 to 190 us.)
 // Below kWideRows head rows two heads a group spread few tokens wider.
 constexpr int64_t kWideRows = 16384;
 template <bool APPEND>
@@ -80,6 +84,7 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x4(const uint64_t (&x)[2]) {
 template <int D, int HEADS, bool APPEND, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, kMinBlocks<APPEND>)
 head_transform_kernel(const RopeArgs a) {
+  pdl_wait();                                         // for what came before
   constexpr int kLanes = D / 8;                       // lanes of a group
   const int sub = threadIdx.x & (kLanes - 1);
   const uint32_t mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
@@ -280,8 +285,17 @@ cudaError_t launch_d(RopeArgs a, cudaStream_t stream) {
     a.kv_chunks = static_cast<int>(ceil_div(a.k.heads, per));
     a.chunks = a.q_chunks + (APPEND ? 2 : 1) * a.kv_chunks;
     const int64_t blocks = ceil_div(a.T * a.chunks, kGroups);
-    kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    // its start overlaps the end of the kernel before
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
   };
   const int64_t heads = a.q.heads + a.k.heads + a.v.heads;
   constexpr int kWide = kWideHeads<APPEND>;
