@@ -539,7 +539,9 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
         return None
     if t.dtype is not dtype or t.shape != (n,):
         raise ValueError(f"{what} must be {dtype} [{n}]")
-    return _ptr(t)
+    if not (t.is_cuda and (t.is_contiguous() or n < 2)):
+        raise ValueError(f"{what} must be a dense CUDA tensor")
+    return t.data_ptr()
 
 
 def _rope(rope: Optional[torch.Tensor]):
@@ -561,14 +563,20 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     given) of bf16 q [T, Hq, D] and k [T, Hkv, D], strided views taken as they
     are; positions int32 [T].  q_out / k_out may be q and k themselves.
     Returns (q_out, k_out)."""
-    T, hq, D = q.shape
-    hk = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != D:
+    # (each attribute of a tensor costs about 0.1 us, a call of few tokens 10)
+    q_shape, k_shape = q.shape, k.shape
+    T, hq, D = q_shape
+    Tk, hk, Dk = k_shape
+    if Tk != T or Dk != D:
         raise ValueError("q and k must agree in tokens and head_dim")
-    q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((T, hk, D), dtype=k.dtype, device=k.device) if k_out is None else k_out
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
+    if q_out is None:
+        q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    elif q_out is not q and q_out.shape != q_shape:
+        raise ValueError("q_out must have the shape of q")
+    if k_out is None:
+        k_out = torch.empty((T, hk, D), dtype=k.dtype, device=k.device)
+    elif k_out is not k and k_out.shape != k_shape:
+        raise ValueError("k_out must have the shape of k")
     ws = attn_workspace(q.device) if ws is None else ws
     table, npos, rot = _rope(rope)
     _check("attn_qk_norm_rope", lib().attn_qk_norm_rope(
@@ -642,17 +650,19 @@ def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.T
     """Norm and rotate the new keys at their cache positions and append them
     with the new values (bf16 [T, Hkv, D]); with q given, norm and rotate it in
     the same launch.  Returns q_out (None without q)."""
-    T, D = k.shape[0], cache.head_dim
-    if k.shape != v.shape or k.shape[1] != cache.heads or k.shape[2] != D:
+    k_shape, D = k.shape, cache.head_dim
+    T, hk, Dk = k_shape
+    if k_shape != v.shape or hk != cache.heads or Dk != D:
         raise ValueError("k and v must be [tokens, kv heads, head_dim] of the cache")
     hq, q_args, out_args = 0, (None, 0, 0), (None, 0, 0)
     if q is not None:
-        hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D:
+        q_shape = q.shape
+        Tq, hq, Dq = q_shape
+        if Tq != T or Dq != D:
             raise ValueError("q and k must agree in tokens and head_dim")
         if q_out is None:
             q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-        if q_out.shape != q.shape:
+        elif q_out is not q and q_out.shape != q_shape:
             raise ValueError("q_out must have the shape of q")
         q_args, out_args = _rows(q, "q"), _rows(q_out, "q_out")
     ws = attn_workspace(k.device) if ws is None else ws
@@ -683,12 +693,13 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
     requests' cached keys (the new ones appended before).  window > 0: only the
     last `window` positions.  lse: optional float32 [T, Hq], written.  Returns
     out, bf16 [T, Hq, D]."""
-    T, hq, D = q.shape
+    shape = q.shape
+    T, hq, D = shape
     if D != cache.head_dim:
         raise ValueError("q and the cache must agree in head_dim")
     if out is None:
         out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-    if out.shape != q.shape:
+    elif out.shape != shape:
         raise ValueError("out must have the shape of q")
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, hq)):
         raise ValueError("lse must be float32 [tokens, q heads]")

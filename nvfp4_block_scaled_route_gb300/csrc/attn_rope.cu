@@ -25,7 +25,7 @@ constexpr int kThreads = 128;
 // of 128 and 21 k tokens into an E4M3 cache: 8 heads of 64 registers 29.8 us
 // and 188 us, 4 of 48 32.4 and 162, 8 of 90 registers 31.3 and 264.
 // (With its start over the end of the kernel before, a launch takes 27.3 and 159.5:
-// 4.96 and 4.74 TB/s.  Into the cache instructions bound it, each group finds its
+// 5.0 and 4.7 TB/s.  Into the cache instructions bound it, each group finds its
 // request, page and rotation anew; groups that keep them for 8 or 16 heads in
 // rounds of 4 took 187 to 190 us.)
 // Below kWideRows head rows two heads a group spread few tokens wider.
