@@ -94,7 +94,8 @@ typedef enum {
  * so results are unchanged.  enable 1 turns it on (process-wide); returns the
  * previous setting.  Default off: measured inside a CUDA graph on the large
  * prefill step it was 2 % slower (4.29 against 4.21 ms), whether the kernels
- * let their dependents launch at entry or after their work.  Host only. */
+ * let their dependents launch at entry or after their work.  Host only.  (The
+ * attention operators are always launched so.) */
 int nvmoe_set_pdl(int enable);
 
 /* Human-readable name of a status code (static string, never NULL). */
