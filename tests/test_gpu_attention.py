@@ -472,6 +472,32 @@ def test_kv_append(nb, reqs, hq, hk, D, page, heads_first, rot, norm, pairs, wit
         assert torch.equal(raw, was)
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_cache_offsets_past_32_bits(nb, n, fp8):
+    """Pages at the far end of a cache of 2.4e9 elements hold and give what pages
+    of a small cache do, bit for bit."""
+    hq, hk, D, page = 16, 8, 128, 16
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    g = torch.Generator(device=DEV).manual_seed(n)
+    q, k, v = (torch.randn(40, h, D, generator=g, device=DEV).bfloat16() for h in (hq, hk, hk))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)   # noqa: E731
+    got = []
+    for pages, ids in ((3, (2, 0, 1)), (146500, (146499, 0, 140000))):
+        kc, vc = (torch.empty(pages, page, hk, D, dtype=dtype, device=DEV) for _ in range(2))
+        cache, table = nb.PagedKVCache(kc, vc), i32(*ids)[None]
+        everything = nb.AttnBatch(i32(0, 40), i32(40), table, max_new=40)
+        nb.kv_append(cache, everything, k, v)
+        batch = nb.AttnBatch(i32(0, n), i32(40), table, max_new=n)
+        out = nb.paged_attention(q[:n].contiguous(), cache, batch)
+        got.append([out] + [c[table[0].long()].view(torch.uint8).flatten(0, 1)[:40].cpu()
+                            for c in (kc, vc)])
+        del kc, vc, cache
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][0].isfinite().all()
+
+
 def test_kv_append_e4m3_rounds_to_nearest_and_saturates(nb):
     """Without a scale the stored bytes are torch's cast of the clamped value."""
     D, page = 128, 16
