@@ -1123,7 +1123,7 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
   const bool few = rows <= kAttnFewRows;
   // few rows: all of a segment; else a tile of the chunk kernel, or two
   a->piece_rows = few ? static_cast<int>(rows)
-                      : (rows <= kAttnTileRows ? kAttnTileRows : 2 * kAttnTileRows);
+                      : (rows <= kAttnTileRows || D < 128 ? kAttnTileRows : 2 * kAttnTileRows);
   const int64_t blocks = few ? 0 : ceil_div(tokens * group, kAttnTileRows) + batch;
   a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
   a->plan_here = batch <= kAttnPlanHere && blocks <= kAttnPlanHere;

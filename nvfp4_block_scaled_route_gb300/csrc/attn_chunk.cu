@@ -6,9 +6,13 @@
 // half of its pages and multicasts them to both.  Where no request has more
 // than 128 rows, single CTAs take blocks of 128: a second tile would idle (16
 // requests of 35 rows on 6000 keys, bf16 and E4M3, 40.6 and 36.5 us against 44.7
-// and 45.7, of 112 rows 57 and 47 against 60 and 61).  Per 128 keys a CTA runs two
-// products of 128 x 128 x D and 128 x 128 exponentials; the tensor pipe is the
-// bound (4 * rows * keys * D flops).  2048 new tokens over 16384 keys, 56 query
+// and 45.7, of 112 rows 57 and 47 against 60 and 61).  So they do with heads of
+// 64, whose tiles are half the bytes, and which need not wait for each other (6
+// prompts of up to 1500 tokens, 24 heads, window 700, 94.9 us against 99.0, without
+// a window 119.5 against 125.6, 2048 of 8192 138.9 against 139.9; heads of 128 lose
+// by it: 16 requests of 280 rows 89.8 against 80.5, 2048 of 16384 629 against 623).
+// Per 128 keys a CTA runs two products of 128 x 128 x D and 128 x 128
+// exponentials; the tensor pipe is the bound (4 * rows * keys * D flops).  2048 new tokens over 16384 keys, 56 query
 // and 8 key heads of 128: 655 us, 1.38 PFLOP/s; per tile a softmax warp's chain
 // takes 1750 cycles, the products 1024.
 //
@@ -1034,8 +1038,9 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
 template <int D, bool FP8>
 cudaError_t launch_cl(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                       int clusters, cudaStream_t stream) {
-  return a.piece_rows == kTile ? launch<D, FP8, 1>(a, mk, mv, clusters, stream)
-                               : launch<D, FP8, 2>(a, mk, mv, clusters, stream);
+  if constexpr (D == 128)
+    if (a.piece_rows > kTile) return launch<D, FP8, 2>(a, mk, mv, clusters, stream);
+  return launch<D, FP8, 1>(a, mk, mv, clusters, stream);
 }
 
 }  // namespace
