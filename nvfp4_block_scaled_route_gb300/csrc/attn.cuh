@@ -1,6 +1,6 @@
-// Shared by the attention operators (attn_rope.cu, attn_rows.cu, attn_chunk.cu, attn_join.cu): the views
-// of head rows, paged cache and batch that the C-ABI layer fills in, and the
-// device helpers that read them.
+// Shared by the attention operators (attn_rope.cu, attn_rows.cu, attn_chunk.cu,
+// attn_join.cu): the views of head rows, paged cache and batch that the C-ABI
+// layer fills in, and the device helpers that read them.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -12,19 +12,19 @@
 // a window 119.5 against 125.6, 2048 of 8192 138.9 against 139.9; heads of 128 lose
 // by it: 16 requests of 280 rows 89.8 against 80.5, 2048 of 16384 629 against 623).
 // Per 128 keys a CTA runs two products of 128 x 128 x D and 128 x 128
-// exponentials; the tensor pipe is the bound (4 * rows * keys * D flops).  2048 new tokens over 16384 keys, 56 query
-// and 8 key heads of 128: 655 us, 1.38 PFLOP/s; per tile a softmax warp's chain
-// takes 1750 cycles, the products 1024.
+// exponentials; the tensor pipe is the bound (4 * rows * keys * D flops).  2048
+// new tokens over 16384 keys, 56 query and 8 key heads of 128: 655 us, 1.38
+// PFLOP/s; per tile a softmax warp's chain takes 1750 cycles, the products 1024.
 //
 //   S = Q K^T       both from shared memory (K-major), into TMEM
 //   P = 2^(cS - m)  TMEM -> registers -> 16 bits -> TMEM
 //   O += P V        P from TMEM, V from shared memory (MN-major)
 //
 // TMEM holds S and P twice: while the softmax of tile j is computed, the tensor
-// cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA
-// would fill TMEM with one S and O each, and the pipe would wait for every
-// softmax.)  The next segment's queries go in before a segment's rows go out,
-// so that its first scores are computed meanwhile.
+// cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA would fill
+// TMEM with one S and O each, and the pipe would wait for every softmax.)  The
+// next segment's queries go in before a segment's rows go out, so that its first
+// scores are computed meanwhile.
 //
 // Roles: warps 0-7 hold the softmax, a row's keys 0-63 and 64-127 in two
 // threads that exchange maxima through shared memory; warps 8 and 9 load key
@@ -623,10 +623,11 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
                 }
               } else {
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                mma_f16(tmem + sb * 128, q_desc + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
-                        desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), C::kIdescS,
-                        ks != 0);
+                for (int ks = 0; ks < D / 16; ++ks)
+                  mma_f16(tmem + sb * 128,
+                          q_desc + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
+                          desc + (((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), C::kIdescS,
+                          ks != 0);
               }
               tc_commit(&bars->s_full[sb]);
             }
