@@ -13,7 +13,7 @@
 // by it: 16 requests of 280 rows 89.8 against 80.5, 2048 of 16384 629 against 623).
 // Per 128 keys a CTA runs two products of 128 x 128 x D and 128 x 128
 // exponentials; the tensor pipe is the bound (4 * rows * keys * D flops).  2048
-// new tokens over 16384 keys, 56 query and 8 key heads of 128: 655 us, 1.38
+// new tokens over 16384 keys, 56 query and 8 key heads of 128: 660 us, 1.37
 // PFLOP/s; per tile a softmax warp's chain takes 1750 cycles, the products 1024.
 //
 //   S = Q K^T       both from shared memory (K-major), into TMEM
