@@ -24,8 +24,9 @@ constexpr int kThreads = 128;
 // rotation) before a row can be stored.  Measured, 4096 tokens of 56 + 8 heads
 // of 128 and 21 k tokens into an E4M3 cache: 8 heads of 64 registers 29.8 us
 // and 188 us, 4 of 48 32.4 and 162, 8 of 90 registers 31.3 and 264.
-// (With its start over the end of the kernel before, a launch takes 27.3 and 159.5:
-// 5.0 and 4.7 TB/s.  Into the cache instructions bound it, each group finds its
+// (With its start over the end of the kernel before, a launch takes 27.4 and 177:
+// 5.0 and 4.3 TB/s; 160 of the latter without the divisions by the scales.  Into the
+// cache instructions bound it, each group finds its
 // request, page and rotation anew; groups that keep them for 8 or 16 heads in
 // rounds of 4 took 187 to 190 us.)
 // Below kWideRows head rows two heads a group spread few tokens wider.
@@ -72,12 +73,6 @@ __device__ __forceinline__ uint2 f32x2_to_bf16x4(const uint64_t (&x)[2]) {
   f32x2_split(x[0], a, b);
   f32x2_split(x[1], c, d);
   return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
-}
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x4(const uint64_t (&x)[2]) {
-  float a, b, c, d;
-  f32x2_split(x[0], a, b);
-  f32x2_split(x[1], c, d);
-  return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 
 // APPEND: k and v go to the cache.  PAIRS: neighbours form the pairs.
@@ -254,13 +249,16 @@ head_transform_kernel(const RopeArgs a) {
       void* dst = plain ? a.cache.v : a.cache.k;
       if (a.cache.fp8) {
         const float* sc = plain ? a.cache.v_scale : a.cache.k_scale;
-        const float inv = sc != nullptr ? 1.0f / sc[h] : 1.0f;
-        const uint64_t inv2 = f32x2(inv, inv);
+        // (the quotient, not a product with the reciprocal: that one rounds to the
+        // other side at some ties, and is infinite for a scale below 2^-128)
+        const float by = sc != nullptr ? sc[h] : 1.0f;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint64_t z[2] = {mul_f32x2(x[s][0], inv2), mul_f32x2(x[s][1], inv2)};
+          float z[4];
+          f32x2_split(x[s][0], z[0], z[1]);
+          f32x2_split(x[s][1], z[2], z[3]);
           *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(dst) + at + (s == 0 ? i0 : i1)) =
-              f32x2_to_e4m3x4(z);
+              pack_e4m3x2(z[0] / by, z[1] / by) | (pack_e4m3x2(z[2] / by, z[3] / by) << 16);
         }
       } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dst) + at;
