@@ -1093,8 +1093,8 @@ namespace {
 
 // One side of a paged cache as [num_pages, heads, page_size, D] by its
 // strides; box: 128 bytes of the row (all of it, if shorter) x up to
-// box_tokens tokens of one page and head.
-bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c, uint32_t box_tokens) {
+// 128 tokens of one page and head.
+bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t el = c.fp8 ? 1 : 2;
@@ -1102,8 +1102,8 @@ bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c, uint3
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), page,
                         static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_pages)};
   cuuint64_t strides[3] = {c.token_stride * el, c.head_stride * el, c.page_stride * el};
-  cuuint32_t box[4] = {line / static_cast<uint32_t>(el), std::min<uint32_t>(page, box_tokens), 1,
-                       1};
+  cuuint32_t box[4] = {line / static_cast<uint32_t>(el), std::min<uint32_t>(page, kAttnTileKeys),
+                       1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                   const_cast<void*>(base), dims, strides, box, estr,
@@ -1121,9 +1121,8 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
   Carve c{base};
   const int64_t group = q_heads / kv_heads, rows = max_new * group;
   const bool few = rows <= kAttnFewRows;
-  // few rows: all of a segment; else a tile of the chunk kernel, or two
-  a->piece_rows = few ? static_cast<int>(rows)
-                      : (rows <= kAttnTileRows || D < 128 ? kAttnTileRows : 2 * kAttnTileRows);
+  // few rows: all of a segment; else a tile of the chunk kernel
+  a->piece_rows = few ? static_cast<int>(rows) : kAttnTileRows;
   const int64_t blocks = few ? 0 : ceil_div(tokens * group, kAttnTileRows) + batch;
   a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
   a->plan_here = batch <= kAttnPlanHere && blocks <= kAttnPlanHere;
@@ -1185,15 +1184,11 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
               a.cache.head_dim, static_cast<uint8_t*>(ws), &a);
   const bool few = a.piece_rows <= kAttnFewRows;
   CUtensorMap map_k, map_v;
-  const bool pairs = a.piece_rows > kAttnTileRows;
-  const uint32_t box = pairs ? kAttnTileKeys / 2 : kAttnTileKeys;
-  if (!make_kv_map(&map_k, a.cache.k, a.cache, box) ||
-      !make_kv_map(&map_v, a.cache.v, a.cache, box))
+  if (!make_kv_map(&map_k, a.cache.k, a.cache) || !make_kv_map(&map_v, a.cache.v, a.cache))
     return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);
-  // shares of the work: a CTA's, or a pair of CTAs' (chunks)
-  const int grid = std::min(pairs ? std::max(nsm / 2, 1) : nsm, kMaxGrid);
+  const int grid = std::min(nsm, kMaxGrid);        // shares of the work
   cudaError_t e;
   if (few) {
     e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);

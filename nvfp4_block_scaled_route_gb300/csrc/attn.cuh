@@ -89,7 +89,7 @@ __device__ __forceinline__ long long share_begin(long long total, int c, int g) 
     return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(g);
   return total * c / g;
 }
-// Takers among `grid` CTAs (or clusters).
+// Takers among `grid` CTAs.
 __device__ __forceinline__ int share_takers(long long total, int grid) {
   return total < grid ? static_cast<int>(total) : grid;
 }
@@ -135,8 +135,7 @@ struct AttnArgs {
   int max_blocks;
   bool plan_here;           // in the chunk kernel itself; else by attn_plan_kernel
 };
-constexpr int kAttnTileRows = 128;    // query rows of a tile of the chunk kernel, which
-                                      // takes blocks (piece_rows) of one tile or two
+constexpr int kAttnTileRows = 128;    // query rows of a tile (block) of the chunk kernel
 // Rows of a segment up to which attention_rows_kernel takes the call: one m16 tile.
 // Two such tiles against the chunk kernel at 28 rows, bf16 and E4M3 caches: 64
 // requests of up to 16384 tokens 273 and 257 us against 244 and 169, of 2000 tokens
@@ -144,7 +143,7 @@ constexpr int kAttnTileRows = 128;    // query rows of a tile of the chunk kerne
 // 1000, bf16, 15 against 19.
 constexpr int kAttnFewRows = 16;
 // map_k, map_v: [num_pages, heads, page_size, D] by strides, boxes of up to
-// 128 (chunk kernel with two tiles: 64) tokens of one page and head.
+// 128 tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
 // Blocks and requests up to which the chunk kernel's CTAs plan for themselves: a
@@ -152,7 +151,7 @@ cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k
 constexpr int kAttnPlanHere = 384;
 cudaError_t launch_attn_plan(const AttnArgs& args, int grid, cudaStream_t stream);
 cudaError_t launch_attention_chunk(const AttnArgs& args, const CUtensorMap& map_k,
-                                   const CUtensorMap& map_v, int clusters, cudaStream_t stream);
+                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
 cudaError_t launch_attn_combine(const AttnArgs& args, int grid, cudaStream_t stream);
 
 // New tokens and cached length of request r as the kernels take them, kept

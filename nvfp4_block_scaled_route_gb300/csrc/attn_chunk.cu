@@ -1,28 +1,25 @@
 // Paged attention of chunks of new tokens on the tcgen05 tensor cores.
 //
 // The rows of a request and key head -- new tokens x query heads of the key
-// head, token-major -- are taken in blocks of 256 by a cluster of two CTAs, a
-// tile of 128 rows each, which share every key and value tile: each CTA loads
-// half of its pages and multicasts them to both.  Where no request has more
-// than 128 rows, single CTAs take blocks of 128: a second tile would idle (16
-// requests of 35 rows on 6000 keys, bf16 and E4M3, 40.6 and 36.5 us against 44.7
-// and 45.7, of 112 rows 57 and 47 against 60 and 61).  So they do with heads of
-// 64, whose tiles are half the bytes, and which need not wait for each other (6
-// prompts of up to 1500 tokens, 24 heads, window 700, 94.9 us against 99.0, without
-// a window 119.5 against 125.6, 2048 of 8192 138.9 against 139.9; heads of 128 lose
-// by it: 16 requests of 280 rows 89.8 against 80.5, 2048 of 16384 629 against 623).
+// head, token-major -- are taken in blocks of 128 by a CTA.  (Clusters of two CTAs
+// that share each key and value tile by multicast took 6 of 629 us off 2048 new
+// tokens of 16384 and 9 of 90 off 16 requests of 280 rows, and cost 3 of 217 on 4 x
+// 512 on an E4M3 cache; but loads of that kind stay out of a library that processes
+// on several GPUs load.)
+//
 // Per 128 keys a CTA runs two products of 128 x 128 x D and 128 x 128
-// exponentials; the tensor pipe is the bound (4 * rows * keys * D flops).  2048
-// new tokens over 16384 keys, 56 query and 8 key heads of 128: 660 us, 1.37
-// PFLOP/s; per tile a softmax warp's chain takes 1750 cycles, the products 1024.
+// exponentials (4 * rows * keys * D flops in all).  The softmax is the bound: its
+// chain takes a warp 1750 cycles a tile, the products 1024 of the tensor pipe, which
+// is two thirds busy.  2048 new tokens over 16384 keys, 56 query and 8 key heads of
+// 128: 671 us, 1.34 PFLOP/s.
 //
 //   S = Q K^T       both from shared memory (K-major), into TMEM
 //   P = 2^(cS - m)  TMEM -> registers -> 16 bits -> TMEM
 //   O += P V        P from TMEM, V from shared memory (MN-major)
 //
 // TMEM holds S and P twice: while the softmax of tile j is computed, the tensor
-// cores run P V (j - 1) and S (j + 1).  (Two query tiles in one CTA would fill
-// TMEM with one S and O each, and the pipe would wait for every softmax.)  The
+// cores run P V (j - 1) and S (j + 1).  (Two query tiles of 128-wide heads in one CTA
+// would fill TMEM with one S, P and O each, and the pipe would wait for every softmax.)  The
 // next segment's queries go in before a segment's rows go out, so that its first
 // scores are computed meanwhile.
 //
@@ -48,7 +45,7 @@
 // the same quotient; weights stay below 2^8, sums are fp32).
 //
 // The work is the flat list of 128-key tiles of all (request, key head, row
-// block) segments, causal limits taken off; cluster c of G takes a run of it of
+// block) segments, causal limits taken off; CTA c of G takes a run of it of
 // equal cost, and attn_combine_kernel joins the segments cut by a border.  Where
 // the runs start is found by each CTA itself for up to kAttnPlanHere requests and
 // row blocks (16 requests of 35 rows 30.2 us, 34.0 with a launch for it), else by
@@ -59,7 +56,7 @@ namespace nvmoe {
 namespace {
 
 constexpr int kKeys = kAttnTileKeys;
-constexpr int kTile = 128;                   // query rows of a tile
+constexpr int kTile = kAttnTileRows;         // query rows of a tile
 constexpr int kLoadK = 8, kLoadV = 9, kIssueS = 10;   // and 11: P V
 constexpr int kConvert = 12;                 // warps 12-15: values to fp16 (E4M3)
 constexpr int kSoftmaxThreads = 256;
@@ -83,39 +80,29 @@ static_assert(kMaxGrid < kPlanThreads && kMaxGrid < 384, "a thread for each star
 struct Block {
   int row0, rows;
   int t0, t1;                                // tiles of the segment (at least one)
-  int a0[2], a1[2];                          // of each query tile; empty if a1 <= a0
-  int kbeg, kend;                            // keys that any row sees
+  int kbeg, kend;                            // keys that any row sees; none if kend is 0
 };
 __device__ __forceinline__ Block block_of(const Request& q, const FastDiv& group, int window,
-                                          int rows, int p) {
+                                          int p) {
   Block b;
-  b.row0 = p * rows;
-  b.rows = min(rows, q.n * static_cast<int>(group.d) - b.row0);
-  b.t0 = b.t1 = b.kbeg = b.kend = 0;
-#pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    b.a0[a] = b.a1[a] = 0;
-    const int rows = min(kTile, b.rows - a * kTile);
-    if (rows <= 0) continue;
-    const int first = q.pos0 + group(b.row0 + a * kTile);
-    const int last = q.pos0 + group(b.row0 + a * kTile + rows - 1);
-    const int end = min(q.len, last + 1);
-    const int beg = window > 0 ? max(0, first - window + 1) : 0;
-    if (end <= beg) continue;
-    b.a0[a] = beg / kKeys;
-    b.a1[a] = (end + kKeys - 1) / kKeys;
-    if (b.t1 == 0) {
-      b.t0 = b.a0[a];
-      b.kbeg = beg;
-    }
-    b.t1 = b.a1[a];
+  b.row0 = p * kTile;
+  b.rows = min(kTile, q.n * static_cast<int>(group.d) - b.row0);
+  b.t0 = b.kbeg = b.kend = 0;
+  b.t1 = 1;                                  // nothing seen: a tile all the same, rows get zeros
+  const int first = q.pos0 + group(b.row0);
+  const int last = q.pos0 + group(b.row0 + b.rows - 1);
+  const int end = min(q.len, last + 1);
+  const int beg = window > 0 ? max(0, first - window + 1) : 0;
+  if (end > beg) {
+    b.t0 = beg / kKeys;
+    b.t1 = (end + kKeys - 1) / kKeys;
+    b.kbeg = beg;
     b.kend = end;
   }
-  if (b.t1 == 0) b.t1 = 1;                   // nothing seen: a tile all the same, rows get zeros
   return b;
 }
-__device__ __forceinline__ int blocks_of(const Request& q, int group, int rows) {
-  return static_cast<int>((static_cast<int64_t>(q.n) * group + rows - 1) / rows);
+__device__ __forceinline__ int blocks_of(const Request& q, int group) {
+  return static_cast<int>((static_cast<int64_t>(q.n) * group + kTile - 1) / kTile);
 }
 
 // Sum of the values of the threads before this one; *total: of all.
@@ -157,8 +144,8 @@ __device__ __forceinline__ int last_le(int lo, int hi, long long x, F f) {
 }
 
 // Prefix sums of the blocks of the requests (block0) and of the cost of the
-// blocks in tiles (cost0, one key head), then where each of the G CTAs (or
-// clusters) of the attention kernel starts.  Called by all THREADS > G threads of a
+// blocks in tiles (cost0, one key head), then where each of the G CTAs of the
+// attention kernel starts.  Called by all THREADS > G threads of a
 // CTA; thread c returns the start of c.
 struct PlanShared {
   long long sums[32];
@@ -173,8 +160,7 @@ __device__ __forceinline__ AttnStart plan(const AttnArgs& a, int G, PlanShared* 
   for (int r0 = 0; r0 < B; r0 += THREADS) {
     const int r = r0 + threadIdx.x;
     int n = 0;
-    if (r < B) n = blocks_of(load_request(a.batch, a.cache.page_shift, r, a.status), group,
-                             a.piece_rows);
+    if (r < B) n = blocks_of(load_request(a.batch, a.cache.page_shift, r, a.status), group);
     const long long at = blocks + block_scan<THREADS>(n, sh->sums, &total);
     if (r < B) block0[r] = static_cast<int>(min(at, static_cast<long long>(a.max_blocks)));
     blocks += total;
@@ -189,7 +175,7 @@ __device__ __forceinline__ AttnStart plan(const AttnArgs& a, int G, PlanShared* 
     if (i < blocks) {
       const int r = last_le(0, B, i, [&](int k) { return block0[k]; });
       const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
-      const Block b = block_of(rq, a.group, a.window, a.piece_rows, i - block0[r]);
+      const Block b = block_of(rq, a.group, a.window, i - block0[r]);
       n = b.t1 - b.t0 + kSegmentTiles;
     }
     const long long at = units + block_scan<THREADS>(n, sh->sums, &total);
@@ -254,7 +240,7 @@ struct Walk {
   __device__ __forceinline__ void load(const AttnArgs& a, int group, int request) {
     r = request;
     rq = load_request(a.batch, a.cache.page_shift, r, a.status);
-    blocks = blocks_of(rq, group, a.piece_rows);
+    blocks = blocks_of(rq, group);
   }
   // (only called while tiles are left; false if the batch ends all the same)
   __device__ __forceinline__ bool next(const AttnArgs& a, int group) {
@@ -268,7 +254,7 @@ struct Walk {
         } while (blocks == 0);
       }
     }
-    b = block_of(rq, a.group, a.window, a.piece_rows, p);
+    b = block_of(rq, a.group, a.window, p);
     return true;
   }
 };
@@ -311,27 +297,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
 
-// One box into the shared memory of both CTAs of the cluster, signalling the
-// barrier at the same offset in each.
-__device__ __forceinline__ void tma_load_4d_both(void* smem_dst, const CUtensorMap* map, int32_t x,
-                                                 int32_t y, int32_t z, int32_t w, uint64_t* bar,
-                                                 uint64_t cache_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7, %8;"
-      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z),
-        "r"(w), "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "l"(cache_hint)
-      : "memory");
-}
-
-// tc_commit on the barrier at the same offset in both CTAs.
-__device__ __forceinline__ void tc_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;"
-      ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
-}
-
 // D[tmem] (+)= A[tmem] x B[smem], 16-bit operands.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
@@ -362,8 +327,7 @@ __device__ __forceinline__ uint32_t raw_at(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// CL: CTAs of a cluster, a query tile each.
-template <int D, bool FP8, int CL>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 attention_chunk_kernel(const __grid_constant__ AttnArgs a,
                        const __grid_constant__ CUtensorMap map_k,
@@ -382,14 +346,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   // a segment ahead of another)
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(swap + 4 * kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CL == 1 ? 0 : static_cast<int>(cluster_ctarank());   // query tile
-  const int cluster = blockIdx.x / CL;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kK + (FP8 ? C::kRaw : C::kV); ++i) {
       mbar_init(&bars->full[i], 1);
-      // every CTA's readers: an issuer, or four converting warps
-      mbar_init(&bars->empty[i], (FP8 && i >= C::kK ? 4 : 1) * CL);
+      // the readers: an issuer, or four converting warps
+      mbar_init(&bars->empty[i], FP8 && i >= C::kK ? 4 : 1);
     }
     for (int i = 0; FP8 && i < C::kV; ++i) {
       mbar_init(&bars->op_full[i], kConvertThreads);
@@ -415,7 +377,6 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   }
   tc_fence_before();
   __syncthreads();
-  if (CL > 1) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   volatile int* abort = &bars->abort;
@@ -427,11 +388,11 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     long long* cost0 = reinterpret_cast<long long*>(sh + 1);
     int* block0 = reinterpret_cast<int*>(cost0 + kAttnPlanHere + 1);
     static_assert(sizeof(PlanShared) + (kAttnPlanHere + 1) * 12 <= C::kBytes, "room");
-    const AttnStart s = plan<C::kThreads>(a, static_cast<int>(gridDim.x) / CL, sh, block0, cost0);
-    if (static_cast<int>(threadIdx.x) == cluster) bars->start = s;
+    const AttnStart s = plan<C::kThreads>(a, static_cast<int>(gridDim.x), sh, block0, cost0);
+    if (threadIdx.x == blockIdx.x) bars->start = s;
     __syncthreads();
   }
-  const AttnStart st = a.plan_here ? bars->start : a.starts[cluster];
+  const AttnStart st = a.plan_here ? bars->start : a.starts[blockIdx.x];
   long long left = st.left;
   const int group = static_cast<int>(a.group.d);
   Walk wk;
@@ -440,21 +401,20 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     wk.load(a, group, st.request);
     wk.h = st.head;
     wk.p = st.block;
-    wk.b = block_of(wk.rq, a.group, a.window, a.piece_rows, wk.p);
+    wk.b = block_of(wk.rq, a.group, a.window, wk.p);
     t = wk.b.t0 + st.tile;
   }
 
   if (warp >= kLoadK) {
     if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kLoadK || warp == kLoadV) {
-    // ---- this CTA's share (128 / CL keys) of the key or value tiles, to all CTAs
-    // of the cluster: lane = box (page part, column block) ----
+    // ---- key or value tiles: lane = box (page part, column block) ----
     const bool keys = warp == kLoadK;
     const CUtensorMap* map = keys ? &map_k : &map_v;
     const int bufs = keys ? C::kK : (FP8 ? C::kRaw : C::kV);
     const int buf0 = keys ? 0 : C::kK;                  // barriers
     uint8_t* base = sq + (keys ? C::kKAt : (FP8 ? C::kRawAt : C::kVAt));
-    const int box = min(kKeys / CL, 1 << a.cache.page_shift);
+    const int box = min(kKeys, 1 << a.cache.page_shift);
     const int b = lane & 7, half = lane >> 3;
     const uint64_t policy = policy_evict_normal();
     int buf = 0;
@@ -465,8 +425,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       left -= stop - t;
       // the segment's queries to L2, ahead of the softmax warps' loads
       if (keys)
-        for (int i = lane; i < min(kTile, wk.b.rows - rank * kTile); i += 32) {
-          const int r = wk.b.row0 + rank * kTile + i, k = a.group(r);
+        for (int i = lane; i < wk.b.rows; i += 32) {
+          const int r = wk.b.row0 + i, k = a.group(r);
           const __nv_bfloat16* q =
               static_cast<const __nv_bfloat16*>(a.q.data) + (wk.rq.first + k) * a.q.token_stride +
               (wk.h * group + r - k * group) * a.q.head_stride;
@@ -476,9 +436,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         }
       for (; t < stop; ++t) {
         const int key = t * kKeys + b * box;
-        const bool in = b * box < kKeys && half < C::kHalves && key < wk.b.kend &&
-                        key + box > wk.b.kbeg;
-        const bool take = in && b * box / (kKeys / CL) == rank;
+        const bool take = b * box < kKeys && half < C::kHalves && key < wk.b.kend &&
+                          key + box > wk.b.kbeg;
         int page = 0;
         if (take) {
           page = a.batch.page_table[wk.r * a.batch.max_pages + (key >> a.cache.page_shift)];
@@ -498,10 +457,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         if (take) {
           uint8_t* dst = base + buf * C::kLoadBytes + half * kKeys * C::kLine + b * box * C::kLine;
           const int x = half * (FP8 ? C::kLine : C::kLine / 2);
-          if (CL > 1)
-            tma_load_4d_both(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
-          else
-            tma_load_4d(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
+          tma_load_4d(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
         }
         if (++buf == bufs) {
           buf = 0;
@@ -559,8 +515,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         fence_proxy_async_smem();
         mbar_arrive(&bars->op_full[out]);
         __syncwarp();
-        if (lane < CL)                                  // this warp has read the raw tile
-          mbar_arrive_cluster(map_shared_rank(smem_u32(&bars->empty[C::kK + in]), lane));
+        if (lane == 0) mbar_arrive(&bars->empty[C::kK + in]);   // this warp has read the raw tile
         if (++in == C::kRaw) {
           in = 0;
           in_phase ^= 1u;
@@ -597,19 +552,18 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     while (left > 0) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       left -= stop - t;
-      const int j0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
-      const int j1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
-      if (keys && j1 > j0) {
+      const int j0 = t;
+      const bool seen = wk.b.kend > 0;
+      if (keys && seen) {
         mbar_wait(&bars->q_ready, q_phase, a.status, abort);
         q_phase ^= 1u;
       }
       for (; t < stop; ++t) {
-        const bool mine = t >= j0 && t < j1;
         const uint32_t sb = n & 1u, parity = (n >> 1) & 1u;
         const uint64_t desc = desc0 + static_cast<uint32_t>(buf) * (tile_bytes >> 4);
         mbar_wait(&full[buf], phase, a.status, abort);
         if (keys) {
-          if (mine) {
+          if (seen) {
             // S (n - 2) is in registers
             mbar_wait(&bars->s_free[sb], parity ^ 1u, a.status, abort);
             tc_fence_after();
@@ -644,7 +598,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (mine) {
+          if (seen) {
             mbar_wait(&bars->p_ready[sb], parity, a.status, abort);
             tc_fence_after();
             if (lane == 0) {
@@ -656,11 +610,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             }
           }
         }
-        if (lane == 0) {
-          if (CL > 1 && !made) tc_commit_both(&empty[buf]);
-          else tc_commit(&empty[buf]);
-        }
-        if (mine) ++n;
+        if (lane == 0) tc_commit(&empty[buf]);
+        if (seen) ++n;
         if (++buf == bufs) {
           buf = 0;
           phase ^= 1u;
@@ -689,16 +640,17 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     // been read once its thread has met the other one at the next tile's.
     float* mine = swap + half * kTile + row;
     const float* other = swap + (half ^ 1) * kTile + row;
-    AttnPiece* piece = a.pieces + cluster;
+    AttnPiece* piece = a.pieces + blockIdx.x;
     bool begun = false;
     // 32-byte stores of the output rows
     const bool wide = ((reinterpret_cast<uintptr_t>(a.out.data) | a.out.token_stride * 2 |
                         a.out.head_stride * 2) & 31) == 0;
     uint32_t n = 0;                                     // tiles so far
     // the segment: its tiles in this CTA, this thread's row
-    int stop = 0, j0 = 0, j1 = 0, rows = 0, row0 = 0, tok = 0, head = 0, slot = 0;
+    int stop = 0, j0 = 0, rows = 0, row0 = 0, tok = 0, head = 0, slot = 0;
     int64_t tk = 0;
-    bool whole = false, busy = false;                   // busy: some row of this warp is real
+    // sees: some row sees a key; busy: some row of this warp is real
+    bool sees = false, whole = false, busy = false;
     float c = 0.0f;                                     // scores in powers of two
     int seg = 0;                                        // parity of the queries' segment
     const auto open = [&] {
@@ -706,17 +658,17 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       whole = t == wk.b.t0 && stop == wk.b.t1;
       slot = t == wk.b.t0 ? 1 : 0;
       left -= stop - t;
-      rows = min(kTile, wk.b.rows - rank * kTile);
-      j0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
-      j1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
-      row0 = wk.b.row0 + rank * kTile;
+      rows = wk.b.rows;
+      j0 = t;
+      sees = wk.b.kend > 0;
+      row0 = wk.b.row0;
       busy = (warp & 3) * 32 < rows;
-      const int my = row0 + min(row, max(rows, 1) - 1);  // rows past the end act as the last
+      const int my = row0 + min(row, rows - 1);  // rows past the end act as the last
       tok = a.group(my);
       tk = wk.rq.first + tok;
       head = wk.h * group + my - tok * group;
-      if (threadIdx.x == 0 && rank == 0 && !whole && slot == 1) {
-        // this cluster begins a cut segment: where its pieces end, for the join
+      if (threadIdx.x == 0 && !whole && slot == 1) {
+        // this CTA begins a cut segment: where its pieces end, for the join
         AttnPiece p;
         p.rows = wk.b.rows;
         p.head = wk.h;
@@ -728,7 +680,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       }
       c = a.scale * 1.4426950408889634f;
       if (FP8) c *= 0.0078125f * (a.cache.k_scale != nullptr ? a.cache.k_scale[wk.h] : 1.0f);
-      if (j1 <= j0) return;
+      if (!sees) return;
       seg ^= 1;
       // the queries, D / 8 lanes a row (the last S with the previous ones has landed)
       constexpr int kLanes = D / 8, kStep = kSoftmaxThreads / kLanes;
@@ -791,7 +743,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     if (more) open();
     while (more) {
       float m = -INFINITY, l = 0.0f;
-      if (j1 > j0) {
+      if (sees) {
         float cr = c;
         const int seg_now = seg;
         const int pos = wk.rq.pos0 + tok;
@@ -800,7 +752,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         // keys that every row of the warp sees (rows come in order)
         const int all_hi = __shfl_sync(0xFFFFFFFFu, vis_hi, 0);
         const int all_lo = __shfl_sync(0xFFFFFFFFu, vis_lo, 31);
-        for (int j = j0; j < j1; ++j, ++n) {
+        for (int j = j0; j < stop; ++j, ++n) {
           const uint32_t sb = n & 1u;
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
           // (S follows the arrivals of all that wrote the queries and their factors)
@@ -897,11 +849,10 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         }
       }
       // ---- the next segment's queries, then this one's rows ----
-      const bool seen = j1 > j0, real = row < rows, live = busy, to_out = whole;
+      const bool seen = sees, real = row < rows, live = busy, to_out = whole;
       const int64_t tk_out = tk;
       const int head_out = head;
-      const int64_t at = (2 * static_cast<int64_t>(cluster) + slot) * a.piece_rows +
-                         rank * kTile + row;
+      const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + slot) * kTile + row;
       const float v_scale =
           FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
       const uint32_t end = n - 1;                       // the last tile
@@ -974,7 +925,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       }
       tc_fence_before();
     }
-    if (threadIdx.x == 0 && rank == 0 && !begun) piece->rows = 0;
+    if (threadIdx.x == 0 && !begun) piece->rows = 0;
     tc_fence_before();
     asm volatile("bar.sync 9, %0;" ::"n"(kSoftmaxThreads) : "memory");
     if (bars->spoilt != 0 && st.left > 0) {
@@ -982,21 +933,17 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       wk.load(a, group, st.request);
       wk.h = st.head;
       wk.p = st.block;
-      wk.b = block_of(wk.rq, a.group, a.window, a.piece_rows, wk.p);
+      wk.b = block_of(wk.rq, a.group, a.window, wk.p);
       t = wk.b.t0 + st.tile;
       for (left = st.left; left > 0; t = wk.b.t0) {
         const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
         const bool whole = t == wk.b.t0 && stop == wk.b.t1;
         left -= stop - t;
-        const int t0 = max(t, rank == 0 ? wk.b.a0[0] : wk.b.a0[1]);
-        const int t1 = min(stop, rank == 0 ? wk.b.a1[0] : wk.b.a1[1]);
-        for (int row = warp; row < min(kTile, wk.b.rows - rank * kTile); row += 8) {
+        for (int row = warp; row < wk.b.rows && wk.b.kend > 0; row += 8) {
           const int64_t at =
-              (2 * static_cast<int64_t>(cluster) + (t == wk.b.t0 ? 1 : 0)) * a.piece_rows +
-              rank * kTile + row;
-          if (t1 > t0)
-            mend_row(a, wk.r, wk.h, wk.b.row0 + rank * kTile + row, t0, t1,
-                     whole ? nullptr : a.piece_o + at * D, a.piece_ml + at);
+              (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.b.t0 ? 1 : 0)) * kTile + row;
+          mend_row(a, wk.r, wk.h, wk.b.row0 + row, t, stop, whole ? nullptr : a.piece_o + at * D,
+                   a.piece_ml + at);
         }
         if (left > 0 && !wk.next(a, group)) break;
       }
@@ -1004,44 +951,32 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   }
   __syncthreads();
   drain_after_abort(abort);
-  if (CL > 1) cluster_sync();           // the other CTA may still write here until now
   if (warp == kIssueS) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool FP8, int CL>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int clusters,
+template <int D, bool FP8>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
   using C = Cfg<D, FP8>;
-  auto kernel = attention_chunk_kernel<D, FP8, CL>;
+  auto kernel = attention_chunk_kernel<D, FP8>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
   // its prologue overlaps the plan; it waits for the plan before it reads anything
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CL;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CL * clusters);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, mk, mv);
-}
-
-template <int D, bool FP8>
-cudaError_t launch_cl(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                      int clusters, cudaStream_t stream) {
-  if constexpr (D == 128)
-    if (a.piece_rows > kTile) return launch<D, FP8, 2>(a, mk, mv, clusters, stream);
-  return launch<D, FP8, 1>(a, mk, mv, clusters, stream);
 }
 
 }  // namespace
@@ -1052,12 +987,12 @@ cudaError_t launch_attn_plan(const AttnArgs& a, int grid, cudaStream_t stream) {
 }
 
 cudaError_t launch_attention_chunk(const AttnArgs& a, const CUtensorMap& map_k,
-                                   const CUtensorMap& map_v, int clusters, cudaStream_t stream) {
+                                   const CUtensorMap& map_v, int grid, cudaStream_t stream) {
   if (a.cache.fp8)
-    return a.cache.head_dim == 128 ? launch_cl<128, true>(a, map_k, map_v, clusters, stream)
-                                   : launch_cl<64, true>(a, map_k, map_v, clusters, stream);
-  return a.cache.head_dim == 128 ? launch_cl<128, false>(a, map_k, map_v, clusters, stream)
-                                 : launch_cl<64, false>(a, map_k, map_v, clusters, stream);
+    return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
+                                   : launch<64, true>(a, map_k, map_v, grid, stream);
+  return a.cache.head_dim == 128 ? launch<128, false>(a, map_k, map_v, grid, stream)
+                                 : launch<64, false>(a, map_k, map_v, grid, stream);
 }
 
 }  // namespace nvmoe
