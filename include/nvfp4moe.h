@@ -704,7 +704,10 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  *   s_j = scale * (q . k_j),  lse = log sum_j exp(s_j),
  *   out = sum_j exp(s_j - lse) v_j        (bf16, rounded once)
  * A token that sees no key (negative position) gets out = 0 and lse = -inf.
- * Sums are fp32; exp(s_j - max) is rounded to 16 bits for the product with v.
+ * Sums are fp32; exp(s_j - max) is rounded to 16 bits for the product with v: to
+ * bf16, on an E4M3 cache to fp16, with all 11 bits down to 2^-24 of the largest,
+ * to within 2^-8 down to 2^-27 (smaller ones are off by at most 2^-35 of the
+ * largest).
  * On an E4M3 cache an element of q counts to within 2^-17 of its row's largest
  * (bf16 exactly down to 2^-9 of it).
  *   out         bf16 [tokens, q_heads, head_dim] with strides

@@ -31,7 +31,9 @@
 // E4M3 caches: keys and values are exact in fp16, so the products run in fp16.
 // A query row is scaled by a power of two to a maximum in [1, 2), which keeps
 // every element above 2^-16 of it exact, and the factor goes back in with the
-// softmax scale.  Values arrive as pairs of neighbouring dimensions (ldmatrix
+// softmax scale.  Weights are taken relative to 2^-15 of the running maximum, so
+// that they are at most 2^15 and have all 11 bits of fp16 down to 2^-29 of the largest.
+// Values arrive as pairs of neighbouring dimensions (ldmatrix
 // moves 16-bit units), so one accumulator tile holds the even dimensions and
 // one the odd.
 #include "attn.cuh"
@@ -49,6 +51,9 @@ constexpr int kGroups = FP8 ? 2 : 1;
 template <bool FP8>
 constexpr int kThreads = kGroups<FP8> * kComputeThreads + 32;
 constexpr int kMaxBufs = 16;
+// Powers of two by which a row's reference stands below its running maximum.
+template <bool FP8>
+constexpr float kLift = FP8 ? 15.0f : 0.0f;
 
 template <int D, bool FP8>
 struct Tile {
@@ -471,7 +476,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         const float4 u = mx[0], v = mx[1];
         const float mn =
             fmaxf(fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)),
-                        fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))), m[e]);
+                        fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))) - kLift<FP8>, m[e]);
         const float use = mn == -INFINITY ? 0.0f : mn;   // a row without keys so far
         const float f = exp2_approx(m[e] - use);
         m[e] = mn;
