@@ -265,39 +265,100 @@ __device__ __forceinline__ float lse_of(float m, float sum) {
 }
 
 
-// Query row `row` (of the request's rows for key head h) once more, by one warp
-// and from the cache, if it has come out infinite or NaN: its sums over the keys
-// of the tiles [t0, t1) that it sees.  To the output, or to the piece's row `po`
-// relative to the piece's maximum po_m.
-//
+// ---- values that are not finite ----
 // The kernels multiply whole tiles, in which a key that a row does not see has
 // weight 0, and 0 * inf is not 0.  They note whether any sum is not finite, and if
 // so come here after the last segment.  What a row does see may make it infinite or
-// NaN all the same.  (A test of each partly visible tile before its product cost
+// NaN all the same; only rows with such a value at a key that they do not see are done
+// once more, key by key.  (A test of each partly visible tile before its product cost
 // 5 to 25 % of a chunk; the note costs nothing that shows.)
-inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, int t0,
-                                             int t1, float* po, const float2* po_ml) {
+
+__device__ __forceinline__ float value_at(const void* x, bool fp8, int64_t i) {
+  return fp8 ? e4m3_to_float(static_cast<const uint8_t*>(x)[i])
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
+}
+
+// Element offset of a key (below the request's length) of request r and head h.
+__device__ __forceinline__ int64_t place_of(const AttnArgs& a, int r, int h, int key) {
+  int64_t page = a.batch.page_table[r * a.batch.max_pages + (key >> a.cache.page_shift)];
+  if (page < 0 || page >= a.cache.num_pages) page = 0;      // (has been reported)
+  return page * a.cache.page_stride +
+         (key & ((1 << a.cache.page_shift) - 1)) * a.cache.token_stride + h * a.cache.head_stride;
+}
+
+// Whether some value of the keys [k0, k1) is not finite, by a warp.
+__device__ __forceinline__ bool any_not_finite(const AttnArgs& a, int r, int h, int k0, int k1) {
+  const int lane = threadIdx.x & 31, el = a.cache.fp8 ? 1 : 2;
+  const int chunks = a.cache.head_dim * el / 16;           // 16 bytes each
+  bool bad = false;
+  for (int i = lane; i < (k1 - k0) * chunks; i += 32) {
+    const int key = k0 + i / chunks;
+    const uint4 u = *reinterpret_cast<const uint4*>(
+        static_cast<const uint8_t*>(a.cache.v) + place_of(a, r, h, key) * el + i % chunks * 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (a.cache.fp8)                                     // NaN: 0x7F and a sign
+        bad = bad || (w[k] & 0x7Fu) == 0x7Fu || (w[k] & 0x7F00u) == 0x7F00u ||
+              (w[k] & 0x7F0000u) == 0x7F0000u || (w[k] & 0x7F000000u) == 0x7F000000u;
+      else
+        bad = bad || (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+    }
+  }
+  return __any_sync(0xFFFFFFFFu, bad);
+}
+
+// Query row `row` (of the request's rows for key head h) once more, by one warp
+// and from the cache, if an element of it has come out infinite or NaN that is so at
+// a hidden key: its sums over the keys of [k0, k1), of which it sees a part.  To the
+// output, or to the piece's row `po` relative to the piece's maximum po_ml->x.
+inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, int k0,
+                                             int k1, float* po, const float2* po_ml) {
   const int lane = threadIdx.x & 31, D = a.cache.head_dim;
   const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
   const int tok = a.group(row), pos = rq.pos0 + tok;
   const int head = h * static_cast<int>(a.group.d) + row - tok * static_cast<int>(a.group.d);
-  const int all_lo = t0 * kAttnTileKeys, all_hi = min(t1 * kAttnTileKeys, rq.len);
-  const int lo = a.window > 0 ? max(all_lo, pos - a.window + 1) : all_lo;
-  const int hi = min(all_hi, pos + 1);
+  const int lo = a.window > 0 ? min(k1, max(k0, pos - a.window + 1)) : k0;
+  const int hi = max(lo, min(k1, pos + 1));
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
                        (rq.first + tok) * a.out.token_stride + head * a.out.head_stride;
-  bool bad = false;
-  for (int d = lane; d < D; d += 32)
-    bad = bad || !isfinite(po != nullptr ? po[d] : __bfloat162float(out[d]));
-  if (!__any_sync(0xFFFFFFFFu, bad) || (lo == all_lo && hi == all_hi)) return;
+  // this lane's elements that are to be explained: bit i is dimension lane + 32 i
+  uint32_t open = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 32 < D) {
+      const int d = lane + i * 32;
+      if (!isfinite(po != nullptr ? po[d] : __bfloat162float(out[d]))) open |= 1u << i;
+    }
+  if (!__any_sync(0xFFFFFFFFu, open != 0)) return;
+  // those with a hidden value that is not finite (few keys are hidden: rows of a block
+  // lie within 128 positions) ...
+  uint32_t hidden = 0;
+  const auto scan = [&](int from, int to, bool nan_only) {
+    uint32_t found = 0;
+#pragma unroll 4
+    for (int key = from; key < to; ++key) {
+      const int64_t at = place_of(a, r, h, key) + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * 32 < D) {
+          const float x = value_at(a.cache.v, a.cache.fp8, at + i * 32);
+          if (nan_only ? isnan(x) : !isfinite(x)) found |= 1u << i;
+        }
+    }
+    return found;
+  };
+  hidden = open & (scan(k0, lo, false) | scan(hi, k1, false));
+  if (!__any_sync(0xFFFFFFFFu, hidden != 0)) return;
+  // ... and no NaN at a key that the row does see: that one stays, whatever its weight
+  // (looked for where NaN stand side by side, next to the hidden ones)
+  hidden &= ~(scan(lo, min(hi, lo + kAttnTileKeys), true) |
+              scan(max(lo, hi - kAttnTileKeys), hi, true));
+  if (!__any_sync(0xFFFFFFFFu, hidden != 0)) return;
 
   float c = a.scale * 1.4426950408889634f, v_scale = 1.0f;
   if (a.cache.fp8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[h];
   if (a.cache.fp8 && a.cache.v_scale != nullptr) v_scale = a.cache.v_scale[h];
-  const auto load = [&](const void* x, int64_t i) {
-    return a.cache.fp8 ? e4m3_to_float(static_cast<const uint8_t*>(x)[i])
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
-  };
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) +
                            (rq.first + tok) * a.q.token_stride + head * a.q.head_stride;
   float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
@@ -305,14 +366,10 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
   for (int key0 = lo; key0 < hi; key0 += 32) {
     // a lane's key: its place and its weight
     const int key = min(key0 + lane, hi - 1);
-    int64_t page = a.batch.page_table[r * a.batch.max_pages + (key >> a.cache.page_shift)];
-    if (page < 0 || page >= a.cache.num_pages) page = 0;    // (has been reported)
-    const int64_t at = page * a.cache.page_stride +
-                       (key & ((1 << a.cache.page_shift) - 1)) * a.cache.token_stride +
-                       h * a.cache.head_stride;
+    const int64_t at = place_of(a, r, h, key);
     float s = 0.0f;
 #pragma unroll 8
-    for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), load(a.cache.k, at + d), s);
+    for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), value_at(a.cache.k, a.cache.fp8, at + d), s);
     s = key0 + lane < hi ? s * c : -INFINITY;
     float mn = fmaxf(m, s);
 #pragma unroll
@@ -330,7 +387,7 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
       const int64_t v = __shfl_sync(0xFFFFFFFFu, at, k) + lane;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i * 32 < D) o[i] = fmaf(wk, load(a.cache.v, v + i * 32), o[i]);
+        if (i * 32 < D) o[i] = fmaf(wk, value_at(a.cache.v, a.cache.fp8, v + i * 32), o[i]);
     }
   }
 #pragma unroll
@@ -344,6 +401,27 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
       if (po != nullptr) po[d] = o[i] * y;
       else out[d] = __float2bfloat16_rn(o[i] * y);
     }
+}
+
+// The rows [row0, row0 + rows) of a segment, of which some sum may not be finite: one
+// of `warps` warps (this one is `warp`).  [kbeg, kend): keys that any of them sees;
+// [t0, t1): the tiles that have been taken.  po, po_ml: the piece's first row, or po null.
+inline __device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, int row0, int rows,
+                                              int kbeg, int kend, int t0, int t1, float* po,
+                                              const float2* po_ml, int warp, int warps) {
+  const int k0 = max(t0 * kAttnTileKeys, kbeg), k1 = min(t1 * kAttnTileKeys, kend);
+  if (rows <= 0 || k1 <= k0) return;
+  // keys that one of the rows does not see: before the last row's window, after the
+  // first row's position
+  const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
+  const int first = rq.pos0 + a.group(row0), last = rq.pos0 + a.group(row0 + rows - 1);
+  const int lo = a.window > 0 ? min(k1, max(k0, last - a.window + 1)) : k0;
+  const int hi = min(k1, max(k0, first + 1));
+  if (!any_not_finite(a, r, h, k0, lo) && !any_not_finite(a, r, h, hi, k1)) return;
+  for (int row = warp; row < rows; row += warps)
+    mend_row(a, r, h, row0 + row, k0, k1,
+             po != nullptr ? po + static_cast<int64_t>(row) * a.cache.head_dim : nullptr,
+             po_ml + row);
 }
 
 }  // namespace nvmoe

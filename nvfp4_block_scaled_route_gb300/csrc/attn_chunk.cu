@@ -951,12 +951,11 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
         const bool whole = t == wk.b.t0 && stop == wk.b.t1;
         left -= stop - t;
-        for (int row = warp; row < wk.b.rows && wk.b.kend > 0; row += 8) {
-          const int64_t at =
-              (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.b.t0 ? 1 : 0)) * kTile + row;
-          mend_row(a, wk.r, wk.h, wk.b.row0 + row, t, stop, whole ? nullptr : a.piece_o + at * D,
-                   a.piece_ml + at);
-        }
+        const int64_t at =
+            (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.b.t0 ? 1 : 0)) * kTile;
+        mend_rows(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
+                  whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp,
+                  kSoftmaxThreads / 32);
         if (left > 0 && !wk.next(a, group)) break;
       }
     }

@@ -700,11 +700,12 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const int stop = static_cast<int>(min(static_cast<long long>(wk.sp.t1), t + left));
     const bool whole = t == wk.sp.t0 && stop == wk.sp.t1;
     left -= stop - t;
-    for (int row = warp; row < wk.rq.n * group; row += kG * kComputeWarps) {
-      const int64_t at =
-          (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows + row;
-      mend_row(a, wk.r, wk.h, row, t, stop, whole ? nullptr : a.piece_o + at * D, a.piece_ml + at);
-    }
+    const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
+    const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
+    const int64_t at =
+        (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows;
+    mend_rows(a, wk.r, wk.h, 0, wk.rq.n * group, kbeg, kend, t, stop,
+              whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp, kG * kComputeWarps);
     if (left > 0 && !wk.next_segment(a)) break;
   }
 }

@@ -115,3 +115,87 @@ def test_paged_attention_large_scores_e4m3(nb, hq, D, n):
     _within(out, want, b_out + 2 * extra[..., None] * v.abs().max() + 700 * 2.0 ** -35 * v.abs().max(),
             "out")
     _within(lse, wlse, b_lse + extra, "lse")
+
+
+# ------------------------------------------------- values that are not finite --
+def _timed(f):
+    f()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    best = math.inf
+    for _ in range(3):
+        start.record()
+        f()
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end))
+    return best
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,prior,hq,hk,D", [(1, 1024, 1200, 32, 4, 128), (4, 1000, 0, 8, 8, 64),
+                                               (160, 2, 6000, 16, 2, 128)])
+def test_paged_attention_visible_nan_costs_little(nb, B, n, prior, hq, hk, D, fp8):
+    """A NaN in a value that every row sees makes that element NaN in every row and leaves
+    the others as they were, bit for bit.  No row has to be done once more for it, so the
+    call takes about as long as without it: at most twice the time and 0.2 ms."""
+    L, page = n + prior, 64
+    pages = -(-L // page)
+    g = torch.Generator(device=DEV).manual_seed(n)
+    k, v = (torch.randn(pages, page, hk, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    if fp8:
+        k, v = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
+    q = torch.randn(B * n, hq, D, generator=g, device=DEV).bfloat16()
+    cache = nb.PagedKVCache(k, v)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    batch = nb.AttnBatch(n * torch.arange(B + 1, dtype=torch.int32, device=DEV), _i32(*[L] * B), table,
+                         max_new=n)
+    ws = nb.paged_attention_workspace(cache, batch, hq, B * n)
+    out = torch.empty_like(q)
+
+    def call():
+        nb.paged_attention(q, cache, batch, out=out, ws=ws)
+    clean_ms = _timed(call)
+    clean = out.clone()
+    at = v.view(torch.uint8)[0, 0, :, 9] if fp8 else v[0, 0, :, 9]
+    at.fill_(0x7F if fp8 else math.nan)
+    nan_ms = _timed(call)
+    assert nb.read_status(ws) == 0
+    assert out[..., 9].isnan().all()
+    rest = [i for i in range(D) if i != 9]
+    assert torch.equal(out[..., rest], clean[..., rest]) and clean.isfinite().all()
+    assert nan_ms < 2 * clean_ms + 0.2, (clean_ms, nan_ms)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n,hq,hk,D", [(4, 4, 1, 128), (70, 4, 2, 64), (150, 6, 1, 128)])
+def test_paged_attention_visible_and_hidden_nan(nb, n, hq, hk, D, fp8):
+    """The same element NaN in a key that all rows see and in one that some do not, and
+    another element NaN only where some rows do not see it: each row's output is NaN just
+    where a key that it sees is."""
+    L = n + 200
+    case = Paged([(n, L)], hk, D, 16, fp8=fp8, seed=51)
+    nan = math.nan
+
+    def put(j, d, value):
+        p, o = int(case.table[0, j // 16]), j % 16
+        x = case.v[p, o].float()
+        x[:, d] = value
+        case.v[p, o] = x.to(case.v.dtype)
+    put(7, 3, nan)                       # everyone
+    put(L - 1, 3, nan)                   # the last token alone sees this one,
+    put(L - 1, 8, nan)                   # and this one
+    put(L - 1 - n // 2, 20, nan)         # the later half
+    q = torch.randn(n, hq, D, generator=torch.Generator().manual_seed(2)).bfloat16()
+    cache, batch = case.handles(nb)
+    ws = nb.paged_attention_workspace(cache, batch, hq, n)
+    for _ in range(2):
+        out = nb.paged_attention(q.to(DEV), cache, batch, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    want, _, bound, _ = case.reference(q)
+    got = out.double().cpu()
+    fine = want.isfinite()
+    assert not fine[..., 3].any() and fine[0, :, 8].all() and not fine[-1, :, 8].any()
+    assert torch.equal(got.isfinite(), fine)
+    over = (got - want).abs()[fine] - bound[fine]
+    assert (over <= 0).all(), over.max()
