@@ -278,10 +278,11 @@ __device__ __forceinline__ float value_at(const void* x, bool fp8, int64_t i) {
              : __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
 }
 
-// Element offset of a key (below the request's length) of request r and head h.
+// Element offset of a key (below the request's length) of request r and head h; -1 in
+// a page out of range, which has been reported and reads as zeros.
 __device__ __forceinline__ int64_t place_of(const AttnArgs& a, int r, int h, int key) {
-  int64_t page = a.batch.page_table[r * a.batch.max_pages + (key >> a.cache.page_shift)];
-  if (page < 0 || page >= a.cache.num_pages) page = 0;      // (has been reported)
+  const int64_t page = a.batch.page_table[r * a.batch.max_pages + (key >> a.cache.page_shift)];
+  if (page < 0 || page >= a.cache.num_pages) return -1;
   return page * a.cache.page_stride +
          (key & ((1 << a.cache.page_shift) - 1)) * a.cache.token_stride + h * a.cache.head_stride;
 }
@@ -293,8 +294,10 @@ __device__ __forceinline__ bool any_not_finite(const AttnArgs& a, int r, int h, 
   bool bad = false;
   for (int i = lane; i < (k1 - k0) * chunks; i += 32) {
     const int key = k0 + i / chunks;
-    const uint4 u = *reinterpret_cast<const uint4*>(
-        static_cast<const uint8_t*>(a.cache.v) + place_of(a, r, h, key) * el + i % chunks * 16);
+    const int64_t at = place_of(a, r, h, key);
+    if (at < 0) continue;
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.cache.v) +
+                                                    at * el + i % chunks * 16);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -338,11 +341,12 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
     uint32_t found = 0;
 #pragma unroll 4
     for (int key = from; key < to; ++key) {
-      const int64_t at = place_of(a, r, h, key) + lane;
+      const int64_t at = place_of(a, r, h, key);
+      if (at < 0) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i * 32 < D) {
-          const float x = value_at(a.cache.v, a.cache.fp8, at + i * 32);
+          const float x = value_at(a.cache.v, a.cache.fp8, at + lane + i * 32);
           if (nan_only ? isnan(x) : !isfinite(x)) found |= 1u << i;
         }
     }
@@ -368,8 +372,10 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
     const int key = min(key0 + lane, hi - 1);
     const int64_t at = place_of(a, r, h, key);
     float s = 0.0f;
+    if (at >= 0)
 #pragma unroll 8
-    for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), value_at(a.cache.k, a.cache.fp8, at + d), s);
+      for (int d = 0; d < D; ++d)
+        s = fmaf(__bfloat162float(q[d]), value_at(a.cache.k, a.cache.fp8, at + d), s);
     s = key0 + lane < hi ? s * c : -INFINITY;
     float mn = fmaxf(m, s);
 #pragma unroll
@@ -384,10 +390,11 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
 #pragma unroll 1
     for (int k = 0; k < min(32, hi - key0); ++k) {
       const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-      const int64_t v = __shfl_sync(0xFFFFFFFFu, at, k) + lane;
+      const int64_t v = __shfl_sync(0xFFFFFFFFu, at, k);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i * 32 < D) o[i] = fmaf(wk, value_at(a.cache.v, a.cache.fp8, v + i * 32), o[i]);
+        if (i * 32 < D && v >= 0)
+          o[i] = fmaf(wk, value_at(a.cache.v, a.cache.fp8, v + lane + i * 32), o[i]);
     }
   }
 #pragma unroll

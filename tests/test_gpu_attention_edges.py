@@ -199,3 +199,34 @@ def test_paged_attention_visible_and_hidden_nan(nb, n, hq, hk, D, fp8):
     assert torch.equal(got.isfinite(), fine)
     over = (got - want).abs()[fine] - bound[fine]
     assert (over <= 0).all(), over.max()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [4, 60])
+def test_paged_attention_bad_page_beside_a_hidden_nan(nb, n, fp8):
+    """A page id out of range reads as zeros in rows that are done once more, too."""
+    L, D, hq = 200, 128, 4
+    case = Paged([(n, L)], 1, D, 16, fp8=fp8, seed=61)
+    # (page 9, whose id is bad, lies in the same 128 keys)
+    p, o = int(case.table[0, (L - 1) // 16]), (L - 1) % 16
+    x = case.v[p, o].float()
+    x[:, 5] = math.nan                   # the last token alone sees it
+    case.v[p, o] = x.to(case.v.dtype)
+    cache, batch = case.handles(nb)
+    batch.page_table[0, 9] = case.k.shape[0] + 7
+    q = torch.randn(n, hq, D, generator=torch.Generator().manual_seed(3)).bfloat16()
+    ws = nb.paged_attention_workspace(cache, batch, hq, n)
+    out = nb.paged_attention(q.to(DEV), cache, batch, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == BAD_INDEX
+    case.table[0, 9] = case.k.shape[0]
+
+    def with_zeros(c):
+        return torch.cat([c.view(torch.uint8), torch.zeros_like(c[:1].view(torch.uint8))]).view(c.dtype)
+    case.k, case.v = with_zeros(case.k), with_zeros(case.v)
+    want, _, bound, _ = case.reference(q)
+    got = out.double().cpu()
+    fine = want.isfinite()
+    assert torch.equal(got.isfinite(), fine) and fine[:-1].all()
+    over = (got - want).abs()[fine] - bound[fine]
+    assert (over <= 0).all(), over.max()
