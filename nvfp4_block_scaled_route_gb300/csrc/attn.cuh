@@ -273,9 +273,72 @@ __device__ __forceinline__ float lse_of(float m, float sum) {
 // once more, key by key.  (A test of each partly visible tile before its product cost
 // 5 to 25 % of a chunk; the note costs nothing that shows.)
 
-__device__ __forceinline__ float value_at(const void* x, bool fp8, int64_t i) {
-  return fp8 ? e4m3_to_float(static_cast<const uint8_t*>(x)[i])
-             : __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
+// This lane's D / 32 neighbouring elements of the cache row at element offset `at`;
+// zeros for a row that is not there (-1).
+template <int D, bool FP8>
+__device__ __forceinline__ void load_part(const void* base, int64_t at, float (&x)[D / 32]) {
+  constexpr int kPer = D / 32;
+  if (at < 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
+    return;
+  }
+  at += (threadIdx.x & 31) * kPer;
+  if constexpr (FP8) {
+    uint32_t u;
+    if constexpr (kPer == 4) u = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + at);
+    else u = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = e4m3_to_float((u >> (8 * i)) & 0xFFu);
+  } else {
+    const uint32_t* p =
+        reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(base) + at);
+    uint32_t u[kPer / 2];
+    if constexpr (kPer == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      u[0] = v.x;
+      u[kPer / 2 - 1] = v.y;
+    } else {
+      u[0] = *p;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      x[i] = __uint_as_float(u[i / 2] << 16);
+      x[i + 1] = __uint_as_float(u[i / 2] & 0xFFFF0000u);
+    }
+  }
+}
+
+// Dot product of the bf16 row q and the cache row at element offset `at`.
+template <int D, bool FP8>
+__device__ __forceinline__ float dot_of(const __nv_bfloat16* q, const void* base, int64_t at) {
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll 4
+  for (int d = 0; d < D; d += 16) {
+    float x[16], k[16];
+    bf16x8_to_float(*reinterpret_cast<const uint4*>(q + d), reinterpret_cast<float (&)[8]>(x[0]));
+    bf16x8_to_float(*reinterpret_cast<const uint4*>(q + d + 8),
+                    reinterpret_cast<float (&)[8]>(x[8]));
+    if constexpr (FP8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at + d);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const uint32_t h = e4m3x2_to_f16x2(w[i >> 2] >> ((i & 2) * 8));
+        const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
+        k[i] = f.x;
+        k[i + 1] = f.y;
+      }
+    } else {
+      const uint4* p =
+          reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at + d);
+      bf16x8_to_float(p[0], reinterpret_cast<float (&)[8]>(k[0]));
+      bf16x8_to_float(p[1], reinterpret_cast<float (&)[8]>(k[8]));
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i & 1] = fmaf(x[i], k[i], s[i & 1]);
+  }
+  return s[0] + s[1];
 }
 
 // Element offset of a key (below the request's length) of request r and head h; -1 in
@@ -288,9 +351,10 @@ __device__ __forceinline__ int64_t place_of(const AttnArgs& a, int r, int h, int
 }
 
 // Whether some value of the keys [k0, k1) is not finite, by a warp.
+template <int D, bool FP8>
 __device__ __forceinline__ bool any_not_finite(const AttnArgs& a, int r, int h, int k0, int k1) {
-  const int lane = threadIdx.x & 31, el = a.cache.fp8 ? 1 : 2;
-  const int chunks = a.cache.head_dim * el / 16;           // 16 bytes each
+  constexpr int el = FP8 ? 1 : 2, chunks = D * el / 16;    // 16 bytes each
+  const int lane = threadIdx.x & 31;
   bool bad = false;
   for (int i = lane; i < (k1 - k0) * chunks; i += 32) {
     const int key = k0 + i / chunks;
@@ -301,7 +365,7 @@ __device__ __forceinline__ bool any_not_finite(const AttnArgs& a, int r, int h, 
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (a.cache.fp8)                                     // NaN: 0x7F and a sign
+      if (FP8)                                             // NaN: 0x7F and a sign
         bad = bad || (w[k] & 0x7Fu) == 0x7Fu || (w[k] & 0x7F00u) == 0x7F00u ||
               (w[k] & 0x7F0000u) == 0x7F0000u || (w[k] & 0x7F000000u) == 0x7F000000u;
       else
@@ -315,68 +379,60 @@ __device__ __forceinline__ bool any_not_finite(const AttnArgs& a, int r, int h, 
 // and from the cache, if an element of it has come out infinite or NaN that is so at
 // a hidden key: its sums over the keys of [k0, k1), of which it sees a part.  To the
 // output, or to the piece's row `po` relative to the piece's maximum po_ml->x.
-inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, int k0,
-                                             int k1, float* po, const float2* po_ml) {
-  const int lane = threadIdx.x & 31, D = a.cache.head_dim;
+template <int D, bool FP8>
+__device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, int k0, int k1,
+                                      float* po, const float2* po_ml) {
+  constexpr int kPer = D / 32;                             // a lane's elements
+  const int lane = threadIdx.x & 31;
   const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
   const int tok = a.group(row), pos = rq.pos0 + tok;
   const int head = h * static_cast<int>(a.group.d) + row - tok * static_cast<int>(a.group.d);
   const int lo = a.window > 0 ? min(k1, max(k0, pos - a.window + 1)) : k0;
   const int hi = max(lo, min(k1, pos + 1));
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
-                       (rq.first + tok) * a.out.token_stride + head * a.out.head_stride;
-  // this lane's elements that are to be explained: bit i is dimension lane + 32 i
-  uint32_t open = 0;
+                       (rq.first + tok) * a.out.token_stride + head * a.out.head_stride +
+                       lane * kPer;
+  if (po != nullptr) po += lane * kPer;
+  uint32_t open = 0;                                       // bits: to be explained
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i * 32 < D) {
-      const int d = lane + i * 32;
-      if (!isfinite(po != nullptr ? po[d] : __bfloat162float(out[d]))) open |= 1u << i;
-    }
+  for (int i = 0; i < kPer; ++i)
+    if (!isfinite(po != nullptr ? po[i] : __bfloat162float(out[i]))) open |= 1u << i;
   if (!__any_sync(0xFFFFFFFFu, open != 0)) return;
   // those with a hidden value that is not finite (few keys are hidden: rows of a block
   // lie within 128 positions) ...
-  uint32_t hidden = 0;
   const auto scan = [&](int from, int to, bool nan_only) {
     uint32_t found = 0;
 #pragma unroll 4
     for (int key = from; key < to; ++key) {
-      const int64_t at = place_of(a, r, h, key);
-      if (at < 0) continue;
+      float x[kPer];
+      load_part<D, FP8>(a.cache.v, place_of(a, r, h, key), x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i * 32 < D) {
-          const float x = value_at(a.cache.v, a.cache.fp8, at + lane + i * 32);
-          if (nan_only ? isnan(x) : !isfinite(x)) found |= 1u << i;
-        }
+      for (int i = 0; i < kPer; ++i)
+        if (nan_only ? isnan(x[i]) : !isfinite(x[i])) found |= 1u << i;
     }
     return found;
   };
-  hidden = open & (scan(k0, lo, false) | scan(hi, k1, false));
-  if (!__any_sync(0xFFFFFFFFu, hidden != 0)) return;
+  open &= scan(k0, lo, false) | scan(hi, k1, false);
+  if (!__any_sync(0xFFFFFFFFu, open != 0)) return;
   // ... and no NaN at a key that the row does see: that one stays, whatever its weight
   // (looked for where NaN stand side by side, next to the hidden ones)
-  hidden &= ~(scan(lo, min(hi, lo + kAttnTileKeys), true) |
-              scan(max(lo, hi - kAttnTileKeys), hi, true));
-  if (!__any_sync(0xFFFFFFFFu, hidden != 0)) return;
+  open &= ~(scan(lo, min(hi, lo + kAttnTileKeys), true) |
+            scan(max(lo, hi - kAttnTileKeys), hi, true));
+  if (!__any_sync(0xFFFFFFFFu, open != 0)) return;
 
   float c = a.scale * 1.4426950408889634f, v_scale = 1.0f;
-  if (a.cache.fp8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[h];
-  if (a.cache.fp8 && a.cache.v_scale != nullptr) v_scale = a.cache.v_scale[h];
+  if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[h];
+  if (FP8 && a.cache.v_scale != nullptr) v_scale = a.cache.v_scale[h];
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) +
                            (rq.first + tok) * a.q.token_stride + head * a.q.head_stride;
-  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
+  float o[kPer] = {}, m = -INFINITY, l = 0.0f;
 #pragma unroll 1
   for (int key0 = lo; key0 < hi; key0 += 32) {
     // a lane's key: its place and its weight
-    const int key = min(key0 + lane, hi - 1);
-    const int64_t at = place_of(a, r, h, key);
-    float s = 0.0f;
-    if (at >= 0)
-#pragma unroll 8
-      for (int d = 0; d < D; ++d)
-        s = fmaf(__bfloat162float(q[d]), value_at(a.cache.k, a.cache.fp8, at + d), s);
-    s = key0 + lane < hi ? s * c : -INFINITY;
+    const bool mine = lane < hi - key0;
+    const int64_t at = mine ? place_of(a, r, h, key0 + lane) : -1;
+    float s = at >= 0 ? dot_of<D, FP8>(q, a.cache.k, at) : 0.0f;
+    s = mine ? s * c : -INFINITY;
     float mn = fmaxf(m, s);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, k));
@@ -385,16 +441,19 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
     m = mn;
     l = l * f + w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= f;
+    for (int i = 0; i < kPer; ++i) o[i] *= f;
     // the lanes' dimensions
-#pragma unroll 1
-    for (int k = 0; k < min(32, hi - key0); ++k) {
-      const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-      const int64_t v = __shfl_sync(0xFFFFFFFFu, at, k);
+    for (int k = 0; k < 32; k += 8) {
+      float wk[8], x[8][kPer];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i * 32 < D && v >= 0)
-          o[i] = fmaf(wk, value_at(a.cache.v, a.cache.fp8, v + lane + i * 32), o[i]);
+      for (int j = 0; j < 8; ++j) {
+        wk[j] = __shfl_sync(0xFFFFFFFFu, w, k + j);
+        load_part<D, FP8>(a.cache.v, __shfl_sync(0xFFFFFFFFu, at, k + j), x[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] = fmaf(wk[j], x[j][i], o[i]);
     }
   }
 #pragma unroll
@@ -402,20 +461,19 @@ inline __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, in
   const float y = po != nullptr ? (m == -INFINITY ? 0.0f : exp2_approx(m - po_ml->x))
                                 : (l == 0.0f ? 0.0f : v_scale / l);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i * 32 < D) {
-      const int d = lane + i * 32;
-      if (po != nullptr) po[d] = o[i] * y;
-      else out[d] = __float2bfloat16_rn(o[i] * y);
-    }
+  for (int i = 0; i < kPer; ++i) {
+    if (po != nullptr) po[i] = o[i] * y;
+    else out[i] = __float2bfloat16_rn(o[i] * y);
+  }
 }
 
 // The rows [row0, row0 + rows) of a segment, of which some sum may not be finite: one
 // of `warps` warps (this one is `warp`).  [kbeg, kend): keys that any of them sees;
 // [t0, t1): the tiles that have been taken.  po, po_ml: the piece's first row, or po null.
-inline __device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, int row0, int rows,
-                                              int kbeg, int kend, int t0, int t1, float* po,
-                                              const float2* po_ml, int warp, int warps) {
+template <int D, bool FP8>
+__device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, int row0, int rows,
+                                       int kbeg, int kend, int t0, int t1, float* po,
+                                       const float2* po_ml, int warp, int warps) {
   const int k0 = max(t0 * kAttnTileKeys, kbeg), k1 = min(t1 * kAttnTileKeys, kend);
   if (rows <= 0 || k1 <= k0) return;
   // keys that one of the rows does not see: before the last row's window, after the
@@ -424,11 +482,10 @@ inline __device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, i
   const int first = rq.pos0 + a.group(row0), last = rq.pos0 + a.group(row0 + rows - 1);
   const int lo = a.window > 0 ? min(k1, max(k0, last - a.window + 1)) : k0;
   const int hi = min(k1, max(k0, first + 1));
-  if (!any_not_finite(a, r, h, k0, lo) && !any_not_finite(a, r, h, hi, k1)) return;
+  if (!any_not_finite<D, FP8>(a, r, h, k0, lo) && !any_not_finite<D, FP8>(a, r, h, hi, k1)) return;
   for (int row = warp; row < rows; row += warps)
-    mend_row(a, r, h, row0 + row, k0, k1,
-             po != nullptr ? po + static_cast<int64_t>(row) * a.cache.head_dim : nullptr,
-             po_ml + row);
+    mend_row<D, FP8>(a, r, h, row0 + row, k0, k1,
+                     po != nullptr ? po + static_cast<int64_t>(row) * D : nullptr, po_ml + row);
 }
 
 }  // namespace nvmoe

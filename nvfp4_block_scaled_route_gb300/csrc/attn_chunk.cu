@@ -953,7 +953,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         left -= stop - t;
         const int64_t at =
             (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.b.t0 ? 1 : 0)) * kTile;
-        mend_rows(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
+        mend_rows<D, FP8>(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
                   whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp,
                   kSoftmaxThreads / 32);
         if (left > 0 && !wk.next(a, group)) break;

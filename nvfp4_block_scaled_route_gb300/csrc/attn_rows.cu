@@ -704,7 +704,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
     const int64_t at =
         (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows;
-    mend_rows(a, wk.r, wk.h, 0, wk.rq.n * group, kbeg, kend, t, stop,
+    mend_rows<D, FP8>(a, wk.r, wk.h, 0, wk.rq.n * group, kbeg, kend, t, stop,
               whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp, kG * kComputeWarps);
     if (left > 0 && !wk.next_segment(a)) break;
   }

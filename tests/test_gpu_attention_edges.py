@@ -230,3 +230,49 @@ def test_paged_attention_bad_page_beside_a_hidden_nan(nb, n, fp8):
     assert torch.equal(got.isfinite(), fine) and fine[:-1].all()
     over = (got - want).abs()[fine] - bound[fine]
     assert (over <= 0).all(), over.max()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_paged_attention_hidden_nan_in_a_long_chunk(nb, D, fp8):
+    """A NaN at the last key, which the last token alone sees: the other rows of its block
+    are done once more, 16 by each warp.  They come out as without it, and in at most
+    0.2 us a row and key."""
+    n, prior, hq, hk, page = 1024, 4096, 56, 8, 64
+    L = n + prior
+    g = torch.Generator(device=DEV).manual_seed(D)
+    k, v = (torch.randn(L // page, page, hk, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    if fp8:
+        k, v = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
+    q = torch.randn(n, hq, D, generator=g, device=DEV).bfloat16()
+    cache = nb.PagedKVCache(k, v)
+    batch = nb.AttnBatch(_i32(0, n), _i32(L),
+                         torch.arange(L // page, dtype=torch.int32, device=DEV)[None], max_new=n)
+    ws = nb.paged_attention_workspace(cache, batch, hq, n)
+    out = torch.empty_like(q)
+
+    def call():
+        nb.paged_attention(q, cache, batch, out=out, ws=ws)
+    clean_ms = _timed(call)
+    clean = out.clone()
+    (v.view(torch.uint8) if fp8 else v)[-1, -1, :, 9].fill_(0x7F if fp8 else math.nan)
+    nan_ms = _timed(call)
+    assert nb.read_status(ws) == 0
+    assert out[-1, :, 9].isnan().all()
+    rest = [i for i in range(D) if i != 9]
+    assert torch.equal(out[:-128], clean[:-128]) and torch.equal(out[-1][:, rest], clean[-1][:, rest])
+    # rows done once more have other roundings: two of bf16 and of 16-bit weights
+    flat = lambda t: t.flatten(0, 1)[:L]                   # noqa: E731
+    for h in (0, hq - 1):
+        x = q[-128:-1, h].double()
+        kk, vv = flat(k)[:, h // 7].double(), flat(v)[:, h // 7].double()
+        s = (x @ kk.T * D ** -0.5).masked_fill(
+            torch.arange(L, device=DEV) > torch.arange(L - 128, L - 1, device=DEV)[:, None], -math.inf)
+        p = torch.softmax(s, 1)[:, :-1]
+        want, ev = p @ vv[:-1], p @ vv[:-1].abs()
+        ds = (x.abs() @ kk.abs().T * D ** -0.5).amax(1, True) * (D + 8) * 2.0 ** -23
+        extra = D ** -0.5 * 2.0 ** -17 * x.abs().amax(1, True) * kk.abs().sum(1).max() if fp8 else 0.0
+        over = (out[-128:-1, h].double() - want).abs() - (
+            (ref.U + 2 * (ds + extra) + 2.0 ** -18) * ev + ref.U * want.abs())
+        assert (over <= 0).all(), over.max()
+    assert nan_ms < 2 * clean_ms + 16 * L * 0.2e-3, (clean_ms, nan_ms)
