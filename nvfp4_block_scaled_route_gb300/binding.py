@@ -4,9 +4,16 @@ Every computation runs in the library's CUDA kernels; this module allocates
 device buffers with PyTorch, passes raw pointers and the current CUDA stream,
 and turns nonzero status codes into exceptions.  There is no fallback: if
 the library is missing or was not built, ``lib()`` raises.
+
+Calls run on the current stream, or on `stream`; inputs have to be ready there.
+Buffers that a call makes (outputs and a workspace that were not given) belong to
+the stream that it runs on, as if it had been made current.  What a kernel finds
+wrong (an index out of range) is recorded in the workspace: pass one as `ws` to
+read it afterwards (read_status).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -169,9 +176,26 @@ def rows_bound(T: int, k: int, E: int) -> int:
     return int(lib().moe_route_rows_bound(T, k, E))
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    ws = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-    return ws
+_here = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where the buffers that a call makes are allocated and zeroed: on the stream
+    that it runs on, so that they are ordered with its kernels there, and their
+    memory goes back to that stream's pool."""
+    return _here if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    if stream is None:                # (no context: it costs as much as a small launch)
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    with _on(stream):
+        return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def read_status(ws: torch.Tensor, stream=None) -> int:
@@ -192,8 +216,9 @@ def fp4_mma_probe(variant: int, iters: int, grid: int, repeats: int = 3, device=
     events on that stream.  Returns a dict: best-launch TFLOP/s, the median
     cycles per MMA of the issuing CTAs, the launch times (ms) and the status."""
     dev = torch.device(device if device is not None else "cuda")
-    cycles = torch.zeros(grid, dtype=torch.int64, device=dev)
-    ws = _workspace(256, dev)
+    with _on(stream):
+        cycles = torch.zeros(grid, dtype=torch.int64, device=dev)
+    ws = _workspace(256, dev, stream)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     N = 128 if variant & PROBE_N128 else 256
     flops = float(grid) * iters * 2.0 * 128 * N * 64
@@ -235,13 +260,11 @@ def route_permute(topk_ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = N
     dev = topk_ids.device
     rows = rows_bound(T, k, E)
     if out is None:
-        out = Route(torch.empty(E + 1, dtype=torch.int32, device=dev),
-                    torch.empty(E, dtype=torch.int32, device=dev),
-                    torch.empty(max(rows, 1), dtype=torch.int32, device=dev),
-                    torch.empty(max(T * k, 1), dtype=torch.int32, device=dev), rows, T, k, E)
+        out = Route(*(_empty(n, torch.int32, dev, stream)
+                      for n in (E + 1, E, max(rows, 1), max(T * k, 1))), rows, T, k, E)
     need = int(lib().moe_route_workspace_size(T, k, E))
     if ws is None:
-        ws = _workspace(need, dev)
+        ws = _workspace(need, dev, stream)
     _check("moe_route_permute", lib().moe_route_permute(
         _ptr(topk_ids), T, k, E, _ptr(out.expert_offsets), _ptr(out.expert_counts),
         _ptr(out.row_token), _ptr(out.slot_of), _ptr(ws), ws.numel(), _stream(stream)))
@@ -261,14 +284,15 @@ def quantize_act(x: torch.Tensor, row_dst: Optional[torch.Tensor] = None, fanout
         out_rows = rows
     dev = x.device
     if out is None:
-        q = torch.empty((out_rows, cols // 2), dtype=torch.uint8, device=dev)
-        sf_row = torch.empty((out_rows, cols // 16), dtype=torch.uint8, device=dev) if rowmajor_sf else None
-        sf_mma = torch.zeros(sf_mma_bytes(out_rows, cols), dtype=torch.uint8, device=dev) if mma_sf else None
-        gs = torch.empty(1, dtype=torch.float32, device=dev)
+        with _on(stream):
+            q = torch.empty((out_rows, cols // 2), dtype=torch.uint8, device=dev)
+            sf_row = torch.empty((out_rows, cols // 16), dtype=torch.uint8, device=dev) if rowmajor_sf else None
+            sf_mma = torch.zeros(sf_mma_bytes(out_rows, cols), dtype=torch.uint8, device=dev) if mma_sf else None
+            gs = torch.empty(1, dtype=torch.float32, device=dev)
     else:
         q, sf_row, sf_mma, gs = out
     if ws is None:
-        ws = _workspace(lib().nvfp4_quantize_workspace_size(rows, cols), dev)
+        ws = _workspace(lib().nvfp4_quantize_workspace_size(rows, cols), dev, stream)
     _check("nvfp4_quantize_act", lib().nvfp4_quantize_act(
         _ptr(x), dtype, rows, cols, _ptr(row_dst), fanout, out_rows, _ptr(q), _ptr(sf_row),
         _ptr(sf_mma), _ptr(gs), _ptr(ws), ws.numel(), _stream(stream)))
@@ -280,10 +304,11 @@ def quantize_weights(w: torch.Tensor, stream=None):
     """fp32 [E, K, N] -> checkpoint (q [E, K/2, N], sf [E, K/16, N], gs [E])."""
     E, K, N = w.shape
     dev = w.device
-    q = torch.empty((E, K // 2, N), dtype=torch.uint8, device=dev)
-    sf = torch.empty((E, K // 16, N), dtype=torch.uint8, device=dev)
-    gs = torch.empty(E, dtype=torch.float32, device=dev)
-    ws = _workspace(lib().nvfp4_quantize_weights_workspace_size(E, K, N), dev)
+    with _on(stream):
+        q = torch.empty((E, K // 2, N), dtype=torch.uint8, device=dev)
+        sf = torch.empty((E, K // 16, N), dtype=torch.uint8, device=dev)
+        gs = torch.empty(E, dtype=torch.float32, device=dev)
+    ws = _workspace(lib().nvfp4_quantize_weights_workspace_size(E, K, N), dev, stream)
     _check("nvfp4_quantize_weights", lib().nvfp4_quantize_weights(
         _ptr(w), E, K, N, _ptr(q), _ptr(sf), _ptr(gs), _ptr(ws), ws.numel(), _stream(stream)))
     return q, sf, gs
@@ -294,8 +319,9 @@ def prepare_weights(q_ckpt: torch.Tensor, sf_ckpt: torch.Tensor, stream=None):
     E, K2, N = q_ckpt.shape
     K = 2 * K2
     dev = q_ckpt.device
-    q = torch.empty(int(lib().moe_nvfp4_prepared_bytes(E, K, N)), dtype=torch.uint8, device=dev)
-    sf = torch.zeros(sf_mma_bytes(E * N, K), dtype=torch.uint8, device=dev)
+    with _on(stream):
+        q = torch.empty(int(lib().moe_nvfp4_prepared_bytes(E, K, N)), dtype=torch.uint8, device=dev)
+        sf = torch.zeros(sf_mma_bytes(E * N, K), dtype=torch.uint8, device=dev)
     _check("moe_nvfp4_prepare_weights", lib().moe_nvfp4_prepare_weights(
         _ptr(q_ckpt), _ptr(sf_ckpt), E, K, N, _ptr(q), _ptr(sf), _stream(stream)))
     return q, sf
@@ -353,10 +379,10 @@ def router_topk(x: torch.Tensor, w_router: torch.Tensor, k: int, mode: int = ROU
     T, H = x.shape
     E = w_router.shape[0]
     dev = x.device
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ids = _empty((T, k), torch.int32, dev, stream)
+    w = _empty((T, k), torch.float32, dev, stream)
     if ws is None:
-        ws = _workspace(lib().moe_router_workspace_size(T, H, E), dev)
+        ws = _workspace(lib().moe_router_workspace_size(T, H, E), dev, stream)
     _check("moe_router_topk", lib().moe_router_topk(
         _ptr(x), _ptr(w_router), T, H, E, k, mode, _ptr(ids), _ptr(w), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -394,10 +420,10 @@ def nvfp4_forward(weights: PreparedWeights, xq: torch.Tensor, xsf_mma: torch.Ten
                   taps: Optional[dict] = None, ws: Optional[torch.Tensor] = None, stream=None):
     dev = xq.device
     if slot_out is None:
-        slot_out = torch.empty((route.rows, weights.H), dtype=torch.float32, device=dev)
+        slot_out = _empty((route.rows, weights.H), torch.float32, dev, stream)
     if ws is None:
         ws = _workspace(forward_workspace_bytes(route.T, route.k, weights.E, weights.H,
-                                                weights.I), dev)
+                                                weights.I), dev, stream)
     t = _taps(taps)
     wst = weights.struct()
     code = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}[slot_out.dtype]
@@ -434,9 +460,9 @@ def amax(x: torch.Tensor, ws: Optional[torch.Tensor] = None, out: Optional[torch
     rows, cols = x.shape
     dtype = {torch.bfloat16: BF16, torch.float32: F32}[x.dtype]
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=x.device)
+        out = _empty(1, torch.float32, x.device, stream)
     if ws is None:
-        ws = _workspace(lib().nvfp4_quantize_workspace_size(rows, cols), x.device)
+        ws = _workspace(lib().nvfp4_quantize_workspace_size(rows, cols), x.device, stream)
     _check("nvfp4_amax", lib().nvfp4_amax(_ptr(x), dtype, rows, cols, _ptr(out), _ptr(ws),
                                           ws.numel(), _stream(stream)))
     return out
@@ -451,10 +477,11 @@ def quantize_act_amax(x: torch.Tensor, amax_in: torch.Tensor, row_dst=None, fano
     dtype = {torch.bfloat16: BF16, torch.float32: F32}[x.dtype]
     out_rows = rows if out_rows is None else out_rows
     dev = x.device
-    q = torch.empty((out_rows, cols // 2), dtype=torch.uint8, device=dev)
-    sf_row = torch.empty((out_rows, cols // 16), dtype=torch.uint8, device=dev) if rowmajor_sf else None
-    sf_mma = torch.zeros(sf_mma_bytes(out_rows, cols), dtype=torch.uint8, device=dev) if mma_sf else None
-    gs = torch.empty(1, dtype=torch.float32, device=dev)
+    with _on(stream):
+        q = torch.empty((out_rows, cols // 2), dtype=torch.uint8, device=dev)
+        sf_row = torch.empty((out_rows, cols // 16), dtype=torch.uint8, device=dev) if rowmajor_sf else None
+        sf_mma = torch.zeros(sf_mma_bytes(out_rows, cols), dtype=torch.uint8, device=dev) if mma_sf else None
+        gs = torch.empty(1, dtype=torch.float32, device=dev)
     _check("nvfp4_quantize_act_amax", lib().nvfp4_quantize_act_amax(
         _ptr(x), dtype, rows, cols, _ptr(row_dst), fanout, out_rows, _ptr(amax_in), _ptr(q),
         _ptr(sf_row), _ptr(sf_mma), _ptr(gs), _stream(stream)))
@@ -469,12 +496,13 @@ def ep_dispatch(topk_ids: torch.Tensor, E: int, G: int, q_tok: torch.Tensor,
     H = q_tok.shape[1] * 2
     dev = topk_ids.device
     S = T * k
-    counts = torch.zeros(G, dtype=torch.int32, device=dev)
-    pos = torch.empty(max(S, 1), dtype=torch.int32, device=dev)
-    rows = torch.empty((max(S, 1), H // 2 + H // 16), dtype=torch.uint8, device=dev)
-    expert = torch.empty(max(S, 1), dtype=torch.int32, device=dev)
+    with _on(stream):
+        counts = torch.zeros(G, dtype=torch.int32, device=dev)
+        pos = torch.empty(max(S, 1), dtype=torch.int32, device=dev)
+        rows = torch.empty((max(S, 1), H // 2 + H // 16), dtype=torch.uint8, device=dev)
+        expert = torch.empty(max(S, 1), dtype=torch.int32, device=dev)
     if ws is None:
-        ws = _workspace(lib().moe_ep_dispatch_workspace_size(T, k, G), dev)
+        ws = _workspace(lib().moe_ep_dispatch_workspace_size(T, k, G), dev, stream)
     _check("moe_ep_dispatch", lib().moe_ep_dispatch(
         _ptr(topk_ids), T, k, E, G, _ptr(q_tok), _ptr(sf_tok), H, _ptr(counts), _ptr(pos),
         _ptr(rows), _ptr(expert), _ptr(ws), ws.numel(), _stream(stream)))
@@ -495,7 +523,7 @@ def ep_gather(slot_out: torch.Tensor, slot_of: torch.Tensor, n: int,
               status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     H = slot_out.shape[1]
     code = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}[slot_out.dtype]
-    out = torch.empty((n, H), dtype=slot_out.dtype, device=slot_out.device)
+    out = _empty((n, H), slot_out.dtype, slot_out.device, stream)
     if n:
         _check("moe_ep_gather", lib().moe_ep_gather(_ptr(slot_out), code, H, slot_out.shape[0],
                                                     _ptr(slot_of), n, _ptr(out), _ptr(status),
@@ -509,7 +537,7 @@ def unpermute_reduce(slot_out: torch.Tensor, slot_of: torch.Tensor, topk_w: torc
     T, k = topk_w.shape
     H = slot_out.shape[1]
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=slot_out.device)
+        y = _empty((T, H), out_dtype, slot_out.device, stream)
     code = {torch.bfloat16: BF16, torch.float32: F32}[y.dtype]
     scode = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}[slot_out.dtype]
     _check("moe_unpermute_reduce", lib().moe_unpermute_reduce(
@@ -570,14 +598,14 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     if Tk != T or Dk != D:
         raise ValueError("q and k must agree in tokens and head_dim")
     if q_out is None:
-        q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+        q_out = _empty((T, hq, D), q.dtype, q.device, stream)
     elif q_out is not q and q_out.shape != q_shape:
         raise ValueError("q_out must have the shape of q")
     if k_out is None:
-        k_out = torch.empty((T, hk, D), dtype=k.dtype, device=k.device)
+        k_out = _empty((T, hk, D), k.dtype, k.device, stream)
     elif k_out is not k and k_out.shape != k_shape:
         raise ValueError("k_out must have the shape of k")
-    ws = attn_workspace(q.device) if ws is None else ws
+    ws = _workspace(256, q.device, stream) if ws is None else ws
     table, npos, rot = _rope(rope)
     _check("attn_qk_norm_rope", lib().attn_qk_norm_rope(
         *_rows(q, "q"), hq, *_rows(k, "k"), hk, T, D,
@@ -661,11 +689,11 @@ def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.T
         if Tq != T or Dq != D:
             raise ValueError("q and k must agree in tokens and head_dim")
         if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+            q_out = _empty((T, hq, D), q.dtype, q.device, stream)
         elif q_out is not q and q_out.shape != q_shape:
             raise ValueError("q_out must have the shape of q")
         q_args, out_args = _rows(q, "q"), _rows(q_out, "q_out")
-    ws = attn_workspace(k.device) if ws is None else ws
+    ws = _workspace(256, k.device, stream) if ws is None else ws
     table, npos, rot = _rope(rope)
     _check("attn_kv_append", lib().attn_kv_append(
         cache._ref, batch.rows(T), *_rows(k, "k"), *_rows(v, "v"), *q_args, hq, *out_args, table,
@@ -698,13 +726,14 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
     if D != cache.head_dim:
         raise ValueError("q and the cache must agree in head_dim")
     if out is None:
-        out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+        out = _empty((T, hq, D), q.dtype, q.device, stream)
     elif out.shape != shape:
         raise ValueError("out must have the shape of q")
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, hq)):
         raise ValueError("lse must be float32 [tokens, q heads]")
     if ws is None:
-        ws = paged_attention_workspace(cache, batch, hq, T)
+        ws = _workspace(lib().attn_paged_workspace_size(batch.batch, T, batch.max_new, hq,
+                                                        cache.heads, D), q.device, stream)
     _check("attn_paged_forward", lib().attn_paged_forward(
         *_rows(q, "q"), hq, cache._ref, batch.rows(T), D ** -0.5 if scale is None else scale,
         window, *_rows(out, "out"), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))

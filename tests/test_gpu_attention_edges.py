@@ -276,3 +276,57 @@ def test_paged_attention_hidden_nan_in_a_long_chunk(nb, D, fp8):
             (ref.U + 2 * (ds + extra) + 2.0 ** -18) * ev + ref.U * want.abs())
         assert (over <= 0).all(), over.max()
     assert nan_ms < 2 * clean_ms + 16 * L * 0.2e-3, (clean_ms, nan_ms)
+
+
+# ----------------------------------------------------------------- streams --
+def test_buffers_made_in_a_call_belong_to_its_stream(nb, monkeypatch):
+    """Calls with stream= and no workspace or outputs make and zero them on that stream:
+    nothing of theirs waits in, or returns to, the current one, which is busy meanwhile."""
+    made = []
+
+    def spy(name):
+        real = getattr(torch, name)
+
+        def f(*a, **kw):
+            t = real(*a, **kw)
+            if t.is_cuda:
+                made.append((name, torch.cuda.current_stream().cuda_stream))
+            return t
+        return f
+    case = Paged([(5, 200), (3, 3), (64, 300)], 2, 128, 16, seed=2)
+    T, hq, D = case.T, 8, 128
+    q = torch.randn(T, hq, D, device=DEV).bfloat16()
+    k = torch.randn(T, 2, D, device=DEV).bfloat16()
+    x = torch.randn(T, 256, device=DEV).bfloat16()
+    w = torch.randn(16, 256, device=DEV).bfloat16()
+    h = torch.randn(4, 256, 128, device=DEV)
+    cache, batch = case.handles(nb)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+
+    def calls(**kw):
+        ids, wts = nb.router_topk(x, w, 2, **kw)
+        route = nb.route_permute(ids, 16, **kw)
+        got = [nb.paged_attention(q, cache, batch, **kw), *nb.qk_norm_rope(q, k, pos, None, **kw),
+               nb.kv_append(cache, batch, k, k, q=q, **kw), ids, wts, route.slot_of,
+               *nb.quantize_act(x, **kw)[:2], nb.amax(x, **kw), *nb.quantize_weights(h, **kw)]
+        return got + [nb.paged_attention(q, cache, batch, **kw)]
+    s = torch.cuda.Stream()
+    calls()
+    # (what the first calls appended is there from now on)
+    want = calls()
+    torch.cuda.synchronize()
+    calls(stream=s)                                  # its pool has memory from here on
+    torch.cuda.synchronize()
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, spy(name))
+    busy = torch.cuda.Event()
+    torch.cuda._sleep(600_000_000)                   # some 0.3 s of the current stream
+    busy.record()
+    got = calls(stream=s)
+    s.synchronize()
+    assert not busy.query(), "the current stream was not busy"
+    monkeypatch.undo()
+    assert len(made) > 20 and all(stream == s.cuda_stream for _, stream in made), made
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
