@@ -663,11 +663,18 @@ class AttnBatch:
         self.struct = AttnBatchArgs(B, self.max_new, 0, page_table.shape[1],
                                     _vector(q_start, B + 1, torch.int32, "q_start"),
                                     _vector(kv_len, B, torch.int32, "kv_len"), _ptr(page_table))
-        self._ref = ctypes.byref(self.struct)
+        self._rows = (0, ctypes.byref(self.struct))
 
     def rows(self, tokens: int):
-        self.struct.tokens = tokens
-        return self._ref
+        """Reference to the arguments with this row count.  They are not changed later
+        (another thread's call may be reading them): another count gets its own."""
+        have, ref = self._rows
+        if have != tokens:
+            args = AttnBatchArgs.from_buffer_copy(self.struct)
+            args.tokens = tokens
+            ref = ctypes.byref(args)
+            self._rows = (tokens, ref)
+        return ref
 
 
 def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.Tensor,

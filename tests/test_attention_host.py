@@ -1,0 +1,60 @@
+"""Host side of the attention binding (no GPU needed)."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+from test_attention_args import nb  # noqa: F401
+
+
+class Device:
+    """What the binding reads of a CUDA tensor."""
+
+    def __init__(self, *shape, dtype=torch.int32, address=1 << 20):
+        self.shape, self.dtype, self.is_cuda, self.address = torch.Size(shape), dtype, True, address
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.address
+
+
+def _batch(nb):
+    return nb.AttnBatch(Device(3), Device(2), Device(2, 4), max_new=5)
+
+
+def _tokens(nb, ref):
+    """The row count that the library reads through a handle's reference."""
+    return ctypes.cast(ref, ctypes.POINTER(nb.AttnBatchArgs)).contents.tokens
+
+
+def test_a_batch_handle_serves_calls_of_different_row_counts(nb):
+    """What one call was given stays as it is while another is made ready."""
+    batch = _batch(nb)
+    first, second = batch.rows(7), batch.rows(3)
+    third = batch.rows(7)
+    assert [_tokens(nb, r) for r in (first, second, third)] == [7, 3, 7]
+    for ref in (first, second):
+        s = ctypes.cast(ref, ctypes.POINTER(nb.AttnBatchArgs)).contents
+        assert (s.batch, s.max_new, s.max_pages) == (2, 5, 4)
+        assert s.q_start == s.kv_len == s.page_table == 1 << 20
+
+
+def test_a_batch_handle_in_two_threads(nb):
+    batch, wrong = _batch(nb), []
+
+    def calls(tokens):
+        for _ in range(20000):
+            if _tokens(nb, batch.rows(tokens)) != tokens:
+                wrong.append(tokens)
+    threads = [threading.Thread(target=calls, args=(t,)) for t in (3, 7, 11)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
