@@ -184,6 +184,12 @@ __device__ __forceinline__ Request load_request(const BatchView& b, int page_shi
   return q;
 }
 
+// First key that a row at cache position pos sees, which may be negative (window up to
+// 2^31 - 1, 0: no window).
+__device__ __forceinline__ int first_key(int pos, int window) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 // Of the boxes of `box` keys that make up a tile from key0 on, how many hold a
 // key of [kbeg, kend).
 __device__ __forceinline__ int boxes_of(int key0, int box, int kbeg, int kend) {
@@ -387,7 +393,7 @@ __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, 
   const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
   const int tok = a.group(row), pos = rq.pos0 + tok;
   const int head = h * static_cast<int>(a.group.d) + row - tok * static_cast<int>(a.group.d);
-  const int lo = a.window > 0 ? min(k1, max(k0, pos - a.window + 1)) : k0;
+  const int lo = min(k1, max(k0, first_key(pos, a.window)));
   const int hi = max(lo, min(k1, pos + 1));
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) +
                        (rq.first + tok) * a.out.token_stride + head * a.out.head_stride +
@@ -480,7 +486,7 @@ __device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, int row0
   // first row's position
   const Request rq = load_request(a.batch, a.cache.page_shift, r, a.status);
   const int first = rq.pos0 + a.group(row0), last = rq.pos0 + a.group(row0 + rows - 1);
-  const int lo = a.window > 0 ? min(k1, max(k0, last - a.window + 1)) : k0;
+  const int lo = min(k1, max(k0, first_key(last, a.window)));
   const int hi = min(k1, max(k0, first + 1));
   if (!any_not_finite<D, FP8>(a, r, h, k0, lo) && !any_not_finite<D, FP8>(a, r, h, hi, k1)) return;
   for (int row = warp; row < rows; row += warps)

@@ -104,7 +104,7 @@ __device__ __forceinline__ Block block_of(const Request& q, const FastDiv& group
   const int first = q.pos0 + group(b.row0);
   const int last = q.pos0 + group(b.row0 + b.rows - 1);
   const int end = min(q.len, last + 1);
-  const int beg = window > 0 ? max(0, first - window + 1) : 0;
+  const int beg = first_key(first, window);
   if (end > beg) {
     b.t0 = beg / kKeys;
     b.t1 = (end + kKeys - 1) / kKeys;
@@ -760,7 +760,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         const int seg_now = seg;
         const int pos = wk.rq.pos0 + tok;
         const int vis_hi = min(pos + 1, wk.rq.len) - half * 64;
-        const int vis_lo = (a.window > 0 ? pos - a.window + 1 : 0) - half * 64;
+        const int vis_lo = first_key(pos, a.window) - half * 64;
         // keys that every row of the warp sees (rows come in order)
         const int all_hi = __shfl_sync(0xFFFFFFFFu, vis_hi, 0);
         const int all_lo = __shfl_sync(0xFFFFFFFFu, vis_lo, 31);

@@ -140,7 +140,7 @@ struct Span {
 __device__ __forceinline__ Span tiles_of(const Request& q, int window) {
   if (q.n == 0) return {0, 0};
   const int end = min(q.len, q.pos0 + q.n);
-  const int begin = window > 0 ? max(0, q.pos0 - window + 1) : 0;
+  const int begin = first_key(q.pos0, window);
   if (end <= begin) return {0, 1};
   return {begin / kKeys, (end + kKeys - 1) / kKeys};
 }
@@ -270,7 +270,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     uint32_t phase[kG] = {};
     bool ok = true;
     while (left > 0 && ok) {
-      const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
+      const int kbeg = first_key(wk.rq.pos0, a.window);
       const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
       const int stop = static_cast<int>(min(static_cast<long long>(wk.sp.t1), t + left));
       left -= stop - t;
@@ -394,7 +394,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
       const int row = e * 8 + g;
       const int pos = wk.rq.pos0 + row / group;
       vis_hi[e] = min(pos + 1, wk.rq.len);
-      vis_lo[e] = a.window > 0 ? pos - a.window + 1 : 0;
+      vis_lo[e] = first_key(pos, a.window);
       m[e] = -INFINITY;
       l[e] = 0.0f;
       cr[e] = FP8 ? c * sfac[row] : c;
@@ -403,10 +403,10 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     }
     // keys that every row sees
     const int all_hi = min(wk.rq.pos0 + 1, wk.rq.len);
-    const int all_lo = a.window > 0 ? wk.rq.pos0 + wk.rq.n - a.window : 0;
+    const int all_lo = first_key(wk.rq.pos0 + wk.rq.n - 1, a.window);
     // keys that any row sees
     const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
-    const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
+    const int kbeg = first_key(wk.rq.pos0, a.window);
 
     for (; t < stop; ++t, ++seq) {
       if (kG == 2 && static_cast<int>(seq & 1u) != side) continue;
@@ -700,7 +700,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const int stop = static_cast<int>(min(static_cast<long long>(wk.sp.t1), t + left));
     const bool whole = t == wk.sp.t0 && stop == wk.sp.t1;
     left -= stop - t;
-    const int kbeg = a.window > 0 ? max(0, wk.rq.pos0 - a.window + 1) : 0;
+    const int kbeg = first_key(wk.rq.pos0, a.window);
     const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
     const int64_t at =
         (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows;

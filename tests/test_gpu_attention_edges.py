@@ -330,3 +330,24 @@ def test_buffers_made_in_a_call_belong_to_its_stream(nb, monkeypatch):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------- windows and offsets --
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("reqs", [[(8, 2), (7, 0), (1, 90), (9, 3)], [(60, 40), (150, 400), (30, 5)]],
+                         ids=["few", "chunk"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20])
+def test_paged_attention_window_without_end(nb, reqs, window, fp8):
+    """A window of almost 2^31 positions is no window, also for tokens whose position is
+    negative."""
+    case = Paged(reqs, 1, 64, 16, fp8=fp8, seed=71)
+    q = torch.randn(case.T, 1, 64, generator=torch.Generator().manual_seed(4)).bfloat16()
+    cache, batch = case.handles(nb)
+    lse = torch.full((case.T, 1), 5.0, device=DEV)
+    ws = nb.paged_attention_workspace(cache, batch, 1, case.T)
+    out = nb.paged_attention(q.to(DEV), cache, batch, window=window, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    want, wlse, b_out, b_lse = case.reference(q)
+    _within(out, want, b_out, "out")
+    _within(lse, wlse, b_lse, "lse")
