@@ -715,9 +715,10 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  *   workspace   attn_paged_workspace_size(...) bytes, whose first word is the
  *               status word.
  * A page id outside [0, num_pages) within a request's length, a kv_len past
- * the page table row or more than max_new new tokens set
- * NVMOE_ERR_DEVICE_BAD_INDEX: the page reads as zeros, the length is cut, the
- * further tokens' rows are not written.  Rows of no request are left alone.
+ * the page table row, more than max_new new tokens, or a q_start that is negative,
+ * descends or passes `tokens` set NVMOE_ERR_DEVICE_BAD_INDEX: the page reads as
+ * zeros, the length is cut, the further tokens' rows are not written, and those
+ * that there are keep their positions.  Rows of no request are left alone.
  * Cache contents past a request's length, and keys and values that a token
  * does not see, are not used, whatever they hold (infinities and NaN too).
  * Limits: q_heads a multiple of kv_heads, tokens * q_heads < 2^31,

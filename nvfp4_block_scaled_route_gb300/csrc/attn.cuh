@@ -157,7 +157,7 @@ cudaError_t launch_attn_combine(const AttnArgs& args, int grid, cudaStream_t str
 // New tokens and cached length of request r as the kernels take them, kept
 // inside the buffers whatever q_start and kv_len hold: rows [first, first + n)
 // of q, the first of them at cache position pos0 (negative if the length is
-// below n), `len` keys.
+// below n), `len` keys.  Tokens past the ends of q count for the positions.
 struct Request {
   int64_t first;
   int n;
@@ -166,14 +166,16 @@ struct Request {
 __device__ __forceinline__ Request load_request(const BatchView& b, int page_shift, int r,
                                                 int* status) {
   Request q;
-  int64_t a = b.q_start[r], e = b.q_start[r + 1];
+  const int64_t begin = b.q_start[r], end = b.q_start[r + 1];
+  int64_t a = begin, e = end;
   const int64_t cap = b.max_pages << page_shift;   // < 2^31, checked on the host
   int64_t len = b.kv_len[r];
   if (a < 0) a = 0;
   if (e > b.tokens) e = b.tokens;
   int64_t n = e > a ? e - a : 0;
-  const int64_t pos0 = len - n;
-  if (n > b.max_new || len > cap) record_status(status, kErrBadIndex);
+  const int64_t pos0 = n > 0 ? len - (end - a) : len;
+  if (n > b.max_new || len > cap || begin < 0 || end < begin || end > b.tokens)
+    record_status(status, kErrBadIndex);
   if (n > b.max_new) n = b.max_new;
   if (len > cap) len = cap;
   if (len < 0) len = 0;

@@ -351,3 +351,46 @@ def test_paged_attention_window_without_end(nb, reqs, window, fp8):
     want, wlse, b_out, b_lse = case.reference(q)
     _within(out, want, b_out, "out")
     _within(lse, wlse, b_lse, "lse")
+
+
+@pytest.mark.parametrize("n", [3, 60])
+@pytest.mark.parametrize("cut", ["end", "begin"])
+def test_paged_attention_token_offsets_outside_the_rows(nb, n, cut):
+    """A request whose token offsets reach past the rows of q is reported, and the rows
+    that are there keep their positions: those at which its keys were appended."""
+    L, D, hq, beyond = 200, 128, 4, 2
+    case = Paged([(n, L)], 1, D, 16, seed=81)
+    q = torch.randn(n, hq, D, generator=torch.Generator().manual_seed(5)).bfloat16()
+    cache, batch = case.handles(nb)
+    batch.q_start.copy_(_i32(0, n + beyond) if cut == "end" else _i32(-beyond, n))
+    batch = nb.AttnBatch(batch.q_start, batch.kv_len, batch.page_table, max_new=n + beyond)
+    ws = nb.paged_attention_workspace(cache, batch, hq, n)
+    out = nb.paged_attention(q.to(DEV), cache, batch, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == BAD_INDEX
+    pad = torch.zeros(beyond, hq, D).bfloat16()
+    case.q_start = torch.tensor([0, n + beyond])
+    want, _, bound, _ = case.reference(torch.cat([q, pad] if cut == "end" else [pad, q]))
+    rows = slice(0, n) if cut == "end" else slice(beyond, n + beyond)
+    _within(out, want[rows], bound[rows], "rows")
+
+
+@pytest.mark.parametrize("m", [1, 30])
+def test_paged_attention_token_offsets_that_descend(nb, m):
+    """Offsets that do not ascend are reported; requests whose own do are computed."""
+    D, page = 64, 16
+    case = Paged([(3 * m, 3 * m + 40), (1, 40), (2 * m, 2 * m + 20)], 1, D, page, seed=82)
+    cache, batch = case.handles(nb)
+    batch.q_start.copy_(_i32(0, 3 * m, 2 * m, 4 * m))
+    q = torch.randn(4 * m, 2, D, generator=torch.Generator().manual_seed(7)).bfloat16()
+    ws = nb.paged_attention_workspace(cache, batch, 2, 4 * m)
+    out = nb.paged_attention(q.to(DEV), cache, batch, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == BAD_INDEX
+    # rows of two requests hold either's; the others their own
+    for r, rows in ((0, slice(0, 2 * m)), (2, slice(3 * m, 4 * m))):
+        first, n = (0, 3 * m) if r == 0 else (2 * m, 2 * m)
+        want, _, bound, _ = ref.attention(q[first:first + n], case.k, case.v, [0, n],
+                                          [case.reqs[r][1]], case.table[r:r + 1])
+        mine = slice(rows.start - first, rows.stop - first)
+        _within(out[rows], want[mine], bound[mine], f"request {r}")
