@@ -722,7 +722,7 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  * Cache contents past a request's length, and keys and values that a token
  * does not see, are not used, whatever they hold (infinities and NaN too).
  * Limits: q_heads a multiple of kv_heads, tokens * q_heads < 2^31,
- * max_pages * page_size < 2^31. */
+ * max_pages * page_size <= 2^31 - 1024. */
 size_t attn_paged_workspace_size(int batch, int64_t tokens, int max_new, int q_heads,
                                  int kv_heads, int head_dim);
 int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,

@@ -1164,6 +1164,9 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
     return NVMOE_ERR_INVALID_ARG;
   if (q_heads % a.cache.heads != 0 || a.batch.tokens > INT32_MAX / q_heads)
     return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  // the kernels count keys in 32 bits, up to eight boxes past a tile's first
+  if ((a.batch.max_pages << a.cache.page_shift) > (int64_t{1} << 31) - 1024)
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(ws)) return NVMOE_ERR_MISALIGNED;
   if (ws_bytes < attn_paged_workspace_size(a.batch.batch, a.batch.tokens, a.batch.max_new, q_heads,
                                            a.cache.heads, a.cache.head_dim))

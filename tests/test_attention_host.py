@@ -2,10 +2,10 @@
 import ctypes
 import threading
 
-import pytest
 import torch
 
-from test_attention_args import nb  # noqa: F401
+from test_attention_args import SHAPE, SMALL, _append, _cache, _forward, nb  # noqa: F401
+from test_attention_args import _batch as _args
 
 
 class Device:
@@ -58,3 +58,17 @@ def test_a_batch_handle_in_two_threads(nb):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_page_tables_of_almost_2_31_positions(nb):
+    """Positions of whole 128-key tiles stay below 2^31: tables past 2^31 - 1024 are
+    refused by the attention, which adds to positions in 32 bits, and taken by the
+    append, which does not (its next refusal is the workspace)."""
+    for page in (16, 32, 512):
+        c = _cache(nb, page_size=page, page_stride=page * 256)
+        last = (1 << 31) // page - 1024 // page
+        assert _forward(nb, c, _args(nb, max_pages=last + 1)) == SHAPE
+        assert _forward(nb, c, _args(nb, max_pages=last), n=0) == SMALL
+        assert _append(nb, c, _args(nb, max_pages=last + 1), n=0) == SMALL
+    c = _cache(nb, page_size=1024, page_stride=1024 * 256)
+    assert _forward(nb, c, _args(nb, max_pages=(1 << 21) - 1), n=0) == SMALL
