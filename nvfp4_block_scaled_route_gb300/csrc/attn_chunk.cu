@@ -769,7 +769,10 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
           // (S follows the arrivals of all that wrote the queries and their factors)
           if (FP8 && j == j0)
-            cr = c * __uint_as_float(static_cast<uint32_t>(q_exp[seg_now * kTile + row]) << 23);
+            // (not 0, which would make NaN of the -inf of a hidden key)
+            cr = fmaxf(0x1p-126f,
+                       c * __uint_as_float(static_cast<uint32_t>(q_exp[seg_now * kTile + row])
+                                           << 23));
           if (!busy) {                                  // what these rows hold is not used
             mbar_arrive(&bars->s_free[sb]);
             if (n > 1) mbar_wait(&bars->pv_done[sb], ((n - 2) >> 1) & 1u, a.status, abort);

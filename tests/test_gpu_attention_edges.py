@@ -394,3 +394,22 @@ def test_paged_attention_token_offsets_that_descend(nb, m):
                                           [case.reqs[r][1]], case.table[r:r + 1])
         mine = slice(rows.start - first, rows.stop - first)
         _within(out[rows], want[mine], bound[mine], f"request {r}")
+
+
+@pytest.mark.parametrize("n", [1, 60])
+@pytest.mark.parametrize("D", [64, 128])
+def test_paged_attention_e4m3_scores_that_vanish(nb, n, D):
+    """Scales and queries so small that the factor of the scores is below the smallest
+    fp32 number: all scores are zero, hidden keys still count for nothing."""
+    case = Paged([(n, n + 70)], 1, D, 16, fp8=True, seed=91)
+    case.k_scale = torch.tensor([1e-30])
+    q = (torch.randn(n, 4, D, generator=torch.Generator().manual_seed(6)) * 1e-25).bfloat16()
+    cache, batch = case.handles(nb)
+    lse = torch.empty(n, 4, device=DEV)
+    ws = nb.paged_attention_workspace(cache, batch, 4, n)
+    out = nb.paged_attention(q.to(DEV), cache, batch, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert nb.read_status(ws) == 0
+    want, wlse, b_out, b_lse = case.reference(q)
+    _within(out, want, b_out, "out")
+    _within(lse, wlse, b_lse, "lse")
