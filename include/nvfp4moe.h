@@ -710,7 +710,8 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  * largest).
  * On an E4M3 cache an element of q counts to within 2^-17 of its row's largest
  * (bf16 exactly down to 2^-9 of it).
- *   out         bf16 [tokens, q_heads, head_dim] with strides
+ *   out         bf16 [tokens, q_heads, head_dim] with strides; shares no element
+ *               with q or the cache (out == q is refused)
  *   lse         float [tokens, q_heads] or NULL (natural logarithm)
  *   workspace   attn_paged_workspace_size(...) bytes, whose first word is the
  *               status word.

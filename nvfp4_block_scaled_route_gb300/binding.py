@@ -727,7 +727,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
     """Causal attention of the new tokens' queries, bf16 [T, Hq, D], over their
     requests' cached keys (the new ones appended before).  window > 0: only the
     last `window` positions.  lse: optional float32 [T, Hq], written.  Returns
-    out, bf16 [T, Hq, D]."""
+    out, bf16 [T, Hq, D], which may not be q itself."""
     shape = q.shape
     T, hq, D = shape
     if D != cache.head_dim:

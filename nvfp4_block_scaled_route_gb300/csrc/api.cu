@@ -1177,6 +1177,7 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
     st = check_rows(out, out_token_stride, out_head_stride, a.batch.tokens, q_heads,
                     a.cache.head_dim);
   if (st != NVMOE_OK) return st;
+  if (out == q) return NVMOE_ERR_INVALID_ARG;      // (rows done once more read q again)
   a.q = {const_cast<void*>(q), q_token_stride, q_head_stride, q_heads};
   a.out = {out, out_token_stride, out_head_stride, q_heads};
   a.lse = lse;

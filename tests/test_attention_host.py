@@ -4,7 +4,7 @@ import threading
 
 import torch
 
-from test_attention_args import SHAPE, SMALL, _append, _cache, _forward, nb  # noqa: F401
+from test_attention_args import INVALID, SHAPE, SMALL, _append, _cache, _forward, nb  # noqa: F401
 from test_attention_args import _batch as _args
 
 
@@ -72,3 +72,11 @@ def test_page_tables_of_almost_2_31_positions(nb):
         assert _append(nb, c, _args(nb, max_pages=last + 1), n=0) == SMALL
     c = _cache(nb, page_size=1024, page_stride=1024 * 256)
     assert _forward(nb, c, _args(nb, max_pages=(1 << 21) - 1), n=0) == SMALL
+
+
+def test_attention_in_place_is_refused(nb):
+    """out may not stand in q's place: a row that is done once more, beside a hidden
+    infinity, reads its query again after rows have gone out."""
+    b = _args(nb)
+    assert _forward(nb, _cache(nb), b, out=1 << 20) == INVALID
+    assert _forward(nb, _cache(nb), b, out=(1 << 20) + 4096, n=0) == SMALL
