@@ -11,7 +11,7 @@
 // exponentials (4 * rows * keys * D flops in all).  The softmax is the bound: its
 // chain takes a warp 1750 cycles a tile, the products 1024 of the tensor pipe, which
 // is two thirds busy.  2048 new tokens over 16384 keys, 56 query and 8 key heads of
-// 128: 671 us, 1.34 PFLOP/s.
+// 128: 668 us, 1.35 PFLOP/s (up to 680 by box).
 //
 //   S = Q K^T       both from shared memory (K-major), into TMEM
 //   P = 2^(cS - m)  TMEM -> registers -> 16 bits -> TMEM
@@ -19,9 +19,9 @@
 //
 // TMEM holds S and P twice: while the softmax of tile j is computed, the tensor
 // cores run P V (j - 1) and S (j + 1).  (Two query tiles of 128-wide heads in one CTA
-// would fill TMEM with one S, P and O each, and the pipe would wait for every softmax.)  The
-// next segment's queries go in before a segment's rows go out, so that its first
-// scores are computed meanwhile.
+// would fill TMEM with one S, P in its place, and one O each, and the pipe would wait
+// for every softmax.)  The next segment's queries go in before a segment's rows go out,
+// so that its first scores are computed meanwhile.
 //
 // Roles: warps 0-7 hold the softmax, a row's keys 0-63 and 64-127 in two
 // threads that exchange maxima through shared memory; warps 8 and 9 load key
@@ -82,9 +82,9 @@ constexpr int kPlanThreads = 1024;
 // What a segment costs beside its tiles (its queries in, a first tile without
 // anything to overlap, its rows out), in tiles, when the work is shared out.
 // Measured, 0 / 2 / 4 / 6 tiles: 4 requests of 512 new tokens on an E4M3 cache
-// 233.4 / 221.5 / 214.0 / 216.4 us, 6 windowed prompts of 64-wide heads
-// 102.3 / 99.2 / 96.4 / 98.1, 16 requests of 5 drafted tokens
-// 37.0 / 34.1 / 33.7 / 34.1.
+// 234.6 / 225.5 / 216.8 / 214.7 us, 6 windowed prompts of 64-wide heads
+// 91.7 / 88.4 / 89.9 / 89.7, 16 requests of 5 drafted tokens
+// 32.9 / 30.1 / 30.3 / 30.8, 2048 new tokens of 16384 678 / 680 / 678 / 682.
 constexpr int kSegmentTiles = 4;
 static_assert(kMaxGrid < kPlanThreads && kMaxGrid < 384, "a thread for each start");
 

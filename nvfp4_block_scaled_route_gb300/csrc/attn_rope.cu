@@ -24,12 +24,14 @@ constexpr int kThreads = 128;
 // rotation) before a row can be stored.  Measured, 4096 tokens of 56 + 8 heads
 // of 128 and 21 k tokens into an E4M3 cache: 8 heads of 64 registers 29.8 us
 // and 188 us, 4 of 48 32.4 and 162, 8 of 90 registers 31.3 and 264.
-// (With its start over the end of the kernel before, a launch takes 27.4 and 177:
+// (With its start over the end of the kernel before, a launch takes 27.4 and 176:
 // 5.0 and 4.3 TB/s; 160 of the latter without the divisions by the scales.  Into the
-// cache instructions bound it, each group finds its
-// request, page and rotation anew; groups that keep them for 8 or 16 heads in
-// rounds of 4 took 187 to 190 us.)
-// Below kWideRows head rows two heads a group spread few tokens wider.
+// cache instructions bound it (76 % of the issue slots): each group finds its request,
+// page and rotation anew, and at 48 registers a thread spills 120 to 148 bytes and
+// reads 244 to 256 back.  Groups that keep what they have found for 8 or 16 heads in
+// rounds of 4 took 187 to 190 us, before the divisions.)
+// Below kWideRows head rows two heads a group spread few tokens wider (into the cache
+// at the same 48 registers, with 52 to 80 bytes of spills).
 constexpr int64_t kWideRows = 16384;
 template <bool APPEND>
 constexpr int kWideHeads = APPEND ? 4 : 8;
