@@ -25,7 +25,7 @@ DEV = "cuda"
 EPS = 1e-6
 BASE = 10000.0
 TOP = 448.0                       # the largest E4M3 number
-LOW, HIGH = -60, 60               # exponents of page scales
+LOW, HIGH = -40, 40               # exponents of page scales
 
 
 # ------------------------------------------------------------------ cases --
