@@ -72,7 +72,9 @@ typedef enum {
   NVMOE_ERR_TIMEOUT = 6,            /* device: a bounded wait ran out        */
   NVMOE_ERR_DEVICE_BAD_INDEX = 7,   /* device: expert id out of [0, E)       */
   NVMOE_ERR_RANGE = 8,              /* device: a value exceeded the range of
-                                       its storage type (fp16 slot rows)     */
+                                       its storage type (fp16 slot rows);
+                                       too few pages or rows for a plan; no
+                                       positive probability                  */
   NVMOE_ERR_DEVICE_BOUNDS = 9       /* device, NVMOE_DEBUG_BOUNDS build only:
                                        an index outside its buffer; the
                                        access was skipped                    */
@@ -83,7 +85,8 @@ typedef enum {
   NVMOE_BF16 = 0,
   NVMOE_F32 = 1,
   NVMOE_F16 = 2,
-  NVMOE_E4M3 = 3   /* key / value caches only */
+  NVMOE_E4M3 = 3,       /* key / value caches only */
+  NVMOE_E4M3_PAGES = 4  /* the same with a scale for each page and head */
 } nvmoe_dtype;
 
 /* Programmatic dependent launch on the multi-launch path (routing,
@@ -107,8 +110,9 @@ const char* nvmoe_status_str(int status);
    overwritten by the next failing call.  Host only, no device work. */
 const char* nvmoe_last_cuda_error(void);
 
-/* Library ABI version (major * 100 + minor): 201 (2.0: nvmoe_taps gained the
- * ready-flag members; 2.1: the attn_* entry points). */
+/* Library ABI version (major * 100 + minor): 202 (2.0: nvmoe_taps gained the
+ * ready-flag members; 2.1: the attn_* entry points; 2.2: NVMOE_E4M3_PAGES,
+ * attn_plan_pages, draft_verify). */
 int nvmoe_version(void);
 
 /* Number of kernels this library has enqueued in this process so far (all
@@ -647,7 +651,11 @@ int attn_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * both taken.
  *   dtype       NVMOE_BF16, or NVMOE_E4M3: the stored value times k_scale[h]
  *               (v_scale[h]) is the key (value); scales are positive and
- *               finite; NULL: 1.
+ *               finite; NULL: 1.  Or NVMOE_E4M3_PAGES: a scale for each page
+ *               and head, k_scale[page * kv_heads + h]; attn_kv_append writes
+ *               them, and those that it writes are powers of two.  Scales
+ *               that come from elsewhere may be any numbers from 2^-40 to
+ *               2^40 (others are taken as the nearer bound).
  *   page_size   a power of two, 16 .. 1024; 1 <= num_pages < 2^31
  *   strides     multiples of 16 bytes, positive, below 2^40 bytes */
 typedef struct {
@@ -657,7 +665,8 @@ typedef struct {
   int kv_heads, head_dim, page_size;
   int64_t num_pages;
   int64_t page_stride, token_stride, head_stride;
-  const float* k_scale;   /* float [kv_heads] or NULL */
+  const float* k_scale;   /* float [kv_heads] or NULL; NVMOE_E4M3_PAGES:
+                             float [num_pages, kv_heads], written by the append */
   const float* v_scale;
 } nvmoe_kv_cache;
 
@@ -686,6 +695,14 @@ typedef struct {
  * outside [0, rope_positions), or whose page id is outside [0, num_pages),
  * sets NVMOE_ERR_DEVICE_BAD_INDEX and nothing of it is written; rows of no
  * request (before q_start[0], from q_start[batch] on) are left alone.
+ * NVMOE_E4M3_PAGES: the scale of a page and head that gets new tokens becomes
+ * the smallest power of two s from 2^-40 to 2^40 with |x| <= 448 s for every
+ * finite new x; a page that holds earlier tokens of the request (new ones not
+ * from offset 0 on) keeps the larger one of that and its own, and its earlier
+ * values are multiplied by old / new and rounded where that is the new one
+ * (between powers of two only values below 2^-6 s lose bits).  What the page
+ * holds past the request's length is left as it is.  A page that gets new
+ * tokens belongs to one request alone.
  *   q NULL (q_heads 0): keys and values only.  q_out may be q itself.
  *   workspace   at least 256 bytes (the status word).
  * Limits: tokens * (q_heads + 2 * kv_heads) < 2^31. */
@@ -730,6 +747,92 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
                        const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, float scale,
                        int window, void* out, int64_t out_token_stride, int64_t out_head_stride,
                        float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------- a serving step --
+ * What stands before and after the layers of a step with paged caches: the
+ * step's lengths and tables, made on the device, and the verification of
+ * drafted tokens.  With attn_kv_append and attn_paged_forward, which read what
+ * attn_plan_pages writes, a step needs nothing from the host and may be
+ * captured whole.
+ *
+ * attn_plan_pages -- an nvmoe_attn_batch for the next step.  A request that
+ * holds kv_before[r] tokens, of which the first cached[r] stand (the others
+ * were drafted and turned down), brings new_tokens[r] more:
+ *   kv_len[r] = cached[r] + new_tokens[r];  new_tokens[r] < 0: the request
+ *   ends, kv_len[r] = 0
+ *   q_start = the running sum of the new tokens
+ * A request holds ceil(kv_len / page_size) pages, the first entries of its row
+ * of page_table.  Those that it lacks come from the pool in the order of the
+ * requests, those that it holds beyond that go back to it (and may be taken
+ * from the next call on).
+ *   ring, ring_size    int32 [ring_size]: the free pages stand from place
+ *                      `first` on, around the end of the ring, which has room
+ *                      for every page there is
+ *   pool_state         int32 {first, number of free pages};  pool_state_out:
+ *                      the same after the step (may be pool_state itself)
+ *   kv_before          int32 [batch] (may be kv_len itself)
+ *   cached             int32 [batch], or NULL: kv_before (may be kv_before or
+ *                      kv_len itself)
+ *   new_tokens         int32 [batch]
+ *   kv_len, q_start, page_table  int32 [batch], [batch + 1], [batch, max_pages]
+ *   positions          int32 [rows] or NULL: cache position of each new row
+ *   slots              int64 [rows] or NULL: page * page_size + offset of it;
+ *                      rows from q_start[batch] on are left alone
+ *   rows               most new tokens of the step
+ *   workspace          at least 256 bytes (the status word)
+ * Where the pages or the rows do not suffice for the requests up to and with
+ * r (each request of the step counted, taken up or not), request r is planned
+ * as if it brought none: NVMOE_ERR_RANGE in the status word; requests that
+ * need no page go on.  A request with kv_before outside [0, max_pages *
+ * page_size], cached outside [0, kv_before] or kv_len past max_pages *
+ * page_size is left as it is (kv_len = kv_before, no new rows):
+ * NVMOE_ERR_DEVICE_BAD_INDEX, as for a pool_state outside the ring (nothing is
+ * taken) and pages given back that the ring has no room for (dropped).  Run
+ * again from the same kv_before, cached and pool_state, a plan is the same.
+ * Limits: page_size a power of two, 16 .. 1024; max_pages * page_size < 2^31;
+ * ring_size and rows below 2^31. */
+int attn_plan_pages(int32_t* ring, int64_t ring_size, const int32_t* pool_state,
+                    int32_t* pool_state_out, int batch, int page_size, int64_t max_pages,
+                    const int32_t* kv_before, const int32_t* cached, const int32_t* new_tokens,
+                    int32_t* kv_len, int32_t* q_start, int32_t* page_table, int32_t* positions,
+                    int64_t* slots, int64_t rows, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream);
+
+/* draft_verify -- drafted tokens against the target's probabilities, from given
+ * random numbers.  Request r has the rows s = q_start[r] .. q_start[r+1] - 1, a
+ * last token and n drafted ones behind it: row s + i of target and draft is the
+ * distribution of token s + i + 1.
+ *   Token x = tokens[s + i + 1], i = 0, 1, .. stands while
+ *     accept_u[s + i] * q(x) < p(x)
+ *   (p, q: rows s + i of target and draft); accepted[r] = k: the first k do.
+ *   next_token[r]: the first token whose running sum of weights passes
+ *   sample_u[r] times their whole sum.  The weights are row s + k of target if
+ *   k = n, else max(p - q, 0) of row s + k (if that holds nothing, as with
+ *   rows that are no distributions, p).
+ * Given numbers that are uniform on [0, 1), the tokens have the target's
+ * distribution.  Probabilities are taken within [0, 1], NaN as 0; rows need not
+ * sum to 1.  accept_u * q < p is decided exactly, running sums are off by 2^-44
+ * or less of themselves.
+ *   target, draft   [rows, vocab] of dtype (NVMOE_F32 or NVMOE_BF16) with a
+ *                   stride between rows (elements);  draft NULL: tokens that
+ *                   were guessed for sure, q = 1 at the token and 0 elsewhere
+ *   tokens          int32 [rows]; accept_u float [rows]; sample_u float [batch]
+ *   accepted, next_token  int32 [batch]
+ *   cached          int32 [batch] or NULL: kv_len[r] - (n - accepted[r]), the
+ *                   tokens of the cache that stand, for attn_plan_pages (may be
+ *                   kv_len itself)
+ *   workspace       at least 256 bytes (the status word)
+ * A request without rows gets 0 and next_token -1.  So does one whose offsets
+ * leave [0, rows] or descend, with NVMOE_ERR_DEVICE_BAD_INDEX.  A token outside
+ * [0, vocab) does not stand, with the same status.  A row without a positive
+ * probability gives next_token -1 and NVMOE_ERR_RANGE.
+ * Limits: rows < 2^31, vocab <= 2^30, batch < 2^28. */
+int draft_verify(const void* target, int64_t target_stride, const void* draft,
+                 int64_t draft_stride, int dtype, int64_t rows, int64_t vocab,
+                 const int32_t* tokens, int batch, const int32_t* q_start, const int32_t* kv_len,
+                 const float* accept_u, const float* sample_u, int32_t* accepted,
+                 int32_t* next_token, int32_t* cached, void* workspace, size_t workspace_bytes,
+                 cudaStream_t stream);
 
 #ifdef __cplusplus
 }

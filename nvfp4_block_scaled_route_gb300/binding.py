@@ -27,7 +27,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libnvfp4moe_debug.so" if os.environ.get("NVMOE_LIBRARY") == "debug"
                         else "libnvfp4moe.so")
 
-BF16, F32, F16, E4M3 = 0, 1, 2, 3
+BF16, F32, F16, E4M3, E4M3_PAGES = 0, 1, 2, 3, 4
 NVMOE_ERR_CUDA = 5
 TILE_ROWS = 128
 
@@ -123,6 +123,10 @@ SIGNATURES = {
     "attn_paged_workspace_size": (_SZ, [_I, _I64, _I, _I, _I, _I]),
     "attn_paged_forward": (_I, [_P, _I64, _I64, _I, _P, _P, _F, _I, _P, _I64, _I64, _P, _P, _SZ,
                                 _P]),
+    "attn_plan_pages": (_I, [_P, _I64, _P, _P, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
+                             _P, _SZ, _P]),
+    "draft_verify": (_I, [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _P,
+                          _P, _SZ, _P]),
 }
 
 
@@ -572,6 +576,12 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
     return t.data_ptr()
 
 
+def _page_scales(t: Optional[torch.Tensor], pages: int, heads: int, what: str):
+    if t is None or t.dtype is not torch.float32 or t.shape != (pages, heads):
+        raise ValueError(f"{what} must be float32 [{pages}, {heads}], as the other side's is by page")
+    return _ptr(t)
+
+
 def _rope(rope: Optional[torch.Tensor]):
     if rope is None:
         return None, 0, 0
@@ -619,7 +629,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
 class PagedKVCache:
     """A paged cache: k and v, bf16 or float8_e4m3fn, [pages, page_size, Hkv, D]
     or with heads_first [pages, Hkv, page_size, D] (D contiguous, other axes
-    strided); k_scale / v_scale float32 [Hkv] for an E4M3 cache (None: 1)."""
+    strided); k_scale / v_scale float32 [Hkv] for an E4M3 cache (None: 1), or
+    float32 [pages, Hkv]: a scale for each page and head, which kv_append sets."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, heads_first: bool = False,
                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None):
@@ -640,10 +651,16 @@ class PagedKVCache:
         self.k, self.v, self.heads_first = k, v, heads_first
         self.k_scale, self.v_scale = k_scale, v_scale
         self.heads, self.head_dim, self.page_size = heads, D, page
-        self.struct = KvCache(
-            k.data_ptr(), v.data_ptr(), BF16 if k.dtype == torch.bfloat16 else E4M3, heads, D,
-            page, pages, sp, st, sh, _vector(k_scale, heads, torch.float32, "k_scale"),
-            _vector(v_scale, heads, torch.float32, "v_scale"))
+        code = BF16 if k.dtype == torch.bfloat16 else E4M3
+        if code == E4M3 and any(s is not None and s.dim() == 2 for s in (k_scale, v_scale)):
+            code = E4M3_PAGES
+            scales = (_page_scales(k_scale, pages, heads, "k_scale"),
+                      _page_scales(v_scale, pages, heads, "v_scale"))
+        else:
+            scales = (_vector(k_scale, heads, torch.float32, "k_scale"),
+                      _vector(v_scale, heads, torch.float32, "v_scale"))
+        self.struct = KvCache(k.data_ptr(), v.data_ptr(), code, heads, D, page, pages, sp, st, sh,
+                              *scales)
         self._ref = ctypes.byref(self.struct)
 
 
@@ -684,7 +701,9 @@ def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.T
               ws: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
     """Norm and rotate the new keys at their cache positions and append them
     with the new values (bf16 [T, Hkv, D]); with q given, norm and rotate it in
-    the same launch.  Returns q_out (None without q)."""
+    the same launch.  On a cache with a scale for each page and head, the scales
+    of the pages that get tokens are set to powers of two that hold them.
+    Returns q_out (None without q)."""
     k_shape, D = k.shape, cache.head_dim
     T, hk, Dk = k_shape
     if k_shape != v.shape or hk != cache.heads or Dk != D:
@@ -745,6 +764,107 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
         *_rows(q, "q"), hq, cache._ref, batch.rows(T), D ** -0.5 if scale is None else scale,
         window, *_rows(out, "out"), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------- a serving step --
+class PagePool:
+    """Free pages of a paged cache, in device int32 tensors: ring [pages], state [2] =
+    {place of the first free page, how many there are}.  The ring has room for every
+    page of the cache."""
+
+    def __init__(self, ring: torch.Tensor, state: torch.Tensor):
+        n = ring.shape[0]
+        self.ring, self.state, self.size = ring, state, n
+        self._ring = _vector(ring, n, torch.int32, "ring")
+        self._state = _vector(state, 2, torch.int32, "state")
+
+    @staticmethod
+    def full(pages: int, device="cuda") -> "PagePool":
+        """All of `pages` pages, in order."""
+        return PagePool(torch.arange(pages, dtype=torch.int32, device=device),
+                        torch.tensor([0, pages], dtype=torch.int32, device=device))
+
+
+def plan_pages(pool: PagePool, batch: AttnBatch, page_size: int, new_tokens: torch.Tensor,
+               cached: Optional[torch.Tensor] = None, kv_before: Optional[torch.Tensor] = None,
+               state_out: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               slots: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               stream=None) -> AttnBatch:
+    """Fills the batch (q_start, kv_len, page_table) for a step that brings new_tokens
+    (int32 [B], negative: the request ends), with pages from and back to the pool.
+    cached int32 [B]: how many of a request's tokens stand (default: all).  The step
+    starts from kv_before and pool.state and leaves batch.kv_len and state_out (default:
+    each in place; with buffers of their own a plan can be made again).  positions int32
+    and slots int64 [rows], if given: cache position and page * page_size + offset of
+    every new row.  Returns batch."""
+    B = batch.batch
+    rows = 2 ** 31 - 1
+    for t in (positions, slots):
+        if t is not None:
+            rows = min(rows, t.shape[0])
+    ws = _workspace(256, batch.kv_len.device, stream) if ws is None else ws
+    s = batch.struct
+    _check("attn_plan_pages", lib().attn_plan_pages(
+        pool._ring, pool.size, pool._state,
+        pool._state if state_out is None else _vector(state_out, 2, torch.int32, "state_out"), B,
+        page_size, s.max_pages,
+        s.kv_len if kv_before is None else _vector(kv_before, B, torch.int32, "kv_before"),
+        _vector(cached, B, torch.int32, "cached"),
+        _vector(new_tokens, B, torch.int32, "new_tokens"), s.kv_len, s.q_start, s.page_table,
+        None if positions is None else _vector(positions, positions.shape[0], torch.int32,
+                                               "positions"),
+        None if slots is None else _vector(slots, slots.shape[0], torch.int64, "slots"), rows,
+        _ptr(ws), ws.numel(), _stream(stream)))
+    return batch
+
+
+def _distributions(t: torch.Tensor, what: str):
+    """(address, row stride) of probabilities [rows, vocab]."""
+    s = t.stride()
+    if len(s) != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor [rows, vocab]")
+    if s[1] != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what}: vocab must be contiguous")
+    return t.data_ptr(), s[0]
+
+
+def draft_verify(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: torch.Tensor,
+                 batch: AttnBatch, accept_u: torch.Tensor, sample_u: torch.Tensor,
+                 accepted: Optional[torch.Tensor] = None,
+                 next_token: Optional[torch.Tensor] = None, cached: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None, stream=None):
+    """How many drafted tokens of each request stand, and the token that follows them.
+    target, draft [T, vocab] (float32 or bf16, both alike): row i is the distribution of
+    token i + 1 of the step's tokens, int32 [T]; draft None: tokens guessed without one.
+    A request's first row is its last token, the others its drafted ones (batch.q_start).
+    accept_u float32 [T], sample_u float32 [B]: uniform on [0, 1).  cached int32 [B], if
+    given: the tokens of batch.kv_len that stand, for plan_pages.  Returns (accepted,
+    next_token), int32 [B]."""
+    T, vocab = target.shape
+    B, dev = batch.batch, target.device
+    code = {torch.float32: F32, torch.bfloat16: BF16}.get(target.dtype)
+    if code is None:
+        raise ValueError("target must be float32 or bf16")
+    d_args = (None, 0)
+    if draft is not None:
+        if draft.shape != target.shape or draft.dtype is not target.dtype:
+            raise ValueError("draft must have the shape and type of target")
+        d_args = _distributions(draft, "draft")
+    if accepted is None:
+        accepted = _empty(B, torch.int32, dev, stream)
+    if next_token is None:
+        next_token = _empty(B, torch.int32, dev, stream)
+    ws = _workspace(256, dev, stream) if ws is None else ws
+    s = batch.struct
+    _check("draft_verify", lib().draft_verify(
+        *_distributions(target, "target"), *d_args, code, T, vocab,
+        _vector(tokens, T, torch.int32, "tokens"), B, s.q_start, s.kv_len,
+        _vector(accept_u, T, torch.float32, "accept_u"),
+        _vector(sample_u, B, torch.float32, "sample_u"),
+        _vector(accepted, B, torch.int32, "accepted"),
+        _vector(next_token, B, torch.int32, "next_token"),
+        _vector(cached, B, torch.int32, "cached"), _ptr(ws), ws.numel(), _stream(stream)))
+    return accepted, next_token
 
 
 # -------------------------------------------------------- whole forward --

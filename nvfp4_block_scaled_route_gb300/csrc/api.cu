@@ -10,6 +10,7 @@
 #include "nvfp4moe.h"
 #include "attn.cuh"
 #include "internal.h"
+#include "serve.cuh"
 
 using namespace nvmoe;
 
@@ -176,13 +177,13 @@ const char* nvmoe_status_str(int s) {
     case NVMOE_ERR_CUDA: return "CUDA error";
     case NVMOE_ERR_TIMEOUT: return "device wait timed out";
     case NVMOE_ERR_DEVICE_BAD_INDEX: return "index out of range (expert id, position or page)";
-    case NVMOE_ERR_RANGE: return "value beyond the range of its storage type";
+    case NVMOE_ERR_RANGE: return "out of range: a value for its storage type, or more than the pages, rows or probabilities hold";
     case NVMOE_ERR_DEVICE_BOUNDS: return "index outside its buffer (debug-bounds build)";
     default: return "unknown status";
   }
 }
 
-int nvmoe_version(void) { return 201; }
+int nvmoe_version(void) { return 202; }
 
 int nvmoe_set_pdl(int enable) {
   const int old = g_pdl.exchange(enable != 0 ? 1 : 0);
@@ -968,7 +969,8 @@ int check_transform(const float* rope, int64_t rope_positions, int rotary_dim, i
 
 int check_cache(const nvmoe_kv_cache* c, KvCacheView* v) {
   if (c == nullptr || c->kv_heads < 1 || c->num_pages < 1) return NVMOE_ERR_INVALID_ARG;
-  if (c->dtype != NVMOE_BF16 && c->dtype != NVMOE_E4M3) return NVMOE_ERR_INVALID_ARG;
+  const bool paged = c->dtype == NVMOE_E4M3_PAGES;
+  if (c->dtype != NVMOE_BF16 && c->dtype != NVMOE_E4M3 && !paged) return NVMOE_ERR_INVALID_ARG;
   const int D = c->head_dim, P = c->page_size;
   if ((D != 64 && D != 128) || P < 16 || P > 1024 || (P & (P - 1)) != 0 ||
       c->num_pages >= (int64_t{1} << 31))
@@ -980,8 +982,15 @@ int check_cache(const nvmoe_kv_cache* c, KvCacheView* v) {
     if (s * el % 16 != 0) return NVMOE_ERR_MISALIGNED;
   }
   if (!aligned16(c->k) || !aligned16(c->v)) return NVMOE_ERR_MISALIGNED;
-  *v = KvCacheView{c->k, c->v, c->dtype == NVMOE_E4M3, c->kv_heads, D, 0, c->num_pages,
-                   c->page_stride, c->token_stride, c->head_stride, c->k_scale, c->v_scale};
+  if (paged) {
+    if (c->k_scale == nullptr || c->v_scale == nullptr) return NVMOE_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) & 3) != 0)
+      return NVMOE_ERR_MISALIGNED;
+  }
+  // (the append writes the scales of pages; those of heads are only read)
+  *v = KvCacheView{c->k, c->v, c->dtype != NVMOE_BF16, paged, c->kv_heads, D, 0, c->num_pages,
+                   c->page_stride, c->token_stride, c->head_stride,
+                   const_cast<float*>(c->k_scale), const_cast<float*>(c->v_scale)};
   while ((1 << v->page_shift) < P) ++v->page_shift;
   if (!v->fp8) v->k_scale = v->v_scale = nullptr;
   return NVMOE_OK;
@@ -1081,11 +1090,12 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
                          static_cast<const __nv_bfloat16*>(q_weight),
                          static_cast<const __nv_bfloat16*>(k_weight), eps};
   return status_of(
-      counted(launch_kv_append({const_cast<void*>(q), q_token_stride, q_head_stride, q_heads},
-                               {const_cast<void*>(k), k_token_stride, k_head_stride, cv.heads},
-                               {const_cast<void*>(v), v_token_stride, v_head_stride, cv.heads}, cv,
-                               bv, tr, {q_out, q_out_token_stride, q_out_head_stride, q_heads},
-                               static_cast<int*>(ws), stream),
+      counted((cv.paged ? launch_page_append : launch_kv_append)(
+                  {const_cast<void*>(q), q_token_stride, q_head_stride, q_heads},
+                  {const_cast<void*>(k), k_token_stride, k_head_stride, cv.heads},
+                  {const_cast<void*>(v), v_token_stride, v_head_stride, cv.heads}, cv, bv, tr,
+                  {q_out, q_out_token_stride, q_out_head_stride, q_heads}, static_cast<int*>(ws),
+                  stream),
               1));
 }
 
@@ -1202,6 +1212,92 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   }
   if (e != cudaSuccess) return fail(e);
   return status_of(counted(launch_attn_combine(a, grid, stream), 1));
+}
+
+// ----------------------------------------------------- a serving step ----
+int attn_plan_pages(int32_t* ring, int64_t ring_size, const int32_t* pool_state,
+                    int32_t* pool_state_out, int batch, int page_size, int64_t max_pages,
+                    const int32_t* kv_before, const int32_t* cached, const int32_t* new_tokens,
+                    int32_t* kv_len, int32_t* q_start, int32_t* page_table, int32_t* positions,
+                    int64_t* slots, int64_t rows, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const NvtxRange nvtx_range("attn_plan_pages");
+  if (batch < 0 || rows < 0 || max_pages < 0 || ring_size < 1 || ws == nullptr ||
+      ring == nullptr || pool_state == nullptr || pool_state_out == nullptr || q_start == nullptr)
+    return NVMOE_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0 ||
+      ring_size >= (int64_t{1} << 31) || rows >= (int64_t{1} << 31) ||
+      max_pages >= (int64_t{1} << 31) / page_size)
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < kStatusBytes) return NVMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(ws)) return NVMOE_ERR_MISALIGNED;
+  if (batch > 0 && (kv_before == nullptr || new_tokens == nullptr || kv_len == nullptr ||
+                    (max_pages > 0 && page_table == nullptr)))
+    return NVMOE_ERR_INVALID_ARG;
+  PlanArgs a{};
+  a.pool = {ring, ring_size, pool_state, pool_state_out};
+  a.batch = batch;
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  a.max_pages = max_pages;
+  a.rows = rows;
+  a.before = kv_before;
+  a.cached = cached;
+  a.new_tokens = new_tokens;
+  a.kv_len = kv_len;
+  a.q_start = q_start;
+  a.page_table = page_table;
+  a.positions = positions;
+  a.slots = slots;
+  a.status = static_cast<int*>(ws);
+  return status_of(counted(launch_plan_pages(a, stream), 1));
+}
+
+int draft_verify(const void* target, int64_t target_stride, const void* draft,
+                 int64_t draft_stride, int dtype, int64_t rows, int64_t vocab,
+                 const int32_t* tokens, int batch, const int32_t* q_start, const int32_t* kv_len,
+                 const float* accept_u, const float* sample_u, int32_t* accepted,
+                 int32_t* next_token, int32_t* cached, void* ws, size_t ws_bytes,
+                 cudaStream_t stream) {
+  const NvtxRange nvtx_range("draft_verify");
+  if (batch < 0 || rows < 0 || vocab < 1 || ws == nullptr ||
+      (dtype != NVMOE_F32 && dtype != NVMOE_BF16))
+    return NVMOE_ERR_INVALID_ARG;
+  // (grid: up to eight CTAs a request)
+  if (rows >= (int64_t{1} << 31) || vocab > (int64_t{1} << 30) || batch >= (1 << 28))
+    return NVMOE_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < kStatusBytes) return NVMOE_ERR_WORKSPACE_TOO_SMALL;
+  const uintptr_t el = dtype == NVMOE_F32 ? 4 : 2;
+  if (!aligned16(ws) || reinterpret_cast<uintptr_t>(target) % el != 0 ||
+      reinterpret_cast<uintptr_t>(draft) % el != 0)
+    return NVMOE_ERR_MISALIGNED;
+  if (batch == 0) return NVMOE_OK;
+  if (q_start == nullptr || sample_u == nullptr || accepted == nullptr || next_token == nullptr ||
+      (cached != nullptr && kv_len == nullptr))
+    return NVMOE_ERR_INVALID_ARG;
+  if (rows > 0 && (target == nullptr || tokens == nullptr || accept_u == nullptr))
+    return NVMOE_ERR_INVALID_ARG;
+  constexpr int64_t kMost = int64_t{1} << 31;      // with rows < 2^31: offsets fit int64
+  if (rows > 1 && (target_stride < vocab || target_stride >= kMost ||
+                   (draft != nullptr && (draft_stride < vocab || draft_stride >= kMost))))
+    return NVMOE_ERR_INVALID_ARG;
+  VerifyArgs a{};
+  a.target = target;
+  a.draft = draft;
+  a.bf16 = dtype == NVMOE_BF16;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.rows = rows;
+  a.vocab = static_cast<int>(vocab);
+  a.batch = batch;
+  a.tokens = tokens;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.accept_u = accept_u;
+  a.sample_u = sample_u;
+  a.accepted = accepted;
+  a.next_token = next_token;
+  a.cached = cached;
+  a.status = static_cast<int*>(ws);
+  return status_of(counted(launch_draft_verify(a, stream), 1));
 }
 
 }  // extern "C"

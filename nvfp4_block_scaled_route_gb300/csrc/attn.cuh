@@ -22,13 +22,22 @@ struct KvCacheView {
   void* k;
   void* v;
   bool fp8;                 // E4M3, else bf16
+  bool paged;               // E4M3 with a scale for each page and head
   int heads, head_dim;
   int page_shift;           // page_size = 1 << page_shift
   int64_t num_pages;
   int64_t page_stride, token_stride, head_stride;   // elements
-  const float* k_scale;     // [heads] or null
-  const float* v_scale;
+  float* k_scale;           // [heads] or null; paged: [num_pages, heads], written by the append
+  float* v_scale;
 };
+
+// Scales of pages: what lies outside is taken as the nearer bound, NaN as the lower.
+// (A softmax reference is moved by their logarithms: with these the sums of two pages
+// stay within fp32 of each other.)
+constexpr float kScaleLow = 0x1p-40f, kScaleHigh = 0x1p40f;
+__device__ __forceinline__ float page_scale(float s) {
+  return fminf(fmaxf(s, kScaleLow), kScaleHigh);
+}
 
 struct BatchView {
   int batch, max_new;
@@ -59,6 +68,11 @@ cudaError_t launch_kv_append(const HeadRows& q, const HeadRows& k, const HeadRow
                              const KvCacheView& cache, const BatchView& batch,
                              const HeadTransform& tr, const HeadRows& q_out, int* status,
                              cudaStream_t stream);
+// The same into pages with scales of their own.
+cudaError_t launch_page_append(const HeadRows& q, const HeadRows& k, const HeadRows& v,
+                               const KvCacheView& cache, const BatchView& batch,
+                               const HeadTransform& tr, const HeadRows& q_out, int* status,
+                               cudaStream_t stream);
 
 // Keys of a tile: the unit in which attention work is shared out.
 constexpr int kAttnTileKeys = 128;
@@ -349,11 +363,17 @@ __device__ __forceinline__ float dot_of(const __nv_bfloat16* q, const void* base
   return s[0] + s[1];
 }
 
-// Element offset of a key (below the request's length) of request r and head h; -1 in
-// a page out of range, which has been reported and reads as zeros.
-__device__ __forceinline__ int64_t place_of(const AttnArgs& a, int r, int h, int key) {
+// Page of a key (below the request's length) of request r; -1 if it is out of range,
+// which has been reported: it reads as zeros.
+__device__ __forceinline__ int64_t page_of(const AttnArgs& a, int r, int key) {
   const int64_t page = a.batch.page_table[r * a.batch.max_pages + (key >> a.cache.page_shift)];
-  if (page < 0 || page >= a.cache.num_pages) return -1;
+  return page < 0 || page >= a.cache.num_pages ? -1 : page;
+}
+
+// Element offset of that key and head h, likewise.
+__device__ __forceinline__ int64_t place_of(const AttnArgs& a, int r, int h, int key) {
+  const int64_t page = page_of(a, r, key);
+  if (page < 0) return -1;
   return page * a.cache.page_stride +
          (key & ((1 << a.cache.page_shift) - 1)) * a.cache.token_stride + h * a.cache.head_stride;
 }
@@ -387,7 +407,7 @@ __device__ __forceinline__ bool any_not_finite(const AttnArgs& a, int r, int h, 
 // and from the cache, if an element of it has come out infinite or NaN that is so at
 // a hidden key: its sums over the keys of [k0, k1), of which it sees a part.  To the
 // output, or to the piece's row `po` relative to the piece's maximum po_ml->x.
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGED>
 __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, int k0, int k1,
                                       float* po, const float2* po_ml) {
   constexpr int kPer = D / 32;                             // a lane's elements
@@ -429,8 +449,8 @@ __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, 
   if (!__any_sync(0xFFFFFFFFu, open != 0)) return;
 
   float c = a.scale * 1.4426950408889634f, v_scale = 1.0f;
-  if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[h];
-  if (FP8 && a.cache.v_scale != nullptr) v_scale = a.cache.v_scale[h];
+  if (FP8 && !PAGED && a.cache.k_scale != nullptr) c *= a.cache.k_scale[h];
+  if (FP8 && !PAGED && a.cache.v_scale != nullptr) v_scale = a.cache.v_scale[h];
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.data) +
                            (rq.first + tok) * a.q.token_stride + head * a.q.head_stride;
   float o[kPer] = {}, m = -INFINITY, l = 0.0f;
@@ -440,6 +460,12 @@ __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, 
     const bool mine = lane < hi - key0;
     const int64_t at = mine ? place_of(a, r, h, key0 + lane) : -1;
     float s = at >= 0 ? dot_of<D, FP8>(q, a.cache.k, at) : 0.0f;
+    float wv = 1.0f;                                     // of the key's value
+    if (PAGED && at >= 0) {
+      const int64_t scale = page_of(a, r, key0 + lane) * a.cache.heads + h;
+      s *= page_scale(a.cache.k_scale[scale]);
+      wv = page_scale(a.cache.v_scale[scale]);
+    }
     s = mine ? s * c : -INFINITY;
     float mn = fmaxf(m, s);
 #pragma unroll
@@ -448,6 +474,7 @@ __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, 
     const float w = exp2_approx(s - use);
     m = mn;
     l = l * f + w;
+    if (PAGED) wv *= w;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] *= f;
     // the lanes' dimensions
@@ -455,7 +482,7 @@ __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, 
       float wk[8], x[8][kPer];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        wk[j] = __shfl_sync(0xFFFFFFFFu, w, k + j);
+        wk[j] = __shfl_sync(0xFFFFFFFFu, PAGED ? wv : w, k + j);
         load_part<D, FP8>(a.cache.v, __shfl_sync(0xFFFFFFFFu, at, k + j), x[j]);
       }
 #pragma unroll
@@ -478,7 +505,7 @@ __device__ __noinline__ void mend_row(const AttnArgs& a, int r, int h, int row, 
 // The rows [row0, row0 + rows) of a segment, of which some sum may not be finite: one
 // of `warps` warps (this one is `warp`).  [kbeg, kend): keys that any of them sees;
 // [t0, t1): the tiles that have been taken.  po, po_ml: the piece's first row, or po null.
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGED>
 __device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, int row0, int rows,
                                        int kbeg, int kend, int t0, int t1, float* po,
                                        const float2* po_ml, int warp, int warps) {
@@ -492,7 +519,7 @@ __device__ __noinline__ void mend_rows(const AttnArgs& a, int r, int h, int row0
   const int hi = min(k1, max(k0, first + 1));
   if (!any_not_finite<D, FP8>(a, r, h, k0, lo) && !any_not_finite<D, FP8>(a, r, h, hi, k1)) return;
   for (int row = warp; row < rows; row += warps)
-    mend_row<D, FP8>(a, r, h, row0 + row, k0, k1,
+    mend_row<D, FP8, PAGED>(a, r, h, row0 + row, k0, k1,
                      po != nullptr ? po + static_cast<int64_t>(row) * D : nullptr, po_ml + row);
 }
 

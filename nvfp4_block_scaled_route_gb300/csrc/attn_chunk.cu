@@ -271,7 +271,13 @@ struct Walk {
   }
 };
 
-template <int D, bool FP8>
+// PAGED: scales of the pages of a tile's keys, for each 16 of them, eight of keys and
+// eight of values; slots by the number of the tile.  A slot is written again once S of
+// the tile kK back is done, whose own start had all softmax threads past the scores of
+// the tile two before that: kK + 3 tiles may be in use.
+constexpr int kScaleSlots = 16, kTileScales = 16;
+
+template <int D, bool FP8, bool PAGED>
 struct Cfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kBytes = kKeys * D * 2;         // an operand tile
@@ -281,12 +287,14 @@ struct Cfg {
   static constexpr int kHalves = kRow / kLine;         // column blocks
   // tiles of keys (as loaded), operand tiles of values (bf16: as loaded), raw
   // tiles of E4M3 values
-  static constexpr int kK = (FP8 ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
+  static constexpr int kK = (FP8 && !PAGED ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
   static constexpr int kRaw = FP8 ? (D == 128 ? 2 : 5) : 0;
   static constexpr int kVAt = kBytes;                  // after the queries: values, keys, raw
   static constexpr int kKAt = kVAt + kV * kBytes, kRawAt = kKAt + kK * kLoadBytes;
   static constexpr int kRing = kRawAt + kRaw * kLoadBytes;
-  static constexpr int kSmem = kRing + 512 + 5 * kTile * 4;
+  static constexpr int kScales = kRing + 512 + 5 * kTile * 4;
+  static constexpr int kSmem = kScales + (PAGED ? kScaleSlots * kTileScales * 4 : 0);
+  static_assert(!PAGED || kK + 3 <= kScaleSlots, "slots");
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr uint32_t kTmemO = 256, kTmemP = 384;   // S: columns 0 and 128
   // instruction descriptors: fp16 operands are format 0, bf16 format 1; V is MN-major
@@ -339,12 +347,12 @@ __device__ __forceinline__ uint32_t raw_at(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+template <int D, bool FP8, bool PAGED>
+__global__ void __launch_bounds__(Cfg<D, FP8, PAGED>::kThreads, 1)
 attention_chunk_kernel(const __grid_constant__ AttnArgs a,
                        const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
-  using C = Cfg<D, FP8>;
+  using C = Cfg<D, FP8, PAGED>;
   // the swizzle goes by the address: tiles start at multiples of 1024 bytes,
   // and there is no room to round up to one
   extern __shared__ __align__(1024) uint8_t sq[];       // queries, operand tiles, raw tiles
@@ -357,11 +365,13 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   // E4M3: each query row's power of two, [segment parity][row] (a thread may be
   // a segment ahead of another)
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(swap + 4 * kTile);
+  float* scales = reinterpret_cast<float*>(sq + C::kScales);   // [slot][kTileScales]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kK + (FP8 ? C::kRaw : C::kV); ++i) {
-      mbar_init(&bars->full[i], 1);
+      // (and the loader's lanes with their copies of scales)
+      mbar_init(&bars->full[i], PAGED && i < C::kK ? 33 : 1);
       // the readers: an issuer, or four converting warps
       mbar_init(&bars->empty[i], FP8 && i >= C::kK ? 4 : 1);
     }
@@ -430,7 +440,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     const int b = lane & 7, half = lane >> 3;
     const uint64_t policy = policy_evict_normal();
     int buf = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, tiles = 0;                      // tiles with scores so far
     bool ok = true;
     while (left > 0 && ok) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
@@ -471,6 +481,21 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           const int x = half * (FP8 ? C::kLine : C::kLine / 2);
           tma_load_4d(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
         }
+        if (PAGED && keys) {
+          // the scales of each 16 keys: lanes 8-15 those of keys, 16-23 of values
+          if (wk.b.kend > 0) {
+            const int k16 = t * kKeys + (lane & 7) * 16;
+            if (lane >= 8 && lane < 24) {
+              const int64_t from =
+                  k16 < wk.b.kend && k16 + 16 > wk.b.kbeg ? page_of(a, wk.r, k16) : -1;
+              const float* src = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
+              cp_async_4(scales + tiles % kScaleSlots * kTileScales + lane - 8,
+                         src + (from < 0 ? 0 : from * a.cache.heads + wk.h), from >= 0);
+            }
+            ++tiles;
+          }
+          cp_async_arrive(&bars->full[n]);
+        }
         if (++buf == bufs) {
           buf = 0;
           phase ^= 1u;
@@ -481,6 +506,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         t = wk.b.t0;
       }
     }
+    if (PAGED && keys) cp_async_wait_all();
   } else if (FP8 && warp >= kConvert) {
     // ---- E4M3 values to fp16: 16 bytes at a time, eight rows of one column side
     // by side (no bank conflicts either way) ----
@@ -691,7 +717,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         begun = true;
       }
       c = a.scale * 1.4426950408889634f;
-      if (FP8) c *= 0.0078125f * (a.cache.k_scale != nullptr ? a.cache.k_scale[wk.h] : 1.0f);
+      if (FP8)
+        c *= 0.0078125f * (!PAGED && a.cache.k_scale != nullptr ? a.cache.k_scale[wk.h] : 1.0f);
       if (!sees) return;
       seg ^= 1;
       // the queries, D / 8 lanes a row (the last S with the previous ones has landed)
@@ -799,17 +826,41 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             for (int i = 0; i < 64; ++i)
               if (i < lw) s[i >> 5][i & 31] = 0xFF800000u;
           }
-          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float top;
+          // PAGED: of each 16 keys the factor of a score and the power of two that the
+          // values' scale adds to a weight
+          float cg[4], lift[4];
+          if (PAGED) {
+            const float4* sc = reinterpret_cast<const float4*>(
+                scales + n % kScaleSlots * kTileScales + half * 4);
+            const float4 ks = sc[0], vs = sc[2];
+            const float kg[4] = {ks.x, ks.y, ks.z, ks.w}, vg[4] = {vs.x, vs.y, vs.z, vs.w};
+            top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 64; i += 8)
+            for (int g = 0; g < 4; ++g) {
+              // (finite and not 0: the score may be -inf or 0)
+              cg[g] = fminf(fmaxf(cr * page_scale(kg[g]), 0x1p-126f), 0x1p126f);
+              lift[g] = log2f(page_scale(vg[g]));
+              float m4 = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              t4[k] = max3(t4[k], __uint_as_float(s[i >> 5][(i & 31) + 2 * k]),
-                           __uint_as_float(s[i >> 5][(i & 31) + 2 * k + 1]));
-          float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+              for (int i = 16 * g; i < 16 * g + 16; i += 2)
+                m4 = max3(m4, __uint_as_float(s[i >> 5][i & 31]),
+                          __uint_as_float(s[i >> 5][(i & 31) + 1]));
+              top = fmaxf(top, fmaf(m4, cg[g], lift[g]));
+            }
+          } else {
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 64; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                t4[k] = max3(t4[k], __uint_as_float(s[i >> 5][(i & 31) + 2 * k]),
+                             __uint_as_float(s[i >> 5][(i & 31) + 2 * k + 1]));
+            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          }
           mine[sb * 2 * kTile] = top;
           asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-          top = fmaxf(top, other[sb * 2 * kTile]) * cr;
+          top = fmaxf(top, other[sb * 2 * kTile]) * (PAGED ? 1.0f : cr);
           // a new reference where some row's maximum has left the old one behind
           if (__any_sync(0xFFFFFFFFu, top > m + (kLift<FP8> + kSlack<FP8>))) {
             const float mn = fmaxf(m, top - kLift<FP8>);
@@ -836,18 +887,28 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           }
           const float use = m == -INFINITY ? 0.0f : m;  // a row without keys so far
           uint64_t sum[2] = {0, 0};
-          const uint64_t c2 = f32x2(cr, cr), use2 = f32x2(-use, -use);
+          float s0, s1, both = 0.0f;
           uint32_t p[32];
+          const uint64_t c2 = f32x2(cr, cr), use2 = f32x2(-use, -use);
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             float x, y;
+            const int g = k >> 3;
+            const uint64_t by = PAGED ? f32x2(cg[g], cg[g]) : c2;
+            const uint64_t plus = PAGED ? f32x2(lift[g] - use, lift[g] - use) : use2;
             f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[k >> 4][(2 * k) & 31]),
-                                        __uint_as_float(s[k >> 4][(2 * k + 1) & 31])), c2, use2),
+                                        __uint_as_float(s[k >> 4][(2 * k + 1) & 31])), by, plus),
                         x, y);
             x = exp2_approx(x);
             y = exp2_approx(y);
             sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
             p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+            if (PAGED && (k & 7) == 7) {
+              // the weights themselves: without the values' scale
+              f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
+              both = fmaf(s0 + s1, exp2_approx(-lift[g]), both);
+              sum[0] = sum[1] = 0;
+            }
           }
           if (n > 1) {                                  // P V (n - 2) has read its weights
             mbar_wait(&bars->pv_done[sb], ((n - 2) >> 1) & 1u, a.status, abort);
@@ -855,9 +916,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             tc_fence_after();
           }
           tmem_st_32x32b_x32(tp + sb * 64, p);
-          float s0, s1;
           f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
+          l += PAGED ? both : s0 + s1;
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&bars->p_ready[sb]);
@@ -869,7 +929,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       const int head_out = head;
       const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + slot) * kTile + row;
       const float v_scale =
-          FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
+          FP8 && !PAGED && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
       const uint32_t end = n - 1;                       // the last tile
       more = left > 0;
       if (more) {
@@ -956,7 +1016,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         left -= stop - t;
         const int64_t at =
             (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.b.t0 ? 1 : 0)) * kTile;
-        mend_rows<D, FP8>(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
+        mend_rows<D, FP8, PAGED>(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
                   whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp,
                   kSoftmaxThreads / 32);
         if (left > 0 && !wk.next(a, group)) break;
@@ -971,12 +1031,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGED = false>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
-  using C = Cfg<D, FP8>;
-  auto kernel = attention_chunk_kernel<D, FP8>;
+  using C = Cfg<D, FP8, PAGED>;
+  auto kernel = attention_chunk_kernel<D, FP8, PAGED>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
   // its prologue overlaps the plan; it waits for the plan before it reads anything
@@ -1002,6 +1062,9 @@ cudaError_t launch_attn_plan(const AttnArgs& a, int grid, cudaStream_t stream) {
 
 cudaError_t launch_attention_chunk(const AttnArgs& a, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int grid, cudaStream_t stream) {
+  if (a.cache.paged)
+    return a.cache.head_dim == 128 ? launch<128, true, true>(a, map_k, map_v, grid, stream)
+                                   : launch<64, true, true>(a, map_k, map_v, grid, stream);
   if (a.cache.fp8)
     return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
                                    : launch<64, true>(a, map_k, map_v, grid, stream);

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
   const int64_t t = p.first + tok;
   const int head = p.head * group + p.row0 + row - tok * group;
   float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (a.cache.v_scale != nullptr) inv *= a.cache.v_scale[p.head];
+  if (a.cache.v_scale != nullptr && !a.cache.paged) inv *= a.cache.v_scale[p.head];
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out.data) + t * a.out.token_stride +
                             head * a.out.head_stride + d) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));

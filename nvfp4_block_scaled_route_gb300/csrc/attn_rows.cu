@@ -90,12 +90,17 @@ struct Bars {
   long long tile;
 };
 
-template <int D, bool FP8>
+// Scales of a key tile's pages (PAGED): eight of keys, a warp's 16 keys each, and
+// eight of values; key tiles take every second buffer of a ring.
+constexpr int kTileScales = 16;
+
+template <int D, bool FP8, bool PAGED>
 constexpr int smem_bytes() {
   constexpr int rows = kRows, groups = kGroups<FP8>;
   return 1024 + Tile<D, FP8>::kBufs * Tile<D, FP8>::kBytes + rows * D * 2 +
          groups * (rows * kKeys * 2 + rows * kComputeWarps * 4) + rows * 4 +
-         (groups - 1) * (rows * D * 4 + rows * 8) + static_cast<int>(sizeof(Bars));
+         (groups - 1) * (rows * D * 4 + rows * 8) + static_cast<int>(sizeof(Bars)) +
+         (PAGED ? kMaxBufs / 2 * kTileScales * 4 : 0);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -168,7 +173,7 @@ struct Walk {
   }
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGED>
 __global__ void __launch_bounds__(kThreads<FP8>, 1)
 attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
@@ -185,6 +190,8 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   float* join_o = sfac + kRows;                       // second group's sums, by thread
   float2* join_ml = reinterpret_cast<float2*>(join_o + (kG - 1) * kRows * D);  // [kRows]
   Bars* bars = reinterpret_cast<Bars*>(join_ml + (kG - 1) * kRows);
+  float* scales = reinterpret_cast<float*>(bars + 1);    // [key buffer][kTileScales]
+  static_assert(!PAGED || kPer % 2 == 0, "key tiles in every second buffer");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();                                       // for what came before
@@ -208,7 +215,8 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   if (lane == 31) scan[warp] = upto;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kG * kPer; ++i) {
-      mbar_init(&bars->full[i], 1);
+      // (and the producer's lanes with their copies of scales)
+      mbar_init(&bars->full[i], PAGED && i % 2 == 0 ? 33 : 1);
       mbar_init(&bars->empty[i], kComputeWarps);
     }
     bars->abort = 0;
@@ -300,6 +308,17 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
             tma_load_4d(ring + n * T::kBytes + half * kKeys * T::kLine + b * box * T::kLine,
                         kv == 0 ? &map_k : &map_v, half * (T::kLine / (FP8 ? 1 : 2)), in_page,
                         wk.h, page, &bars->full[n], policy);
+          if (PAGED && kv == 0) {
+            // the scales of each 16 keys: lanes 8-15 those of keys, 16-23 of values
+            const int i = lane & 7, k16 = t * kKeys + i * 16;
+            if (lane >= 8 && lane < 24) {
+              const int64_t from = k16 < kend && k16 + 16 > kbeg ? page_of(a, wk.r, k16) : -1;
+              const float* src = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
+              cp_async_4(scales + n / 2 * kTileScales + lane - 8,
+                         src + (from < 0 ? 0 : from * a.cache.heads + wk.h), from >= 0);
+            }
+            cp_async_arrive(&bars->full[n]);
+          }
           if (++buf[side] == kPer) {
             buf[side] = 0;
             phase[side] ^= 1u;
@@ -312,6 +331,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         t = wk.sp.t0;
       }
     }
+    if (PAGED) cp_async_wait_all();
     __syncthreads();
     drain_after_abort(abort);
     return;
@@ -346,7 +366,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const int slot = t == wk.sp.t0 ? 1 : 0;         // a cut segment: begun here, or before
     left -= stop - t;
     float c = a.scale * 1.4426950408889634f;        // scores in powers of two
-    if (FP8 && a.cache.k_scale != nullptr) c *= a.cache.k_scale[wk.h];
+    if (FP8 && !PAGED && a.cache.k_scale != nullptr) c *= a.cache.k_scale[wk.h];
 
     // queries to shared memory
     constexpr int kLanes = D / 8;
@@ -445,6 +465,16 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
           }
         }
       }
+      // The scales of the pages of these 16 keys.  That of the values goes into the
+      // 16-bit weights, p v_scale, and so the reference is one of s + log2(v_scale):
+      // the products that are summed are at most 2^kLift, whatever the scales.
+      float ks = 1.0f, vs = 1.0f, lift = 0.0f;
+      if (PAGED) {
+        const float* sc = scales + (side * kPer + buf) / 2 * kTileScales + w;
+        ks = page_scale(sc[0]);
+        vs = page_scale(sc[8]);
+        lift = static_cast<float>(static_cast<int>((__float_as_uint(vs) + 0x7FFFFFu) >> 23) - 127);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[buf]);
       next_buffer();
@@ -458,7 +488,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& x = s[n][2 * e + j];
-            x *= cr[e];
+            x *= PAGED ? cr[e] * ks : cr[e];
             if (masked) {
               const int key = key0 + w * 16 + n * 8 + c2 + j;
               if (key >= vis_hi[e] || key < vis_lo[e]) x = -INFINITY;
@@ -467,7 +497,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
           }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        if ((lane & 3) == 0) smax[(e * 8 + g) * kComputeWarps + w] = top;
+        if ((lane & 3) == 0) smax[(e * 8 + g) * kComputeWarps + w] = PAGED ? top + lift : top;
       }
       group_sync(side);
 #pragma unroll
@@ -488,7 +518,8 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
           const float p1 = exp2_approx(s[n][2 * e + 1] - use);
           sum += p0 + p1;
           *reinterpret_cast<uint32_t*>(sp_ + mat_at<kPRow>(row, w * 2 + n) + c2 * 2) =
-              FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              PAGED ? pack_f16x2(p0 * vs, p1 * vs)
+                    : (FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1));
         }
         l[e] = fmaf(l[e], f, sum);
 #pragma unroll
@@ -614,7 +645,7 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         }
       }
     }
-    const float v_scale = FP8 && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
+    const float v_scale = FP8 && !PAGED && a.cache.v_scale != nullptr ? a.cache.v_scale[wk.h] : 1.0f;
     const int64_t pc = 2 * static_cast<int64_t>(blockIdx.x) + slot;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -705,19 +736,19 @@ attention_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const int kend = min(wk.rq.len, wk.rq.pos0 + wk.rq.n);
     const int64_t at =
         (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows;
-    mend_rows<D, FP8>(a, wk.r, wk.h, 0, wk.rq.n * group, kbeg, kend, t, stop,
+    mend_rows<D, FP8, PAGED>(a, wk.r, wk.h, 0, wk.rq.n * group, kbeg, kend, t, stop,
               whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp, kG * kComputeWarps);
     if (left > 0 && !wk.next_segment(a)) break;
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGED = false>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
-  constexpr int bytes = smem_bytes<D, FP8>();
+  constexpr int bytes = smem_bytes<D, FP8, PAGED>();
   static_assert(bytes <= 232448, "shared memory");
-  auto kernel = attention_rows_kernel<D, FP8>;
+  auto kernel = attention_rows_kernel<D, FP8, PAGED>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), bytes);
   if (e != cudaSuccess) return e;
   // its start overlaps the end of the kernel before
@@ -738,6 +769,9 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
 
 cudaError_t launch_attention_rows(const AttnArgs& a, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream) {
+  if (a.cache.paged)
+    return a.cache.head_dim == 128 ? launch<128, true, true>(a, map_k, map_v, grid, stream)
+                                   : launch<64, true, true>(a, map_k, map_v, grid, stream);
   if (a.cache.fp8)
     return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
                                    : launch<64, true>(a, map_k, map_v, grid, stream);

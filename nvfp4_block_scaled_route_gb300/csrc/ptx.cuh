@@ -144,6 +144,21 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Four bytes to shared memory, zeros where `take` is false (src is then not read);
+// cp_async_arrive: an arrival on `bar` once the calling thread's copies so far have
+// landed (counted in the barrier's number of arrivals).
+__device__ __forceinline__ void cp_async_4(void* smem_dst, const void* gmem_src, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+               ::"r"(smem_u32(smem_dst)), "l"(gmem_src), "r"(take ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- TMA ----
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map,
                                             int32_t x, int32_t y, uint64_t* bar,

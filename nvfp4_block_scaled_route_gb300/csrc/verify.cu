@@ -1,0 +1,321 @@
+// Drafted tokens held against the target's probabilities, with given random numbers.
+//
+// Request r has the rows s .. s + n of target and draft (n drafted tokens); row i of
+// either is the distribution of token i + 1.  Token s + i + 1 stands while
+// u_i q(x) < p(x), in order; the token after the last one that stands is drawn by the
+// inverse of the running sum from p of that row, or, where a drafted token was turned
+// down, from max(p - q, 0): the first token whose running sum passes v times the whole.
+// So what is drawn has the target's distribution, whatever the draft's (Leviathan,
+// Kalman and Matias, "Fast Inference from Transformers via Speculative Decoding", 2023).
+//
+// Of all the rows only one of p, and of q, is read whole: the bound is HBM for large
+// batches, for few requests the launch and four dependent loads.  A cluster takes a
+// request, its CTAs and their warps one run of the vocabulary each.  They find the sums
+// of the runs, exchange them through distributed shared memory, and the warp in whose
+// run the sum is passed reads that once more (from L2) to find the token.
+//
+// Which token that is must not hang on how a sum is rounded: a row of 2^17 tokens has
+// as many borders, and fp32 sums would put the wrong token out for every few hundredth
+// row.  A lane sums pairs of fp32 numbers, value and rest: p - q is exact that way, and
+// a sum is off by some 2^-45 of itself; lanes, warps and CTAs are joined in fp64.  (fp64
+// for each value would take longer than its load: 2 adds a cycle and SM.)
+#include <cuda_bf16.h>
+
+#include "serve.cuh"
+
+namespace nvmoe {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8;
+
+// Within [0, 1]; NaN is 0.
+__device__ __forceinline__ float probability(float x) { return __saturatef(x); }
+__device__ __forceinline__ float load_one(const float* p) { return *p; }
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// A sum of fp32 numbers as a value and what it lacks.
+struct Sum {
+  float hi = 0.0f, lo = 0.0f;
+  // (Knuth's exact sum of two numbers: hi + x = t + rest)
+  __device__ __forceinline__ void add(float x, float rest_x) {
+    const float t = hi + x, b = t - hi;
+    lo += (hi - (t - b)) + (x - b) + rest_x;
+    hi = t;
+  }
+  __device__ __forceinline__ double value() const {
+    return static_cast<double>(hi) + static_cast<double>(lo);
+  }
+};
+
+// The weights of a row: p, or what p has over q, or p without one token.
+template <typename T>
+struct Row {
+  static constexpr int kVec = 16 / sizeof(T);
+  const T* p;
+  const T* q;                // null: p alone
+  int vocab, without;        // a token that does not count, or -1
+  int shift;                 // elements of p's first 16 bytes that lie before the row
+  bool together;             // q's lie likewise
+
+  __device__ __forceinline__ int vectors() const { return (vocab + shift + kVec - 1) / kVec; }
+  static __device__ __forceinline__ int shift_of(const T* x) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  }
+
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(w[i]);
+      } else {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+  // The elements of vector v of x, zeros outside the row.
+  __device__ __forceinline__ void load(const T* x, int v, bool whole, float (&out)[kVec]) const {
+    const int e0 = v * kVec - shift;
+    if (whole && e0 >= 0 && e0 + kVec <= vocab) {
+      unpack(*reinterpret_cast<const uint4*>(x + e0), out);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        const int e = e0 + k;
+        out[k] = e >= 0 && e < vocab ? load_one(x + e) : 0.0f;
+      }
+    }
+  }
+  // Weights of vector v: value and rest, exact (where p >= q: p - q and what that
+  // difference lacks).
+  __device__ __forceinline__ void weigh(int v, const float (&pv)[kVec], const float (&qv)[kVec],
+                                        float (&w)[kVec], float (&rest)[kVec]) const {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const float a = probability(pv[k]), b = probability(qv[k]);
+      const float d = a - b;
+      const bool more = a > b && v * kVec - shift + k != without;
+      w[k] = more ? d : 0.0f;
+      rest[k] = more ? (a - d) - b : 0.0f;
+    }
+  }
+  __device__ __forceinline__ double weight(int e) const {
+    if (e >= vocab || e == without) return 0.0;
+    const double a = probability(load_one(p + e));
+    const double b = q != nullptr ? static_cast<double>(probability(load_one(q + e))) : 0.0;
+    return a > b ? a - b : 0.0;
+  }
+
+  // A lane's sum over the vectors v0, v0 + step, .. below v1.
+  __device__ __forceinline__ double sum(int v0, int v1, int step) const {
+    constexpr int kUnroll = 16 / kVec;                  // 64 bytes of a row in flight: more spill
+    Sum s[2];
+    for (int v = v0; v < v1; v += kUnroll * step) {
+      float pv[kUnroll][kVec], qv[kUnroll][kVec];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) pv[u][k] = qv[u][k] = 0.0f;
+        if (v + u * step < v1) {
+          load(p, v + u * step, true, pv[u]);
+          if (q != nullptr) load(q, v + u * step, together, qv[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float w[kVec], rest[kVec];
+        weigh(v + u * step, pv[u], qv[u], w, rest);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) s[k & 1].add(w[k], rest[k]);
+      }
+    }
+    return s[0].value() + s[1].value();
+  }
+};
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ double scan_lanes(double x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Of the lanes' runs, `upto` the sum to the end of each and `own` that of the run: the
+// first that passes x, else (by rounding) the last that holds anything; -1 if none does.
+__device__ __forceinline__ int pick(double upto, double own, double x) {
+  const uint32_t passed = __ballot_sync(0xFFFFFFFFu, own > 0.0 && upto > x);
+  if (passed != 0) return __ffs(passed) - 1;
+  const uint32_t any = __ballot_sync(0xFFFFFFFFu, own > 0.0);
+  return any != 0 ? 31 - __clz(any) : -1;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyArgs a) {
+  __shared__ double cta_sum[2][kMaxCtas], warp_sum[kWarps];
+  __shared__ int stands;
+  pdl_wait();
+  const int r = blockIdx.x / cluster_size(), rank = static_cast<int>(cluster_ctarank());
+  const int ctas = static_cast<int>(cluster_size());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t begin = a.q_start[r], end = a.q_start[r + 1];
+  const bool bad = begin < 0 || end < begin || end > a.rows;
+  const int n = bad ? -1 : static_cast<int>(end - begin) - 1;        // drafted tokens
+  if (n < 0) {                                          // (the whole cluster)
+    if (rank == 0 && threadIdx.x == 0) {
+      if (bad) record_status(a.status, kErrBadIndex);
+      a.accepted[r] = 0;
+      a.next_token[r] = -1;
+      if (a.cached != nullptr) a.cached[r] = a.kv_len[r];
+    }
+    return;
+  }
+  cluster_arrive_relaxed();                             // (started: waited for below)
+  const T* target = static_cast<const T*>(a.target) + begin * a.target_stride;
+  const T* draft = a.draft == nullptr ? nullptr
+                                      : static_cast<const T*>(a.draft) + begin * a.draft_stride;
+  // ---- how many stand: a lane a token ----
+  if (warp == 0) {
+    int k = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      bool ok = false;
+      if (i < n) {
+        const int x = a.tokens[begin + i + 1];
+        if (x < 0 || x >= a.vocab) {
+          record_status(a.status, kErrBadIndex);        // does not stand
+        } else {
+          const float p = probability(load_one(target + i * a.target_stride + x));
+          const float q =
+              draft != nullptr ? probability(load_one(draft + i * a.draft_stride + x)) : 1.0f;
+          // (a product of two fp32 numbers is exact in fp64)
+          ok = static_cast<double>(a.accept_u[begin + i]) * q < static_cast<double>(p);
+        }
+      }
+      const uint32_t not_ok = ~__ballot_sync(0xFFFFFFFFu, ok);
+      if (not_ok != 0) {
+        k = i0 + __ffs(not_ok) - 1;
+        break;
+      }
+      k = i0 + 32;
+    }
+    if (lane == 0) stands = min(k, n);
+  }
+  __syncthreads();
+  const int k = stands;
+  Row<T> row;
+  row.p = target + k * a.target_stride;
+  row.q = k < n && draft != nullptr ? draft + k * a.draft_stride : nullptr;
+  row.vocab = a.vocab;
+  row.without = k < n && draft == nullptr ? a.tokens[begin + k + 1] : -1;
+  row.shift = Row<T>::shift_of(row.p);
+  row.together = row.q != nullptr && Row<T>::shift_of(row.q) == row.shift;
+
+  const int runs = ctas * kWarps, run = rank * kWarps + warp;
+  const long long vectors = row.vectors();
+  const int v0 = static_cast<int>(vectors * run / runs);
+  const int v1 = static_cast<int>(vectors * (run + 1) / runs);
+  double whole = 0.0;
+  int winner = -1;
+  for (int round = 0; round < 2; ++round) {
+    double s = row.sum(v0 + lane, v1, 32);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) warp_sum[warp] = s;
+    __syncthreads();
+    if (round == 0) cluster_wait();                     // the others' shared memory is there
+    if (warp == 0) {
+      double t = lane < kWarps ? warp_sum[lane] : 0.0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      if (lane < ctas) st_cluster_f64(&cta_sum[round][rank], lane, t);
+    }
+    cluster_sync();
+    whole = 0.0;
+    for (int c = 0; c < ctas; ++c) whole += cta_sum[round][c];
+    winner = round;
+    // nothing left over: the target's own row (and if that holds nothing, no token)
+    if (whole > 0.0 || (row.q == nullptr && row.without < 0)) break;
+    row.q = nullptr;
+    row.without = -1;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    a.accepted[r] = k;
+    if (a.cached != nullptr) a.cached[r] = a.kv_len[r] - (n - k);
+    if (!(whole > 0.0)) {
+      record_status(a.status, kErrRange);
+      a.next_token[r] = -1;
+    }
+  }
+  if (!(whole > 0.0)) return;
+
+  // ---- the run in which the sum passes x: CTA, then warp ----
+  const double x = fmax(static_cast<double>(a.sample_u[r]) * whole, 0.0);   // (NaN: 0)
+  double own = lane < ctas ? cta_sum[winner][lane] : 0.0;
+  double upto = scan_lanes(own);
+  const int cta = pick(upto, own, x);
+  if (cta != rank) return;
+  const double before_cta = __shfl_sync(0xFFFFFFFFu, upto - own, cta);
+  own = lane < kWarps ? warp_sum[lane] : 0.0;
+  upto = before_cta + scan_lanes(own);
+  const int w = pick(upto, own, x);
+  if (w != warp) return;
+  const double before_warp = __shfl_sync(0xFFFFFFFFu, upto - own, w);
+  // ---- a lane takes neighbouring vectors; the one that passes x ----
+  const int per = (v1 - v0 + 31) / 32;
+  const int a0 = min(v1, v0 + lane * per), a1 = min(v1, a0 + per);
+  own = row.sum(a0, a1, 1);
+  upto = before_warp + scan_lanes(own);
+  const int l = pick(upto, own, x);
+  double base = __shfl_sync(0xFFFFFFFFu, upto - own, l);
+  // ---- its elements, a lane each ----
+  const int e0 = max(0, __shfl_sync(0xFFFFFFFFu, a0, l) * Row<T>::kVec - row.shift);
+  const int e1 = min(a.vocab, __shfl_sync(0xFFFFFFFFu, a1, l) * Row<T>::kVec - row.shift);
+  int token = -1;
+  for (int e = e0; e < e1; e += 32) {
+    own = e + lane < e1 ? row.weight(e + lane) : 0.0;
+    upto = base + scan_lanes(own);
+    const uint32_t passed = __ballot_sync(0xFFFFFFFFu, own > 0.0 && upto > x);
+    if (passed != 0) {
+      token = e + __ffs(passed) - 1;
+      break;
+    }
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, own > 0.0);
+    if (any != 0) token = e + 31 - __clz(any);
+    base = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  if (lane == 0) a.next_token[r] = token;
+}
+
+template <typename T>
+cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
+  // a CTA for every 4096 tokens, up to 8
+  int ctas = 1;
+  while (ctas < kMaxCtas && a.vocab > int64_t{ctas} * 4096) ctas *= 2;
+  // its start overlaps the end of the kernel before
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, draft_verify_kernel<T>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_draft_verify(const VerifyArgs& a, cudaStream_t stream) {
+  return a.bf16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+}
+
+}  // namespace nvmoe
