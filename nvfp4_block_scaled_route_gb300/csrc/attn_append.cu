@@ -27,15 +27,19 @@ struct PageUnits {
   uint32_t blocks;
 };
 
-template <int D, int THREADS, int R, bool TOKENS, bool PAIRS>
-__global__ void __launch_bounds__(THREADS)
+// A thread holds R tokens' eight bf16 as they came, and turns them twice, for the largest
+// and for the store: 64 registers a thread, as the queries' rows take (which are most of
+// the bytes, in the same launch).
+constexpr int kR = 4;
+
+template <int D, int THREADS, int HEADS, bool TOKENS, bool PAIRS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 page_append_kernel(const RopeArgs a, const PageUnits units) {
-  constexpr int kLanes = D / 8, kGroups = THREADS / kLanes, kRound = kGroups * R;
-  constexpr int kHeads = TOKENS ? 2 : 4;                // of a group of lanes, of q
+  constexpr int R = kR, kLanes = D / 8, kGroups = THREADS / kLanes, kRound = kGroups * R;
   __shared__ float warp_max[THREADS / 32];
   pdl_wait();                                           // for what came before
   if (blockIdx.x >= units.blocks) {
-    transform_heads<D, kHeads, true, PAIRS, false>(
+    transform_heads<D, HEADS, true, PAIRS, false>(
         a, (blockIdx.x - units.blocks) * kGroups + threadIdx.x / kLanes);
     return;
   }
@@ -109,51 +113,68 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
   const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(src.data) +
                             (p0 - to_pos) * src.token_stride + head * src.head_stride;
 
-  // Up to kRound tokens are held in registers from the search for the largest to the
-  // store; more (pages of D * page_size > THREADS * 8 * R) are read and turned twice.
+  // Up to kRound tokens stay in registers from the search for the largest to the store;
+  // more (pages of D * page_size > 512 * 8 * R) are read twice.
   const int rounds = (count + kRound - 1) / kRound;
-  const int steps = rounds == 1 ? 1 : 2 * rounds;
+  const int steps = 2 * rounds;
   float most = 0.0f, by = 1.0f, inv = 1.0f;
   bool exact = true;
+  uint2 raw[R][2];
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
     const int base = (step < rounds ? step : step - rounds) * kRound + group;
-    uint64_t x[R][2][2];
-    uint2 raw[R][2];
+    if (step == 0 || rounds > 1) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int j = base + i * kGroups;
-      raw[i][0] = raw[i][1] = make_uint2(0, 0);
-      if (j < count) {
-        const __nv_bfloat16* p = in + j * src.token_stride;
-        raw[i][0] = *reinterpret_cast<const uint2*>(p + i0);
-        raw[i][1] = *reinterpret_cast<const uint2*>(p + i1);
+      for (int i = 0; i < R; ++i) {
+        const int j = base + i * kGroups;
+        if (j < count) {
+          const __nv_bfloat16* p = in + j * src.token_stride;
+          raw[i][0] = *reinterpret_cast<const uint2*>(p + i0);
+          raw[i][1] = *reinterpret_cast<const uint2*>(p + i1);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int j = base + i * kGroups;
-      bf16x4_to_f32x2(raw[i][0], x[i][0]);
-      bf16x4_to_f32x2(raw[i][1], x[i][1]);
-      if (!value && j < count) {
+      if (j >= count) break;
+      uint64_t x[2][2];
+      bf16x4_to_f32x2(raw[i][0], x[0]);
+      bf16x4_to_f32x2(raw[i][1], x[1]);
+      if (!value) {
         HeadTurn<D, PAIRS> turn;
         turn.load(a.tr, a.tr.k_weight, false, sub, i0, i1, p0 + j);
-        turn.apply(x[i], a.tr.eps, mask);
+        turn.apply(x, a.tr.eps, mask);
       }
-    }
-    if (step < rounds) {
-      // (infinities saturate and NaN stays NaN: neither counts for the scale)
-#pragma unroll
-      for (int i = 0; i < R; ++i)
+      if (step < rounds) {
+        // (infinities saturate and NaN stays NaN: neither counts for the scale)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float u, v;
-          f32x2_split(x[i][k >> 1][k & 1], u, v);
+          f32x2_split(x[k >> 1][k & 1], u, v);
           u = fabsf(u);
           v = fabsf(v);
           most = fmaxf(most, u < INFINITY ? u : 0.0f);
           most = fmaxf(most, v < INFINITY ? v : 0.0f);
         }
+      } else {
+        uint8_t* p = out + (old + j) * a.cache.token_stride;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          float z[4];
+          f32x2_split(x[s][0], z[0], z[1]);
+          f32x2_split(x[s][1], z[2], z[3]);
+          if (exact) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] *= inv;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] /= by;
+          }
+          *reinterpret_cast<uint32_t*>(p + (s == 0 ? i0 : i1)) =
+              pack_e4m3x2(z[0], z[1]) | (pack_e4m3x2(z[2], z[3]) << 16);
+        }
+      }
     }
     if (step == rounds - 1) {
       // ---- the scale ----
@@ -197,24 +218,6 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
       exact = (__float_as_uint(by) & 0x7FFFFFu) == 0;
       inv = 1.0f / by;
     }
-    if (rounds == 1 || step >= rounds) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int j = base + i * kGroups;
-        if (j >= count) continue;
-        uint8_t* p = out + (old + j) * a.cache.token_stride;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          float z[4];
-          f32x2_split(x[i][s][0], z[0], z[1]);
-          f32x2_split(x[i][s][1], z[2], z[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) z[k] = exact ? z[k] * inv : z[k] / by;
-          *reinterpret_cast<uint32_t*>(p + (s == 0 ? i0 : i1)) =
-              pack_e4m3x2(z[0], z[1]) | (pack_e4m3x2(z[2], z[3]) << 16);
-        }
-      }
-    }
   }
 }
 
@@ -244,13 +247,12 @@ cudaError_t launch_d(RopeArgs a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a, units);
   };
-  // threads and tokens of a thread so that a page's new tokens stay in registers
+  // threads so that a page's new tokens stay in registers
   if (tokens) return go(page_append_kernel<D, 128, 2, true, PAIRS>, 128, 2);
   const int64_t elements = page * D;
-  if (elements <= 128 * 8 * 2) return go(page_append_kernel<D, 128, 2, false, PAIRS>, 128, 4);
-  if (elements <= 128 * 8 * 8) return go(page_append_kernel<D, 128, 8, false, PAIRS>, 128, 4);
-  if (elements <= 256 * 8 * 8) return go(page_append_kernel<D, 256, 8, false, PAIRS>, 256, 4);
-  return go(page_append_kernel<D, 512, 8, false, PAIRS>, 512, 4);
+  if (elements <= 128 * 8 * kR) return go(page_append_kernel<D, 128, 8, false, PAIRS>, 128, 8);
+  if (elements <= 256 * 8 * kR) return go(page_append_kernel<D, 256, 8, false, PAIRS>, 256, 8);
+  return go(page_append_kernel<D, 512, 8, false, PAIRS>, 512, 8);
 }
 
 }  // namespace
