@@ -271,13 +271,17 @@ struct Walk {
   }
 };
 
-// PAGED: scales of the pages of a tile's keys, for each 16 of them, eight of keys and
-// eight of values; slots by the number of the tile.  A slot is written again once S of
-// the tile kK back is done, whose own start had all softmax threads past the scores of
-// the tile two before that: kK + 3 tiles may be in use.
-constexpr int kScaleSlots = 16, kTileScales = 16;
+// PAGED: E4M3 pages with scales of their own, PAGED of them (1 for pages of 64 tokens
+// and more, else 4) in a thread's 64 keys of a tile.  The keys' loader keeps them in
+// slots by the number of the tile, three numbers for each: the keys' scale, the
+// values' as a logarithm and inverted.  A slot is written again once S of the tile kK
+// back is done, whose own start had all softmax threads past the scores of the tile two
+// before that: kK + 3 tiles may be in use.  (With a fourth buffer of keys there is room
+// for eight slots of 1 x 2 x 3.)
+template <int PAGED>
+constexpr int kTileScales = 2 * PAGED;                 // of one kind
 
-template <int D, bool FP8, bool PAGED>
+template <int D, bool FP8, int PAGED>
 struct Cfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kBytes = kKeys * D * 2;         // an operand tile
@@ -287,14 +291,19 @@ struct Cfg {
   static constexpr int kHalves = kRow / kLine;         // column blocks
   // tiles of keys (as loaded), operand tiles of values (bf16: as loaded), raw
   // tiles of E4M3 values
-  static constexpr int kK = (FP8 && !PAGED ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
+  static constexpr int kK = (FP8 && PAGED < 4 ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
   static constexpr int kRaw = FP8 ? (D == 128 ? 2 : 5) : 0;
   static constexpr int kVAt = kBytes;                  // after the queries: values, keys, raw
   static constexpr int kKAt = kVAt + kV * kBytes, kRawAt = kKAt + kK * kLoadBytes;
   static constexpr int kRing = kRawAt + kRaw * kLoadBytes;
-  static constexpr int kScales = kRing + 512 + 5 * kTile * 4;
-  static constexpr int kSmem = kScales + (PAGED ? kScaleSlots * kTileScales * 4 : 0);
-  static_assert(!PAGED || kK + 3 <= kScaleSlots, "slots");
+  // the scales' slots: behind the words of the rows, in what they leave of 5 * kTile * 4
+  // bytes if that does
+  static constexpr int kWords = 4 * kTile * 4 + 2 * kTile;
+  static constexpr int kSlots = kK + 3 <= 8 ? 8 : 16;
+  static constexpr int kScaleBytes = kSlots * 3 * kTileScales<PAGED> * 4;
+  static constexpr int kSmem =
+      kRing + 512 + (kWords + kScaleBytes <= 5 * kTile * 4 ? 5 * kTile * 4 : kWords + kScaleBytes);
+  static_assert(kK + 3 <= kSlots, "slots");
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr uint32_t kTmemO = 256, kTmemP = 384;   // S: columns 0 and 128
   // instruction descriptors: fp16 operands are format 0, bf16 format 1; V is MN-major
@@ -347,7 +356,7 @@ __device__ __forceinline__ uint32_t raw_at(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D, bool FP8, bool PAGED>
+template <int D, bool FP8, int PAGED>
 __global__ void __launch_bounds__(Cfg<D, FP8, PAGED>::kThreads, 1)
 attention_chunk_kernel(const __grid_constant__ AttnArgs a,
                        const __grid_constant__ CUtensorMap map_k,
@@ -365,13 +374,14 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   // E4M3: each query row's power of two, [segment parity][row] (a thread may be
   // a segment ahead of another)
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(swap + 4 * kTile);
-  float* scales = reinterpret_cast<float*>(sq + C::kScales);   // [slot][kTileScales]
+  constexpr int kTS = kTileScales<PAGED>;
+  float* scales = reinterpret_cast<float*>(q_exp + 2 * kTile);  // [slot][3][kTS]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kK + (FP8 ? C::kRaw : C::kV); ++i) {
-      // (and the loader's lanes with their copies of scales)
-      mbar_init(&bars->full[i], PAGED && i < C::kK ? 33 : 1);
+      // (and the loader's lanes that bring scales)
+      mbar_init(&bars->full[i], PAGED && i < C::kK ? 1 + 2 * kTS : 1);
       // the readers: an issuer, or four converting warps
       mbar_init(&bars->empty[i], FP8 && i >= C::kK ? 4 : 1);
     }
@@ -442,9 +452,23 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     int buf = 0;
     uint32_t phase = 0, tiles = 0;                      // tiles with scores so far
     bool ok = true;
+    // Scales: lanes 0 .. kTS-1 bring those of keys, the next kTS those of values; each
+    // is read a tile ahead, so that its way (the page, then the scale) does not hold up
+    // the loads of tiles.
+    const bool brings = PAGED && keys && lane < 2 * kTS;
+    const int part = lane < kTS ? lane : lane - kTS;
+    const auto scale_of = [&](int tile) {
+      const int k = tile * kKeys + part * (kKeys / (kTS > 0 ? kTS : 1));
+      if (k >= wk.b.kend || k + kKeys / (kTS > 0 ? kTS : 1) <= wk.b.kbeg) return kScaleLow;
+      const int64_t from = page_of(a, wk.r, k);
+      if (from < 0) return kScaleLow;                   // (of zeros)
+      return page_scale((lane < kTS ? a.cache.k_scale : a.cache.v_scale)[from * a.cache.heads + wk.h]);
+    };
+    float scale = kScaleLow;
     while (left > 0 && ok) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       left -= stop - t;
+      if (brings) scale = scale_of(t);
       // the segment's queries to L2, ahead of the softmax warps' loads
       if (keys)
         for (int i = lane; i < wk.b.rows; i += 32) {
@@ -481,20 +505,19 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           const int x = half * (FP8 ? C::kLine : C::kLine / 2);
           tma_load_4d(dst, map, x, in_page, wk.h, page, &bars->full[n], policy);
         }
-        if (PAGED && keys) {
-          // the scales of each 16 keys: lanes 8-15 those of keys, 16-23 of values
+        if (brings) {
           if (wk.b.kend > 0) {
-            const int k16 = t * kKeys + (lane & 7) * 16;
-            if (lane >= 8 && lane < 24) {
-              const int64_t from =
-                  k16 < wk.b.kend && k16 + 16 > wk.b.kbeg ? page_of(a, wk.r, k16) : -1;
-              const float* src = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
-              cp_async_4(scales + tiles % kScaleSlots * kTileScales + lane - 8,
-                         src + (from < 0 ? 0 : from * a.cache.heads + wk.h), from >= 0);
+            float* to = scales + tiles % C::kSlots * (3 * kTS) + part;
+            if (lane < kTS) {
+              to[0] = scale;
+            } else {
+              to[kTS] = log2f(scale);
+              to[2 * kTS] = 1.0f / scale;
             }
             ++tiles;
           }
-          cp_async_arrive(&bars->full[n]);
+          mbar_arrive(&bars->full[n]);
+          if (t + 1 < stop) scale = scale_of(t + 1);
         }
         if (++buf == bufs) {
           buf = 0;
@@ -506,7 +529,6 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         t = wk.b.t0;
       }
     }
-    if (PAGED && keys) cp_async_wait_all();
   } else if (FP8 && warp >= kConvert) {
     // ---- E4M3 values to fp16: 16 bytes at a time, eight rows of one column side
     // by side (no bank conflicts either way) ----
@@ -796,10 +818,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           mbar_wait(&bars->s_full[sb], (n >> 1) & 1u, a.status, abort);
           // (S follows the arrivals of all that wrote the queries and their factors)
           if (FP8 && j == j0)
-            // (not 0, which would make NaN of the -inf of a hidden key)
-            cr = fmaxf(0x1p-126f,
+            // (not 0, which would make NaN of the -inf of a hidden key; nor when the scale
+            // of a page comes in, or infinite then)
+            cr = fmaxf(PAGED ? 0x1p-86f : 0x1p-126f,
                        c * __uint_as_float(static_cast<uint32_t>(q_exp[seg_now * kTile + row])
                                            << 23));
+          if (PAGED) cr = fminf(cr, 0x1p86f);
           if (!busy) {                                  // what these rows hold is not used
             mbar_arrive(&bars->s_free[sb]);
             if (n > 1) mbar_wait(&bars->pv_done[sb], ((n - 2) >> 1) & 1u, a.status, abort);
@@ -827,26 +851,25 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
               if (i < lw) s[i >> 5][i & 31] = 0xFF800000u;
           }
           float top;
-          // PAGED: of each 16 keys the factor of a score and the power of two that the
-          // values' scale adds to a weight
-          float cg[4], lift[4];
+          // PAGED: the factor of the scores of a page's keys, and the power of two that
+          // the values' scale adds to a weight, taken along in the exponent: the
+          // reference is one of s + log2(scale)
+          constexpr int kG = PAGED ? PAGED : 1;
+          float cg[kG], lift[kG], inv_scale[kG];
           if (PAGED) {
-            const float4* sc = reinterpret_cast<const float4*>(
-                scales + n % kScaleSlots * kTileScales + half * 4);
-            const float4 ks = sc[0], vs = sc[2];
-            const float kg[4] = {ks.x, ks.y, ks.z, ks.w}, vg[4] = {vs.x, vs.y, vs.z, vs.w};
+            const float* sc = scales + n % C::kSlots * (3 * kTS) + half * PAGED;
             top = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              // (finite and not 0: the score may be -inf or 0)
-              cg[g] = fminf(fmaxf(cr * page_scale(kg[g]), 0x1p-126f), 0x1p126f);
-              lift[g] = log2f(page_scale(vg[g]));
-              float m4 = -INFINITY;
+            for (int g = 0; g < kG; ++g) {
+              cg[g] = cr * sc[g];
+              lift[g] = sc[kTS + g];
+              inv_scale[g] = sc[2 * kTS + g];
+              float m4[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 16 * g; i < 16 * g + 16; i += 2)
-                m4 = max3(m4, __uint_as_float(s[i >> 5][i & 31]),
-                          __uint_as_float(s[i >> 5][(i & 31) + 1]));
-              top = fmaxf(top, fmaf(m4, cg[g], lift[g]));
+              for (int i = 64 / kG * g; i < 64 / kG * (g + 1); i += 2)
+                m4[(i >> 1) & 1] = max3(m4[(i >> 1) & 1], __uint_as_float(s[i >> 5][i & 31]),
+                                        __uint_as_float(s[i >> 5][(i & 31) + 1]));
+              top = fmaxf(top, fmaf(fmaxf(m4[0], m4[1]), cg[g], lift[g]));
             }
           } else {
             float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -893,7 +916,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             float x, y;
-            const int g = k >> 3;
+            const int g = k / (32 / kG);
             const uint64_t by = PAGED ? f32x2(cg[g], cg[g]) : c2;
             const uint64_t plus = PAGED ? f32x2(lift[g] - use, lift[g] - use) : use2;
             f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[k >> 4][(2 * k) & 31]),
@@ -903,10 +926,10 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             y = exp2_approx(y);
             sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
             p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-            if (PAGED && (k & 7) == 7) {
+            if (PAGED && k % (32 / kG) == 32 / kG - 1) {
               // the weights themselves: without the values' scale
               f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
-              both = fmaf(s0 + s1, exp2_approx(-lift[g]), both);
+              both = fmaf(s0 + s1, inv_scale[g], both);
               sum[0] = sum[1] = 0;
             }
           }
@@ -1016,7 +1039,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         left -= stop - t;
         const int64_t at =
             (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.b.t0 ? 1 : 0)) * kTile;
-        mend_rows<D, FP8, PAGED>(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
+        mend_rows<D, FP8, PAGED != 0>(a, wk.r, wk.h, wk.b.row0, wk.b.rows, wk.b.kbeg, wk.b.kend, t, stop,
                   whole ? nullptr : a.piece_o + at * D, a.piece_ml + at, warp,
                   kSoftmaxThreads / 32);
         if (left > 0 && !wk.next(a, group)) break;
@@ -1031,7 +1054,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   }
 }
 
-template <int D, bool FP8, bool PAGED = false>
+template <int D, bool FP8, int PAGED = 0>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
@@ -1062,9 +1085,12 @@ cudaError_t launch_attn_plan(const AttnArgs& a, int grid, cudaStream_t stream) {
 
 cudaError_t launch_attention_chunk(const AttnArgs& a, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int grid, cudaStream_t stream) {
+  if (a.cache.paged && a.cache.page_shift >= 6)
+    return a.cache.head_dim == 128 ? launch<128, true, 1>(a, map_k, map_v, grid, stream)
+                                   : launch<64, true, 1>(a, map_k, map_v, grid, stream);
   if (a.cache.paged)
-    return a.cache.head_dim == 128 ? launch<128, true, true>(a, map_k, map_v, grid, stream)
-                                   : launch<64, true, true>(a, map_k, map_v, grid, stream);
+    return a.cache.head_dim == 128 ? launch<128, true, 4>(a, map_k, map_v, grid, stream)
+                                   : launch<64, true, 4>(a, map_k, map_v, grid, stream);
   if (a.cache.fp8)
     return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
                                    : launch<64, true>(a, map_k, map_v, grid, stream);
