@@ -1103,7 +1103,9 @@ namespace {
 
 // One side of a paged cache as [num_pages, heads, page_size, D] by its
 // strides; box: 128 bytes of the row (all of it, if shorter) x up to
-// 128 tokens of one page and head.
+// 128 tokens of one page and head.  E4M3 rows are 128 bytes or less: with L2 lines
+// promoted to 256, tokens-first caches also fetched the next head's (64 tokens on up to
+// 16384 keys, pages of 64: 184 us, 156 without).
 bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
@@ -1119,7 +1121,8 @@ bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
                   const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  c.fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
