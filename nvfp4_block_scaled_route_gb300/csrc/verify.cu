@@ -21,6 +21,7 @@
 // for each value would take longer than its load: 2 adds a cycle and SM.)
 #include <cuda_bf16.h>
 
+#include "attn.cuh"
 #include "serve.cuh"
 
 namespace nvmoe {
@@ -34,17 +35,25 @@ __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// A sum of fp32 numbers as a value and what it lacks.
-struct Sum {
-  float hi = 0.0f, lo = 0.0f;
+// Sums of fp32 numbers as a value and what it lacks, two side by side (one instruction
+// for both).
+struct Sums {
+  uint64_t hi = 0, lo = 0;
   // (Knuth's exact sum of two numbers: hi + x = t + rest)
-  __device__ __forceinline__ void add(float x, float rest_x) {
-    const float t = hi + x, b = t - hi;
-    lo += (hi - (t - b)) + (x - b) + rest_x;
+  __device__ __forceinline__ void add(uint64_t x) {
+    const uint64_t t = add_f32x2(hi, x), b = sub(t, hi);
+    lo = add_f32x2(lo, add_f32x2(sub(hi, sub(t, b)), sub(x, b)));
     hi = t;
   }
+  static __device__ __forceinline__ uint64_t sub(uint64_t x, uint64_t y) {
+    return fma_f32x2(y, f32x2(-1.0f, -1.0f), x);        // (a product with -1 is exact)
+  }
   __device__ __forceinline__ double value() const {
-    return static_cast<double>(hi) + static_cast<double>(lo);
+    float a, b, c, d;
+    f32x2_split(hi, a, b);
+    f32x2_split(lo, c, d);
+    return (static_cast<double>(a) + static_cast<double>(b)) +
+           static_cast<double>(c + d);                  // (rests: 2^-24 of the sums)
   }
 };
 
@@ -63,75 +72,93 @@ struct Row {
     return static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   }
 
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        x[i] = __uint_as_float(w[i]);
-      } else {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-  }
-  // The elements of vector v of x, zeros outside the row.
-  __device__ __forceinline__ void load(const T* x, int v, bool whole, float (&out)[kVec]) const {
+  // The elements of vector v of x as they are, zeros outside the row.
+  __device__ __forceinline__ uint4 load(const T* x, int v, bool whole) const {
     const int e0 = v * kVec - shift;
-    if (whole && e0 >= 0 && e0 + kVec <= vocab) {
-      unpack(*reinterpret_cast<const uint4*>(x + e0), out);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) {
-        const int e = e0 + k;
-        out[k] = e >= 0 && e < vocab ? load_one(x + e) : 0.0f;
-      }
-    }
-  }
-  // Weights of vector v: value and rest, exact (where p >= q: p - q and what that
-  // difference lacks).
-  __device__ __forceinline__ void weigh(int v, const float (&pv)[kVec], const float (&qv)[kVec],
-                                        float (&w)[kVec], float (&rest)[kVec]) const {
+    if (whole && e0 >= 0 && e0 + kVec <= vocab) return *reinterpret_cast<const uint4*>(x + e0);
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
-      const float a = probability(pv[k]), b = probability(qv[k]);
-      const float d = a - b;
-      const bool more = a > b && v * kVec - shift + k != without;
-      w[k] = more ? d : 0.0f;
-      rest[k] = more ? (a - d) - b : 0.0f;
+      const int e = e0 + k;
+      if (e < 0 || e >= vocab) continue;
+      if constexpr (sizeof(T) == 4)
+        w[k] = __float_as_uint(x[e]);
+      else
+        w[k / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[e])) << (k % 2 * 16);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // Elements 2 k and 2 k + 1 of a vector.
+  static __device__ __forceinline__ void pair(const uint4& u, int k, float& x, float& y) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 4) {
+      x = __uint_as_float(w[2 * k & 3]);
+      y = __uint_as_float(w[(2 * k + 1) & 3]);
+    } else {
+      x = __uint_as_float(w[k & 3] << 16);
+      y = __uint_as_float(w[k & 3] & 0xFFFF0000u);
+    }
+  }
+  // A vector without element k.
+  static __device__ __forceinline__ uint4 drop(uint4 u, int k) {
+    const int word = k * static_cast<int>(sizeof(T)) / 4;
+    const uint32_t keep = sizeof(T) == 4 ? 0u : (k % 2 == 0 ? 0xFFFF0000u : 0xFFFFu);
+    if (word == 0) u.x &= keep;
+    if (word == 1) u.y &= keep;
+    if (word == 2) u.z &= keep;
+    if (word == 3) u.w &= keep;
+    return u;
   }
   __device__ __forceinline__ double weight(int e) const {
     if (e >= vocab || e == without) return 0.0;
-    const double a = probability(load_one(p + e));
-    const double b = q != nullptr ? static_cast<double>(probability(load_one(q + e))) : 0.0;
-    return a > b ? a - b : 0.0;
+    const float a = probability(load_one(p + e));
+    const float b = q != nullptr ? probability(load_one(q + e)) : 0.0f;
+    return a > b ? static_cast<double>(a) - static_cast<double>(b) : 0.0;
   }
 
   // A lane's sum over the vectors v0, v0 + step, .. below v1.
-  __device__ __forceinline__ double sum(int v0, int v1, int step) const {
-    constexpr int kUnroll = 16 / kVec;                  // 64 bytes of a row in flight: more spill
-    Sum s[2];
+  template <bool DIFFERENCE>
+  __device__ __forceinline__ double sum_of(int v0, int v1, int step) const {
+    constexpr int kUnroll = 4;
+    Sums s[2];
     for (int v = v0; v < v1; v += kUnroll * step) {
-      float pv[kUnroll][kVec], qv[kUnroll][kVec];
+      uint4 pv[kUnroll], qv[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) pv[u][k] = qv[u][k] = 0.0f;
+        pv[u] = qv[u] = make_uint4(0, 0, 0, 0);
         if (v + u * step < v1) {
-          load(p, v + u * step, true, pv[u]);
-          if (q != nullptr) load(q, v + u * step, together, qv[u]);
+          pv[u] = load(p, v + u * step, true);
+          if (!DIFFERENCE && without >= 0 && v + u * step == (without + shift) / kVec)
+            pv[u] = drop(pv[u], (without + shift) % kVec);
+          if (DIFFERENCE) qv[u] = load(q, v + u * step, together);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        float w[kVec], rest[kVec];
-        weigh(v + u * step, pv[u], qv[u], w, rest);
+      for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) s[k & 1].add(w[k], rest[k]);
-      }
+        for (int k = 0; k < kVec / 2; ++k) {
+          float a0, a1;
+          pair(pv[u], k, a0, a1);
+          a0 = probability(a0);
+          a1 = probability(a1);
+          const uint64_t a = f32x2(a0, a1);
+          if (DIFFERENCE) {
+            // p - min(p, q) and what that difference lacks: exact
+            float b0, b1;
+            pair(qv[u], k, b0, b1);
+            const uint64_t b = f32x2(fminf(fmaxf(b0, 0.0f), a0), fminf(fmaxf(b1, 0.0f), a1));
+            const uint64_t d = Sums::sub(a, b);
+            s[k & 1].lo = add_f32x2(s[k & 1].lo, Sums::sub(Sums::sub(a, d), b));
+            s[k & 1].add(d);
+          } else {
+            s[k & 1].add(a);
+          }
+        }
     }
     return s[0].value() + s[1].value();
+  }
+  __device__ __forceinline__ double sum(int v0, int v1, int step) const {
+    return q != nullptr ? sum_of<true>(v0, v1, step) : sum_of<false>(v0, v1, step);
   }
 };
 
@@ -157,7 +184,7 @@ __device__ __forceinline__ int pick(double upto, double own, double x) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyArgs a) {
-  __shared__ double cta_sum[2][kMaxCtas], warp_sum[kWarps];
+  __shared__ double run_sum[2][kMaxCtas * kWarps];       // of all CTAs' warps
   __shared__ int stands;
   pdl_wait();
   const int r = blockIdx.x / cluster_size(), rank = static_cast<int>(cluster_ctarank());
@@ -220,25 +247,25 @@ __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyA
   const long long vectors = row.vectors();
   const int v0 = static_cast<int>(vectors * run / runs);
   const int v1 = static_cast<int>(vectors * (run + 1) / runs);
-  double whole = 0.0;
-  int winner = -1;
+  // a lane's runs of all: kMaxCtas * kWarps / 32 neighbours
+  constexpr int kPer = kMaxCtas * kWarps / 32;
+  double own[kPer], mine = 0.0, upto = 0.0, whole = 0.0;
   for (int round = 0; round < 2; ++round) {
     double s = row.sum(v0 + lane, v1, 32);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (lane == 0) warp_sum[warp] = s;
-    __syncthreads();
     if (round == 0) cluster_wait();                     // the others' shared memory is there
-    if (warp == 0) {
-      double t = lane < kWarps ? warp_sum[lane] : 0.0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-      if (lane < ctas) st_cluster_f64(&cta_sum[round][rank], lane, t);
-    }
+    if (lane < ctas) st_cluster_f64(&run_sum[round][run], lane, s);
     cluster_sync();
-    whole = 0.0;
-    for (int c = 0; c < ctas; ++c) whole += cta_sum[round][c];
-    winner = round;
+    mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int k = lane * kPer + i;
+      own[i] = k < runs ? run_sum[round][k] : 0.0;
+      mine += own[i];
+    }
+    upto = scan_lanes(mine);
+    whole = __shfl_sync(0xFFFFFFFFu, upto, 31);
     // nothing left over: the target's own row (and if that holds nothing, no token)
     if (whole > 0.0 || (row.q == nullptr && row.without < 0)) break;
     row.q = nullptr;
@@ -254,38 +281,44 @@ __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyA
   }
   if (!(whole > 0.0)) return;
 
-  // ---- the run in which the sum passes x: CTA, then warp ----
+  // ---- the run in which the sum passes x ----
   const double x = fmax(static_cast<double>(a.sample_u[r]) * whole, 0.0);   // (NaN: 0)
-  double own = lane < ctas ? cta_sum[winner][lane] : 0.0;
-  double upto = scan_lanes(own);
-  const int cta = pick(upto, own, x);
-  if (cta != rank) return;
-  const double before_cta = __shfl_sync(0xFFFFFFFFu, upto - own, cta);
-  own = lane < kWarps ? warp_sum[lane] : 0.0;
-  upto = before_cta + scan_lanes(own);
-  const int w = pick(upto, own, x);
-  if (w != warp) return;
-  const double before_warp = __shfl_sync(0xFFFFFFFFu, upto - own, w);
+  int l = pick(upto, mine, x);
+  // (walked by every lane over its own; lane l's counts)
+  double upto_run = upto - mine, before_run = upto_run;
+  int at = -1;
+  bool passed_run = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (!passed_run && own[i] > 0.0) {
+      before_run = upto_run;
+      at = lane * kPer + i;
+      passed_run = upto_run + own[i] > x;
+    }
+    upto_run += own[i];
+  }
+  if (__shfl_sync(0xFFFFFFFFu, at, l) != run) return;
+  const double before_warp = __shfl_sync(0xFFFFFFFFu, before_run, l);
   // ---- a lane takes neighbouring vectors; the one that passes x ----
   const int per = (v1 - v0 + 31) / 32;
   const int a0 = min(v1, v0 + lane * per), a1 = min(v1, a0 + per);
-  own = row.sum(a0, a1, 1);
-  upto = before_warp + scan_lanes(own);
-  const int l = pick(upto, own, x);
-  double base = __shfl_sync(0xFFFFFFFFu, upto - own, l);
+  mine = row.sum(a0, a1, 1);
+  upto = before_warp + scan_lanes(mine);
+  l = pick(upto, mine, x);
+  double base = __shfl_sync(0xFFFFFFFFu, upto - mine, l);
   // ---- its elements, a lane each ----
   const int e0 = max(0, __shfl_sync(0xFFFFFFFFu, a0, l) * Row<T>::kVec - row.shift);
   const int e1 = min(a.vocab, __shfl_sync(0xFFFFFFFFu, a1, l) * Row<T>::kVec - row.shift);
   int token = -1;
   for (int e = e0; e < e1; e += 32) {
-    own = e + lane < e1 ? row.weight(e + lane) : 0.0;
-    upto = base + scan_lanes(own);
-    const uint32_t passed = __ballot_sync(0xFFFFFFFFu, own > 0.0 && upto > x);
+    mine = e + lane < e1 ? row.weight(e + lane) : 0.0;
+    upto = base + scan_lanes(mine);
+    const uint32_t passed = __ballot_sync(0xFFFFFFFFu, mine > 0.0 && upto > x);
     if (passed != 0) {
       token = e + __ffs(passed) - 1;
       break;
     }
-    const uint32_t any = __ballot_sync(0xFFFFFFFFu, own > 0.0);
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, mine > 0.0);
     if (any != 0) token = e + 31 - __clz(any);
     base = __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
@@ -294,9 +327,15 @@ __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyA
 
 template <typename T>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
-  // a CTA for every 4096 tokens, up to 8
+  // A CTA for every 4096 tokens, up to 8; fewer where the requests fill the SMs (two CTAs
+  // each) without.
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   int ctas = 1;
-  while (ctas < kMaxCtas && a.vocab > int64_t{ctas} * 4096) ctas *= 2;
+  while (ctas < kMaxCtas && a.vocab > int64_t{ctas} * 4096 && int64_t{a.batch} * ctas * 2 <= 2 * sms)
+    ctas *= 2;
   // its start overlaps the end of the kernel before
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
