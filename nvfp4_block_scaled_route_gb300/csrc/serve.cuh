@@ -64,9 +64,9 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // To the same place of CTA `rank`'s shared memory.
-__device__ __forceinline__ void st_cluster_f64(double* p, uint32_t rank, double v) {
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(map_shared_rank(smem_u32(p), rank)), "d"(v)
-               : "memory");
+__device__ __forceinline__ void st_cluster_f32x2(void* p, uint32_t rank, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};"
+               ::"r"(map_shared_rank(smem_u32(p), rank)), "f"(x), "f"(y) : "memory");
 }
 
 }  // namespace nvmoe

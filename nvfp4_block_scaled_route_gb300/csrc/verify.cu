@@ -16,11 +16,9 @@
 //
 // Which token that is must not hang on how a sum is rounded: a row of 2^17 tokens has
 // as many borders, and fp32 sums would put the wrong token out for every few hundredth
-// row.  A lane sums pairs of fp32 numbers, value and rest: p - q is exact that way, and
-// a sum is off by some 2^-45 of itself; lanes, warps and CTAs are joined in fp64.  (fp64
-// for each value would take longer than its load: 2 adds a cycle and SM.)
-#include <cuda_bf16.h>
-
+// row.  Sums are pairs of fp32 numbers, value and rest: p - q is exact that way, and a
+// sum is off by some 2^-45 of itself.  (fp64, of which an SM has two adds a cycle, took
+// 39 us for 64 requests of 129280 tokens even where it only joined lanes and warps.)
 #include "attn.cuh"
 #include "serve.cuh"
 
@@ -35,11 +33,31 @@ __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Sums of fp32 numbers as a value and what it lacks, two side by side (one instruction
-// for both).
+// A sum as a value and what it lacks, |rest| at most half a step of the value.
+struct alignas(8) Sum {
+  float hi, lo;
+};
+// (Knuth's exact sum of two numbers, the rests, and Dekker's of a large and a small one)
+__device__ __forceinline__ Sum operator+(const Sum& x, const Sum& y) {
+  const float t = x.hi + y.hi, b = t - x.hi;
+  const float e = ((x.hi - (t - b)) + (y.hi - b)) + (x.lo + y.lo);
+  const float hi = t + e;
+  return {hi, e - (hi - t)};
+}
+__device__ __forceinline__ Sum operator-(const Sum& x, const Sum& y) {
+  return x + Sum{-y.hi, -y.lo};
+}
+__device__ __forceinline__ bool operator>(const Sum& x, const Sum& y) {
+  return x.hi > y.hi || (x.hi == y.hi && x.lo > y.lo);
+}
+__device__ __forceinline__ bool positive(const Sum& x) { return x.hi > 0.0f; }
+__device__ __forceinline__ Sum shfl(const Sum& x, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
+}
+
+// Two sums side by side (one instruction for both), a lane's while it runs over a row.
 struct Sums {
   uint64_t hi = 0, lo = 0;
-  // (Knuth's exact sum of two numbers: hi + x = t + rest)
   __device__ __forceinline__ void add(uint64_t x) {
     const uint64_t t = add_f32x2(hi, x), b = sub(t, hi);
     lo = add_f32x2(lo, add_f32x2(sub(hi, sub(t, b)), sub(x, b)));
@@ -48,12 +66,11 @@ struct Sums {
   static __device__ __forceinline__ uint64_t sub(uint64_t x, uint64_t y) {
     return fma_f32x2(y, f32x2(-1.0f, -1.0f), x);        // (a product with -1 is exact)
   }
-  __device__ __forceinline__ double value() const {
+  __device__ __forceinline__ Sum value() const {
     float a, b, c, d;
     f32x2_split(hi, a, b);
     f32x2_split(lo, c, d);
-    return (static_cast<double>(a) + static_cast<double>(b)) +
-           static_cast<double>(c + d);                  // (rests: 2^-24 of the sums)
+    return Sum{a, c} + Sum{b, d};
   }
 };
 
@@ -109,16 +126,17 @@ struct Row {
     if (word == 3) u.w &= keep;
     return u;
   }
-  __device__ __forceinline__ double weight(int e) const {
-    if (e >= vocab || e == without) return 0.0;
+  __device__ __forceinline__ Sum weight(int e) const {
+    if (e >= vocab || e == without) return {0.0f, 0.0f};
     const float a = probability(load_one(p + e));
-    const float b = q != nullptr ? probability(load_one(q + e)) : 0.0f;
-    return a > b ? static_cast<double>(a) - static_cast<double>(b) : 0.0;
+    const float b = q != nullptr ? fminf(probability(load_one(q + e)), a) : 0.0f;
+    const float d = a - b;
+    return {d, (a - d) - b};
   }
 
   // A lane's sum over the vectors v0, v0 + step, .. below v1.
   template <bool DIFFERENCE>
-  __device__ __forceinline__ double sum_of(int v0, int v1, int step) const {
+  __device__ __forceinline__ Sum sum_of(int v0, int v1, int step) const {
     constexpr int kUnroll = 4;
     Sums s[2];
     for (int v = v0; v < v1; v += kUnroll * step) {
@@ -157,34 +175,35 @@ struct Row {
     }
     return s[0].value() + s[1].value();
   }
-  __device__ __forceinline__ double sum(int v0, int v1, int step) const {
+  __device__ __forceinline__ Sum sum(int v0, int v1, int step) const {
     return q != nullptr ? sum_of<true>(v0, v1, step) : sum_of<false>(v0, v1, step);
   }
 };
 
 // Sum over the lanes up to this one.
-__device__ __forceinline__ double scan_lanes(double x) {
+__device__ __forceinline__ Sum scan_lanes(Sum x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
+    const Sum y = {__shfl_up_sync(0xFFFFFFFFu, x.hi, o), __shfl_up_sync(0xFFFFFFFFu, x.lo, o)};
+    if (lane >= o) x = x + y;
   }
   return x;
 }
 
 // Of the lanes' runs, `upto` the sum to the end of each and `own` that of the run: the
 // first that passes x, else (by rounding) the last that holds anything; -1 if none does.
-__device__ __forceinline__ int pick(double upto, double own, double x) {
-  const uint32_t passed = __ballot_sync(0xFFFFFFFFu, own > 0.0 && upto > x);
+__device__ __forceinline__ int pick(const Sum& upto, const Sum& own, const Sum& x, bool* passes) {
+  const uint32_t passed = __ballot_sync(0xFFFFFFFFu, positive(own) && upto > x);
+  *passes = passed != 0;
   if (passed != 0) return __ffs(passed) - 1;
-  const uint32_t any = __ballot_sync(0xFFFFFFFFu, own > 0.0);
+  const uint32_t any = __ballot_sync(0xFFFFFFFFu, positive(own));
   return any != 0 ? 31 - __clz(any) : -1;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyArgs a) {
-  __shared__ double run_sum[2][kMaxCtas * kWarps];       // of all CTAs' warps
+  __shared__ Sum run_sum[2][kMaxCtas * kWarps];       // of all CTAs' warps
   __shared__ int stands;
   pdl_wait();
   const int r = blockIdx.x / cluster_size(), rank = static_cast<int>(cluster_ctarank());
@@ -249,78 +268,79 @@ __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyA
   const int v1 = static_cast<int>(vectors * (run + 1) / runs);
   // a lane's runs of all: kMaxCtas * kWarps / 32 neighbours
   constexpr int kPer = kMaxCtas * kWarps / 32;
-  double own[kPer], mine = 0.0, upto = 0.0, whole = 0.0;
+  Sum own[kPer], mine, upto, whole;
   for (int round = 0; round < 2; ++round) {
-    double s = row.sum(v0 + lane, v1, 32);
+    Sum s = row.sum(v0 + lane, v1, 32);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    for (int o = 16; o > 0; o >>= 1)
+      s = s + Sum{__shfl_xor_sync(0xFFFFFFFFu, s.hi, o), __shfl_xor_sync(0xFFFFFFFFu, s.lo, o)};
     if (round == 0) cluster_wait();                     // the others' shared memory is there
-    if (lane < ctas) st_cluster_f64(&run_sum[round][run], lane, s);
+    if (lane < ctas) st_cluster_f32x2(&run_sum[round][run], lane, s.hi, s.lo);
     cluster_sync();
-    mine = 0.0;
+    mine = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int k = lane * kPer + i;
-      own[i] = k < runs ? run_sum[round][k] : 0.0;
-      mine += own[i];
+      own[i] = k < runs ? run_sum[round][k] : Sum{0.0f, 0.0f};
+      mine = mine + own[i];
     }
     upto = scan_lanes(mine);
-    whole = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    whole = shfl(upto, 31);
     // nothing left over: the target's own row (and if that holds nothing, no token)
-    if (whole > 0.0 || (row.q == nullptr && row.without < 0)) break;
+    if (positive(whole) || (row.q == nullptr && row.without < 0)) break;
     row.q = nullptr;
     row.without = -1;
   }
   if (rank == 0 && threadIdx.x == 0) {
     a.accepted[r] = k;
     if (a.cached != nullptr) a.cached[r] = a.kv_len[r] - (n - k);
-    if (!(whole > 0.0)) {
+    if (!positive(whole)) {
       record_status(a.status, kErrRange);
       a.next_token[r] = -1;
     }
   }
-  if (!(whole > 0.0)) return;
+  if (!positive(whole)) return;
 
-  // ---- the run in which the sum passes x ----
-  const double x = fmax(static_cast<double>(a.sample_u[r]) * whole, 0.0);   // (NaN: 0)
-  int l = pick(upto, mine, x);
-  // (walked by every lane over its own; lane l's counts)
-  double upto_run = upto - mine, before_run = upto_run;
+  // ---- the run in which the sum passes x = u * whole ----
+  const float u = fmaxf(a.sample_u[r], 0.0f);           // (NaN: 0)
+  Sum x = {u * whole.hi, 0.0f};
+  x = x + Sum{fmaf(u, whole.hi, -x.hi), u * whole.lo};
+  bool passes;
+  int l = pick(upto, mine, x, &passes);
+  // (every lane walks over its own; lane l's count)
+  Sum next = upto - mine, before = next;
   int at = -1;
-  bool passed_run = false;
+  bool passed = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (!passed_run && own[i] > 0.0) {
-      before_run = upto_run;
+    const Sum after = next + own[i];
+    if (!passed && positive(own[i])) {
+      before = next;
       at = lane * kPer + i;
-      passed_run = upto_run + own[i] > x;
+      passed = after > x;
     }
-    upto_run += own[i];
+    next = after;
   }
   if (__shfl_sync(0xFFFFFFFFu, at, l) != run) return;
-  const double before_warp = __shfl_sync(0xFFFFFFFFu, before_run, l);
+  before = shfl(before, l);
   // ---- a lane takes neighbouring vectors; the one that passes x ----
   const int per = (v1 - v0 + 31) / 32;
   const int a0 = min(v1, v0 + lane * per), a1 = min(v1, a0 + per);
   mine = row.sum(a0, a1, 1);
-  upto = before_warp + scan_lanes(mine);
-  l = pick(upto, mine, x);
-  double base = __shfl_sync(0xFFFFFFFFu, upto - mine, l);
+  upto = before + scan_lanes(mine);
+  l = pick(upto, mine, x, &passes);
+  before = shfl(upto - mine, l);
   // ---- its elements, a lane each ----
   const int e0 = max(0, __shfl_sync(0xFFFFFFFFu, a0, l) * Row<T>::kVec - row.shift);
   const int e1 = min(a.vocab, __shfl_sync(0xFFFFFFFFu, a1, l) * Row<T>::kVec - row.shift);
   int token = -1;
   for (int e = e0; e < e1; e += 32) {
-    mine = e + lane < e1 ? row.weight(e + lane) : 0.0;
-    upto = base + scan_lanes(mine);
-    const uint32_t passed = __ballot_sync(0xFFFFFFFFu, mine > 0.0 && upto > x);
-    if (passed != 0) {
-      token = e + __ffs(passed) - 1;
-      break;
-    }
-    const uint32_t any = __ballot_sync(0xFFFFFFFFu, mine > 0.0);
-    if (any != 0) token = e + 31 - __clz(any);
-    base = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    mine = e + lane < e1 ? row.weight(e + lane) : Sum{0.0f, 0.0f};
+    upto = before + scan_lanes(mine);
+    l = pick(upto, mine, x, &passes);
+    if (l >= 0) token = e + l;
+    if (passes) break;
+    before = shfl(upto, 31);
   }
   if (lane == 0) a.next_token[r] = token;
 }
