@@ -203,7 +203,8 @@ __device__ __forceinline__ int pick(const Sum& upto, const Sum& own, const Sum& 
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyArgs a) {
-  __shared__ Sum run_sum[2][kMaxCtas * kWarps];       // of all CTAs' warps
+  __shared__ Sum run_sum[2][kMaxCtas * kWarps];          // of all CTAs' warps
+  __shared__ Sum warp_sum[kWarps];
   __shared__ int stands;
   pdl_wait();
   const int r = blockIdx.x / cluster_size(), rank = static_cast<int>(cluster_ctarank());
@@ -321,13 +322,23 @@ __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyA
     }
     next = after;
   }
-  if (__shfl_sync(0xFFFFFFFFu, at, l) != run) return;
+  at = __shfl_sync(0xFFFFFFFFu, at, l);
+  if (at / kWarps != rank) return;
   before = shfl(before, l);
-  // ---- a lane takes neighbouring vectors; the one that passes x ----
-  const int per = (v1 - v0 + 31) / 32;
-  const int a0 = min(v1, v0 + lane * per), a1 = min(v1, a0 + per);
+  // ---- a thread of that CTA takes neighbouring vectors of the run ----
+  const int w0 = static_cast<int>(vectors * at / runs), w1 = static_cast<int>(vectors * (at + 1) / runs);
+  const int per = (w1 - w0 + kThreads - 1) / kThreads;
+  const int a0 = min(w1, w0 + static_cast<int>(threadIdx.x) * per), a1 = min(w1, a0 + per);
   mine = row.sum(a0, a1, 1);
-  upto = before + scan_lanes(mine);
+  const Sum in_warp = scan_lanes(mine);
+  if (lane == 31) warp_sum[warp] = in_warp;
+  __syncthreads();
+  Sum held = lane < kWarps ? warp_sum[lane] : Sum{0.0f, 0.0f};
+  upto = before + scan_lanes(held);
+  l = pick(upto, held, x, &passes);
+  if (l != warp) return;
+  before = shfl(upto - held, l);
+  upto = before + in_warp;
   l = pick(upto, mine, x, &passes);
   before = shfl(upto - mine, l);
   // ---- its elements, a lane each ----
