@@ -19,7 +19,7 @@ BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
 SOURCES = ["api.cu", "quantize.cu", "route.cu", "reduce.cu", "gemm.cu", "router.cu", "peak.cu",
            "ep.cu", "attn_rope.cu", "attn_append.cu", "attn_join.cu", "attn_rows.cu",
-           "attn_chunk.cu", "plan.cu", "verify.cu"]
+           "attn_chunk.cu", "attn_keys.cu", "plan.cu", "verify.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "quant.cuh", "attn.cuh", "attn_turn.cuh", "serve.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",

@@ -1140,10 +1140,11 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
   a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
   a->plan_here = batch <= kAttnPlanHere && blocks <= kAttnPlanHere;
   a->status = c.take<int>(kStatusBytes);
-  a->pieces = c.take<AttnPiece>(kMaxGrid * sizeof(AttnPiece));
-  a->piece_ml = c.take<float2>(2 * kMaxGrid * a->piece_rows * sizeof(float2));
-  a->piece_o = c.take<float>(2 * kMaxGrid * static_cast<size_t>(a->piece_rows) * D *
-                             sizeof(float));
+  // (two CTAs an SM take few rows over pages with scales)
+  const size_t ctas = few ? 2 * kMaxGrid : kMaxGrid;
+  a->pieces = c.take<AttnPiece>(ctas * sizeof(AttnPiece));
+  a->piece_ml = c.take<float2>(2 * ctas * a->piece_rows * sizeof(float2));
+  a->piece_o = c.take<float>(2 * ctas * static_cast<size_t>(a->piece_rows) * D * sizeof(float));
   if (!few) {
     a->starts = c.take<AttnStart>(kMaxGrid * sizeof(AttnStart));
     a->plan_block0 = c.take<int>((static_cast<size_t>(batch) + 1) * sizeof(int));
@@ -1200,15 +1201,18 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   attn_layout(a.batch.batch, a.batch.tokens, a.batch.max_new, q_heads, a.cache.heads,
               a.cache.head_dim, static_cast<uint8_t*>(ws), &a);
   const bool few = a.piece_rows <= kAttnFewRows;
+  const bool by_keys = a.cache.paged && a.cache.head_dim == 128;
   CUtensorMap map_k, map_v;
   if (!make_kv_map(&map_k, a.cache.k, a.cache) || !make_kv_map(&map_v, a.cache.v, a.cache))
     return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);
-  const int grid = std::min(nsm, kMaxGrid);        // shares of the work
+  // shares of the work
+  const int grid = few && by_keys ? 2 * std::min(nsm, kMaxGrid) : std::min(nsm, kMaxGrid);
   cudaError_t e;
   if (few) {
-    e = counted(launch_attention_rows(a, map_k, map_v, grid, stream), 1);
+    e = counted(by_keys ? launch_attention_keys(a, map_k, map_v, grid, stream)
+                        : launch_attention_rows(a, map_k, map_v, grid, stream), 1);
   } else {
     e = a.plan_here ? cudaSuccess : counted(launch_attn_plan(a, grid, stream), 1);
     if (e == cudaSuccess) e = counted(launch_attention_chunk(a, map_k, map_v, grid, stream), 1);

@@ -99,7 +99,7 @@ struct AttnStart {
 // First tile of share c when `total` tiles are dealt to g <= total takers (so
 // that none is without).
 __device__ __forceinline__ long long share_begin(long long total, int c, int g) {
-  if (total < (1 << 22))       // (c <= g <= 256: the product fits 32 bits)
+  if (total < (1 << 22))       // (c <= g <= 512: the product fits 32 bits)
     return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(g);
   return total * c / g;
 }
@@ -159,6 +159,9 @@ constexpr int kAttnFewRows = 16;
 // map_k, map_v: [num_pages, heads, page_size, D] by strides, boxes of up to
 // 128 tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
+                                  const CUtensorMap& map_v, int grid, cudaStream_t stream);
+// The same for pages with scales and 128-wide heads.
+cudaError_t launch_attention_keys(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
 // Blocks and requests up to which the chunk kernel's CTAs plan for themselves: a
 // thread for each (of 384 or 512).

@@ -273,11 +273,10 @@ struct Walk {
 
 // PAGED: E4M3 pages with scales of their own, PAGED of them (1 for pages of 64 tokens
 // and more, else 4) in a thread's 64 keys of a tile.  The keys' loader keeps them in
-// slots by the number of the tile, three numbers for each: the keys' scale, the
-// values' as a logarithm and inverted.  A slot is written again once S of the tile kK
+// slots by the number of the tile, those of keys and those of values.  A slot is written again once S of the tile kK
 // back is done, whose own start had all softmax threads past the scores of the tile two
 // before that: kK + 3 tiles may be in use.  (With a fourth buffer of keys there is room
-// for eight slots of 1 x 2 x 3.)
+// for eight slots of 2 x 2.)
 template <int PAGED>
 constexpr int kTileScales = 2 * PAGED;                 // of one kind
 
@@ -300,7 +299,7 @@ struct Cfg {
   // bytes if that does
   static constexpr int kWords = 4 * kTile * 4 + 2 * kTile;
   static constexpr int kSlots = kK + 3 <= 8 ? 8 : 16;
-  static constexpr int kScaleBytes = kSlots * 3 * kTileScales<PAGED> * 4;
+  static constexpr int kScaleBytes = kSlots * 2 * kTileScales<PAGED> * 4;
   static constexpr int kSmem =
       kRing + 512 + (kWords + kScaleBytes <= 5 * kTile * 4 ? 5 * kTile * 4 : kWords + kScaleBytes);
   static_assert(kK + 3 <= kSlots, "slots");
@@ -375,7 +374,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   // a segment ahead of another)
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(swap + 4 * kTile);
   constexpr int kTS = kTileScales<PAGED>;
-  float* scales = reinterpret_cast<float*>(q_exp + 2 * kTile);  // [slot][3][kTS]
+  float* scales = reinterpret_cast<float*>(q_exp + 2 * kTile);  // [slot][2][kTS]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -452,23 +451,21 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     int buf = 0;
     uint32_t phase = 0, tiles = 0;                      // tiles with scores so far
     bool ok = true;
-    // Scales: lanes 0 .. kTS-1 bring those of keys, the next kTS those of values; each
-    // is read a tile ahead, so that its way (the page, then the scale) does not hold up
-    // the loads of tiles.
-    const bool brings = PAGED && keys && lane < 2 * kTS;
-    const int part = lane < kTS ? lane : lane - kTS;
-    const auto scale_of = [&](int tile) {
+    // Scales: lanes 8 .. 8+kTS-1 bring those of keys, 16 .. those of values, without
+    // waiting for them.
+    const int part = lane & 7;
+    const bool brings = PAGED && keys && lane >= 8 && lane < 24 && part < kTS;
+    const auto page_for = [&](int tile) {               // (read a tile ahead)
       const int k = tile * kKeys + part * (kKeys / (kTS > 0 ? kTS : 1));
-      if (k >= wk.b.kend || k + kKeys / (kTS > 0 ? kTS : 1) <= wk.b.kbeg) return kScaleLow;
-      const int64_t from = page_of(a, wk.r, k);
-      if (from < 0) return kScaleLow;                   // (of zeros)
-      return page_scale((lane < kTS ? a.cache.k_scale : a.cache.v_scale)[from * a.cache.heads + wk.h]);
+      return k < wk.b.kend && k + kKeys / (kTS > 0 ? kTS : 1) > wk.b.kbeg
+                 ? a.batch.page_table[wk.r * a.batch.max_pages + (k >> a.cache.page_shift)]
+                 : -1;
     };
-    float scale = kScaleLow;
+    int scale_page = -1;
     while (left > 0 && ok) {
       const int stop = static_cast<int>(min(static_cast<long long>(wk.b.t1), t + left));
       left -= stop - t;
-      if (brings) scale = scale_of(t);
+      if (brings) scale_page = page_for(t);
       // the segment's queries to L2, ahead of the softmax warps' loads
       if (keys)
         for (int i = lane; i < wk.b.rows; i += 32) {
@@ -507,17 +504,16 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         }
         if (brings) {
           if (wk.b.kend > 0) {
-            float* to = scales + tiles % C::kSlots * (3 * kTS) + part;
-            if (lane < kTS) {
-              to[0] = scale;
-            } else {
-              to[kTS] = log2f(scale);
-              to[2 * kTS] = 1.0f / scale;
-            }
+            // (a page out of range has been reported: zeros)
+            const bool there = scale_page >= 0 && scale_page < a.cache.num_pages;
+            cp_async_4(scales + tiles % C::kSlots * (2 * kTS) + (lane < 16 ? 0 : kTS) + part,
+                       (lane < 16 ? a.cache.k_scale : a.cache.v_scale) +
+                           (there ? scale_page * int64_t{a.cache.heads} + wk.h : 0),
+                       there);
             ++tiles;
           }
-          mbar_arrive(&bars->full[n]);
-          if (t + 1 < stop) scale = scale_of(t + 1);
+          cp_async_arrive(&bars->full[n]);
+          if (t + 1 < stop) scale_page = page_for(t + 1);
         }
         if (++buf == bufs) {
           buf = 0;
@@ -529,6 +525,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         t = wk.b.t0;
       }
     }
+    if (PAGED && keys) cp_async_wait_all();
   } else if (FP8 && warp >= kConvert) {
     // ---- E4M3 values to fp16: 16 bytes at a time, eight rows of one column side
     // by side (no bank conflicts either way) ----
@@ -857,13 +854,13 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           constexpr int kG = PAGED ? PAGED : 1;
           float cg[kG], lift[kG], inv_scale[kG];
           if (PAGED) {
-            const float* sc = scales + n % C::kSlots * (3 * kTS) + half * PAGED;
+            const float* sc = scales + n % C::kSlots * (2 * kTS) + half * PAGED;
             top = -INFINITY;
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-              cg[g] = cr * sc[g];
-              lift[g] = sc[kTS + g];
-              inv_scale[g] = sc[2 * kTS + g];
+              cg[g] = cr * page_scale(sc[g]);
+              lift[g] = __log2f(page_scale(sc[kTS + g]));
+              inv_scale[g] = exp2_approx(-lift[g]);
               float m4[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int i = 64 / kG * g; i < 64 / kG * (g + 1); i += 2)

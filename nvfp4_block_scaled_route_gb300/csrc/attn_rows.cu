@@ -769,9 +769,7 @@ cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& 
 
 cudaError_t launch_attention_rows(const AttnArgs& a, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream) {
-  if (a.cache.paged)
-    return a.cache.head_dim == 128 ? launch<128, true, true>(a, map_k, map_v, grid, stream)
-                                   : launch<64, true, true>(a, map_k, map_v, grid, stream);
+  if (a.cache.paged) return launch<64, true, true>(a, map_k, map_v, grid, stream);
   if (a.cache.fp8)
     return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
                                    : launch<64, true>(a, map_k, map_v, grid, stream);
