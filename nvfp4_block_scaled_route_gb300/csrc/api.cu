@@ -1104,9 +1104,10 @@ namespace {
 // One side of a paged cache as [num_pages, heads, page_size, D] by its
 // strides; box: 128 bytes of the row (all of it, if shorter) x up to
 // 128 tokens of one page and head.  E4M3 rows are 128 bytes or less: with L2 lines
-// promoted to 256, tokens-first caches also fetched the next head's (64 tokens on up to
-// 16384 keys, pages of 64: 184 us, 156 without).
-bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
+// promoted to 256, tokens-first caches also fetch the next head's, which is `wide`
+// where that is read at the same time, and else not (64 tokens on up to 16384 keys,
+// pages of 64: a scale per head 184 us, 156 without; a scale per page 127, 132 without).
+bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c, bool wide) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t el = c.fp8 ? 1 : 2;
@@ -1121,7 +1122,8 @@ bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c) {
                   const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  c.fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  c.fp8 && !wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                 : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -1203,7 +1205,9 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   const bool few = a.piece_rows <= kAttnFewRows;
   const bool by_keys = a.cache.paged && a.cache.head_dim == 128;
   CUtensorMap map_k, map_v;
-  if (!make_kv_map(&map_k, a.cache.k, a.cache) || !make_kv_map(&map_v, a.cache.v, a.cache))
+  // (neighbouring heads are read at the same time)
+  const bool wide = few && by_keys && a.cache.heads % 2 == 0 && a.cache.head_stride == 128;
+  if (!make_kv_map(&map_k, a.cache.k, a.cache, wide) || !make_kv_map(&map_v, a.cache.v, a.cache, wide))
     return fail(cudaErrorInvalidValue);  // tensor-map encoding refused
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);

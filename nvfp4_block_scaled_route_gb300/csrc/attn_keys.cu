@@ -14,19 +14,23 @@
 // A query is the sum of two E4M3 numbers (8 bits of its elements down to 2^-9 of its
 // row's largest, to within 2^-17 of that below).  A weight is the sum of four, the
 // later ones 2^8, 2^16 and 2^24 times what is left, each with columns of its own in O^T:
-// the products are exact, and weights have 8 bits down to 2^-26 of the largest and are
-// off by 2^-38 of it below.  (In the sum they go with the scale of their value's page,
-// as a power of two in the exponent; without it, in the row's weight sum.)
+// the products are exact, and weights, fp16 numbers of 11 bits, are right to within 2^-8
+// down to 2^-22 of the row's largest and to within 2^-34 of that below.  (In the sum they
+// go with the scale of their value's page, as a power of two in the exponent; without it,
+// in the row's weight sum.)
 //
 // A thread holds one key and half of the rows, so the scales of pages are one number for
 // it, and a row's maximum would have to be looked for across threads.  It is not: m is a
-// reference as in the chunk kernel, and only when some thread finds a score 2^8 above it
+// reference as in the chunk kernel, and only when some thread finds a weight above 2^4
 // (a barrier with a vote) is the maximum exchanged and O^T rescaled.
 //
 // The chain of a tile (scores to registers, vote, exponentials, four conversions, weights
 // to shared memory) takes 1300 cycles of latency and its bytes 1080 of HBM, and between
 // two segments the queries' way in and the rows' way out take some 3000, so an SM runs
-// two CTAs, with half of the shared memory each.
+// two CTAs, with half of the shared memory each (one: 138 us where two take 126; one with
+// two tiles in the work at a time: 142).  64 tokens on up to 16384 keys, 56 query and 8
+// key heads, pages of 16: 126 us, 5.4 TB/s (121 with heads first: whole pages of a head
+// side by side); attention_rows_kernel, which turns the values to 16 bits, took 200.
 //
 // The work is the flat list of 128-key tiles of all (request, key head) segments in equal
 // shares, as in attention_rows_kernel; attn_combine_kernel joins what is cut.
@@ -46,9 +50,10 @@ constexpr int kLevels = 4;                             // E4M3 numbers of a weig
 constexpr int kTileBytes = kKeys * kD;
 constexpr int kScaleSlots = 8, kTileScales = 8;       // scales of 16 keys each
 constexpr uint32_t kTmemColumns = 128;
-// Powers of two by which a row's reference stands below its maximum when it is set, and
-// by which the maximum may stand above it: weights are at most 2^8 (E4M3 ends at 448).
-constexpr float kLift = 4.0f, kSlack = 8.0f;
+// Powers of two by which a row's maximum may stand above its reference, the maximum when
+// it was set: weights are at most 2^4, what their first number leaves, 2^-4 of them, times
+// 2^8 then at most 2^8 (E4M3 ends at 448; past that it would be cut).
+constexpr float kSlack = 4.0f;
 
 // RG: rows of a softmax group; both have as many.
 template <int RG>
@@ -120,9 +125,9 @@ struct Walk {
     kend = min(rq.len, rq.pos0 + rq.n);
   }
   // (only called while tiles are left; false if the batch ends all the same)
-  __device__ __forceinline__ bool next(const AttnArgs& a) {
-    if (++h < a.cache.heads) return true;
-    h = 0;
+  __device__ __forceinline__ bool next(const AttnArgs& a, int step) {
+    if ((h += step) < a.cache.heads) return true;
+    h %= step;
     do {
       if (r + 1 >= a.batch.batch) return false;
       load(a, r + 1);
@@ -169,6 +174,13 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
+// Two fp16 as E4M3 (satfinite, nearest even), the lower one in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2_f16x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+
 template <int RG>
 __global__ void __launch_bounds__(kThreads, 2)
 attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
@@ -189,7 +201,12 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   pdl_trigger();
   pdl_wait();                                          // for what came before
 
-  // ---- this CTA's share of the tiles ----
+  // ---- this CTA's share of the tiles: of the even or of the odd heads, if there are as
+  // many of both (two CTAs that start together then read the halves of the same 256 bytes
+  // of a tokens-first cache), which the CTAs `me` of [0, ctas) and of [ctas, 2 ctas) take
+  const int step = a.cache.heads % 2 == 0 ? 2 : 1, ctas = static_cast<int>(gridDim.x) / step;
+  const int side = step == 2 ? static_cast<int>(blockIdx.x & 1u) : 0;
+  const int share = static_cast<int>(blockIdx.x) / step, me = share + side * ctas;
   long long* scan = reinterpret_cast<long long*>(smem);           // [kThreads / 32] warp sums
   const int per = (a.batch.batch + kThreads - 1) / kThreads;
   const int r_begin = min(a.batch.batch, static_cast<int>(threadIdx.x) * per);
@@ -197,7 +214,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   long long mine = 0;
   for (int r = r_begin; r < r_end; ++r) {
     const Span s = tiles_of(load_request(a.batch, a.cache.page_shift, r, a.status), a.window);
-    mine += static_cast<long long>(s.t1 - s.t0) * a.cache.heads;
+    mine += static_cast<long long>(s.t1 - s.t0) * (a.cache.heads / step);
   }
   long long upto = mine;
 #pragma unroll
@@ -233,14 +250,14 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const int takers = share_takers(total, gridDim.x);
-  AttnPiece* piece = a.pieces + blockIdx.x;
-  if (static_cast<int>(blockIdx.x) >= takers) {
+  const int takers = share_takers(total, ctas);
+  AttnPiece* piece = a.pieces + me;
+  if (share >= takers) {
     if (threadIdx.x == 0) piece->rows = 0;
     return;
   }
-  const long long lo = share_begin(total, blockIdx.x, takers);
-  const long long hi = share_begin(total, blockIdx.x + 1, takers);
+  const long long lo = share_begin(total, share, takers);
+  const long long hi = share_begin(total, share + 1, takers);
   long long first = before + upto - mine;
   if (lo >= first && lo < first + mine) {
     int r = r_begin;
@@ -248,7 +265,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     while (true) {
       rq = load_request(a.batch, a.cache.page_shift, r, a.status);
       const Span s = tiles_of(rq, a.window);
-      const long long c = static_cast<long long>(s.t1 - s.t0) * a.cache.heads;
+      const long long c = static_cast<long long>(s.t1 - s.t0) * (a.cache.heads / step);
       if (lo < first + c || r + 1 >= r_end) break;
       first += c;
       ++r;
@@ -272,8 +289,9 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     wk.r = bars->r;
     wk.set(a, bars->rq);
     const int span = max(1, wk.sp.t1 - wk.sp.t0);
-    wk.h = static_cast<int>(bars->tile / span);
-    return wk.sp.t0 + static_cast<int>(bars->tile - static_cast<long long>(wk.h) * span);
+    const int k = static_cast<int>(bars->tile / span);
+    wk.h = k * step + side;
+    return wk.sp.t0 + static_cast<int>(bars->tile - static_cast<long long>(k) * span);
   };
   int t = start();
   long long left = hi - lo;
@@ -289,12 +307,11 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     const uint64_t policy = policy_evict_first();
     // Scales: lanes 8-15 bring those of keys, 16-23 those of values, of 16 keys each,
     // without waiting for them.  (Brought through registers, one tile ahead, a tile took
-    // the time of a load from HBM: 192 us instead of XXX, 64 tokens on up to 16384 keys.)
+    // the time of a load from HBM: 192 us instead of 141, 64 tokens on up to 16384 keys.)
     const bool brings = keys && lane >= 8 && lane < 24;
     const int off = brings ? (lane & 7) * 16 : lane * box, span = brings ? 16 : box;
     const float* side = lane < 16 ? a.cache.k_scale : a.cache.v_scale;
-    // Page numbers: 32 at a time, a lane each, the next ones while these are used.  (Read
-    // for each tile, even two tiles ahead, they held up the loads: 138 us instead of XXX.)
+    // Page numbers: 32 at a time, a lane each, the next ones while these are used.
     const int box_shift = min(7, a.cache.page_shift);
     const auto pages_from = [&](int chunk) {
       const int64_t i = int64_t{chunk} * 32 + lane;
@@ -342,7 +359,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         }
       }
       if (left > 0) {
-        if (!wk.next(a)) break;
+        if (!wk.next(a, step)) break;
         t = wk.sp.t0;
       }
     }
@@ -401,7 +418,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         }
       }
       if (left > 0) {
-        if (!wk.next(a)) break;
+        if (!wk.next(a, step)) break;
         t = wk.sp.t0;
       }
     }
@@ -429,14 +446,14 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
       if (threadIdx.x == 0 && !whole && slot == 1) {
         // this CTA begins a cut segment: where its pieces end, for the join
         const long long end = hi + (wk.sp.t1 - stop);
-        int last = blockIdx.x + 1;
+        int last = share + 1;
         while (last + 1 < takers && share_begin(total, last + 1, takers) < end) ++last;
         AttnPiece p;
         p.rows = rows;
         p.head = wk.h;
         p.first = wk.rq.first;
         p.row0 = 0;
-        p.last = last;
+        p.last = last + side * ctas;
         *piece = p;
         begun = true;
       }
@@ -556,7 +573,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
                                     fmaxf(my_join[2 * RG + r], my_join[3 * RG + r]));
             f[r] = 1.0f;
             if (top > above[r]) {
-              const float mn = top - kLift;
+              const float mn = top;
               f[r] = above[r] == -3.0e38f ? 0.0f : exp2_approx(m[r] - mn);
               m[r] = mn;
               above[r] = mn + kSlack;
@@ -593,18 +610,20 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         uint8_t* to = smem + C::kPAt + sb * C::kPBytes;
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {
-          float x0 = p[r], x1 = p[r + 1];
+          // 2^11 p of two rows as fp16; what a number leaves of it is exact
+          const uint32_t w = pack_f16x2(p[r] * 2048.0f, p[r + 1] * 2048.0f);
+          __half2 x = reinterpret_cast<const __half2&>(w);
           const int row = g * RG + r;
           const uint32_t at0 = tile_at(row, key), at1 = tile_at(row + 1, key);
 #pragma unroll
           for (int level = 0; level < kLevels; ++level) {
-            const uint32_t e = pack_e4m3x2(x0, x1);
+            const float up = level == 0 ? 0x1p-11f : (level == 1 ? 0x1p-3f : (level == 2 ? 0x1p5f : 0x1p13f));
+            const __half2 y = __hmul2(x, __float2half2_rn(up));
+            const uint32_t e = pack_e4m3x2_f16x2(reinterpret_cast<const uint32_t&>(y));
             to[level * C::kRows * 128 + at0] = static_cast<uint8_t>(e);
             to[level * C::kRows * 128 + at1] = static_cast<uint8_t>(e >> 8);
-            const uint32_t h = e4m3x2_to_f16x2(e);
-            const float2 f = __half22float2(reinterpret_cast<const __half2&>(h));
-            x0 = (x0 - f.x) * 256.0f;
-            x1 = (x1 - f.y) * 256.0f;
+            const uint32_t back = e4m3x2_to_f16x2(e);
+            x = __hfma2(reinterpret_cast<const __half2&>(back), __float2half2_rn(-1.0f / up), x);
           }
         }
         if (g == 0 && (t * kKeys < wk.kbeg || (t + 1) * kKeys > wk.kend)) {
@@ -636,9 +655,9 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
       const Walk out_wk = wk;
       const int out_rows = rows;
       const bool to_out = whole;
-      const int64_t po = (2 * static_cast<int64_t>(blockIdx.x) + slot) * a.piece_rows;
+      const int64_t po = (2 * static_cast<int64_t>(me) + slot) * a.piece_rows;
       const uint32_t last = n - 1;
-      more = left > 0 && wk.next(a);
+      more = left > 0 && wk.next(a, step);
       if (more) {
         t = wk.sp.t0;
         open();
@@ -689,11 +708,11 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         const bool all = t == wk.sp.t0 && end == wk.sp.t1;
         left -= end - t;
         const int64_t at =
-            (2 * static_cast<int64_t>(blockIdx.x) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows;
+            (2 * static_cast<int64_t>(me) + (t == wk.sp.t0 ? 1 : 0)) * a.piece_rows;
         mend_rows<kD, true, true>(a, wk.r, wk.h, 0, wk.rq.n * group, wk.kbeg, wk.kend, t, end,
                                   all ? nullptr : a.piece_o + at * kD, a.piece_ml + at, warp,
                                   kSoftmaxThreads / 32);
-        if (left > 0 && !wk.next(a)) break;
+        if (left > 0 && !wk.next(a, step)) break;
       }
     }
   }

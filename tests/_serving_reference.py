@@ -6,9 +6,11 @@ rounding u = 2^-8 of weights and of the output, scores off by ds, fp32 sums) hol
 keys and values with their scales multiplied in, and two terms come in:
  * a query element below 2^-9 of its row's largest counts to within 2^-17 of that
    largest: ds grows by 2^-17 max|q| scale sum |k_i| over those elements;
- * a weight times its value's scale, p vs, is fp16 relative to a reference at which the
-   largest is 2^10 or more: those that fall below 2^-14 are off by 2^-25 at most, 2^-35
-   of the largest, for each of n keys, times a value of 448 at most.
+ * a weight times its value's scale, p vs, is held to within u of itself down to a floor
+   below which it is off by 2^-34 of the row's largest at most (16-bit weights: fp16
+   relative to a reference at which the largest is 2^10 or more, off by 2^-25 below 2^-14;
+   sums of E4M3 numbers: the last of them, 2^24 times what the others leave, off by 2^-10,
+   where the largest is 1 or more), for each of n keys, times a value of 448 at most.
 """
 import math
 
@@ -55,7 +57,7 @@ def request_attention(q, k, v, vs, pos0, scale, window):
     if L:
         p = torch.where(none[..., None], 0.0, torch.softmax(s, -1))
         lse = torch.logsumexp(s, -1)
-        tiny = L * 448 * 2.0 ** -35 * (p * vs).amax(-1)
+        tiny = L * 448 * 2.0 ** -34 * (p * vs).amax(-1)
     else:
         p, lse = s, torch.full((n, g), -math.inf, dtype=torch.float64)
         tiny = torch.zeros(n, g, dtype=torch.float64)

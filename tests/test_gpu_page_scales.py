@@ -570,3 +570,27 @@ def test_pages_past_32_bit_offsets(nb):
         mean = got.cumsum(0) / torch.arange(1, 71, device=DEV)[:, None, None]
         size = got.abs().cumsum(0) / torch.arange(1, 71, device=DEV)[:, None, None]
         assert ((out - mean[first:]).abs() <= 2.0 ** -8 * (mean[first:].abs() + size[first:]) + 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_small_weights_beside_large_ones_that_come_later(nb, n):
+    """Scores that rise by up to 2^4 and less over the first, so that references stay where
+    they are while weights grow, and one key 20 powers of two above thousands whose weights
+    together are a hundredth of its own: both within the bounds of single weights."""
+    L, D = 4096, 128
+    pages = Pages([(n, L)], 1, D, 64)
+    for scale in pages.scale:
+        scale[:] = 2.0 ** -4
+    k = torch.zeros(L, D, dtype=torch.float64)
+    k[:, 0] = torch.linspace(0, 1, L).double()             # a slow rise ...
+    k[L // 2, 1] = 14.0                                    # ... and one key far above
+    raw = sref.e4m3(k * 16)
+    v = sref.e4m3(torch.randn(L, D, generator=pages.g).double() * 64 + 64)
+    for which, x in ((0, raw), (1, v)):
+        for i in range(L // 64):
+            pages.raw[which][int(pages.table[0, i]), :, 0] = \
+                x[i * 64:(i + 1) * 64].to(torch.float8_e4m3fn).view(torch.uint8)
+    q = torch.zeros(n, 2, D)
+    q[:, 0, 0], q[:, 1, 0] = 4 * math.log(2) * D ** 0.5, 4 * math.log(2) * D ** 0.5
+    q[:, 1, 1] = math.log(2) * D ** 0.5
+    check_attention(nb, pages, 2, q=q.bfloat16())
