@@ -394,3 +394,113 @@ def test_verify_rows_past_32_bit_offsets(nb):
     assert accepted.tolist() == [2] and nxt.tolist() == [V - 9]
     accepted, nxt = nb.draft_verify(p, None, tokens, batch, u, ints([0], torch.float32) + 0.3)
     assert accepted.tolist() == [1] and nxt.tolist() == [V - 9]
+
+
+# --------------------------------------------------------------- together --
+@pytest.fixture(scope="module")
+def ex():
+    import os
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    import decoder_block
+    return decoder_block
+
+
+@pytest.mark.parametrize("page_scales", [False, True], ids=["bf16", "page-scales"])
+def test_drafted_steps_from_a_graph(nb, ex, monkeypatch, page_scales):
+    """Steps of three drafted tokens from a graph: each step's answer is that of its own
+    numbers, the lengths go on from the tokens that stand, every page is held once, and the
+    attention of the last step is that of what the cache holds."""
+    from _serving_reference import request_attention, verify
+    seen = {}
+    inner = nb.paged_attention
+
+    def recorded(q, cache, batch, **kw):
+        seen["q"], seen["out"] = q, inner(q, cache, batch, **kw)
+        return seen["out"]
+    monkeypatch.setattr(nb, "paged_attention", recorded)
+    torch.manual_seed(3)
+    R, n, prompt = 3, 3, 37
+    block = ex.DecoderBlock(hidden=512, q_heads=4, inter=256, positions=256)
+    pages = ex.PageTable(R, 160, 16)
+    cache = block.cache(pages, page_scales=page_scales)
+    ex.prefill(block, cache, pages, torch.randn(R, prompt, 512, device=DEV).bfloat16(), 20)
+    embed = torch.nn.functional.normalize(torch.randn(300, 512, device=DEV)).bfloat16()
+    decode = ex.DraftedDecoder(block, cache, pages, embed, ints([5, 6, 7]), n)
+    cached, stood = [prompt] * R, 0
+    assert decode.cached.tolist() == cached
+    for _ in range(8):
+        last = decode.last.tolist()
+        tokens, accepted, following = (t.cpu() for t in decode())
+        assert decode.status() == 0
+        assert tokens[:, 0].tolist() == last
+        assert pages.kv_len.tolist() == [c + n + 1 for c in cached]
+        q_start = pages.q_start.cpu()
+        assert q_start.tolist() == [i * (n + 1) for i in range(R + 1)]
+        want = verify(decode.target.cpu(), decode.draft.flatten(0, 1).cpu(), tokens.flatten(), q_start,
+                      decode.accept_u.cpu(), decode.sample_u.cpu())
+        assert accepted.tolist() == want[0] and following.tolist() == want[1]
+        cached = [c + 1 + k for c, k in zip(cached, want[0])]
+        assert decode.cached.tolist() == cached
+        stood += sum(want[0])
+        table, ring, (first, free) = pages.table.tolist(), pages.pool.ring.tolist(), pages.pool.state.tolist()
+        held = [p for r, length in enumerate(pages.kv_len.tolist()) for p in table[r][:-(-length // 16)]]
+        assert sorted(held + [ring[(first + i) % len(ring)] for i in range(free)]) == list(range(pages.num_pages))
+    assert 0 < stood < 8 * R * n                           # some stand, some do not
+    k, v = cache.k.double().cpu(), cache.v.double().cpu()
+    if page_scales:
+        k, v = (x * s.double().cpu()[:, None, :, None] for x, s in ((k, cache.k_scale), (v, cache.v_scale)))
+    for r in range(R):
+        length = int(pages.kv_len[r])
+        at = torch.tensor(table[r][:-(-length // 16)])
+        vs = cache.v_scale.double().cpu()[at] if page_scales else torch.ones(len(at), block.hk).double()
+        rows = slice(r * (n + 1), (r + 1) * (n + 1))
+        for h in range(block.hk):
+            g = block.hq // block.hk
+            out, _, bound, _ = request_attention(
+                seen["q"][rows, h * g:(h + 1) * g].double().cpu(), k[at, :, h].flatten(0, 1)[:length],
+                v[at, :, h].flatten(0, 1)[:length], vs[:, h].repeat_interleave(16)[:length], length - n - 1,
+                block.D ** -0.5, 0)
+            err = (seen["out"][rows, h * g:(h + 1) * g].double().cpu() - out).abs()
+            assert (err <= bound).all(), (err - bound).max()
+
+
+def test_the_example_runs_with_drafted_tokens(ex, capsys):
+    y, whole, last = ex.main(["--requests", "2", "--prompt", "100", "--chunk", "33", "--new", "5", "--drafts", "2",
+                              "--page-scales"])
+    assert y.isfinite().all() and whole.isfinite().all() and last.shape == (2,)
+    assert "drafted tokens" in capsys.readouterr().out
+
+
+def test_two_steps_on_two_streams(nb):
+    """Plans, appends and attention of two batches at once, on streams and workspaces of
+    their own, give what they give one after the other."""
+    def make(seed):
+        g = torch.Generator().manual_seed(seed)
+        pool = nb.PagePool(torch.randperm(64, generator=g).int().to(DEV), ints([0, 64]))
+        batch = nb.AttnBatch(ints([0] * 4), ints([0] * 3), ints([[0] * 8] * 3), max_new=40)
+        side = [torch.zeros(64, 16, 2, 128, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+        cache = nb.PagedKVCache(*side, k_scale=torch.ones(64, 2, device=DEV), v_scale=torch.ones(64, 2, device=DEV))
+        x = torch.randn(120, 8, 128, generator=g).bfloat16().to(DEV)
+        new = [ints([40, 23, 7]), ints([1, 3, 2])]
+        ws = [nb.attn_workspace(), nb.paged_attention_workspace(cache, batch, 4, 120)]
+        return pool, batch, cache, x, new, ws
+
+    def steps(state, stream):
+        pool, batch, cache, x, new, (ws, ws_attn) = state
+        outs = []
+        for add, rows in zip(new, (70, 6)):
+            nb.plan_pages(pool, batch, 16, add, ws=ws, stream=stream)
+            q, k, v = x[:rows, :4], x[:rows, 4:6], x[:rows, 6:]
+            nb.kv_append(cache, batch, k, v, ws=ws, stream=stream)
+            outs.append(nb.paged_attention(q, cache, batch, ws=ws_attn, stream=stream))
+        return outs + [cache.k.view(torch.uint8), cache.v_scale, batch.kv_len, pool.ring]
+    alone = [[t.clone() for t in steps(make(seed), None)] for seed in (1, 2)]
+    states = [make(seed) for seed in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    both = [steps(state, stream) for state, stream in zip(states, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
