@@ -1,4 +1,6 @@
-"""Thin ctypes binding of libnvfp4moe.so (argument marshalling only).
+"""Thin binding of libnvfp4moe.so (argument marshalling only): ctypes, and for the
+attention and serving operators, whose small calls the host would bound, an extension
+module (csrc/hostcall.c) that checks tensors and passes arguments.
 
 Every computation runs in the library's CUDA kernels; this module allocates
 device buffers with PyTorch, passes raw pointers and the current CUDA stream,
@@ -143,6 +145,42 @@ def lib():
             f.argtypes = args
         _lib = l
     return _lib
+
+
+_host = None
+
+
+def _calls():
+    """The extension module, its entry points bound to the library's."""
+    global _host
+    if _host is None:
+        l, h = lib(), _hostcall()
+        h.bind(*(ctypes.cast(getattr(l, name), ctypes.c_void_p).value for name in (
+            "attn_qk_norm_rope", "attn_kv_append", "attn_paged_forward", "attn_plan_pages",
+            "draft_verify")))
+        _host = h
+    return _host
+
+
+def _hostcall():
+    global _vector, _head_rows
+    try:
+        from . import _hostcall as h
+    except ImportError as e:
+        raise RuntimeError("_hostcall is missing: run __graft_entry__.build() first") from e
+    _vector, _head_rows = h.vector, h.rows
+    return h
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
+    """Address of the dense CUDA tensor t [n] of this type, None for None (the
+    extension's function takes this one's place on the first call)."""
+    return _hostcall().vector(t, n, dtype, what)
+
+
+def _head_rows(t: torch.Tensor, dtype, what: str):
+    """(address, token stride, head stride) of head rows [T, heads, D]; likewise."""
+    return _hostcall().rows(t, dtype, what)
 
 
 def _check(fn: str, status: int):
@@ -556,24 +594,7 @@ def attn_workspace(device="cuda") -> torch.Tensor:
     return _workspace(256, device)
 
 
-def _rows(t: torch.Tensor, what: str):
-    """(address, token stride, head stride) of bf16 head rows [T, heads, D]."""
-    s = t.stride()
-    if t.dtype is not torch.bfloat16 or len(s) != 3 or not t.is_cuda:
-        raise ValueError(f"{what} must be a bf16 CUDA tensor [tokens, heads, head_dim]")
-    if s[2] != 1:
-        raise ValueError(f"{what}: head_dim must be contiguous")
-    return t.data_ptr(), s[0], s[1]
-
-
-def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != (n,):
-        raise ValueError(f"{what} must be {dtype} [{n}]")
-    if not (t.is_cuda and (t.is_contiguous() or n < 2)):
-        raise ValueError(f"{what} must be a dense CUDA tensor")
-    return t.data_ptr()
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _page_scales(t: Optional[torch.Tensor], pages: int, heads: int, what: str):
@@ -617,12 +638,12 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
         raise ValueError("k_out must have the shape of k")
     ws = _workspace(256, q.device, stream) if ws is None else ws
     table, npos, rot = _rope(rope)
-    _check("attn_qk_norm_rope", lib().attn_qk_norm_rope(
-        *_rows(q, "q"), hq, *_rows(k, "k"), hk, T, D,
-        _vector(positions, T, torch.int32, "positions"), table, npos, rot, int(interleaved),
-        _vector(q_weight, D, torch.bfloat16, "q_weight"),
-        _vector(k_weight, D, torch.bfloat16, "k_weight"), eps, *_rows(q_out, "q_out"),
-        *_rows(k_out, "k_out"), _ptr(ws), ws.numel(), _stream(stream)))
+    _check("attn_qk_norm_rope", _calls().attn_qk_norm_rope(
+        *_head_rows(q, _bf16, "q"), hq, *_head_rows(k, _bf16, "k"), hk, T, D,
+        _vector(positions, T, _i32, "positions"), table, npos, rot, int(interleaved),
+        _vector(q_weight, D, _bf16, "q_weight"),
+        _vector(k_weight, D, _bf16, "k_weight"), eps, *_head_rows(q_out, _bf16, "q_out"),
+        *_head_rows(k_out, _bf16, "k_out"), _ptr(ws), ws.numel(), _stream(stream)))
     return q_out, k_out
 
 
@@ -657,11 +678,10 @@ class PagedKVCache:
             scales = (_page_scales(k_scale, pages, heads, "k_scale"),
                       _page_scales(v_scale, pages, heads, "v_scale"))
         else:
-            scales = (_vector(k_scale, heads, torch.float32, "k_scale"),
-                      _vector(v_scale, heads, torch.float32, "v_scale"))
+            scales = (_vector(k_scale, heads, _f32, "k_scale"),
+                      _vector(v_scale, heads, _f32, "v_scale"))
         self.struct = KvCache(k.data_ptr(), v.data_ptr(), code, heads, D, page, pages, sp, st, sh,
                               *scales)
-        self._ref = ctypes.byref(self.struct)
 
 
 class AttnBatch:
@@ -678,20 +698,23 @@ class AttnBatch:
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.batch, self.max_new = B, int(max_new)
         self.struct = AttnBatchArgs(B, self.max_new, 0, page_table.shape[1],
-                                    _vector(q_start, B + 1, torch.int32, "q_start"),
-                                    _vector(kv_len, B, torch.int32, "kv_len"), _ptr(page_table))
-        self._rows = (0, ctypes.byref(self.struct))
+                                    _vector(q_start, B + 1, _i32, "q_start"),
+                                    _vector(kv_len, B, _i32, "kv_len"), _ptr(page_table))
+        self._arguments = self.struct
 
-    def rows(self, tokens: int):
-        """Reference to the arguments with this row count.  They are not changed later
-        (another thread's call may be reading them): another count gets its own."""
-        have, ref = self._rows
-        if have != tokens:
+    def arguments(self, tokens: int) -> AttnBatchArgs:
+        """The arguments with this row count.  They are not changed later (another
+        thread's call may be reading them): another count gets its own."""
+        args = self._arguments
+        if args.tokens != tokens:
             args = AttnBatchArgs.from_buffer_copy(self.struct)
             args.tokens = tokens
-            ref = ctypes.byref(args)
-            self._rows = (tokens, ref)
-        return ref
+            self._arguments = args
+        return args
+
+    def rows(self, tokens: int):
+        """Reference to them."""
+        return ctypes.byref(self.arguments(tokens))
 
 
 def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.Tensor,
@@ -718,14 +741,14 @@ def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.T
             q_out = _empty((T, hq, D), q.dtype, q.device, stream)
         elif q_out is not q and q_out.shape != q_shape:
             raise ValueError("q_out must have the shape of q")
-        q_args, out_args = _rows(q, "q"), _rows(q_out, "q_out")
+        q_args, out_args = _head_rows(q, _bf16, "q"), _head_rows(q_out, _bf16, "q_out")
     ws = _workspace(256, k.device, stream) if ws is None else ws
     table, npos, rot = _rope(rope)
-    _check("attn_kv_append", lib().attn_kv_append(
-        cache._ref, batch.rows(T), *_rows(k, "k"), *_rows(v, "v"), *q_args, hq, *out_args, table,
-        npos, rot, int(interleaved), _vector(q_weight, D, torch.bfloat16, "q_weight"),
-        _vector(k_weight, D, torch.bfloat16, "k_weight"), eps, _ptr(ws), ws.numel(),
-        _stream(stream)))
+    _check("attn_kv_append", _calls().attn_kv_append(
+        cache.struct, batch.arguments(T), *_head_rows(k, _bf16, "k"), *_head_rows(v, _bf16, "v"),
+        *q_args, hq, *out_args, table, npos, rot, int(interleaved),
+        _vector(q_weight, D, _bf16, "q_weight"), _vector(k_weight, D, _bf16, "k_weight"), eps,
+        _ptr(ws), ws.numel(), _stream(stream)))
     return q_out
 
 
@@ -760,9 +783,10 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
     if ws is None:
         ws = _workspace(lib().attn_paged_workspace_size(batch.batch, T, batch.max_new, hq,
                                                         cache.heads, D), q.device, stream)
-    _check("attn_paged_forward", lib().attn_paged_forward(
-        *_rows(q, "q"), hq, cache._ref, batch.rows(T), D ** -0.5 if scale is None else scale,
-        window, *_rows(out, "out"), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    _check("attn_paged_forward", _calls().attn_paged_forward(
+        *_head_rows(q, _bf16, "q"), hq, cache.struct, batch.arguments(T),
+        D ** -0.5 if scale is None else scale, window, *_head_rows(out, _bf16, "out"), _ptr(lse),
+        _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 
@@ -775,8 +799,8 @@ class PagePool:
     def __init__(self, ring: torch.Tensor, state: torch.Tensor):
         n = ring.shape[0]
         self.ring, self.state, self.size = ring, state, n
-        self._ring = _vector(ring, n, torch.int32, "ring")
-        self._state = _vector(state, 2, torch.int32, "state")
+        self._ring = _vector(ring, n, _i32, "ring")
+        self._state = _vector(state, 2, _i32, "state")
 
     @staticmethod
     def full(pages: int, device="cuda") -> "PagePool":
@@ -804,14 +828,14 @@ def plan_pages(pool: PagePool, batch: AttnBatch, page_size: int, new_tokens: tor
             rows = min(rows, t.shape[0])
     ws = _workspace(256, batch.kv_len.device, stream) if ws is None else ws
     s = batch.struct
-    _check("attn_plan_pages", lib().attn_plan_pages(
+    _check("attn_plan_pages", _calls().attn_plan_pages(
         pool._ring, pool.size, pool._state,
-        pool._state if state_out is None else _vector(state_out, 2, torch.int32, "state_out"), B,
+        pool._state if state_out is None else _vector(state_out, 2, _i32, "state_out"), B,
         page_size, s.max_pages,
-        s.kv_len if kv_before is None else _vector(kv_before, B, torch.int32, "kv_before"),
-        _vector(cached, B, torch.int32, "cached"),
-        _vector(new_tokens, B, torch.int32, "new_tokens"), s.kv_len, s.q_start, s.page_table,
-        None if positions is None else _vector(positions, positions.shape[0], torch.int32,
+        s.kv_len if kv_before is None else _vector(kv_before, B, _i32, "kv_before"),
+        _vector(cached, B, _i32, "cached"),
+        _vector(new_tokens, B, _i32, "new_tokens"), s.kv_len, s.q_start, s.page_table,
+        None if positions is None else _vector(positions, positions.shape[0], _i32,
                                                "positions"),
         None if slots is None else _vector(slots, slots.shape[0], torch.int64, "slots"), rows,
         _ptr(ws), ws.numel(), _stream(stream)))
@@ -856,14 +880,14 @@ def draft_verify(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: to
         next_token = _empty(B, torch.int32, dev, stream)
     ws = _workspace(256, dev, stream) if ws is None else ws
     s = batch.struct
-    _check("draft_verify", lib().draft_verify(
+    _check("draft_verify", _calls().draft_verify(
         *_distributions(target, "target"), *d_args, code, T, vocab,
-        _vector(tokens, T, torch.int32, "tokens"), B, s.q_start, s.kv_len,
-        _vector(accept_u, T, torch.float32, "accept_u"),
-        _vector(sample_u, B, torch.float32, "sample_u"),
-        _vector(accepted, B, torch.int32, "accepted"),
-        _vector(next_token, B, torch.int32, "next_token"),
-        _vector(cached, B, torch.int32, "cached"), _ptr(ws), ws.numel(), _stream(stream)))
+        _vector(tokens, T, _i32, "tokens"), B, s.q_start, s.kv_len,
+        _vector(accept_u, T, _f32, "accept_u"),
+        _vector(sample_u, B, _f32, "sample_u"),
+        _vector(accepted, B, _i32, "accepted"),
+        _vector(next_token, B, _i32, "next_token"),
+        _vector(cached, B, _i32, "cached"), _ptr(ws), ws.numel(), _stream(stream)))
     return accepted, next_token
 
 

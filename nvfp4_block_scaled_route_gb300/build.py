@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +25,24 @@ HEADERS = ["internal.h", "ptx.cuh", "quant.cuh", "attn.cuh", "attn_turn.cuh", "s
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
+
+
+def _hostcall() -> str:
+    """Compiles the extension module that checks and passes arguments (csrc/hostcall.c)."""
+    src, out = os.path.join(CSRC, "hostcall.c"), os.path.join(PKG, "_hostcall.so")
+    header = os.path.join(ROOT, "include", "nvfp4moe.h")
+    if os.path.exists(out) and all(os.path.getmtime(out) > os.path.getmtime(f) for f in (src, header)):
+        return out
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = f"{out}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"),
+           "-I", cuda, "-I", sysconfig.get_paths()["include"], src, "-o", tmp]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout.decode(errors="replace"))
+        raise RuntimeError("hostcall.c does not compile")
+    os.replace(tmp, out)
+    return out
 
 
 def nvcc() -> str:
@@ -60,6 +79,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
     """Compile (if needed) and return the path of libnvfp4moe.so (or of the
     debug-bounds library).  both: build the two variants, their translation
     units compiled concurrently; returns the normal library's path."""
+    _hostcall()
     variants = [False, True] if both else [debug_bounds]
     jobs = []          # (variant, lib, build dir, stamp, objs, procs)
     cc = None
