@@ -49,19 +49,21 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
   const HeadRows& src = value ? a.v : a.k;
   const int ps = a.cache.page_shift;
 
+  if (TOKENS && threadIdx.x < kLanes) {
+    // the row's way in starts before its request is known
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src.data) +
+                             unit * src.token_stride + head * src.head_stride + threadIdx.x * 8;
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+  }
   // ---- the page: request r, whose row t has position t + to_pos ----
   int r;
   if (TOKENS) {
-    r = request_of(a.batch, unit);
+    r = request_of<32>(a.batch, unit, threadIdx.x & 31, 0xFFFFFFFFu);
     if (r < 0) return;
   } else {
-    int hi = a.batch.batch - 1;
-    r = 0;
-    while (r < hi) {
-      const int mid = (r + hi + 1) >> 1;
-      if ((max(0, a.batch.q_start[mid]) >> ps) + 2ll * mid <= unit) r = mid;
-      else hi = mid - 1;
-    }
+    r = last_below<32>(a.batch.batch, threadIdx.x & 31, 0xFFFFFFFFu, [&](int i) {
+      return (max(0, a.batch.q_start[i]) >> ps) + 2ll * i <= unit;
+    });
   }
   const int64_t begin = a.batch.q_start[r], end = a.batch.q_start[r + 1];
   const int64_t row0 = max(begin, int64_t{0}), row1 = min(end, a.batch.tokens);

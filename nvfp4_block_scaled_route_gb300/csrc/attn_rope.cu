@@ -27,8 +27,8 @@ constexpr int kThreads = 128;
 // (With its start over the end of the kernel before, a launch takes 27.4 and 176:
 // 5.0 and 4.3 TB/s; 160 of the latter without the divisions by the scales.  Into the
 // cache instructions bound it (76 % of the issue slots): each group finds its request,
-// page and rotation anew, and at 48 registers a thread spills 116 to 132 bytes and
-// reads 216 to 240 back.  Groups that keep what they have found for 8 or 16 heads in
+// page and rotation anew, and at 48 registers a thread spills 104 to 108 bytes and
+// reads 204 to 224 back.  Groups that keep what they have found for 8 or 16 heads in
 // rounds of 4 took 187 to 190 us, before the divisions.)
 // Below kWideRows head rows two heads a group spread few tokens wider (into the cache
 // at the same 48 registers, with 52 to 68 bytes of spills).

@@ -20,18 +20,31 @@ struct RopeArgs {
   int* status;
 };
 
-// The request that holds row t: the last r with q_start[r] <= t (so empty
-// requests are passed over); -1 for a row of no request.
-__device__ __forceinline__ int request_of(const BatchView& b, uint32_t row) {
-  const int64_t t = row;
-  if (t >= b.q_start[b.batch] || t < b.q_start[0]) return -1;
-  int lo = 0, hi = b.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (b.q_start[mid] <= t) lo = mid;
-    else hi = mid - 1;
+// The last i of [0, n) with below(i), which holds up to there and not after (0 if it
+// holds nowhere), by the lanes of `mask`: LANES neighbours, of which this is number `sub`,
+// probe at a time (each round is a load that the next one waits for).
+template <int LANES, typename F>
+__device__ __forceinline__ int last_below(int n, int sub, uint32_t mask, F below) {
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + LANES - 1) / LANES, at = sub * step;
+    const uint32_t yes = (__ballot_sync(mask, at < n && below(lo + at)) & mask) >> (__ffs(mask) - 1);
+    const int skip = (31 - __clz(yes | 1u)) * step;
+    n = min(step, n - skip);
+    lo += skip;
   }
   return lo;
+}
+
+// The request that holds row t: the last r with q_start[r] <= t (so empty
+// requests are passed over); -1 for a row of no request.
+template <int LANES>
+__device__ __forceinline__ int request_of(const BatchView& b, uint32_t row, int sub,
+                                          uint32_t mask) {
+  const int64_t t = row;
+  const int first = b.q_start[0], end = b.q_start[b.batch];
+  const int r = last_below<LANES>(b.batch, sub, mask, [&](int i) { return b.q_start[i] <= t; });
+  return t >= end || t < first ? -1 : r;
 }
 
 // Four bf16 (8 bytes) as two pairs of floats.
@@ -199,7 +212,7 @@ __device__ __forceinline__ void transform_heads(const RopeArgs& a, uint32_t item
   int64_t pos = 0;
   int64_t slot = 0;                                   // element offset of (page, offset)
   if (APPEND) {
-    const int r = request_of(a.batch, t);
+    const int r = request_of<kLanes>(a.batch, t, sub, mask);
     if (r < 0) return;
     pos = static_cast<int64_t>(a.batch.kv_len[r]) - a.batch.q_start[r + 1] + t;
     const int64_t page_i = pos >> a.cache.page_shift;
