@@ -280,7 +280,7 @@ struct Walk {
 template <int PAGED>
 constexpr int kTileScales = 2 * PAGED;                 // of one kind
 
-template <int D, bool FP8, int PAGED>
+template <int D, bool FP8, int PAGED, bool HALF>
 struct Cfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kBytes = kKeys * D * 2;         // an operand tile
@@ -290,7 +290,7 @@ struct Cfg {
   static constexpr int kHalves = kRow / kLine;         // column blocks
   // tiles of keys (as loaded), operand tiles of values (bf16: as loaded), raw
   // tiles of E4M3 values
-  static constexpr int kK = (FP8 && PAGED < 4 ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
+  static constexpr int kK = (FP8 && PAGED < 4 && !HALF ? 4 : 3) * (D == 128 ? 1 : 2), kV = 3 * (D == 128 ? 1 : 2);
   static constexpr int kRaw = FP8 ? (D == 128 ? 2 : 5) : 0;
   static constexpr int kVAt = kBytes;                  // after the queries: values, keys, raw
   static constexpr int kKAt = kVAt + kV * kBytes, kRawAt = kKAt + kK * kLoadBytes;
@@ -300,8 +300,11 @@ struct Cfg {
   static constexpr int kWords = 4 * kTile * 4 + 2 * kTile;
   static constexpr int kSlots = kK + 3 <= 8 ? 8 : 16;
   static constexpr int kScaleBytes = kSlots * 2 * kTileScales<PAGED> * 4;
-  static constexpr int kSmem =
-      kRing + 512 + (kWords + kScaleBytes <= 5 * kTile * 4 ? 5 * kTile * 4 : kWords + kScaleBytes);
+  static constexpr int kBytesOfWords =
+      kWords + kScaleBytes <= 5 * kTile * 4 ? 5 * kTile * 4 : kWords + kScaleBytes;
+  // HALF: 16 dimensions of the second copies' sums, and their references and weight sums
+  static constexpr int kPart = kRing + 512 + kBytesOfWords;
+  static constexpr int kSmem = kPart + (HALF ? kTile * 16 * 4 + kTile / 2 * 8 : 0);
   static_assert(kK + 3 <= kSlots, "slots");
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr uint32_t kTmemO = 256, kTmemP = 384;   // S: columns 0 and 128
@@ -311,6 +314,11 @@ struct Cfg {
       FP8 ? idesc_e4m3_f32(kTile, kKeys) : idesc_bf16_f32(kTile, kKeys);
   static constexpr uint32_t kIdescO = (idesc_bf16_f32(kTile, D) ^ kFormats) | (1u << 16);
 };
+
+// All softmax threads.
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 9, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
 
 struct Bars {
   uint64_t full[14], empty[14];                        // loaded tiles: keys, then values
@@ -355,12 +363,15 @@ __device__ __forceinline__ uint32_t raw_at(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D, bool FP8, int PAGED>
-__global__ void __launch_bounds__(Cfg<D, FP8, PAGED>::kThreads, 1)
+// HALF: up to 64 rows of a request and key head.  They stand twice among the 128 rows of a
+// tile's products, and the copies have 64 keys of a tile each: a thread then has 32 of
+// them.  (The copies' references and sums are their own, joined at the end.)
+template <int D, bool FP8, int PAGED, bool HALF>
+__global__ void __launch_bounds__(Cfg<D, FP8, PAGED, HALF>::kThreads, 1)
 attention_chunk_kernel(const __grid_constant__ AttnArgs a,
                        const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v) {
-  using C = Cfg<D, FP8, PAGED>;
+  using C = Cfg<D, FP8, PAGED, HALF>;
   // the swizzle goes by the address: tiles start at multiples of 1024 bytes,
   // and there is no room to round up to one
   extern __shared__ __align__(1024) uint8_t sq[];       // queries, operand tiles, raw tiles
@@ -686,17 +697,21 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   } else {
     // ---- softmax: a row's keys 0-63 and 64-127 in two threads ----
     if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int half = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + half * 64 + lanes;                     // this thread's scores,
-    const uint32_t tp = tmem + C::kTmemP + half * 32 + lanes;         // weights,
+    const int half = warp >> 2, quarter = warp & 3;
+    constexpr int kMine = HALF ? 32 : 64;                             // keys of a thread
+    const int copy = HALF ? quarter >> 1 : 0;
+    const int place = quarter * 32 + lane;                            // row of the products
+    const int row = HALF ? place & 63 : place;                        // of the block
+    const int key0 = half * 64 + copy * 32;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + key0 + lanes;                          // this thread's scores,
+    const uint32_t tp = tmem + C::kTmemP + key0 / 2 + lanes;          // weights,
     const uint32_t to = tmem + C::kTmemO + half * (D / 2) + lanes;    // output columns
     const int pair_bar = 1 + (warp & 3);                              // the two warps of 32 rows
     // words of a row's two threads: [tile parity][half][row].  A tile's word has
     // been read once its thread has met the other one at the next tile's.
-    float* mine = swap + half * kTile + row;
-    const float* other = swap + (half ^ 1) * kTile + row;
+    float* mine = swap + half * kTile + place;
+    const float* other = swap + (half ^ 1) * kTile + place;
     AttnPiece* piece = a.pieces + blockIdx.x;
     bool begun = false;
     // 32-byte stores of the output rows
@@ -719,7 +734,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       j0 = t;
       sees = wk.b.kend > 0;
       row0 = wk.b.row0;
-      busy = (warp & 3) * 32 < rows;
+      busy = (HALF ? quarter & 1 : quarter) * 32 < rows;
       const int my = row0 + min(row, rows - 1);  // rows past the end act as the last
       tok = a.group(my);
       tk = wk.rq.first + tok;
@@ -743,9 +758,10 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       // the queries, D / 8 lanes a row (the last S with the previous ones has landed)
       constexpr int kLanes = D / 8, kStep = kSoftmaxThreads / kLanes;
       const int ch = threadIdx.x & (kLanes - 1), i0 = threadIdx.x / kLanes;
-      uint4 u[kTile / kStep];
+      constexpr int kTurns = (HALF ? kTile / 2 : kTile) / kStep;
+      uint4 u[kTurns];
 #pragma unroll
-      for (int i = 0; i < kTile / kStep; ++i) {
+      for (int i = 0; i < kTurns; ++i) {
         u[i] = make_uint4(0, 0, 0, 0);
         if (i0 + i * kStep < rows) {
           const int r = row0 + i0 + i * kStep, k = a.group(r);
@@ -755,7 +771,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         }
       }
 #pragma unroll
-      for (int i = 0; i < kTile / kStep; ++i) {
+      for (int i = 0; i < kTurns; ++i) {
         if (FP8) {
           float x[8], most = 0.0f;
           bf16x8_to_float(u[i], x);
@@ -770,7 +786,10 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           const bool finite = e != 255;
           e = e == 0 || e == 255 ? 127 : min(max(e, 8), 253);
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
-          if (ch == 0) q_exp[seg * kTile + i0 + i * kStep] = static_cast<uint8_t>(e);
+          if (ch == 0) {
+            q_exp[seg * kTile + i0 + i * kStep] = static_cast<uint8_t>(e);
+            if (HALF) q_exp[seg * kTile + 64 + i0 + i * kStep] = static_cast<uint8_t>(e);
+          }
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int k = 0; k < 8; k += 4) {
@@ -790,6 +809,10 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           uint8_t* to = sq + raw_at<D>(i0 + i * kStep, ch >> 1) + (ch & 1) * 8;
           *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(to + kTile * D) = make_uint2(lo[0], lo[1]);
+          if (HALF) {                                     // (64 rows on: the swizzle stays)
+            *reinterpret_cast<uint2*>(to + 64 * D) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + (kTile + 64) * D) = make_uint2(lo[0], lo[1]);
+          }
         } else {
           *reinterpret_cast<uint4*>(sq + tile_at(i0 + i * kStep, ch)) = u[i];
         }
@@ -797,6 +820,14 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
       fence_proxy_async_smem();
       mbar_arrive(&bars->q_ready);
     };
+    if constexpr (HALF) {
+      // no weights where the other copy has its own
+      const uint32_t zeros[32] = {};
+      tmem_st_32x32b_x32(tmem + C::kTmemP + half * 32 + lanes, zeros);
+      tmem_st_32x32b_x32(tmem + C::kTmemP + 64 + half * 32 + lanes, zeros);
+      tmem_st_wait();
+      tc_fence_before();
+    }
     bool more = left > 0;
     if (more) open();
     while (more) {
@@ -805,8 +836,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         float cr = c;
         const int seg_now = seg;
         const int pos = wk.rq.pos0 + tok;
-        const int vis_hi = min(pos + 1, wk.rq.len) - half * 64;
-        const int vis_lo = first_key(pos, a.window) - half * 64;
+        const int vis_hi = min(pos + 1, wk.rq.len) - key0;
+        const int vis_lo = first_key(pos, a.window) - key0;
         // keys that every row of the warp sees (rows come in order)
         const int all_hi = __shfl_sync(0xFFFFFFFFu, vis_hi, 0);
         const int all_lo = __shfl_sync(0xFFFFFFFFu, vis_lo, 31);
@@ -818,7 +849,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             // (not 0, which would make NaN of the -inf of a hidden key; nor when the scale
             // of a page comes in, or infinite then)
             cr = fmaxf(PAGED ? 0x1p-86f : 0x1p-126f,
-                       c * __uint_as_float(static_cast<uint32_t>(q_exp[seg_now * kTile + row])
+                       c * __uint_as_float(static_cast<uint32_t>(q_exp[seg_now * kTile + place])
                                            << 23));
           if (PAGED) cr = fminf(cr, 0x1p86f);
           if (!busy) {                                  // what these rows hold is not used
@@ -829,32 +860,33 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           }
           __syncwarp();
           tc_fence_after();
-          uint32_t s[2][32];
+          uint32_t s[kMine / 32][32];
           tmem_ld_32x32b_x32(ts + sb * 128, s[0]);
-          tmem_ld_32x32b_x32(ts + sb * 128 + 32, s[1]);
+          if constexpr (!HALF) tmem_ld_32x32b_x32(ts + sb * 128 + 32, s[1]);
           tmem_ld_wait();
           tc_fence_before();
           mbar_arrive(&bars->s_free[sb]);
-          if (j * kKeys + 64 > all_hi) {
+          if (j * kKeys + kMine > all_hi) {
             const int h = vis_hi - j * kKeys;
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < kMine; ++i)
               if (i >= h) s[i >> 5][i & 31] = 0xFF800000u;              // -inf
           }
           if (j * kKeys < all_lo) {
             const int lw = vis_lo - j * kKeys;
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < kMine; ++i)
               if (i < lw) s[i >> 5][i & 31] = 0xFF800000u;
           }
           float top;
           // PAGED: the factor of the scores of a page's keys, and the power of two that
           // the values' scale adds to a weight, taken along in the exponent: the
           // reference is one of s + log2(scale)
-          constexpr int kG = PAGED ? PAGED : 1;
+          constexpr int kG = PAGED == 4 ? kMine / 16 : 1;
           float cg[kG], lift[kG], inv_scale[kG];
           if (PAGED) {
-            const float* sc = scales + n % C::kSlots * (2 * kTS) + half * PAGED;
+            const float* sc = scales + n % C::kSlots * (2 * kTS) + half * PAGED +
+                              (PAGED == 4 ? copy * kG : 0);
             top = -INFINITY;
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
@@ -863,7 +895,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
               inv_scale[g] = exp2_approx(-lift[g]);
               float m4[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 64 / kG * g; i < 64 / kG * (g + 1); i += 2)
+              for (int i = kMine / kG * g; i < kMine / kG * (g + 1); i += 2)
                 m4[(i >> 1) & 1] = max3(m4[(i >> 1) & 1], __uint_as_float(s[i >> 5][i & 31]),
                                         __uint_as_float(s[i >> 5][(i & 31) + 1]));
               top = fmaxf(top, fmaf(fmaxf(m4[0], m4[1]), cg[g], lift[g]));
@@ -871,7 +903,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           } else {
             float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
+            for (int i = 0; i < kMine; i += 8)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 t4[k] = max3(t4[k], __uint_as_float(s[i >> 5][(i & 31) + 2 * k]),
@@ -908,12 +940,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           const float use = m == -INFINITY ? 0.0f : m;  // a row without keys so far
           uint64_t sum[2] = {0, 0};
           float s0, s1, both = 0.0f;
-          uint32_t p[32];
+          uint32_t p[kMine / 2];
           const uint64_t c2 = f32x2(cr, cr), use2 = f32x2(-use, -use);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < kMine / 2; ++k) {
             float x, y;
-            const int g = k / (32 / kG);
+            const int g = k / (kMine / 2 / kG);
             const uint64_t by = PAGED ? f32x2(cg[g], cg[g]) : c2;
             const uint64_t plus = PAGED ? f32x2(lift[g] - use, lift[g] - use) : use2;
             f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[k >> 4][(2 * k) & 31]),
@@ -923,7 +955,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             y = exp2_approx(y);
             sum[k & 1] = add_f32x2(sum[k & 1], f32x2(x, y));
             p[k] = FP8 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-            if (PAGED && k % (32 / kG) == 32 / kG - 1) {
+            if (PAGED && k % (kMine / 2 / kG) == kMine / 2 / kG - 1) {
               // the weights themselves: without the values' scale
               f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
               both = fmaf(s0 + s1, inv_scale[g], both);
@@ -935,7 +967,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
             __syncwarp();
             tc_fence_after();
           }
-          tmem_st_32x32b_x32(tp + sb * 64, p);
+          if constexpr (HALF) tmem_st_32x32b_x16(tp + sb * 64, p);
+          else tmem_st_32x32b_x32(tp + sb * 64, p);
           f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
           l += PAGED ? both : s0 + s1;
           tmem_st_wait();
@@ -944,7 +977,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         }
       }
       // ---- the next segment's queries, then this one's rows ----
-      const bool seen = sees, real = row < rows, live = busy, to_out = whole;
+      const bool seen = sees, real = row < rows && copy == 0, live = busy, to_out = whole;
       const int64_t tk_out = tk;
       const int head_out = head;
       const int64_t at = (2 * static_cast<int64_t>(blockIdx.x) + slot) * kTile + row;
@@ -957,7 +990,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         t = wk.b.t0;
       }
       if (more) open();
-      if (!live) continue;
+      if (!HALF && !live) continue;
       if (seen) {
         mbar_wait(&bars->pv_done[end & 1u], (end >> 1) & 1u, a.status, abort);
         __syncwarp();
@@ -967,6 +1000,22 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         mine[((n + 1) & 1u) * 2 * kTile] = l;
         asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
         l += other[((n + 1) & 1u) * 2 * kTile];
+      }
+      // HALF: the second copy's part, 16 dimensions at a time
+      float f0 = 1.0f, f1 = 0.0f;
+      float* part = reinterpret_cast<float*>(sq + C::kPart) + half * 64 + row;   // [16][kTile]
+      float2* part_ml = reinterpret_cast<float2*>(sq + C::kPart + kTile * 16 * 4) + row;
+      if constexpr (HALF) {
+        if (copy == 1 && half == 0) *part_ml = make_float2(m, l);
+        softmax_sync();
+        if (copy == 0) {
+          const float2 ml = *part_ml;
+          const float mn = fmaxf(m, ml.x), use = mn == -INFINITY ? 0.0f : mn;
+          f0 = exp2_approx(m - use);
+          f1 = exp2_approx(ml.x - use);
+          l = l * f0 + ml.y * f1;
+          m = mn;
+        }
       }
       // (a tile that saw no key here: zeros)
       const float inv = l == 0.0f ? 0.0f : v_scale / l;
@@ -983,6 +1032,21 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if constexpr (HALF) {
+#pragma unroll
+          for (int k0 = 0; k0 < 32; k0 += 16) {
+            if (copy == 1)
+#pragma unroll
+              for (int k = 0; k < 16; ++k) part[k * kTile] = __uint_as_float(o[k0 + k]);
+            softmax_sync();
+            if (copy == 0)
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                o[k0 + k] = __float_as_uint(
+                    fmaf(part[k * kTile], f1, __uint_as_float(o[k0 + k]) * f0));
+            softmax_sync();
+          }
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) probe = fmaf(__uint_as_float(o[k]), 0.0f, probe);
@@ -1022,7 +1086,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     }
     if (threadIdx.x == 0 && !begun) piece->rows = 0;
     tc_fence_before();
-    asm volatile("bar.sync 9, %0;" ::"n"(kSoftmaxThreads) : "memory");
+    softmax_sync();
     if (bars->spoilt != 0 && st.left > 0) {
       // ---- rows that hidden keys may have spoilt: the same walk again ----
       wk.load(a, group, st.request);
@@ -1051,12 +1115,12 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   }
 }
 
-template <int D, bool FP8, int PAGED = 0>
+template <int D, bool FP8, int PAGED = 0, bool HALF = false>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid,
                    cudaStream_t stream) {
   static PerDeviceOnce once;
-  using C = Cfg<D, FP8, PAGED>;
-  auto kernel = attention_chunk_kernel<D, FP8, PAGED>;
+  using C = Cfg<D, FP8, PAGED, HALF>;
+  auto kernel = attention_chunk_kernel<D, FP8, PAGED, HALF>;
   cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
   // its prologue overlaps the plan; it waits for the plan before it reads anything
@@ -1082,12 +1146,17 @@ cudaError_t launch_attn_plan(const AttnArgs& a, int grid, cudaStream_t stream) {
 
 cudaError_t launch_attention_chunk(const AttnArgs& a, const CUtensorMap& map_k,
                                    const CUtensorMap& map_v, int grid, cudaStream_t stream) {
-  if (a.cache.paged && a.cache.page_shift >= 6)
-    return a.cache.head_dim == 128 ? launch<128, true, 1>(a, map_k, map_v, grid, stream)
-                                   : launch<64, true, 1>(a, map_k, map_v, grid, stream);
-  if (a.cache.paged)
-    return a.cache.head_dim == 128 ? launch<128, true, 4>(a, map_k, map_v, grid, stream)
-                                   : launch<64, true, 4>(a, map_k, map_v, grid, stream);
+  if (a.cache.paged) {
+    const bool half = int64_t{a.batch.max_new} * a.group.d <= kTile / 2;
+    const auto by_rows = [&](auto whole, auto halves) {
+      return (half ? halves : whole)(a, map_k, map_v, grid, stream);
+    };
+    if (a.cache.page_shift >= 6)
+      return a.cache.head_dim == 128 ? by_rows(launch<128, true, 1>, launch<128, true, 1, true>)
+                                     : by_rows(launch<64, true, 1>, launch<64, true, 1, true>);
+    return a.cache.head_dim == 128 ? by_rows(launch<128, true, 4>, launch<128, true, 4, true>)
+                                   : by_rows(launch<64, true, 4>, launch<64, true, 4, true>);
+  }
   if (a.cache.fp8)
     return a.cache.head_dim == 128 ? launch<128, true>(a, map_k, map_v, grid, stream)
                                    : launch<64, true>(a, map_k, map_v, grid, stream);
