@@ -273,10 +273,11 @@ struct Walk {
 
 // PAGED: E4M3 pages with scales of their own, PAGED of them (1 for pages of 64 tokens
 // and more, else 4) in a thread's 64 keys of a tile.  The keys' loader keeps them in
-// slots by the number of the tile, those of keys and those of values.  A slot is written again once S of the tile kK
+// slots by the number of the tile, and the warp that issues S makes them ready.  A slot is
+// written again once S of the tile kK
 // back is done, whose own start had all softmax threads past the scores of the tile two
 // before that: kK + 3 tiles may be in use.  (With a fourth buffer of keys there is room
-// for eight slots of 2 x 2.)
+// for eight slots of 3 x 2.)
 template <int PAGED>
 constexpr int kTileScales = 2 * PAGED;                 // of one kind
 
@@ -299,7 +300,7 @@ struct Cfg {
   // bytes if that does
   static constexpr int kWords = 4 * kTile * 4 + 2 * kTile;
   static constexpr int kSlots = kK + 3 <= 8 ? 8 : 16;
-  static constexpr int kScaleBytes = kSlots * 2 * kTileScales<PAGED> * 4;
+  static constexpr int kScaleBytes = kSlots * 3 * kTileScales<PAGED> * 4;
   static constexpr int kBytesOfWords =
       kWords + kScaleBytes <= 5 * kTile * 4 ? 5 * kTile * 4 : kWords + kScaleBytes;
   // HALF: 16 dimensions of the second copies' sums, and their references and weight sums
@@ -385,7 +386,8 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
   // a segment ahead of another)
   uint8_t* q_exp = reinterpret_cast<uint8_t*>(swap + 4 * kTile);
   constexpr int kTS = kTileScales<PAGED>;
-  float* scales = reinterpret_cast<float*>(q_exp + 2 * kTile);  // [slot][2][kTS]
+  // [slot][3][kTS]: those of keys, of values as logarithms, and inverted
+  float* scales = reinterpret_cast<float*>(q_exp + 2 * kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -401,7 +403,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
     }
     mbar_init(&bars->q_ready, kSoftmaxThreads);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_full[i], PAGED ? 2 : 1);      // (and the scales made ready)
       mbar_init(&bars->s_free[i], kSoftmaxThreads);
       mbar_init(&bars->p_ready[i], kSoftmaxThreads);
       mbar_init(&bars->pv_done[i], 1);
@@ -517,7 +519,7 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           if (wk.b.kend > 0) {
             // (a page out of range has been reported: zeros)
             const bool there = scale_page >= 0 && scale_page < a.cache.num_pages;
-            cp_async_4(scales + tiles % C::kSlots * (2 * kTS) + (lane < 16 ? 0 : kTS) + part,
+            cp_async_4(scales + tiles % C::kSlots * (3 * kTS) + (lane < 16 ? 0 : kTS) + part,
                        (lane < 16 ? a.cache.k_scale : a.cache.v_scale) +
                            (there ? scale_page * int64_t{a.cache.heads} + wk.h : 0),
                        there);
@@ -652,6 +654,19 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
                           ks != 0);
               }
               tc_commit(&bars->s_full[sb]);
+            }
+            if (PAGED) {
+              // while they run: the keys' scales, and the values' as logarithms and inverted
+              const int part = lane & 7;
+              float* sc = scales + n % C::kSlots * (3 * kTS) + part;
+              if (part < kTS && lane < 8) sc[0] = page_scale(sc[0]);
+              if (part < kTS && lane >= 8 && lane < 16) {
+                const float log_scale = __log2f(page_scale(sc[kTS]));
+                sc[kTS] = log_scale;
+                sc[2 * kTS] = exp2_approx(-log_scale);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->s_full[sb]);
             }
           }
         } else {
@@ -885,14 +900,14 @@ attention_chunk_kernel(const __grid_constant__ AttnArgs a,
           constexpr int kG = PAGED == 4 ? kMine / 16 : 1;
           float cg[kG], lift[kG], inv_scale[kG];
           if (PAGED) {
-            const float* sc = scales + n % C::kSlots * (2 * kTS) + half * PAGED +
+            const float* sc = scales + n % C::kSlots * (3 * kTS) + half * PAGED +
                               (PAGED == 4 ? copy * kG : 0);
             top = -INFINITY;
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-              cg[g] = cr * page_scale(sc[g]);
-              lift[g] = __log2f(page_scale(sc[kTS + g]));
-              inv_scale[g] = exp2_approx(-lift[g]);
+              cg[g] = cr * sc[g];
+              lift[g] = sc[kTS + g];
+              inv_scale[g] = sc[2 * kTS + g];
               float m4[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int i = kMine / kG * g; i < kMine / kG * (g + 1); i += 2)
