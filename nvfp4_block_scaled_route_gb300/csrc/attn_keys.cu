@@ -70,7 +70,7 @@ struct Cfg {
   // buffers of keys and of values
   static constexpr int kK = 3, kV = RG > 4 ? 2 : 3;
   static constexpr int kWordsAt = kRingAt + (kK + kV) * kTileBytes;
-  static constexpr int kScaleBytes = kScaleSlots * 2 * kTileScales * 4;
+  static constexpr int kScaleBytes = kScaleSlots * 3 * kTileScales * 4;
   static_assert(kK + 3 <= kScaleSlots, "slots");
   // of a row, [segment parity]: its factor, its first and last key + 1
   static constexpr int kRowBytes = 2 * kRows * 12;
@@ -192,8 +192,8 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     return;
   }
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kWordsAt);
-  float* scales = reinterpret_cast<float*>(smem + C::kWordsAt + 512);   // [slot][2][kTileScales]
-  float* row_factor = scales + kScaleSlots * 2 * kTileScales;           // [parity][kRows]
+  float* scales = reinterpret_cast<float*>(smem + C::kWordsAt + 512);   // [slot][3][kTileScales]
+  float* row_factor = scales + kScaleSlots * 3 * kTileScales;           // [parity][kRows]
   int* row_lo = reinterpret_cast<int*>(row_factor + 2 * C::kRows);
   int* row_hi = row_lo + 2 * C::kRows;
   float* join = reinterpret_cast<float*>(row_hi + 2 * C::kRows);        // [group][warp][RG]
@@ -231,7 +231,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     }
     mbar_init(&bars->q_ready, kSoftmaxThreads);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_full[i], 2);                  // (and the scales made ready)
       mbar_init(&bars->s_free[i], kSoftmaxThreads);
       mbar_init(&bars->p_ready[i], kSoftmaxThreads);
       mbar_init(&bars->pv_done[i], 1);
@@ -343,7 +343,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
           mbar_arrive_expect_tx(&full[buf], static_cast<uint32_t>(loads * box * kD));
         if (brings) {
           const int64_t from = take && there ? page * int64_t{a.cache.heads} + wk.h : 0;
-          cp_async_4(scales + tiles % kScaleSlots * (2 * kTileScales) + lane - 8, side + from,
+          cp_async_4(scales + tiles % kScaleSlots * (3 * kTileScales) + lane - 8, side + from,
                      take && there);
           cp_async_arrive(&full[buf]);
         } else if (take) {
@@ -399,6 +399,17 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
             }
             tc_commit(&bars->s_full[sb]);
           }
+          // while they run: the keys' scales, and the values' as logarithms and inverted
+          float* sc = scales + n % kScaleSlots * (3 * kTileScales) + (lane & 7);
+          if (lane < 8) {
+            sc[0] = page_scale(sc[0]);
+          } else if (lane < 16) {
+            const float log_scale = __log2f(page_scale(sc[kTileScales]));
+            sc[kTileScales] = log_scale;
+            sc[2 * kTileScales] = exp2_approx(-log_scale);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->s_full[sb]);
         } else {
           mbar_wait(&bars->p_ready[sb], parity, a.status, abort);
           tc_fence_after();
@@ -540,9 +551,8 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         tmem_ld_n<RG>(tmem + sb * C::kN1 + g * RG + lanes, s);
         tc_fence_before();
         mbar_arrive(&bars->s_free[sb]);
-        const float* sc = scales + n % kScaleSlots * (2 * kTileScales) + (key >> 4);
-        const float ks = page_scale(sc[0]), lift = __log2f(page_scale(sc[kTileScales]));
-        const float inv_scale = exp2_approx(-lift);
+        const float* sc = scales + n % kScaleSlots * (3 * kTileScales) + (key >> 4);
+        const float ks = sc[0], lift = sc[kTileScales], inv_scale = sc[2 * kTileScales];
         // (S follows the arrivals of all that wrote the queries and the rows' words)
         float y[RG];
         bool over = false;
