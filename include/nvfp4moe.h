@@ -702,7 +702,7 @@ typedef struct {
  * values are multiplied by old / new and rounded where that is the new one
  * (between powers of two only values below 2^-6 s lose bits).  What the page
  * holds past the request's length is left as it is.  A page that gets new
- * tokens belongs to one request alone.
+ * tokens belongs to one request alone and stands once in its table row.
  *   q NULL (q_heads 0): keys and values only.  q_out may be q itself.
  *   workspace   at least 256 bytes (the status word).
  * Limits: tokens * (q_heads + 2 * kv_heads) < 2^31. */

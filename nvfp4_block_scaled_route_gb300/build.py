@@ -29,7 +29,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 def _hostcall() -> str:
     """Compiles the extension module that checks and passes arguments (csrc/hostcall.c)."""
-    src, out = os.path.join(CSRC, "hostcall.c"), os.path.join(PKG, "_hostcall.so")
+    src = os.path.join(CSRC, "hostcall.c")
+    out = os.path.join(PKG, "_hostcall" + sysconfig.get_config_var("EXT_SUFFIX"))
     header = os.path.join(ROOT, "include", "nvfp4moe.h")
     if os.path.exists(out) and all(os.path.getmtime(out) > os.path.getmtime(f) for f in (src, header)):
         return out

@@ -537,6 +537,20 @@ def test_append_twice_and_from_a_graph(nb):
     assert all(torch.equal(a, b) for a, b in zip(replayed, state())) and nb.read_status(ws) == 0
 
 
+def test_append_with_queries_in_place(nb):
+    """q_out may be q itself: the same rows as into a buffer of its own."""
+    for reqs in ([(3, 20), (1, 16)], [(100, 130), (60, 60)]):
+        pages = Pages(reqs, 2, 128, 16)
+        x = torch.randn(pages.tokens, 10, 128, generator=pages.g).bfloat16().to(DEV)
+        rope = rope_table(130, 128).to(DEV)
+        w = torch.ones(128).bfloat16().to(DEV)
+        cache, batch = pages.handles(nb)
+        q, k, v = x.split([6, 2, 2], 1)
+        apart = nb.kv_append(cache, batch, k, v, rope, w, q=q, q_weight=w)
+        again = nb.kv_append(cache, batch, k, v, rope, w, q=q, q_weight=w, q_out=q)
+        assert again is q and torch.equal(apart, q)
+
+
 def pages_free(pages):
     used = {int(p) for r, (_, length) in enumerate(pages.reqs)
             for p in pages.table[r, :-(-length // pages.page)]}

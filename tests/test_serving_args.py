@@ -125,3 +125,77 @@ def test_draft_verify_binding_refuses(nb):
                dict(cached=Device(3))):
         with pytest.raises(ValueError, match="must"):
             nb.draft_verify(batch=batch, **{**good, **kw})
+
+
+# --------------------------------------------------------- the extension --
+def test_the_extension_checks_head_rows(nb):
+    class Rows(Cache):
+        def __init__(self, *shape, dtype=torch.bfloat16, strides=None):
+            super().__init__(*shape, dtype=dtype)
+            self.strides = strides
+
+        def stride(self, i=None):
+            return self.strides or super().stride(i)
+    rows = nb._calls().rows
+    assert rows(Rows(5, 4, 128), torch.bfloat16, "q") == (1 << 20, 512, 128)
+    assert rows(Rows(5, 4, 128, strides=(1024, 128, 1)), torch.bfloat16, "q") == (1 << 20, 1024, 128)
+    for bad in (Rows(5, 4, 128, dtype=torch.float16), Rows(5, 128)):
+        with pytest.raises(ValueError, match="q must be a bf16 CUDA tensor"):
+            rows(bad, torch.bfloat16, "q")
+    cpu = Rows(5, 4, 128)
+    cpu.is_cuda = False
+    with pytest.raises(ValueError, match="q must be a bf16 CUDA tensor"):
+        rows(cpu, torch.bfloat16, "q")
+    with pytest.raises(ValueError, match="head_dim must be contiguous"):
+        rows(Rows(5, 4, 128, strides=(512, 1, 4)), torch.bfloat16, "q")
+    with pytest.raises(AttributeError):
+        rows(3, torch.bfloat16, "q")
+
+
+def test_the_extension_checks_vectors(nb):
+    vector = nb._calls().vector
+    assert vector(None, 3, torch.int32, "x") is None
+    assert vector(Device(3), 3, torch.int32, "x") == 1 << 20
+    for bad, n in ((Device(3), 4), (Device(3, dtype=torch.int64), 3), (Device(3, 1), 3)):
+        with pytest.raises(ValueError, match=r"x must be torch.int32 \[%d\]" % n):
+            vector(bad, n, torch.int32, "x")
+    loose = Device(3)
+    loose.is_contiguous = lambda: False
+    with pytest.raises(ValueError, match="x must be a dense CUDA tensor"):
+        vector(loose, 3, torch.int32, "x")
+    with pytest.raises(TypeError):
+        vector(Device(3), 3)
+
+
+def test_the_extension_passes_arguments_as_they_are(nb):
+    """Each call's refusals are those of the entry point itself; what is no argument at all
+    raises before it."""
+    host = nb._calls()
+    plan = [FAKE, 8, FAKE, FAKE, 2, 16, 4, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 10, FAKE, 0, None]
+    assert host.attn_plan_pages(*plan) == SMALL
+    for at, value, want in ((1, 0, INVALID), (5, 24, SHAPE), (6, 1 << 40, SHAPE), (0, None, INVALID),
+                            (15, 1 << 31, SHAPE), (16, None, INVALID), (16, FAKE + 4, SMALL)):
+        assert host.attn_plan_pages(*plan[:at], value, *plan[at + 1:]) == want
+    with pytest.raises(TypeError):
+        host.attn_plan_pages(*plan[:-1])
+    with pytest.raises(TypeError):
+        host.attn_plan_pages("ring", *plan[1:])
+    with pytest.raises(OverflowError):
+        host.attn_plan_pages(FAKE, 1 << 70, *plan[2:])
+    cache = nb.KvCache(FAKE, FAKE, nb.E4M3_PAGES, 2, 128, 16, 8, 16 * 256, 256, 128, FAKE, FAKE)
+    batch = nb.AttnBatchArgs(2, 1, 2, 4, FAKE, FAKE, FAKE)
+    call = [FAKE, 512, 128, 4, cache, batch, 1.0, 0, FAKE + 4096, 512, 128, None, FAKE, 0, None]
+    assert host.attn_paged_forward(*call) == SMALL
+    assert host.attn_paged_forward(*call[:6], float("nan"), *call[7:]) == INVALID
+    assert host.attn_paged_forward(*call[:7], -1, *call[8:]) == INVALID
+    with pytest.raises(TypeError):
+        host.attn_paged_forward(*call[:4], 7, *call[5:])
+    append = [cache, batch, FAKE, 256, 128, FAKE, 256, 128, None, 0, 0, 0, None, 0, 0, None, 0, 0, 0, None, None, 1e-6,
+              FAKE, 0, None]
+    assert host.attn_kv_append(*append) == SMALL
+    assert host.attn_kv_append(*append[:21], -1.0, FAKE, 256, None) == INVALID
+    verify = [FAKE, 100, FAKE, 100, 1, 6, 100, FAKE, 2, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None]
+    assert host.draft_verify(*verify) == SMALL
+    rope = [FAKE, 512, 128, 4, FAKE, 256, 128, 2, 3, 128, FAKE, FAKE, 16, 128, 0, FAKE, FAKE, 1e-6, FAKE, 512, 128,
+            FAKE, 256, 128, FAKE, 0, None]
+    assert host.attn_qk_norm_rope(*rope) == SMALL
