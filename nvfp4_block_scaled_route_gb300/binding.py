@@ -163,12 +163,12 @@ def _calls():
 
 
 def _hostcall():
-    global _vector, _head_rows
+    global _vector, _head_rows, _run, _dense
     try:
         from . import _hostcall as h
     except ImportError as e:
         raise RuntimeError("_hostcall is missing: run __graft_entry__.build() first") from e
-    _vector, _head_rows = h.vector, h.rows
+    _vector, _head_rows, _run, _dense = h.vector, h.rows, h.run, h.dense
     return h
 
 
@@ -181,6 +181,16 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype, what: str):
 def _head_rows(t: torch.Tensor, dtype, what: str):
     """(address, token stride, head stride) of head rows [T, heads, D]; likewise."""
     return _hostcall().rows(t, dtype, what)
+
+
+def _run(t: torch.Tensor, dtype, what: str):
+    """(address, length) of a dense CUDA tensor of one axis; likewise."""
+    return _hostcall().run(t, dtype, what)
+
+
+def _dense(t: torch.Tensor):
+    """(address, number of elements) of a dense CUDA tensor; likewise."""
+    return _hostcall().dense(t)
 
 
 def _check(fn: str, status: int):
@@ -595,6 +605,7 @@ def attn_workspace(device="cuda") -> torch.Tensor:
 
 
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_i64 = torch.int64
 
 
 def _page_scales(t: Optional[torch.Tensor], pages: int, heads: int, what: str):
@@ -643,7 +654,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
         _vector(positions, T, _i32, "positions"), table, npos, rot, int(interleaved),
         _vector(q_weight, D, _bf16, "q_weight"),
         _vector(k_weight, D, _bf16, "k_weight"), eps, *_head_rows(q_out, _bf16, "q_out"),
-        *_head_rows(k_out, _bf16, "k_out"), _ptr(ws), ws.numel(), _stream(stream)))
+        *_head_rows(k_out, _bf16, "k_out"), *_dense(ws), _stream(stream)))
     return q_out, k_out
 
 
@@ -696,10 +707,10 @@ class AttnBatch:
         if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32:
             raise ValueError("page_table must be int32 [B, max_pages]")
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
-        self.batch, self.max_new = B, int(max_new)
-        self.struct = AttnBatchArgs(B, self.max_new, 0, page_table.shape[1],
-                                    _vector(q_start, B + 1, _i32, "q_start"),
-                                    _vector(kv_len, B, _i32, "kv_len"), _ptr(page_table))
+        self.batch, self.max_new, self.max_pages = B, int(max_new), page_table.shape[1]
+        self.addresses = (_vector(q_start, B + 1, _i32, "q_start"),
+                          _vector(kv_len, B, _i32, "kv_len"), _ptr(page_table))
+        self.struct = AttnBatchArgs(B, self.max_new, 0, self.max_pages, *self.addresses)
         self._arguments = self.struct
 
     def arguments(self, tokens: int) -> AttnBatchArgs:
@@ -748,7 +759,7 @@ def kv_append(cache: PagedKVCache, batch: AttnBatch, k: torch.Tensor, v: torch.T
         cache.struct, batch.arguments(T), *_head_rows(k, _bf16, "k"), *_head_rows(v, _bf16, "v"),
         *q_args, hq, *out_args, table, npos, rot, int(interleaved),
         _vector(q_weight, D, _bf16, "q_weight"), _vector(k_weight, D, _bf16, "k_weight"), eps,
-        _ptr(ws), ws.numel(), _stream(stream)))
+        *_dense(ws), _stream(stream)))
     return q_out
 
 
@@ -786,7 +797,7 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, batch: AttnBatch,
     _check("attn_paged_forward", _calls().attn_paged_forward(
         *_head_rows(q, _bf16, "q"), hq, cache.struct, batch.arguments(T),
         D ** -0.5 if scale is None else scale, window, *_head_rows(out, _bf16, "out"), _ptr(lse),
-        _ptr(ws), ws.numel(), _stream(stream)))
+        *_dense(ws), _stream(stream)))
     return out
 
 
@@ -822,23 +833,21 @@ def plan_pages(pool: PagePool, batch: AttnBatch, page_size: int, new_tokens: tor
     and slots int64 [rows], if given: cache position and page * page_size + offset of
     every new row.  Returns batch."""
     B = batch.batch
-    rows = 2 ** 31 - 1
-    for t in (positions, slots):
-        if t is not None:
-            rows = min(rows, t.shape[0])
+    rows, at_positions, at_slots = 2 ** 31 - 1, None, None
+    if positions is not None:
+        at_positions, rows = _run(positions, _i32, "positions")
+    if slots is not None:
+        at_slots, n = _run(slots, _i64, "slots")
+        rows = min(rows, n)
     ws = _workspace(256, batch.kv_len.device, stream) if ws is None else ws
-    s = batch.struct
+    q_start, kv_len, table = batch.addresses
     _check("attn_plan_pages", _calls().attn_plan_pages(
         pool._ring, pool.size, pool._state,
         pool._state if state_out is None else _vector(state_out, 2, _i32, "state_out"), B,
-        page_size, s.max_pages,
-        s.kv_len if kv_before is None else _vector(kv_before, B, _i32, "kv_before"),
-        _vector(cached, B, _i32, "cached"),
-        _vector(new_tokens, B, _i32, "new_tokens"), s.kv_len, s.q_start, s.page_table,
-        None if positions is None else _vector(positions, positions.shape[0], _i32,
-                                               "positions"),
-        None if slots is None else _vector(slots, slots.shape[0], torch.int64, "slots"), rows,
-        _ptr(ws), ws.numel(), _stream(stream)))
+        page_size, batch.max_pages,
+        kv_len if kv_before is None else _vector(kv_before, B, _i32, "kv_before"),
+        _vector(cached, B, _i32, "cached"), _vector(new_tokens, B, _i32, "new_tokens"), kv_len,
+        q_start, table, at_positions, at_slots, rows, *_dense(ws), _stream(stream)))
     return batch
 
 
@@ -879,15 +888,13 @@ def draft_verify(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: to
     if next_token is None:
         next_token = _empty(B, torch.int32, dev, stream)
     ws = _workspace(256, dev, stream) if ws is None else ws
-    s = batch.struct
+    q_start, kv_len, _ = batch.addresses
     _check("draft_verify", _calls().draft_verify(
         *_distributions(target, "target"), *d_args, code, T, vocab,
-        _vector(tokens, T, _i32, "tokens"), B, s.q_start, s.kv_len,
-        _vector(accept_u, T, _f32, "accept_u"),
-        _vector(sample_u, B, _f32, "sample_u"),
-        _vector(accepted, B, _i32, "accepted"),
-        _vector(next_token, B, _i32, "next_token"),
-        _vector(cached, B, _i32, "cached"), _ptr(ws), ws.numel(), _stream(stream)))
+        _vector(tokens, T, _i32, "tokens"), B, q_start, kv_len,
+        _vector(accept_u, T, _f32, "accept_u"), _vector(sample_u, B, _f32, "sample_u"),
+        _vector(accepted, B, _i32, "accepted"), _vector(next_token, B, _i32, "next_token"),
+        _vector(cached, B, _i32, "cached"), *_dense(ws), _stream(stream)))
     return accepted, next_token
 
 

@@ -10,7 +10,7 @@
 #include "nvfp4moe.h"
 
 /* ---- checks ---- */
-static PyObject *s_dtype, *s_shape, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_stride;
+static PyObject *s_dtype, *s_shape, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_stride, *s_numel;
 
 static int is_true(PyObject* t, PyObject* name, int call) {
   PyObject* v = call ? PyObject_CallMethodNoArgs(t, name) : PyObject_GetAttr(t, name);
@@ -27,6 +27,27 @@ static int has_dtype(PyObject* t, PyObject* dtype) {
   return d == dtype;
 }
 
+/* Whether t is a CUDA tensor, its memory dense (of fewer than two elements: or not). */
+static int is_dense(PyObject* t, long long n) {
+  const int ok = is_true(t, s_is_cuda, 0);
+  return ok > 0 && n > 1 ? is_true(t, s_is_contiguous, 1) : ok;
+}
+
+/* Length of the vector t of this type, -1 if it is none, -2 with an exception. */
+static long long length_of(PyObject* t, PyObject* dtype) {
+  const int ok = has_dtype(t, dtype);
+  if (ok <= 0) return ok < 0 ? -2 : -1;
+  PyObject* shape = PyObject_GetAttr(t, s_shape);
+  if (shape == NULL) return -2;
+  long long n = -1;
+  if (PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 1) {
+    n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+    if (n == -1 && PyErr_Occurred()) n = -2;
+  }
+  Py_DECREF(shape);
+  return n;
+}
+
 /* vector(t, n, dtype, what): address of the dense CUDA tensor [n], None for None. */
 static PyObject* vector(PyObject* self, PyObject* const* args, Py_ssize_t count) {
   (void)self;
@@ -35,28 +56,50 @@ static PyObject* vector(PyObject* self, PyObject* const* args, Py_ssize_t count)
   if (t == Py_None) Py_RETURN_NONE;
   const long long n = PyLong_AsLongLong(args[1]);
   if (n == -1 && PyErr_Occurred()) return NULL;
-  int ok = has_dtype(t, args[2]);
-  if (ok < 0) return NULL;
-  if (ok) {
-    PyObject* shape = PyObject_GetAttr(t, s_shape);
-    if (shape == NULL) return NULL;
-    ok = 0;
-    if (PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 1) {
-      const long long have = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
-      if (have == -1 && PyErr_Occurred()) {
-        Py_DECREF(shape);
-        return NULL;
-      }
-      ok = have == n;
-    }
-    Py_DECREF(shape);
-  }
-  if (!ok) return PyErr_Format(PyExc_ValueError, "%U must be %S [%lld]", args[3], args[2], n);
-  ok = is_true(t, s_is_cuda, 0);
-  if (ok > 0 && n > 1) ok = is_true(t, s_is_contiguous, 1);
+  const long long have = length_of(t, args[2]);
+  if (have == -2) return NULL;
+  if (have != n || n < 0)
+    return PyErr_Format(PyExc_ValueError, "%U must be %S [%lld]", args[3], args[2], n);
+  const int ok = is_dense(t, n);
   if (ok < 0) return NULL;
   if (!ok) return PyErr_Format(PyExc_ValueError, "%U must be a dense CUDA tensor", args[3]);
   return PyObject_CallMethodNoArgs(t, s_data_ptr);
+}
+
+/* run(t, dtype, what): (address, length) of a dense CUDA tensor of one axis. */
+static PyObject* run(PyObject* self, PyObject* const* args, Py_ssize_t count) {
+  (void)self;
+  if (count != 3) return PyErr_Format(PyExc_TypeError, "run takes 3 arguments");
+  PyObject* t = args[0];
+  const long long n = length_of(t, args[1]);
+  if (n == -2) return NULL;
+  if (n < 0) return PyErr_Format(PyExc_ValueError, "%U must be %S of one axis", args[2], args[1]);
+  const int ok = is_dense(t, n);
+  if (ok < 0) return NULL;
+  if (!ok) return PyErr_Format(PyExc_ValueError, "%U must be a dense CUDA tensor", args[2]);
+  PyObject* p = PyObject_CallMethodNoArgs(t, s_data_ptr);
+  PyObject* out = p != NULL ? Py_BuildValue("(NL)", p, n) : NULL;
+  return out;
+}
+
+/* dense(t): (address, number of elements) of a dense CUDA tensor. */
+static PyObject* dense(PyObject* self, PyObject* t) {
+  (void)self;
+  int ok = is_true(t, s_is_cuda, 0);
+  if (ok == 0) PyErr_SetString(PyExc_ValueError, "expected a CUDA tensor");
+  if (ok <= 0) return NULL;
+  ok = is_true(t, s_is_contiguous, 1);
+  if (ok == 0)
+    PyErr_SetString(PyExc_ValueError,
+                    "expected a contiguous tensor (the library reads dense row-major memory)");
+  if (ok <= 0) return NULL;
+  PyObject* n = PyObject_CallMethodNoArgs(t, s_numel);
+  PyObject* p = n != NULL ? PyObject_CallMethodNoArgs(t, s_data_ptr) : NULL;
+  if (p == NULL) {
+    Py_XDECREF(n);
+    return NULL;
+  }
+  return Py_BuildValue("(NN)", p, n);
 }
 
 /* rows(t, dtype, what): (address, token stride, head stride) of head rows [T, heads, D]. */
@@ -229,7 +272,11 @@ static PyObject* bind(PyObject* self, PyObject* const* args, Py_ssize_t count) {
 }
 
 #define METHOD(name, fn) {name, (PyCFunction)(void (*)(void))fn, METH_FASTCALL, NULL}
-static PyMethodDef methods[] = {METHOD("vector", vector), METHOD("rows", rows), METHOD("bind", bind),
+static PyMethodDef methods[] = {METHOD("vector", vector),
+                                METHOD("run", run),
+                                {"dense", dense, METH_O, NULL},
+                                METHOD("rows", rows),
+                                METHOD("bind", bind),
                                 METHOD("attn_qk_norm_rope", call_qk_norm_rope),
                                 METHOD("attn_kv_append", call_kv_append),
                                 METHOD("attn_paged_forward", call_paged_forward),
@@ -245,6 +292,8 @@ PyMODINIT_FUNC PyInit__hostcall(void) {
   s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_stride = PyUnicode_InternFromString("stride");
-  if (!s_dtype || !s_shape || !s_is_cuda || !s_is_contiguous || !s_data_ptr || !s_stride) return NULL;
+  s_numel = PyUnicode_InternFromString("numel");
+  if (!s_dtype || !s_shape || !s_is_cuda || !s_is_contiguous || !s_data_ptr || !s_stride || !s_numel)
+    return NULL;
   return PyModule_Create(&module);
 }

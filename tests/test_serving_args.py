@@ -19,6 +19,14 @@ def test_page_scales_are_not_optional(nb):
         assert call(nb, _cache(nb, **{**paged, "token_stride": 136}), _batch(nb)) == MISALIGNED
 
 
+class Workspace(Device):
+    def __init__(self):
+        super().__init__(256, dtype=torch.uint8)
+
+    def numel(self):
+        return 256
+
+
 class Cache(Device):
     """A dense cache side, as the handle reads it."""
 
@@ -71,7 +79,7 @@ def test_plan_pages_refuses(nb, want, kw):
 def test_plan_pages_binding_refuses(nb):
     pool = nb.PagePool(Device(8), Device(2))
     batch = nb.AttnBatch(Device(3), Device(2), Device(2, 4), max_new=5)
-    ws = Device(256, dtype=torch.uint8)
+    ws = Workspace()
     for kw in (dict(new_tokens=Device(3)), dict(new_tokens=Device(2, dtype=torch.int64)),
                dict(cached=Device(1)), dict(kv_before=Device(3)), dict(state_out=Device(3)),
                dict(positions=Device(7, dtype=torch.int64)), dict(slots=Device(7))):
@@ -117,7 +125,7 @@ def test_draft_verify_binding_refuses(nb):
     batch = nb.AttnBatch(Device(3), Device(2), Device(2, 4), max_new=5)
     good = dict(target=Rows(6, 50), draft=Rows(6, 50), tokens=Device(6), accept_u=Device(6, dtype=f32),
                 sample_u=Device(2, dtype=f32), accepted=Device(2), next_token=Device(2),
-                ws=Device(256, dtype=torch.uint8))
+                ws=Workspace())
     for kw in (dict(target=Rows(6, 50, dtype=torch.float16)), dict(draft=Rows(6, 49)), dict(draft=Rows(5, 50)),
                dict(draft=Rows(6, 50, dtype=torch.bfloat16)), dict(target=Rows(6, 50, strides=(1, 6))),
                dict(tokens=Device(5)), dict(tokens=Device(6, dtype=torch.int64)), dict(accept_u=Device(6)),
@@ -165,6 +173,17 @@ def test_the_extension_checks_vectors(nb):
         vector(loose, 3, torch.int32, "x")
     with pytest.raises(TypeError):
         vector(Device(3), 3)
+
+
+def test_the_extension_takes_any_dense_tensor_as_memory(nb):
+    dense = nb._calls().dense
+    assert dense(Workspace()) == (1 << 20, 256)
+    host, loose = Workspace(), Workspace()
+    host.is_cuda, loose.is_contiguous = False, lambda: False
+    with pytest.raises(ValueError, match="expected a CUDA tensor"):
+        dense(host)
+    with pytest.raises(ValueError, match="expected a contiguous tensor"):
+        dense(loose)
 
 
 def test_the_extension_passes_arguments_as_they_are(nb):
