@@ -212,8 +212,10 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   const int r_begin = min(a.batch.batch, static_cast<int>(threadIdx.x) * per);
   const int r_end = min(a.batch.batch, r_begin + per);
   long long mine = 0;
+  Request rq;                                          // of this thread, where it has one
   for (int r = r_begin; r < r_end; ++r) {
-    const Span s = tiles_of(load_request(a.batch, a.cache.page_shift, r, a.status), a.window);
+    rq = load_request(a.batch, a.cache.page_shift, r, a.status);
+    const Span s = tiles_of(rq, a.window);
     mine += static_cast<long long>(s.t1 - s.t0) * (a.cache.heads / step);
   }
   long long upto = mine;
@@ -261,9 +263,8 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   long long first = before + upto - mine;
   if (lo >= first && lo < first + mine) {
     int r = r_begin;
-    Request rq;
     while (true) {
-      rq = load_request(a.batch, a.cache.page_shift, r, a.status);
+      if (per > 1) rq = load_request(a.batch, a.cache.page_shift, r, a.status);
       const Span s = tiles_of(rq, a.window);
       const long long c = static_cast<long long>(s.t1 - s.t0) * (a.cache.heads / step);
       if (lo < first + c || r + 1 >= r_end) break;
