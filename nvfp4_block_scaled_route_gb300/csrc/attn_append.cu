@@ -25,27 +25,41 @@ namespace {
 // and drafted tokens), a unit is a token, and the first one in a page takes the page.
 struct PageUnits {
   uint32_t blocks;
+  uint64_t share;                                       // blocks / all, in 2^-32, rounded up
 };
 
-// A thread holds R tokens' eight bf16 as they came, and turns them twice, for the largest
-// and for the store: 64 registers a thread, as the queries' rows take (which are most of
-// the bytes, in the same launch).
+// A thread takes R tokens' eight elements: values stay in registers as they came, turned
+// keys go to shared memory as fp32 until the scale is known.  (64 registers a thread, as
+// the queries' rows take, which are most of the bytes in the same launch.  Keys turned a
+// second time instead: 165 us where this takes 152, three prompts of 8192 tokens at most,
+// 64 + 8 + 8 heads of 128.)
 constexpr int kR = 4;
+constexpr int kHeldBytes = kR * 8 * 4;                  // a thread
 
 template <int D, int THREADS, int HEADS, bool TOKENS, bool PAIRS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 page_append_kernel(const RopeArgs a, const PageUnits units) {
   constexpr int R = kR, kLanes = D / 8, kGroups = THREADS / kLanes, kRound = kGroups * R;
   __shared__ float warp_max[THREADS / 32];
+  extern __shared__ float4 smem[];
   pdl_wait();                                           // for what came before
-  if (blockIdx.x >= units.blocks) {
-    transform_heads<D, HEADS, true, PAIRS, false>(
-        a, (blockIdx.x - units.blocks) * kGroups + threadIdx.x / kLanes);
+  // Single tokens: appending blocks first.  Else they are spread evenly over the others,
+  // which wait for bytes where these compute (152 -> 148 us; the division that single
+  // tokens do without is 0.3-0.9 us of a launch of 4.8).
+  uint32_t mine = blockIdx.x, others = blockIdx.x - units.blocks;
+  bool append = mine < units.blocks;
+  if (!TOKENS) {
+    mine = static_cast<uint32_t>(blockIdx.x * units.share >> 32);
+    append = static_cast<uint32_t>((blockIdx.x + uint64_t{1}) * units.share >> 32) != mine;
+    others = blockIdx.x - mine;
+  }
+  if (!append) {
+    transform_heads<D, HEADS, true, PAIRS, false>(a, others * kGroups + threadIdx.x / kLanes);
     return;
   }
-  const bool value = blockIdx.x & 1;
-  const uint32_t unit = (blockIdx.x >> 1) / static_cast<uint32_t>(a.cache.heads);
-  const int head = static_cast<int>((blockIdx.x >> 1) - unit * a.cache.heads);
+  const bool value = mine & 1;
+  const uint32_t unit = (mine >> 1) / static_cast<uint32_t>(a.cache.heads);
+  const int head = static_cast<int>((mine >> 1) - unit * a.cache.heads);
   const HeadRows& src = value ? a.v : a.k;
   const int ps = a.cache.page_shift;
 
@@ -115,29 +129,49 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
   const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(src.data) +
                             (p0 - to_pos) * src.token_stride + head * src.head_stride;
 
-  // Up to kRound tokens stay in registers from the search for the largest to the store;
-  // more (pages of D * page_size > 512 * 8 * R) are read twice.
+  // Up to kRound tokens are read once; more (pages of D * page_size > 512 * 8 * R) twice.
   const int rounds = (count + kRound - 1) / kRound;
-  const int steps = 2 * rounds;
+  const int steps = rounds == 1 ? 1 : 2 * rounds;
   float most = 0.0f, by = 1.0f, inv = 1.0f;
   bool exact = true;
   uint2 raw[R][2];
+  float4* held = smem + threadIdx.x;                    // [R][2][THREADS]
+  uint64_t w[2][2];
+  HeadTurn<D, PAIRS>::weights(value ? nullptr : a.tr.k_weight, i0, i1, w);
+  const int64_t step_in = kGroups * src.token_stride, step_out = kGroups * a.cache.token_stride;
+  // eight values in the page's scale, to their place
+  const auto put = [&](uint8_t* p, const uint64_t (&x)[2][2]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float z[4];
+      f32x2_split(x[s][0], z[0], z[1]);
+      f32x2_split(x[s][1], z[2], z[3]);
+      if (exact) {
+        const uint64_t by2 = f32x2(inv, inv);
+        f32x2_split(mul_f32x2(x[s][0], by2), z[0], z[1]);
+        f32x2_split(mul_f32x2(x[s][1], by2), z[2], z[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] /= by;
+      }
+      *reinterpret_cast<uint32_t*>(p + (s == 0 ? i0 : i1)) =
+          pack_e4m3x2(z[0], z[1]) | (pack_e4m3x2(z[2], z[3]) << 16);
+    }
+  };
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
     const int base = (step < rounds ? step : step - rounds) * kRound + group;
-    if (step == 0 || rounds > 1) {
+    const __nv_bfloat16* p = in + base * src.token_stride;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int j = base + i * kGroups;
-        if (j < count) {
-          const __nv_bfloat16* p = in + j * src.token_stride;
-          raw[i][0] = *reinterpret_cast<const uint2*>(p + i0);
-          raw[i][1] = *reinterpret_cast<const uint2*>(p + i1);
-        }
+    for (int i = 0; i < R; ++i, p += step_in) {
+      if (base + i * kGroups < count) {
+        raw[i][0] = *reinterpret_cast<const uint2*>(p + i0);
+        raw[i][1] = *reinterpret_cast<const uint2*>(p + i1);
       }
     }
+    uint8_t* to = out + (old + base) * a.cache.token_stride;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < R; ++i, to += step_out) {
       const int j = base + i * kGroups;
       if (j >= count) break;
       uint64_t x[2][2];
@@ -145,37 +179,24 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
       bf16x4_to_f32x2(raw[i][1], x[1]);
       if (!value) {
         HeadTurn<D, PAIRS> turn;
-        turn.load(a.tr, a.tr.k_weight, false, sub, i0, i1, p0 + j);
+        turn.load(a.tr, w, a.tr.k_weight != nullptr, false, sub, p0 + j);
         turn.apply(x, a.tr.eps, mask);
+        if (rounds == 1) {
+          held[(2 * i) * THREADS] = reinterpret_cast<const float4&>(x[0]);
+          held[(2 * i + 1) * THREADS] = reinterpret_cast<const float4&>(x[1]);
+        }
       }
       if (step < rounds) {
-        // (infinities saturate and NaN stays NaN: neither counts for the scale)
+        // Infinities saturate and NaN stays NaN: neither counts for the scale.  (x * 0 + x
+        // is x or, of those, NaN, which the maximum leaves out.)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float u, v;
-          f32x2_split(x[k >> 1][k & 1], u, v);
-          u = fabsf(u);
-          v = fabsf(v);
-          most = fmaxf(most, u < INFINITY ? u : 0.0f);
-          most = fmaxf(most, v < INFINITY ? v : 0.0f);
+          f32x2_split(fma_f32x2(x[k >> 1][k & 1], 0, x[k >> 1][k & 1]), u, v);
+          most = fmaxf(most, fmaxf(fabsf(u), fabsf(v)));
         }
       } else {
-        uint8_t* p = out + (old + j) * a.cache.token_stride;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          float z[4];
-          f32x2_split(x[s][0], z[0], z[1]);
-          f32x2_split(x[s][1], z[2], z[3]);
-          if (exact) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[k] *= inv;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[k] /= by;
-          }
-          *reinterpret_cast<uint32_t*>(p + (s == 0 ? i0 : i1)) =
-              pack_e4m3x2(z[0], z[1]) | (pack_e4m3x2(z[2], z[3]) << 16);
-        }
+        put(to, x);
       }
     }
     if (step == rounds - 1) {
@@ -220,41 +241,66 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
       exact = (__float_as_uint(by) & 0x7FFFFFu) == 0;
       inv = 1.0f / by;
     }
+    if (rounds == 1) {
+      uint8_t* to = out + (old + base) * a.cache.token_stride;
+#pragma unroll
+      for (int i = 0; i < R; ++i, to += step_out) {
+        if (base + i * kGroups >= count) break;
+        uint64_t x[2][2];
+        if (value) {
+          bf16x4_to_f32x2(raw[i][0], x[0]);
+          bf16x4_to_f32x2(raw[i][1], x[1]);
+        } else {
+          reinterpret_cast<float4&>(x[0]) = held[(2 * i) * THREADS];
+          reinterpret_cast<float4&>(x[1]) = held[(2 * i + 1) * THREADS];
+        }
+        put(to, x);
+      }
+    }
   }
 }
 
+// units: pages, or tokens where there are fewer.
+template <int D, int THREADS, int HEADS, bool TOKENS, bool PAIRS>
+cudaError_t launch_with(RopeArgs a, int64_t units, cudaStream_t stream) {
+  const auto kernel = page_append_kernel<D, THREADS, HEADS, TOKENS, PAIRS>;
+  static PerDeviceOnce once;
+  const cudaError_t e = set_smem_attr_once(once, reinterpret_cast<const void*>(kernel),
+                                           kHeldBytes * THREADS);
+  if (e != cudaSuccess) return e;
+  // (tokens * (q heads + 2 key heads) < 2^31, and a page has 16 tokens at least)
+  const int64_t kv = units * a.cache.heads * 2;
+  a.q_chunks = static_cast<int>(ceil_div(a.q.heads, HEADS));
+  a.kv_chunks = 0;
+  a.chunks = a.q_chunks;
+  const int64_t blocks = kv + ceil_div(a.T * a.chunks, THREADS / (D / 8));
+  // (blocks < 2^32: the last block's number times this is below kv + 1)
+  const uint64_t share = ((static_cast<uint64_t>(kv) << 32) + blocks - 1) / blocks;
+  // its start overlaps the end of the kernel before
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = kHeldBytes * THREADS;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a,
+                            PageUnits{static_cast<uint32_t>(kv), share});
+}
+
 template <int D, bool PAIRS>
-cudaError_t launch_d(RopeArgs a, cudaStream_t stream) {
+cudaError_t launch_d(const RopeArgs& a, cudaStream_t stream) {
   const int64_t page = int64_t{1} << a.cache.page_shift;
   const int64_t by_page = a.T / page + 2 * int64_t{a.batch.batch};
-  const bool tokens = a.T <= by_page;
-  const auto go = [&](auto kernel, int threads, int q_heads) {
-    PageUnits units;
-    // (tokens * (q heads + 2 key heads) < 2^31, and a page has 16 tokens at least)
-    const int64_t kv = std::min(a.T, by_page) * a.cache.heads * 2;
-    units.blocks = static_cast<uint32_t>(kv);
-    a.q_chunks = static_cast<int>(ceil_div(a.q.heads, q_heads));
-    a.kv_chunks = 0;
-    a.chunks = a.q_chunks;
-    const int64_t blocks = kv + ceil_div(a.T * a.chunks, threads / (D / 8));
-    // its start overlaps the end of the kernel before
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, units);
-  };
-  // threads so that a page's new tokens stay in registers
-  if (tokens) return go(page_append_kernel<D, 128, 2, true, PAIRS>, 128, 2);
+  // threads so that a page's new tokens are held
+  if (a.T <= by_page) return launch_with<D, 128, 2, true, PAIRS>(a, a.T, stream);
   const int64_t elements = page * D;
-  if (elements <= 128 * 8 * kR) return go(page_append_kernel<D, 128, 8, false, PAIRS>, 128, 8);
-  if (elements <= 256 * 8 * kR) return go(page_append_kernel<D, 256, 8, false, PAIRS>, 256, 8);
-  return go(page_append_kernel<D, 512, 8, false, PAIRS>, 512, 8);
+  if (elements <= 128 * 8 * kR) return launch_with<D, 128, 8, false, PAIRS>(a, by_page, stream);
+  if (elements <= 256 * 8 * kR) return launch_with<D, 256, 8, false, PAIRS>(a, by_page, stream);
+  return launch_with<D, 512, 8, false, PAIRS>(a, by_page, stream);
 }
 
 }  // namespace

@@ -77,18 +77,28 @@ struct HeadTurn {
     i1 = !PAIRS && inside ? rotary_dim / 2 + sub * 4 : sub * 8 + 4;
   }
 
-  // plain: rows that stay as they are.
-  __device__ __forceinline__ void load(const HeadTransform& tr, const __nv_bfloat16* weight,
-                                       bool plain, int sub, int i0, int i1, int64_t pos) {
-    const int half = tr.rotary_dim / 2;
-    turned = !plain && sub * 8 < tr.rotary_dim;         // (rotary_dim is 0 without rope)
-    normed = weight != nullptr;
-    const uint64_t one = f32x2(1.0f, 1.0f);
-    uint64_t w[2][2] = {{one, one}, {one, one}};
-    if (!plain && weight != nullptr) {
+  // The weights of this lane's elements, ones without.
+  static __device__ __forceinline__ void weights(const __nv_bfloat16* weight, int i0, int i1,
+                                                 uint64_t (&w)[2][2]) {
+    w[0][0] = w[0][1] = w[1][0] = w[1][1] = f32x2(1.0f, 1.0f);
+    if (weight != nullptr) {
       bf16x4_to_f32x2(*reinterpret_cast<const uint2*>(weight + i0), w[0]);
       bf16x4_to_f32x2(*reinterpret_cast<const uint2*>(weight + i1), w[1]);
     }
+  }
+
+  // plain: rows that stay as they are.
+  __device__ __forceinline__ void load(const HeadTransform& tr, const __nv_bfloat16* weight,
+                                       bool plain, int sub, int i0, int i1, int64_t pos) {
+    uint64_t w[2][2];
+    weights(plain ? nullptr : weight, i0, i1, w);
+    load(tr, w, weight != nullptr, plain, sub, pos);
+  }
+  __device__ __forceinline__ void load(const HeadTransform& tr, const uint64_t (&w)[2][2],
+                                       bool with_norm, bool plain, int sub, int64_t pos) {
+    const int half = tr.rotary_dim / 2;
+    turned = !plain && sub * 8 < tr.rotary_dim;         // (rotary_dim is 0 without rope)
+    normed = with_norm;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
