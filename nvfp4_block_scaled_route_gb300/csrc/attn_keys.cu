@@ -29,8 +29,8 @@
 // two segments the queries' way in and the rows' way out take some 3000, so an SM runs
 // two CTAs, with half of the shared memory each (one: 138 us where two take 126; one with
 // two tiles in the work at a time: 142).  64 tokens on up to 16384 keys, 56 query and 8
-// key heads, pages of 16: 126 us, 5.4 TB/s (121 with heads first: whole pages of a head
-// side by side); attention_rows_kernel, which turns the values to 16 bits, took 200.
+// key heads, pages of 16: 123 us, 5.5 TB/s (122 with heads first, 119 with pages of 128 then);
+// attention_rows_kernel, which turns the values to 16 bits, took 200.
 //
 // The work is the flat list of 128-key tiles of all (request, key head) segments in equal
 // shares, as in attention_rows_kernel; attn_combine_kernel joins what is cut.

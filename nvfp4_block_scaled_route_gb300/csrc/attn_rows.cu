@@ -37,6 +37,9 @@
 // Values arrive as pairs of neighbouring dimensions (ldmatrix
 // moves 16-bit units), so one accumulator tile holds the even dimensions and
 // one the odd.
+//
+// PAGED: scales of pages, for 64-wide heads (attn_keys.cu has the 128-wide ones).  They
+// come with the key tiles by cp.async; a score takes its key's, a weight its value's.
 #include "attn.cuh"
 
 namespace nvmoe {
