@@ -19,14 +19,22 @@
 // row.  Sums are pairs of fp32 numbers, value and rest: p - q is exact that way, and a
 // sum is off by some 2^-45 of itself.  (fp64, of which an SM has two adds a cycle, took
 // 39 us for 64 requests of 129280 tokens even where it only joined lanes and warps.)
+//
+// Those 64 requests take 17 us, of which 6 are what two requests of few tokens take (the
+// launch, the loads before the row is known, the joins): loads are asked for one by one as
+// their predecessors are used (four at a time, then all four used: 21.5), and the row's
+// ragged ends are apart from the loop, whose code is fetched anew by each launch.
 #include "attn.cuh"
 #include "serve.cuh"
 
 namespace nvmoe {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxCtas = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8, kCtasPerSm = 4;
+// Vectors of a row on their way to a thread.  (2 / 3 / 4: 64 requests of 129280 tokens with
+// two CTAs each 29.2 / 25.5 / 23.3 us, with eight 17 all three.)
+constexpr int kAhead = 4;
 
 // Within [0, 1]; NaN is 0.
 __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
@@ -89,19 +97,19 @@ struct Row {
     return static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   }
 
-  // The elements of vector v of x as they are, zeros outside the row.
-  __device__ __forceinline__ uint4 load(const T* x, int v, bool whole) const {
-    const int e0 = v * kVec - shift;
-    if (whole && e0 >= 0 && e0 + kVec <= vocab) return *reinterpret_cast<const uint4*>(x + e0);
+  // The elements of vector v, all within the row, of p or of a q that lies otherwise.
+  __device__ __forceinline__ uint4 load(const T* x, int v) const {
+    return *reinterpret_cast<const uint4*>(x + v * kVec - shift);
+  }
+  __device__ __forceinline__ uint4 load_apart(const T* x, int v) const {
+    x += v * kVec - shift;
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
-      const int e = e0 + k;
-      if (e < 0 || e >= vocab) continue;
       if constexpr (sizeof(T) == 4)
-        w[k] = __float_as_uint(x[e]);
+        w[k] = __float_as_uint(x[k]);
       else
-        w[k / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[e])) << (k % 2 * 16);
+        w[k / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[k])) << (k % 2 * 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -134,25 +142,27 @@ struct Row {
     return {d, (a - d) - b};
   }
 
-  // A lane's sum over the vectors v0, v0 + step, .. below v1.
-  template <bool DIFFERENCE>
+  // A lane's sum over the whole vectors v0, v0 + step, .. below v1.  The next kAhead are on
+  // their way at any time.
+  template <bool DIFFERENCE, bool TOGETHER, int kAhead>
   __device__ __forceinline__ Sum sum_of(int v0, int v1, int step) const {
-    constexpr int kUnroll = 4;
+    const int drops = !DIFFERENCE && without >= 0 ? (without + shift) / kVec : -1;
     Sums s[2];
-    for (int v = v0; v < v1; v += kUnroll * step) {
-      uint4 pv[kUnroll], qv[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        pv[u] = qv[u] = make_uint4(0, 0, 0, 0);
-        if (v + u * step < v1) {
-          pv[u] = load(p, v + u * step, true);
-          if (!DIFFERENCE && without >= 0 && v + u * step == (without + shift) / kVec)
-            pv[u] = drop(pv[u], (without + shift) % kVec);
-          if (DIFFERENCE) qv[u] = load(q, v + u * step, together);
-        }
+    uint4 pv[kAhead], qv[kAhead];
+    const auto fetch = [&](int u, int v) {
+      pv[u] = qv[u] = make_uint4(0, 0, 0, 0);
+      if (v < v1) {
+        pv[u] = load(p, v);
+        if (DIFFERENCE) qv[u] = TOGETHER ? load(q, v) : load_apart(q, v);
       }
+    };
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+    for (int u = 0; u < kAhead; ++u) fetch(u, v0 + u * step);
+#pragma unroll 1
+    for (int v = v0; v < v1; v += kAhead * step) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (!DIFFERENCE && v + u * step == drops) pv[u] = drop(pv[u], (without + shift) % kVec);
 #pragma unroll
         for (int k = 0; k < kVec / 2; ++k) {
           float a0, a1;
@@ -172,11 +182,29 @@ struct Row {
             s[k & 1].add(a);
           }
         }
+        fetch(u, v + (u + kAhead) * step);
+      }
     }
     return s[0].value() + s[1].value();
   }
+  // The same over all vectors; the row's first and last, if not whole, element by element.
   __device__ __forceinline__ Sum sum(int v0, int v1, int step) const {
-    return q != nullptr ? sum_of<true>(v0, v1, step) : sum_of<false>(v0, v1, step);
+    const int whole = (vocab + shift) / kVec;           // vectors up to the last whole one's end
+    Sum edge = {0.0f, 0.0f};
+    const auto elements = [&](int e0, int e1) {
+#pragma unroll 1
+      for (int e = e0; e < e1; ++e) edge = edge + weight(e);
+    };
+    if (whole < v1 && whole >= v0 && (whole - v0) % step == 0)
+      elements(max(0, whole * kVec - shift), vocab);
+    v1 = min(v1, whole);
+    if (v0 == 0 && shift > 0 && v1 > 0) {
+      elements(0, kVec - shift);
+      v0 = step;
+    }
+    return edge + (q == nullptr ? sum_of<false, true, kAhead>(v0, v1, step)
+                                : together ? sum_of<true, true, kAhead>(v0, v1, step)
+                                           : sum_of<true, false, 1>(v0, v1, step));
   }
 };
 
@@ -202,7 +230,7 @@ __device__ __forceinline__ int pick(const Sum& upto, const Sum& own, const Sum& 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(const VerifyArgs a) {
   __shared__ Sum run_sum[2][kMaxCtas * kWarps];          // of all CTAs' warps
   __shared__ Sum warp_sum[kWarps];
   __shared__ int stands;
@@ -358,15 +386,20 @@ __global__ void __launch_bounds__(kThreads, 2) draft_verify_kernel(const VerifyA
 
 template <typename T>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
-  // A CTA for every 4096 tokens, up to 8; fewer where the requests fill the SMs (two CTAs
-  // each) without.
+  // A CTA for every 4096 tokens, up to 8, for every 8192 where there are more of them than
+  // SMs, and as many as are resident at once.  (Clusters of more than two CTAs leave places
+  // free in each group of SMs: 76 requests of 129280 tokens take 19.2 us with 7 CTAs each and
+  // 23.2 with 8, which are as many as there are places; 64 requests 18.2 with 4, 16.9 with 8;
+  // 64 of 32003 tokens 8.8 and 9.8.)
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  const int64_t places = int64_t{kCtasPerSm} * sms;
   int ctas = 1;
-  while (ctas < kMaxCtas && a.vocab > int64_t{ctas} * 4096 && int64_t{a.batch} * ctas * 2 <= 2 * sms)
-    ctas *= 2;
+  while (ctas < kMaxCtas && a.vocab > int64_t{ctas} * (int64_t{a.batch} * ctas <= sms ? 4096 : 8192) &&
+         int64_t{a.batch} * (ctas + 1) <= (ctas < 2 ? places : places * 15 / 16))
+    ++ctas;
   // its start overlaps the end of the kernel before
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

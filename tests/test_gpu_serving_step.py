@@ -233,6 +233,14 @@ def test_verify(nb, counts, vocab, pad, dtype, given):
         run_verify(nb, p, q if given else None, *rest, pad=pad)
 
 
+@pytest.mark.parametrize("requests", [19, 40, 72, 90, 110, 140, 180, 290, 350])
+def test_verify_shares_of_any_number_of_blocks(nb, requests):
+    """Blocks of a request: 1 to 8, by how many requests fit the GPU at once."""
+    g = torch.Generator().manual_seed(requests)
+    p, q, *rest = drafted(g, [2] * requests, 59999, off=0.8)
+    run_verify(nb, p, q, *rest)
+
+
 def test_verify_rows_that_differ_in_alignment(nb):
     g = torch.Generator().manual_seed(3)
     p, q, tokens, q_start, u, v = drafted(g, [3, 2, 4], 5001)
