@@ -23,40 +23,45 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
   const auto at = [&](int i) {
     return (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0)) * a.piece_rows + row;
   };
-  // batches of independent loads: what bounds this kernel is their latency
-  constexpr int kBatch = 8;
-  float top = -INFINITY;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    float m[kBatch];
+  // What bounds this kernel is the latency of its loads: a lane of the row's takes the
+  // maximum and sum of a piece, and kBatch pieces' rows are on their way meanwhile.
+  constexpr int kLanes = D / 4, kBatch = 8;
+  const int sub = threadIdx.x & (kLanes - 1);
+  const uint32_t lanes = (kLanes == 32 ? 0xFFFFFFFFu : (1u << (kLanes & 31)) - 1u)
+                         << (threadIdx.x & 31 & ~(kLanes - 1));
+  const auto load_ml = [&](int i) {
+    return i < n ? a.piece_ml[at(i)] : make_float2(-INFINITY, 0.0f);
+  };
+  const auto load_o = [&](int i) {
+    return i < n ? *reinterpret_cast<const float4*>(a.piece_o + at(i) * D + d)
+                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  float2 ml = load_ml(sub);
+  float4 x[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      m[i] = i0 + i < n ? a.piece_ml[at(i0 + i)].x : -INFINITY;
+  for (int i = 0; i < kBatch; ++i) x[i] = load_o(i);
+  float top = ml.x;
+  for (int i = sub + kLanes; i < n; i += kLanes) top = fmaxf(top, load_ml(i).x);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
-  }
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
   const float use = top == -INFINITY ? 0.0f : top;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float sum = 0.0f;
+  float sum = 0.0f, f = 0.0f;
   for (int i0 = 0; i0 < n; i0 += kBatch) {
-    float2 ml[kBatch];
-    float4 x[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.0f);
-      x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i0 + i < n) {
-        ml[i] = a.piece_ml[at(i0 + i)];
-        x[i] = *reinterpret_cast<const float4*>(a.piece_o + at(i0 + i) * D + d);
-      }
+    if (i0 % kLanes == 0) {
+      if (i0 > 0) ml = load_ml(i0 + sub);
+      f = exp2_approx(ml.x - use);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float f = exp2_approx(ml[i].x - use);
-      sum = fmaf(f, ml[i].y, sum);
-      o.x = fmaf(f, x[i].x, o.x);
-      o.y = fmaf(f, x[i].y, o.y);
-      o.z = fmaf(f, x[i].z, o.z);
-      o.w = fmaf(f, x[i].w, o.w);
+      const int from = (i0 + i) & (kLanes - 1);
+      const float fi = __shfl_sync(lanes, f, from, kLanes);
+      sum = fmaf(fi, __shfl_sync(lanes, ml.y, from, kLanes), sum);
+      o.x = fmaf(fi, x[i].x, o.x);
+      o.y = fmaf(fi, x[i].y, o.y);
+      o.z = fmaf(fi, x[i].z, o.z);
+      o.w = fmaf(fi, x[i].w, o.w);
+      x[i] = load_o(i0 + kBatch + i);
     }
   }
   const int group = static_cast<int>(a.group.d);
