@@ -74,7 +74,7 @@ struct Cfg {
   static_assert(kK + 3 <= kScaleSlots, "slots");
   // of a row, [segment parity]: its factor, its first and last key + 1
   static constexpr int kRowBytes = 2 * kRows * 12;
-  static constexpr int kJoinBytes = 2 * 4 * RG * 4;    // a word of each warp and row
+  static constexpr int kJoinBytes = 2 * 5 * RG * 4;    // words of rows: of each warp, of all
   static constexpr int kSmem = kWordsAt + 512 + kScaleBytes + kRowBytes + kJoinBytes;
   static_assert(kSmem <= 115712, "shared memory of two CTAs an SM");
   static constexpr uint32_t kIdescS = idesc_e4m3_f32(kKeys, kN1);
@@ -174,6 +174,31 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
+// RG values of each lane joined over the warp: the result of row lane / (32 / RG) in each.
+// (Lanes exchange halves of what they hold: RG + 4 - log2 RG exchanges, and as many fewer
+// instructions to fetch, where each value by itself takes 5 RG.)
+template <int RG, typename Op>
+__device__ __forceinline__ float join_rows(const float (&x)[RG], Op op) {
+  const int lane = threadIdx.x & 31;
+  float v[RG];
+#pragma unroll
+  for (int r = 0; r < RG; ++r) v[r] = x[r];
+#pragma unroll
+  for (int h = RG / 2, o = 16; o > 0; h /= 2, o /= 2) {
+    if (h > 0) {
+      const bool upper = (lane & o) != 0;
+#pragma unroll
+      for (int r = 0; r < h; ++r) {
+        const float keep = upper ? v[r + h] : v[r], send = upper ? v[r] : v[r + h];
+        v[r] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, o));
+      }
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+    }
+  }
+  return v[0];
+}
+
 // Two fp16 as E4M3 (satfinite, nearest even), the lower one in the low byte.
 __device__ __forceinline__ uint32_t pack_e4m3x2_f16x2(uint32_t x) {
   uint16_t r;
@@ -196,7 +221,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   float* row_factor = scales + kScaleSlots * 3 * kTileScales;           // [parity][kRows]
   int* row_lo = reinterpret_cast<int*>(row_factor + 2 * C::kRows);
   int* row_hi = row_lo + 2 * C::kRows;
-  float* join = reinterpret_cast<float*>(row_hi + 2 * C::kRows);        // [group][warp][RG]
+  float* join = reinterpret_cast<float*>(row_hi + 2 * C::kRows);        // [group][5][RG]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();                                          // for what came before
@@ -441,7 +466,9 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     // ---- softmax: group g has the rows g * RG .., a thread a key (and a dimension) ----
     const int g = warp >> 2, key = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float* my_join = join + g * 4 * RG;
+    float* my_join = join + g * 5 * RG;                // a word of each warp and row
+    float* inverse = my_join + 4 * RG;                 // of the rows' weight sums
+    constexpr int kRowLanes = 32 / RG;                 // that join_rows leaves a row
     bool begun = false;
     uint32_t n = 0;                                    // tiles so far
     int seg = 0;                                       // parity of the segment
@@ -569,13 +596,8 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         for (int r = 0; r < RG; ++r) over = over || y[r] > above[r];
         if (group_any(g, over)) {
           // ---- new references: the rows' maxima over the tile ----
-#pragma unroll
-          for (int r = 0; r < RG; ++r) {
-            float top = y[r];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            if (lane == 0) my_join[(warp & 3) * RG + r] = top;
-          }
+          const float warp_top = join_rows<RG>(y, [](float a, float b) { return fmaxf(a, b); });
+          if (lane % kRowLanes == 0) my_join[(warp & 3) * RG + lane / kRowLanes] = warp_top;
           group_sync(g);
           float f[RG];
 #pragma unroll
@@ -650,23 +672,33 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         tc_fence_before();
         mbar_arrive(&bars->p_ready[sb]);
       }
-      // ---- weight sums over the threads ----
+      // ---- weight sums over the threads, a thread's for its row ----
+      const int64_t po = (2 * static_cast<int64_t>(me) + slot) * a.piece_rows;
+      {
+        const float warp_sum = join_rows<RG>(l, [](float a, float b) { return a + b; });
+        if (lane % kRowLanes == 0) my_join[(warp & 3) * RG + lane / kRowLanes] = warp_sum;
+        group_sync(g);
+        const int row = g * RG + key;
+        if (key < RG && row < rows) {
+          const float sum = (my_join[key] + my_join[RG + key]) + (my_join[2 * RG + key] + my_join[3 * RG + key]);
+          float mr = -INFINITY;                        // no key seen, as where pieces are joined
 #pragma unroll
-      for (int r = 0; r < RG; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
-        if (lane == 0) my_join[(warp & 3) * RG + r] = l[r];
+          for (int r = 0; r < RG; ++r)
+            if (r == key && above[r] != -3.0e38f) mr = m[r];
+          inverse[key] = sum == 0.0f ? 0.0f : 1.0f / sum;
+          if (!whole) {
+            a.piece_ml[po + row] = make_float2(mr, sum);
+          } else if (a.lse != nullptr) {
+            const int tok = a.group(row);
+            a.lse[(wk.rq.first + tok) * a.q.heads + wk.h * group + row - tok * group] = lse_of(mr, sum);
+          }
+        }
+        group_sync(g);
       }
-      group_sync(g);
-#pragma unroll
-      for (int r = 0; r < RG; ++r)
-        l[r] = (my_join[r] + my_join[RG + r]) + (my_join[2 * RG + r] + my_join[3 * RG + r]);
-      group_sync(g);                                   // before the words are written again
       // ---- the next segment's queries, then this one's rows ----
       const Walk out_wk = wk;
       const int out_rows = rows;
       const bool to_out = whole;
-      const int64_t po = (2 * static_cast<int64_t>(me) + slot) * a.piece_rows;
       const uint32_t last = n - 1;
       more = left > 0 && wk.next(a, step);
       if (more) {
@@ -688,23 +720,24 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
       }
       tc_fence_before();
       float probe = 0.0f;                              // NaN if some sum is not finite
+      const int tok0 = a.group(g * RG);
+      int of_group = g * RG - tok0 * group;            // the row's query head, of the key head's
+      __nv_bfloat16* to_row = static_cast<__nv_bfloat16*>(a.out.data) +
+                              (out_wk.rq.first + tok0) * a.out.token_stride +
+                              (out_wk.h * group + of_group) * a.out.head_stride + key;
+      float* to_piece = a.piece_o + (po + g * RG) * kD + key;
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
-        if (above[r] == -3.0e38f) m[r] = -INFINITY;    // no key seen, as where pieces are joined
-        const int row = g * RG + r;
-        if (row >= out_rows) break;
+        if (g * RG + r >= out_rows) break;
         probe = fmaf(o[r], 0.0f, probe);
-        const int tok = a.group(row);
-        const int64_t tk = out_wk.rq.first + tok;
-        const int head = out_wk.h * group + row - tok * group;
-        if (to_out) {
-          static_cast<__nv_bfloat16*>(
-              a.out.data)[tk * a.out.token_stride + head * a.out.head_stride + key] =
-              __float2bfloat16_rn(l[r] == 0.0f ? 0.0f : o[r] * (1.0f / l[r]));
-          if (key == 0 && a.lse != nullptr) a.lse[tk * a.q.heads + head] = lse_of(m[r], l[r]);
-        } else {
-          a.piece_o[(po + row) * kD + key] = o[r];
-          if (key == 0) a.piece_ml[po + row] = make_float2(m[r], l[r]);
+        if (to_out)
+          *to_row = __float2bfloat16_rn(o[r] * inverse[r]);
+        else
+          to_piece[r * kD] = o[r];
+        to_row += a.out.head_stride;
+        if (++of_group == group) {
+          of_group = 0;
+          to_row += a.out.token_stride - group * a.out.head_stride;
         }
       }
       if (probe != 0.0f) bars->spoilt = 1;
