@@ -43,6 +43,7 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
   __shared__ float warp_max[THREADS / 32];
   extern __shared__ float4 smem[];
   pdl_wait();                                           // for what came before
+  pdl_trigger();
   // Single tokens: appending blocks first.  Else they are spread evenly over the others,
   // which wait for bytes where these compute (152 -> 148 us; the division that single
   // tokens do without is 0.3-0.9 us of a launch of 4.8).

@@ -13,6 +13,7 @@ namespace {
 template <int D>
 __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
   pdl_wait();
+  pdl_trigger();
   const AttnPiece p = a.pieces[blockIdx.x];
   const int item = blockIdx.y * 256 + threadIdx.x;
   const int row = item / (D / 4), d = (item % (D / 4)) * 4;

@@ -223,6 +223,26 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
   int* row_hi = row_lo + 2 * C::kRows;
   float* join = reinterpret_cast<float*>(row_hi + 2 * C::kRows);        // [group][5][RG]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == kThreads - 32) {                  // (a warp that has no request as a rule)
+    for (int i = 0; i < C::kK + C::kV; ++i) {
+      // (and the loader's lanes that bring scales)
+      mbar_init(&bars->full[i], i < C::kK ? 1 + 2 * kTileScales : 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    mbar_init(&bars->q_ready, kSoftmaxThreads);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 2);                  // (and the scales made ready)
+      mbar_init(&bars->s_free[i], kSoftmaxThreads);
+      mbar_init(&bars->p_ready[i], kSoftmaxThreads);
+      mbar_init(&bars->pv_done[i], 1);
+      mbar_init(&bars->done[i], 1);
+    }
+    bars->abort = 0;
+    bars->spoilt = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
   pdl_trigger();
   pdl_wait();                                          // for what came before
 
@@ -250,26 +270,6 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     if (lane >= o) upto += v;
   }
   if (lane == 31) scan[warp] = upto;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kK + C::kV; ++i) {
-      // (and the loader's lanes that bring scales)
-      mbar_init(&bars->full[i], i < C::kK ? 1 + 2 * kTileScales : 1);
-      mbar_init(&bars->empty[i], 1);
-    }
-    mbar_init(&bars->q_ready, kSoftmaxThreads);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 2);                  // (and the scales made ready)
-      mbar_init(&bars->s_free[i], kSoftmaxThreads);
-      mbar_init(&bars->p_ready[i], kSoftmaxThreads);
-      mbar_init(&bars->pv_done[i], 1);
-      mbar_init(&bars->done[i], 1);
-    }
-    bars->abort = 0;
-    bars->spoilt = 0;
-    fence_mbarrier_init();
-    prefetch_tensormap(&map_k);
-    prefetch_tensormap(&map_v);
-  }
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
@@ -315,9 +315,11 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
     wk.r = bars->r;
     wk.set(a, bars->rq);
     const int span = max(1, wk.sp.t1 - wk.sp.t0);
-    const int k = static_cast<int>(bars->tile / span);
+    const long long tile = bars->tile;
+    const int k = tile >> 32 == 0 ? static_cast<int>(static_cast<uint32_t>(tile) / static_cast<uint32_t>(span))
+                                  : static_cast<int>(tile / span);
     wk.h = k * step + side;
-    return wk.sp.t0 + static_cast<int>(bars->tile - static_cast<long long>(k) * span);
+    return wk.sp.t0 + static_cast<int>(tile - static_cast<long long>(k) * span);
   };
   int t = start();
   long long left = hi - lo;
