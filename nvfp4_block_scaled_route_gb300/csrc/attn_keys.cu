@@ -60,11 +60,12 @@ template <int RG>
 struct Cfg {
   static_assert(2 * RG <= kAttnFewRows, "rows");
   static constexpr int kRows = 2 * RG;
-  static constexpr int kN1 = (kRows + 15) / 16 * 16, kN2 = kLevels * kRows;
-  static_assert(kN2 % 16 == 0 && kN2 <= 256, "columns of a product");
+  // columns of the two products: a row's Qhi and, kRows on, its Qlo; a weight's levels
+  static constexpr int kN1 = 2 * kRows, kN2 = kLevels * kRows;
+  static_assert(kN1 % 16 == 0 && kN2 % 16 == 0 && kN2 <= 256, "columns of a product");
   static constexpr uint32_t kTmemO = 2 * kN1;          // S: columns 0 and kN1
   static_assert(kTmemO + kN2 <= kTmemColumns, "TMEM");
-  static constexpr int kQAt = 0, kQBytes = kN1 * kD;   // Qhi, Qlo
+  static constexpr int kQAt = 0, kQBytes = kRows * kD;  // Qhi, Qlo
   static constexpr int kPAt = 2 * kQBytes, kPBytes = kN2 * kKeys;
   static constexpr int kRingAt = kPAt + 2 * kPBytes;
   // buffers of keys and of values
@@ -420,11 +421,9 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
           tc_fence_after();
           if (lane == 0) {
 #pragma unroll
-            for (int ks = 0; ks < 2 * kD / 32; ++ks) {  // with Qhi, then with Qlo
-              const int part = ks / (kD / 32), at = ks % (kD / 32) * 32;
-              mma_f8(tmem + sb * C::kN1, desc + (at >> 4),
-                     row_desc + ((part * C::kQBytes + at) >> 4), C::kIdescS, ks != 0);
-            }
+            for (int ks = 0; ks < kD / 32; ++ks)
+              mma_f8(tmem + sb * C::kN1, desc + (ks * 32 >> 4), row_desc + (ks * 32 >> 4),
+                     C::kIdescS, ks != 0);
             tc_commit(&bars->s_full[sb]);
           }
           // while they run: the keys' scales, and the values' as logarithms and inverted
@@ -503,9 +502,9 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
       const float c = a.scale * 1.4426950408889634f * 0.0078125f;
       constexpr int kLanes = kD / 8, kStep = kSoftmaxThreads / kLanes;
       const int ch = threadIdx.x & (kLanes - 1);
-#pragma unroll
-      for (int i = 0; i < C::kN1 / kStep; ++i) {
-        const int row = threadIdx.x / kLanes + i * kStep;
+      static_assert(C::kRows <= kStep, "a row for each group of lanes");
+      const int row = threadIdx.x / kLanes;
+      if (row < C::kRows) {
         const int tok = a.group(row);
         uint4 u = make_uint4(0, 0, 0, 0);
         if (row < rows)
@@ -544,7 +543,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         uint8_t* to = smem + C::kQAt + tile_at(row, ch * 8);
         *reinterpret_cast<uint2*>(to) = make_uint2(hi8[0], hi8[1]);
         *reinterpret_cast<uint2*>(to + C::kQBytes) = make_uint2(lo8[0], lo8[1]);
-        if (ch == 0 && row < C::kRows) {
+        if (ch == 0) {
           // (finite and not 0 once the scale of a page comes in)
           const int at = seg * C::kRows + row, pos = wk.rq.pos0 + tok;
           row_factor[at] = fminf(
@@ -577,8 +576,12 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         mbar_wait(&bars->s_full[sb], parity, a.status, abort);
         __syncwarp();
         tc_fence_after();
-        uint32_t s[RG];
-        tmem_ld_n<RG>(tmem + sb * C::kN1 + g * RG + lanes, s);
+        uint32_t s[RG], s_lo[RG];
+#pragma unroll
+        for (int i = 0; i < RG; i += 4) tmem_ld_x4(tmem + sb * C::kN1 + g * RG + i + lanes, s + i);
+        tmem_ld_n<RG>(tmem + sb * C::kN1 + C::kRows + g * RG + lanes, s_lo);
+#pragma unroll
+        for (int r = 0; r < RG; ++r) asm volatile("" : "+r"(s[r]));
         tc_fence_before();
         mbar_arrive(&bars->s_free[sb]);
         const float* sc = scales + n % kScaleSlots * (3 * kTileScales) + (key >> 4);
@@ -588,7 +591,7 @@ attention_keys_kernel(const __grid_constant__ AttnArgs a, const __grid_constant_
         bool over = false;
 #pragma unroll
         for (int r = 0; r < RG; ++r)
-          y[r] = fmaf(__uint_as_float(s[r]), row_factor[words + r] * ks, lift);
+          y[r] = fmaf(__uint_as_float(s[r]) + __uint_as_float(s_lo[r]), row_factor[words + r] * ks, lift);
         if (t * kKeys + kKeys > all_hi || t * kKeys < all_lo) {
 #pragma unroll
           for (int r = 0; r < RG; ++r)
