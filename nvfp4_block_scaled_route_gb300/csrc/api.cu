@@ -1106,7 +1106,7 @@ namespace {
 // 128 tokens of one page and head.  E4M3 rows are 128 bytes or less: with L2 lines
 // promoted to 256, tokens-first caches also fetch the next head's, which is `wide`
 // where that is read at the same time, and else not (64 tokens on up to 16384 keys,
-// pages of 64: a scale per head 184 us, 156 without; a scale per page 127, 132 without).
+// pages of 64: a scale per head 184 us, 156 without; a scale per page 124, 128 without).
 bool make_kv_map(CUtensorMap* map, const void* base, const KvCacheView& c, bool wide) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;

@@ -8,7 +8,7 @@ namespace {
 // the segment that CTA x begins, a thread four dimensions of a row.  With the
 // largest maximum M, o = sum_c 2^(m_c - M) o_c and l likewise, in the order of
 // the CTAs, so results do not depend on timing.  Its data fit the L2; it is bound
-// by latency (3 us of the 8 of one request of 1000 keys, whose launch overlaps
+// by latency (2 us of the 8 of one request of 1000 keys, whose launch overlaps
 // the pieces' kernel).
 template <int D>
 __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a) {
