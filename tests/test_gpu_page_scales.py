@@ -266,6 +266,22 @@ def test_many_requests(nb, n):
     check_attention(nb, Pages(reqs, 1, 64, 16), 2)
 
 
+@pytest.mark.parametrize("hk", [1, 2])
+@pytest.mark.parametrize("batch", [384, 385, 900])
+def test_many_requests_of_wide_heads(nb, hk, batch):
+    """More requests than a block of the few-row kernel has threads, with empty ones between."""
+    reqs = [(0 if i % 7 == 3 else 1 + i % 3, 3 + (i * 37) % 300) for i in range(batch)]
+    check_attention(nb, Pages(reqs, hk, 128, 16), 4 * hk)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("reqs,hk,hq", [([(2, 9000)], 1, 5), ([(1, 100), (1, 20000), (3, 129)], 1, 4),
+                                        ([(4, 30000)], 2, 8), ([(40, 12000)], 1, 2)])
+def test_an_axis_in_many_pieces(nb, reqs, hk, hq, D):
+    """A request's keys over most blocks of the GPU: more pieces than a row has lanes in the join."""
+    check_attention(nb, Pages(reqs, hk, D, 64, True), hq)
+
+
 @pytest.mark.parametrize("n", [2, 40])
 def test_results_are_the_same_bits_from_a_graph_and_another_stream(nb, n):
     pages = Pages([(n, 700), (n, 41)], 2, 128, 16)
