@@ -1,4 +1,4 @@
-// Joining the pieces of paged attention (attn_rows.cu, attn_chunk.cu).
+// Joining the pieces of paged attention (attn_rows.cu, attn_keys.cu, attn_chunk.cu).
 #include "attn.cuh"
 
 namespace nvmoe {
