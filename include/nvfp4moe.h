@@ -726,7 +726,7 @@ int attn_kv_append(const nvmoe_kv_cache* cache, const nvmoe_attn_batch* batch, c
  * to within 2^-8 down to 2^-27 (smaller ones are off by at most 2^-35 of the
  * largest).
  * With scales of pages that holds of the weight times its value's scale, to within
- * 2^-8 down to 2^-22 of the row's largest and 2^-34 of that below.
+ * 2^-8 down to 2^-22 of the row's largest and 2^-31 of that below.
  * On an E4M3 cache an element of q counts to within 2^-17 of its row's largest
  * (bf16 exactly down to 2^-9 of it).
  *   out         bf16 [tokens, q_heads, head_dim] with strides; shares no element

@@ -14,14 +14,15 @@
 // A query is the sum of two E4M3 numbers (8 bits of its elements down to 2^-9 of its
 // row's largest, to within 2^-17 of that below).  A weight is the sum of four, the
 // later ones 2^8, 2^16 and 2^24 times what is left, each with columns of its own in O^T:
-// the products are exact, and weights, fp16 numbers of 11 bits, are right to within 2^-8
-// down to 2^-22 of the row's largest and to within 2^-34 of that below.  (In the sum they
-// go with the scale of their value's page, as a power of two in the exponent; without it,
-// in the row's weight sum.)
+// the products are exact, and of weights, fp16 numbers of 11 bits, nothing is lost down to
+// 2^-17 of their reference; they are right to within 2^-8 down to 2^-22 of the row's
+// largest and to within 2^-31 of that below, where the last numbers are E4M3's small ones.
+// (In the sum they go with the scale of their value's page, as a power of two in the
+// exponent; without it, in the row's weight sum.)
 //
 // A thread holds one key and half of the rows, so the scales of pages are one number for
 // it, and a row's maximum would have to be looked for across threads.  It is not: m is a
-// reference as in the chunk kernel, and only when some thread finds a weight above 2^4
+// reference as in the chunk kernel, and only when some thread finds a weight above 2^2
 // (a barrier with a vote) is the maximum exchanged and O^T rescaled.
 //
 // The chain of a tile (scores to registers, vote, exponentials, four conversions, weights
@@ -54,9 +55,12 @@ constexpr int kTileBytes = kKeys * kD;
 constexpr int kScaleSlots = 8, kTileScales = 8;       // scales of 16 keys each
 constexpr uint32_t kTmemColumns = 128;
 // Powers of two by which a row's maximum may stand above its reference, the maximum when
-// it was set: weights are at most 2^4, what their first number leaves, 2^-4 of them, times
-// 2^8 then at most 2^8 (E4M3 ends at 448; past that it would be cut).
-constexpr float kSlack = 4.0f;
+// it was set.  No number of a weight may pass 448, where E4M3 ends: it would be cut.  A
+// number between 2^e and 2^(e+1) leaves 2^(e-4) at most, the next one is at most 2^(e+4).
+// Below 2^2 the first leaves 2^-3, the second is at most 2^5 and leaves 1, the third at
+// most 2^8; of the fp16 weight's 11 bits that is one, which it holds.  (Below 2^4, half of
+// the weights above 2^3 lose up to 2^-9.9 of themselves in the third and fourth.)
+constexpr float kSlack = 2.0f;
 
 // RG: rows of a softmax group; both have as many.
 template <int RG>

@@ -1,0 +1,79 @@
+"""What attention over pages with scales promises about a single weight, held apart from
+the roundings that hide it elsewhere."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def nb():
+    import __graft_entry__
+    __graft_entry__.build()
+    from nvfp4_block_scaled_route_gb300 import binding
+    return binding
+
+
+# ------------------------------------------------- weights of single tokens --
+def two_keys(nb, group, low, high, a, seed):
+    """Attention over two keys that count, of which the first has weight 1 and value a_d in
+    dimension d, the second, a tile later, a weight w spread over its logarithm between 2^low
+    and 2^high and the value 1.  (out, w) in 64 bits, [B, heads, group, 128] and [.., 1].
+
+    The other keys have scores of -200 and less: weights of 0.  512 requests of 4 key heads
+    and two tiles each: most of them are not cut, so a row's reference is that of its first
+    tile, score 0, when the second comes in."""
+    B, H, D, page = 512, 4, 128, 128
+    g = torch.Generator().manual_seed(seed)
+    k = torch.zeros(2 * B, page, H, D)
+    k[..., 1] = -256.0
+    k[:, 0] = 0.0
+    k[B:, 0, :, 0] = 1.0
+    v = torch.zeros(2 * B, page, H, D)
+    v[:B, 0] = a
+    v[B:, 0] = 1.0
+    ones = torch.ones(2 * B, H)
+    # the score of the second key is q k_scale: any scale will do
+    k_scale = ones.clone()
+    k_scale[B:] = 1 + torch.rand(B, H, generator=g)
+    y = low + (high - low) * torch.rand(B, H, group, generator=g)
+    q = torch.zeros(B, H, group, D)
+    q[..., 0] = y * float(np.log(2)) / k_scale[B:, :, None]
+    q[..., 1] = 1.0
+    q = q.bfloat16()
+    w = torch.exp(q[..., :1].double() * k_scale[B:, :, None, None].double())
+    cache = nb.PagedKVCache(k.to(torch.float8_e4m3fn).to(DEV), v.to(torch.float8_e4m3fn).to(DEV),
+                            k_scale=k_scale.to(DEV), v_scale=ones.to(DEV))
+    table = torch.stack([torch.arange(B), torch.arange(B, 2 * B)], 1).int().to(DEV)
+    batch = nb.AttnBatch(torch.arange(B + 1, dtype=torch.int32, device=DEV),
+                         torch.full((B,), 2 * page, dtype=torch.int32, device=DEV), table, max_new=1)
+    out = nb.paged_attention(q.flatten(1, 2).to(DEV), cache, batch, scale=1.0)
+    return out.double().cpu().unflatten(1, (H, group)), w
+
+
+@pytest.mark.parametrize("group", [7, 8, 14, 16])
+def test_weights_above_their_reference(nb, group):
+    """Weights of up to 2^4 times the first are fp16 numbers, right to within 2^-11: values
+    of the other sign take away what is common to both keys.  Of out = (a + w) / (1 + w) the
+    first weight is exact, w is off by 2^-11 of itself and 2^-18 for the score, its
+    exponential and the sums in 32 bits, the output by 2^-8."""
+    a = torch.tensor([1.0, 1.5, 2.0, 3.0, 4.0, 4.5, 5.0, 5.5, 6.0, 6.5, 7.0, 7.5, 8.0, 9.0, 10.0, 11.0,
+                      12.0, 13.0, 14.0, 15.0, 16.0]).repeat(7)[:128].neg()
+    out, w = two_keys(nb, group, 0.0, 4.0, a, group)
+    want = (a.double() + w) / (1 + w)
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 * w + 2.0 ** -18 * (a.double().abs() + w)) / (1 + w)
+    assert ((out - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("group", [7, 14])
+def test_weights_far_below_their_reference(nb, group):
+    """Weights down to 2^-22 of the largest are right to within 2^-8, those below to within
+    2^-31 of the largest; the output by 2^-8."""
+    for low, high in ((-22.0, -2.0), (-34.0, -22.0)):
+        out, w = two_keys(nb, group, low, high, torch.zeros(128), group)
+        want = w / (1 + w)
+        bound = 2.0 ** -7 * want + 2.0 ** -18 * want + torch.where(w < 2.0 ** -22, 2.0 ** -31, 0.0)
+        assert ((out - want).abs() <= bound).all()
