@@ -813,8 +813,8 @@ int attn_plan_pages(int32_t* ring, int64_t ring_size, const int32_t* pool_state,
  *   rows that are no distributions, p).
  * Given numbers that are uniform on [0, 1), the tokens have the target's
  * distribution.  Probabilities are taken within [0, 1], NaN as 0; rows need not
- * sum to 1.  accept_u * q < p is decided exactly, running sums are off by 2^-44
- * or less of themselves.
+ * sum to 1.  accept_u * q < p is decided exactly, running sums are off by 2^-38
+ * or less of themselves (2^-45 as a rule).
  *   target, draft   [rows, vocab] of dtype (NVMOE_F32 or NVMOE_BF16) with a
  *                   stride between rows (elements);  draft NULL: tokens that
  *                   were guessed for sure, q = 1 at the token and 0 elsewhere

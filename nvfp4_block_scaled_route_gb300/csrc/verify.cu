@@ -16,9 +16,16 @@
 //
 // Which token that is must not hang on how a sum is rounded: a row of 2^17 tokens has
 // as many borders, and fp32 sums would put the wrong token out for every few hundredth
-// row.  Sums are pairs of fp32 numbers, value and rest: p - q is exact that way, and a
-// sum is off by some 2^-45 of itself.  (fp64, of which an SM has two adds a cycle, took
-// 39 us for 64 requests of 129280 tokens even where it only joined lanes and warps.)
+// row.  Sums are pairs of fp32 numbers, value and rest, and p - q is exact that way.  What
+// they lose grows with the square of their length n, where the rest takes what the value
+// lost without being cut back: n (n + 3) 2^-48 of themselves at most (with q: without it
+// half).  So a thread with more than 24 additions to each of its sums puts blocks of 8
+// together, 32 of them as pairs that are cut back (3 * 2^-48 for each), and these in fp64.
+// With the joins of lanes and warps, 15 deep, and the ends of a ragged row, running sums are
+// off by 2^-38 of themselves at most, for every vocabulary that memory holds; as a rule,
+// when errors do not all point one way, by 2^-45.  (fp64 throughout, of which an SM has two
+// adds a cycle, took more than twice the time of the pairs even where it only joined lanes
+// and warps.)
 //
 // Those 64 requests take 17 us, of which 6 are what two requests of few tokens take (the
 // launch, the loads before the row is known, the joins): loads are asked for one by one as
@@ -58,10 +65,19 @@ __device__ __forceinline__ Sum operator-(const Sum& x, const Sum& y) {
 __device__ __forceinline__ bool operator>(const Sum& x, const Sum& y) {
   return x.hi > y.hi || (x.hi == y.hi && x.lo > y.lo);
 }
+__device__ __forceinline__ double wide(const Sum& x) { return static_cast<double>(x.hi) + x.lo; }
+__device__ __forceinline__ Sum narrow(double x) {
+  const float hi = static_cast<float>(x);
+  return {hi, static_cast<float>(x - hi)};
+}
 __device__ __forceinline__ bool positive(const Sum& x) { return x.hi > 0.0f; }
 __device__ __forceinline__ Sum shfl(const Sum& x, int lane) {
   return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
+
+// Additions to a thread's sum that need no blocks; additions of a block, blocks of a
+// stretch.
+constexpr int kPlain = 24, kBlock = 8, kBlocks = 32;
 
 // Two sums side by side (one instruction for both), a lane's while it runs over a row.
 struct Sums {
@@ -86,6 +102,8 @@ struct Sums {
 template <typename T>
 struct Row {
   static constexpr int kVec = 16 / sizeof(T);
+  static constexpr int kAdds = kVec / 4;               // to each of a thread's sums, of a vector
+  static constexpr int kStretch = kBlocks * kBlock / kAdds;      // vectors
   const T* p;
   const T* q;                // null: p alone
   int vocab, without;        // a token that does not count, or -1
@@ -143,10 +161,13 @@ struct Row {
   }
 
   // A lane's sum over the whole vectors v0, v0 + step, .. below v1.  The next kAhead are on
-  // their way at any time.
-  template <bool DIFFERENCE, bool TOGETHER, int kAhead>
+  // their way at any time.  LONG: put together from blocks.
+  template <bool LONG, bool DIFFERENCE, bool TOGETHER, int kAhead>
   __device__ __forceinline__ Sum sum_of(int v0, int v1, int step) const {
     const int drops = !DIFFERENCE && without >= 0 ? (without + shift) / kVec : -1;
+    static_assert(kBlock % (kAhead * kAdds) == 0, "blocks of whole turns");
+    Sum total = {0.0f, 0.0f};
+    int added = 0;
     Sums s[2];
     uint4 pv[kAhead], qv[kAhead];
     const auto fetch = [&](int u, int v) {
@@ -184,10 +205,16 @@ struct Row {
         }
         fetch(u, v + (u + kAhead) * step);
       }
+      added += kAhead * kAdds;
+      if (LONG && (added % kBlock == 0 || v + kAhead * step >= v1)) {
+        total = total + (s[0].value() + s[1].value());
+        s[0] = s[1] = Sums{};
+      }
     }
-    return s[0].value() + s[1].value();
+    return LONG ? total : s[0].value() + s[1].value();
   }
   // The same over all vectors; the row's first and last, if not whole, element by element.
+  template <bool LONG>
   __device__ __forceinline__ Sum sum(int v0, int v1, int step) const {
     const int whole = (vocab + shift) / kVec;           // vectors up to the last whole one's end
     Sum edge = {0.0f, 0.0f};
@@ -202,9 +229,23 @@ struct Row {
       elements(0, kVec - shift);
       v0 = step;
     }
-    return edge + (q == nullptr ? sum_of<false, true, kAhead>(v0, v1, step)
-                                : together ? sum_of<true, true, kAhead>(v0, v1, step)
-                                           : sum_of<true, false, 1>(v0, v1, step));
+    const auto stretch = [&](int end) {
+      return q == nullptr ? sum_of<LONG, false, true, kAhead>(v0, end, step)
+                          : together ? sum_of<LONG, true, true, kAhead>(v0, end, step)
+                                     : sum_of<LONG, true, false, 1>(v0, end, step);
+    };
+    if (!LONG) return edge + stretch(v1);
+    const bool one = v0 + kStretch * step >= v1;
+    double far = 0.0;                                   // of the stretches before
+#pragma unroll 1
+    while (true) {
+      edge = edge + stretch(min(v1, v0 + kStretch * step));
+      if (one) return edge;
+      far += wide(edge);
+      edge = Sum{0.0f, 0.0f};
+      v0 += kStretch * step;
+      if (v0 >= v1) return narrow(far);
+    }
   }
 };
 
@@ -229,7 +270,7 @@ __device__ __forceinline__ int pick(const Sum& upto, const Sum& own, const Sum& 
   return any != 0 ? 31 - __clz(any) : -1;
 }
 
-template <typename T>
+template <typename T, bool LONG>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(const VerifyArgs a) {
   __shared__ Sum run_sum[2][kMaxCtas * kWarps];          // of all CTAs' warps
   __shared__ Sum warp_sum[kWarps];
@@ -299,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   constexpr int kPer = kMaxCtas * kWarps / 32;
   Sum own[kPer], mine, upto, whole;
   for (int round = 0; round < 2; ++round) {
-    Sum s = row.sum(v0 + lane, v1, 32);
+    Sum s = row.template sum<LONG>(v0 + lane, v1, 32);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       s = s + Sum{__shfl_xor_sync(0xFFFFFFFFu, s.hi, o), __shfl_xor_sync(0xFFFFFFFFu, s.lo, o)};
@@ -357,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   const int w0 = static_cast<int>(vectors * at / runs), w1 = static_cast<int>(vectors * (at + 1) / runs);
   const int per = (w1 - w0 + kThreads - 1) / kThreads;
   const int a0 = min(w1, w0 + static_cast<int>(threadIdx.x) * per), a1 = min(w1, a0 + per);
-  mine = row.sum(a0, a1, 1);
+  mine = row.template sum<LONG>(a0, a1, 1);
   const Sum in_warp = scan_lanes(mine);
   if (lane == 31) warp_sum[warp] = in_warp;
   __syncthreads();
@@ -372,14 +413,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) draft_verify_kernel(cons
   // ---- its elements, a lane each ----
   const int e0 = max(0, __shfl_sync(0xFFFFFFFFu, a0, l) * Row<T>::kVec - row.shift);
   const int e1 = min(a.vocab, __shfl_sync(0xFFFFFFFFu, a1, l) * Row<T>::kVec - row.shift);
+  double done = LONG ? wide(before) : 0.0;
   int token = -1;
   for (int e = e0; e < e1; e += 32) {
     mine = e + lane < e1 ? row.weight(e + lane) : Sum{0.0f, 0.0f};
-    upto = before + scan_lanes(mine);
+    const Sum here = scan_lanes(mine);
+    upto = before + here;
     l = pick(upto, mine, x, &passes);
     if (l >= 0) token = e + l;
     if (passes) break;
-    before = shfl(upto, 31);
+    if (LONG) {                                         // (these may be thousands)
+      done += wide(shfl(here, 31));
+      before = narrow(done);
+    } else {
+      before = shfl(upto, 31);
+    }
   }
   if (lane == 0) a.next_token[r] = token;
 }
@@ -400,6 +448,9 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
   while (ctas < kMaxCtas && a.vocab > int64_t{ctas} * (int64_t{a.batch} * ctas <= sms ? 4096 : 8192) &&
          int64_t{a.batch} * (ctas + 1) <= (ctas < 2 ? places : places * 15 / 16))
     ++ctas;
+  // additions to each of a thread's sums
+  const int64_t run = ceil_div(int64_t{a.vocab} / Row<T>::kVec + 2, ctas * kWarps);
+  const bool plain = ceil_div(run, 32) * Row<T>::kAdds <= kPlain;
   // its start overlaps the end of the kernel before
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -412,7 +463,9 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, draft_verify_kernel<T>, a);
+  // (blocks for all: 64 requests of 129280 tokens 17.7 us where this takes 17.2)
+  return cudaLaunchKernelEx(
+      &cfg, plain ? draft_verify_kernel<T, false> : draft_verify_kernel<T, true>, a);
 }
 
 }  // namespace

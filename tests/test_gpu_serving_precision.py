@@ -1,5 +1,5 @@
-"""What attention over pages with scales promises about a single weight, held apart from
-the roundings that hide it elsewhere."""
+"""What the serving operators promise about single weights and running sums, held apart
+from the roundings that hide them elsewhere."""
 import numpy as np
 import pytest
 import torch
@@ -77,3 +77,53 @@ def test_weights_far_below_their_reference(nb, group):
         want = w / (1 + w)
         bound = 2.0 ** -7 * want + 2.0 ** -18 * want + torch.where(w < 2.0 ** -22, 2.0 ** -31, 0.0)
         assert ((out - want).abs() <= bound).all()
+
+
+# --------------------------------------------------- sums of the vocabulary --
+def numbers_away_from_borders(weights, count, runs, rng, margin):
+    """fp32 numbers u for which the token is decided: u times the whole is `margin` of it or
+    more away from the running sums on either side.  (u, tokens)."""
+    upto = np.cumsum(weights.astype(np.longdouble))
+    whole, V = upto[-1], len(weights)
+    us, tokens = [], []
+    while len(us) < count:
+        # behind the large numbers at the front of a run
+        at = rng.integers(0, runs) * (V // runs) + rng.integers(128, V // runs)
+        u = np.float32(upto[at] / whole)
+        x = np.longdouble(u) * whole
+        i = int(np.searchsorted(upto, x, side="right"))
+        if 0 < i < V and min(x - upto[i - 1], upto[i] - x) >= margin * whole:
+            us.append(u)
+            tokens.append(i)
+    return torch.tensor(np.array(us)), tokens
+
+
+@pytest.mark.parametrize("requests,runs,vocab", [(400, 8, 1 << 21), (400, 8, 1 << 20), (30, 64, 24 * 8192 - 64),
+                                                 (30, 64, 1 << 21)])
+@pytest.mark.parametrize("given", [False, True])
+def test_running_sums_of_small_numbers_behind_large_ones(nb, given, requests, runs, vocab):
+    """Running sums are off by 2^-38 of themselves at most, however many small numbers come
+    behind large ones: 400 requests have a CTA each, and each of its threads adds up
+    thousands of numbers (30: eight CTAs).  The whole and the running sum may both be off, so
+    numbers that are 2^-37 away from the borders have to find their token."""
+    if given and requests * vocab > 1 << 29:
+        vocab >>= 1
+    rng = np.random.default_rng(vocab)
+    weights = np.full(vocab, 1.37 * 2.0 ** -34, np.float32)
+    weights.reshape(runs, -1)[:, :128] = 0.91 * 2.0 ** -7 / runs
+    rows, p, draft = requests, torch.from_numpy(weights), None
+    q_start = torch.arange(requests + 1, dtype=torch.int32, device=DEV)
+    if given:                                              # p - q, which 24 bits do not hold
+        p, q = torch.from_numpy(weights * np.float32(1.7)), torch.from_numpy(weights * np.float32(0.31))
+        p[5] = q[5] = 0.0                                  # the drafted token: never stands
+        weights = p.double().numpy() - q.double().numpy()
+        rows, q_start = 2 * requests, 2 * q_start
+        draft = q.to(DEV).expand(rows, vocab).contiguous()
+    u, want = numbers_away_from_borders(weights, requests, runs, rng, 2.0 ** -37)
+    batch = nb.AttnBatch(q_start, torch.full((requests,), 9, dtype=torch.int32, device=DEV),
+                         torch.zeros(requests, 1, dtype=torch.int32, device=DEV), max_new=2)
+    target = p.to(DEV).expand(rows, vocab).contiguous()
+    accepted, nxt = nb.draft_verify(target, draft, torch.full((rows,), 5, dtype=torch.int32, device=DEV), batch,
+                                    torch.full((rows,), 0.5, device=DEV), u.to(DEV))
+    assert accepted.tolist() == [0] * requests
+    assert nxt.tolist() == want
