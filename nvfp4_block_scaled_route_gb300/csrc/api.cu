@@ -1142,8 +1142,8 @@ size_t attn_layout(int batch, int64_t tokens, int max_new, int q_heads, int kv_h
   a->max_blocks = static_cast<int>(std::min<int64_t>(blocks, INT32_MAX - 1));
   a->plan_here = batch <= kAttnPlanHere && blocks <= kAttnPlanHere;
   a->status = c.take<int>(kStatusBytes);
-  // (two CTAs an SM take few rows over pages with scales)
-  const size_t ctas = few ? 2 * kMaxGrid : kMaxGrid;
+  // (few rows of 128-wide heads over pages with scales: what the cache is is not known here)
+  const size_t ctas = few && D == 128 ? std::max(kMaxGrid, kAttnKeysGrid) : kMaxGrid;
   a->pieces = c.take<AttnPiece>(ctas * sizeof(AttnPiece));
   a->piece_ml = c.take<float2>(2 * ctas * a->piece_rows * sizeof(float2));
   a->piece_o = c.take<float>(2 * ctas * static_cast<size_t>(a->piece_rows) * D * sizeof(float));
@@ -1212,7 +1212,7 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
   const int nsm = sm_count();
   if (nsm <= 0) return fail(cudaErrorNoDevice);
   // shares of the work
-  const int grid = few && by_keys ? 2 * std::min(nsm, kMaxGrid) : std::min(nsm, kMaxGrid);
+  const int grid = few && by_keys ? std::min(2 * nsm, kAttnKeysGrid) : std::min(nsm, kMaxGrid);
   cudaError_t e;
   if (few) {
     e = counted(by_keys ? launch_attention_keys(a, map_k, map_v, grid, stream)

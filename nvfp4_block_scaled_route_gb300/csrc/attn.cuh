@@ -160,7 +160,9 @@ constexpr int kAttnFewRows = 16;
 // 128 tokens of one page and head.
 cudaError_t launch_attention_rows(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
-// The same for pages with scales and 128-wide heads.
+// The same for pages with scales and 128-wide heads, on an even number of CTAs: two for
+// each of the 152 SMs.
+constexpr int kAttnKeysGrid = 304;
 cudaError_t launch_attention_keys(const AttnArgs& args, const CUtensorMap& map_k,
                                   const CUtensorMap& map_v, int grid, cudaStream_t stream);
 // Blocks and requests up to which the chunk kernel's CTAs plan for themselves: a

@@ -218,3 +218,13 @@ def test_the_extension_passes_arguments_as_they_are(nb):
     rope = [FAKE, 512, 128, 4, FAKE, 256, 128, 2, 3, 128, FAKE, FAKE, 16, 128, 0, FAKE, FAKE, 1e-6, FAKE, 512, 128,
             FAKE, 256, 128, FAKE, 0, None]
     assert host.attn_qk_norm_rope(*rope) == SMALL
+
+
+@pytest.mark.parametrize("head_dim,ctas", [(64, 256), (128, 304)])
+@pytest.mark.parametrize("rows", [1, 7, 16])
+def test_the_workspace_of_few_rows_holds_the_pieces_that_there_are(nb, head_dim, ctas, rows):
+    """Two pieces of every CTA, each a row's sums with its maximum and weight sum: 256 CTAs, or
+    two on each of 152 SMs for the kernel that takes 128-wide heads over pages with scales."""
+    size = nb.lib().attn_paged_workspace_size(64, 64, 1, 8 * rows, 8, head_dim)
+    pieces = 2 * ctas * rows * (head_dim * 4 + 8)
+    assert pieces <= size <= pieces + 32768
