@@ -788,9 +788,11 @@ int attn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_str
  * need no page go on.  A request with kv_before outside [0, max_pages *
  * page_size], cached outside [0, kv_before] or kv_len past max_pages *
  * page_size is left as it is (kv_len = kv_before, no new rows):
- * NVMOE_ERR_DEVICE_BAD_INDEX, as for a pool_state outside the ring (nothing is
- * taken) and pages given back that the ring has no room for (dropped).  Run
- * again from the same kv_before, cached and pool_state, a plan is the same.
+ * NVMOE_ERR_DEVICE_BAD_INDEX, as for pages given back that the ring has no room
+ * for (dropped), and for a pool_state outside the ring: nothing is taken, pages
+ * given back are dropped, ring and pool_state stay as they are, and a
+ * pool_state_out of its own becomes {0, 0}.  Run again from the same kv_before,
+ * cached and pool_state, a plan is the same.
  * Limits: page_size a power of two, 16 .. 1024; max_pages * page_size < 2^31;
  * ring_size and rows below 2^31. */
 int attn_plan_pages(int32_t* ring, int64_t ring_size, const int32_t* pool_state,

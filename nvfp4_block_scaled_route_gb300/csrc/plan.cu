@@ -105,13 +105,14 @@ __global__ void __launch_bounds__(kThreads, 1) plan_pages_kernel(const PlanArgs 
   };
   read(static_cast<int>(threadIdx.x));
   long long ring0 = a.pool.state[0], free = a.pool.state[1];
-  if (ring0 < 0 || ring0 >= a.pool.size || free < 0 || free > a.pool.size) {
-    record_status(a.status, kErrBadIndex);              // nothing can be taken
-    ring0 = free = 0;
+  long long size = a.pool.size;
+  if (ring0 < 0 || ring0 >= size || free < 0 || free > size) {
+    record_status(a.status, kErrBadIndex);              // nothing can be taken or given back
+    ring0 = free = size = 0;
   }
   const auto ring_at = [&](long long i) {               // (i < 2 * size)
     i += ring0;
-    if (i >= a.pool.size) i -= a.pool.size;
+    if (i >= size) i -= size;
     return a.pool.ring + i;
   };
 
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_pages_kernel(const PlanArgs 
     // ---- pages taken, and given back (from the last thread on: the rows begin with the
     // first) ----
     const long long taken = done_take - begin_take;
-    const long long most = a.pool.size - free;          // places behind the ring's end
+    const long long most = size - free;                 // places behind the ring's end
     const long long given = max(0ll, min(done_give, most) - begin_give);
 #pragma unroll 1
     for (long long v = workers - 1 - worker; v < taken + given; v += workers) {
@@ -218,13 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1) plan_pages_kernel(const PlanArgs 
     __syncthreads();                                    // before the next pass's words
   }
   if (worker == 0) {
-    if (done_give > a.pool.size - free) {
+    if (done_give > size - free) {
       record_status(a.status, kErrBadIndex);
-      done_give = a.pool.size - free;
+      done_give = size - free;
     }
     a.q_start[a.batch] = static_cast<int32_t>(done_rows);
+    if (size == 0 && a.pool.state_out == a.pool.state) return;    // (a bad pool stays as it was)
     ring0 += done_take;
-    a.pool.state_out[0] = static_cast<int32_t>(ring0 >= a.pool.size ? ring0 - a.pool.size : ring0);
+    a.pool.state_out[0] = static_cast<int32_t>(ring0 >= size ? ring0 - size : ring0);
     a.pool.state_out[1] = static_cast<int32_t>(free - done_take + done_give);
   }
 }

@@ -135,6 +135,31 @@ def test_plan_of_a_bad_pool(nb):
     assert want[6] == [3, 7] and want[7] == {BAD_INDEX}
 
 
+@pytest.mark.parametrize("state", [[-1, 3], [9, 3], [0, 10], [0, -1]])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,rows", [(5, 40), (1200, 4000)])
+def test_plan_on_a_bad_pool_leaves_it_as_it_is(nb, state, in_place, B, rows):
+    """Pages given back have no place to go: the ring stays, and a pool planned in place
+    says the same the next time."""
+    pool, out = nb.PagePool(ints(range(100, 109)), ints(state)), ints([-5, -5])
+    before, table = ints([40] * B), ints([[3 * r, 3 * r + 1, 3 * r + 2, -1] for r in range(B)])
+    new = [-1, 1, 5, -1, 9] * (B // 5)
+    batch = nb.AttnBatch(ints([-5] * (B + 1)), ints([-5] * B), table, max_new=9)
+    pos, slots = ints([-5] * rows), ints([-5] * rows, torch.int64)
+    for _ in range(2):
+        ws = nb.attn_workspace()
+        nb.plan_pages(pool, batch, 16, ints(new), kv_before=before, state_out=None if in_place else out, positions=pos,
+                      slots=slots, ws=ws)
+        assert nb.read_status(ws) in (BAD_INDEX, RANGE)
+        assert pool.ring.tolist() == list(range(100, 109)) and pool.state.tolist() == state
+        assert in_place or out.tolist() == [0, 0]
+        # 41 and 45 tokens fit the pages that are there, 49 do not
+        assert batch.kv_len.tolist() == [0, 41, 45, 0, 40] * (B // 5)
+        assert int(batch.q_start[-1]) == 6 * (B // 5)
+        assert slots[:6].tolist() == [3 * 16 + 40] + [6 * 16 + i for i in range(40, 45)] and pos[0] == 40
+        assert slots[6 * (B // 5):].eq(-5).all()
+
+
 def test_plan_of_nothing(nb):
     s = Requests(random.Random(4), 0, 16, 4, 3, 0)
     pool = nb.PagePool(ints(s.ring), ints(s.state))
