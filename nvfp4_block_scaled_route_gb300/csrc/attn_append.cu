@@ -180,8 +180,9 @@ page_append_kernel(const RopeArgs a, const PageUnits units) {
       bf16x4_to_f32x2(raw[i][1], x[1]);
       if (!value) {
         HeadTurn<D, PAIRS> turn;
-        turn.load(a.tr, w, a.tr.k_weight != nullptr, false, sub, p0 + j);
-        turn.apply(x, a.tr.eps, mask);
+        const bool turned = sub * 8 < a.tr.rotary_dim;
+        turn.load(a.tr, w, turned, sub, p0 + j);
+        turn.apply(x, turned, a.tr.k_weight != nullptr, a.tr.eps, mask);
         if (rounds == 1) {
           held[(2 * i) * THREADS] = reinterpret_cast<const float4&>(x[0]);
           held[(2 * i + 1) * THREADS] = reinterpret_cast<const float4&>(x[1]);
