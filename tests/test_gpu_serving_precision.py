@@ -127,3 +127,45 @@ def test_running_sums_of_small_numbers_behind_large_ones(nb, given, requests, ru
                                     torch.full((rows,), 0.5, device=DEV), u.to(DEV))
     assert accepted.tolist() == [0] * requests
     assert nxt.tolist() == want
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("requests,vocab", [(3, 300001), (320, 40003), (300, 600011)])
+def test_long_rows_at_any_alignment(nb, requests, vocab, given, dtype):
+    """Sums from blocks and from stretches of blocks, rows that begin anywhere, the draft's at
+    another place of 16 bytes than the target's."""
+    g = torch.Generator(device=DEV).manual_seed(vocab)
+    drafts = 1 if requests > 9 else 4
+    rows = requests * (drafts + 1)
+
+    def distributions(pad):
+        wide = torch.zeros(rows, vocab + 9, device=DEV, dtype=dtype)
+        x = torch.randn(1, vocab, generator=g, device=DEV).expand(rows, vocab)
+        row = torch.softmax(2 * x[:1] + torch.randn(1, vocab, generator=g, device=DEV), 1)
+        wide[:, pad:pad + vocab] = row
+        return wide[:, pad:pad + vocab]
+    p, q = distributions(1), distributions(2) if given else None
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    u, v = torch.rand(rows, generator=g, device=DEV), torch.rand(requests, generator=g, device=DEV)
+    q_start = torch.arange(0, rows + 1, drafts + 1, dtype=torch.int32, device=DEV)
+    batch = nb.AttnBatch(q_start, torch.full((requests,), 9, dtype=torch.int32, device=DEV),
+                         torch.zeros(requests, 1, dtype=torch.int32, device=DEV), max_new=drafts + 1)
+    accepted, nxt = nb.draft_verify(p, q, tokens, batch, u, v)
+    # one row of probabilities for all: what is drawn from it, in 64 bits
+    pd = p[0].double()
+    weights = (pd - q[0].double()).clamp(min=0) if given else pd
+    for r in range(requests):
+        k = 0
+        while k < drafts:
+            x = int(tokens[r * (drafts + 1) + k + 1])
+            if not float(u[r * (drafts + 1) + k]) * (float(q[0, x]) if given else 1.0) < float(p[0, x]):
+                break
+            k += 1
+        w = pd if k == drafts else weights
+        if k < drafts and not given:
+            w = pd.clone()
+            w[int(tokens[r * (drafts + 1) + k + 1])] = 0
+        upto = w.cumsum(0)
+        want = int(torch.searchsorted(upto, (float(v[r]) * upto[-1]).reshape(1), right=True))
+        assert (int(accepted[r]), int(nxt[r])) == (k, want), r
