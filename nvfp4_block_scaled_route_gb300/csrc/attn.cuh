@@ -1,5 +1,5 @@
-// Shared by the attention operators (attn_rope.cu, attn_rows.cu, attn_chunk.cu,
-// attn_join.cu): the views of head rows, paged cache and batch that the C-ABI
+// Shared by the attention operators (attn_rope.cu, attn_append.cu, attn_rows.cu,
+// attn_keys.cu, attn_chunk.cu, attn_join.cu): the views of head rows, paged cache and batch that the C-ABI
 // layer fills in, and the device helpers that read them.
 #pragma once
 

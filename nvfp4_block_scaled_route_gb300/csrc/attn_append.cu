@@ -31,8 +31,8 @@ struct PageUnits {
 // A thread takes R tokens' eight elements: values stay in registers as they came, turned
 // keys go to shared memory as fp32 until the scale is known.  (64 registers a thread, as
 // the queries' rows take, which are most of the bytes in the same launch.  Keys turned a
-// second time instead: 165 us where this takes 152, three prompts of 8192 tokens at most,
-// 64 + 8 + 8 heads of 128.)
+// second time instead: 165 us where this then took 152, 148 by now, three prompts of 8192
+// tokens at most, 56 + 8 + 8 heads of 128.)
 constexpr int kR = 4;
 constexpr int kHeldBytes = kR * 8 * 4;                  // a thread
 

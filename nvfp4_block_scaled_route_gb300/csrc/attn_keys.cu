@@ -28,9 +28,9 @@
 // The chain of a tile (scores to registers, vote, exponentials, four conversions, weights
 // to shared memory) takes 1300 cycles of latency and its bytes 1080 of HBM, and between
 // two segments the queries' way in and the rows' way out take some 4000, so an SM runs
-// two CTAs, with half of the shared memory each (one: 138 us where two take 126; one with
-// two tiles in the work at a time: 142).  64 tokens on up to 16384 keys, 56 query and 8
-// key heads, pages of 16: 122 us, 5.6 TB/s (116 with heads first);
+// two CTAs, with half of the shared memory each (at a time when two took 126 us, one took
+// 138, and one with two tiles in the work at a time 142).  64 tokens on up to 16384 keys,
+// 56 query and 8 key heads, pages of 16: 122 us, 5.6 TB/s (117 with heads first);
 // attention_rows_kernel, which turns the values to 16 bits, took 200.  Up to 1000 keys: 28
 // us.  Of a request with one tile (7.6 us) 6.5 are this kernel, most of them the fetching
 // of code that runs once and six loads on one another, so values of rows are joined over
